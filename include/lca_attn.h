@@ -251,6 +251,116 @@ LCA_API lca_status lca_cad_plan(const int32_t* doc_len, int32_t n_docs, int32_t 
                                 int32_t max_shard, double tolerance, lca_cad_shard* shards, int32_t max_shards,
                                 int32_t* n_shards, int64_t* server_cells);
 
+/* ------------------------------------------------------------------ paged cache
+ * Serving: keys and values of earlier tokens live in pages of a cache, and a
+ * batch of requests adds new tokens to it.  lca_paged_plan gives every new
+ * token a place, lca_paged_write stores its key and value there, and
+ * lca_attn_paged attends the new tokens to their requests' keys.  Lengths,
+ * tables and page lists are read from device memory when the kernels run, so
+ * a captured graph of the three calls serves later batches of the same shape.
+ * A block table has one row per request: entry c is the page that holds the
+ * request's tokens [c * page_size, (c + 1) * page_size). */
+typedef enum { LCA_BF16 = 0, LCA_F16 = 1 } lca_dtype;
+
+/* Token t of page p, KV head h starts at element
+ *     p * page_stride + t * token_stride + h * head_stride
+ * of k and of v (device or managed memory); its d elements are contiguous.
+ * Any order of the axes is fine ([page][token][head] and
+ * [page][head][token] among them, and K and V as parts of one array), as long
+ * as the rows of k, and those of v, do not overlap.  Strides are multiples of
+ * 8 elements, 8 to 2^38; k and v are 16-byte aligned; d must be 128.
+ * page_size is a multiple of 8 (LCA_ERR_UNSUPPORTED otherwise) and
+ * n_pages * page_size < 2^31. */
+typedef struct {
+  void* k;
+  void* v;
+  int32_t n_pages, page_size, Hkv, d;
+  int32_t dtype; /* lca_dtype */
+  int64_t page_stride, token_stride, head_stride;
+} lca_paged_cache;
+
+/* The batch's bookkeeping.  Request i has ctx_len[i] tokens in the cache and
+ * new_len[i] new ones (0 allowed).  With have = ceil(ctx / page_size) and
+ * want = ceil((ctx + new) / page_size), entries [have, want) of its table row
+ * are filled with the next unused entries of free_pages, request after
+ * request, starting at free_pages[taken[0]]; the other entries keep their
+ * values.  Outputs (all int32, device):
+ *   q_start [n_seq + 1]  first row of each request's new tokens, packed
+ *   k_len [n_seq]        ctx + new
+ *   slots [n_rows]       page * page_size + offset of each new token; -1 for
+ *                        rows behind the last request
+ *   positions [n_rows]   position of each new token in its request; 0 behind
+ *   state [4]            {entries of free_pages used so far, pages that were
+ *                        missing, requests whose lengths were unusable, new
+ *                        tokens}
+ * The call depends on nothing it writes, so it can be repeated.  Pass
+ * state[0:1] of one call as `taken` of the next.  What cannot be served is
+ * answered on the device, without a fault: an entry of free_pages outside
+ * [0, n_pages) or past n_free becomes table entry -1, and a token on a page
+ * outside [0, n_pages) gets slot -1; a negative length counts as 0; tokens
+ * past max_pages * page_size get slot -1 and k_len stops there; rows past
+ * n_rows are dropped (q_start stops there).
+ * ctx_len, new_len [n_seq], free_pages [n_free], taken [1]: int32, device.
+ * block_table: int32, device, n_seq rows of max_pages entries, table_stride
+ * entries apart (>= max_pages).  n_rows: rows of the packed batch, at least
+ * the new tokens; 0 to 2^31 - 1.  Outputs must not overlap one another or an
+ * input (LCA_ERR_INVALID_ARG). */
+LCA_API lca_status lca_paged_plan(const int32_t* ctx_len, const int32_t* new_len, int32_t n_seq,
+                                  const int32_t* free_pages, int32_t n_free, const int32_t* taken,
+                                  int32_t* block_table, int64_t table_stride, int32_t max_pages, int32_t page_size,
+                                  int32_t n_pages, int32_t n_rows, int32_t* q_start, int32_t* k_len, int32_t* slots,
+                                  int32_t* positions, int32_t* state, void* stream);
+
+/* Stores row r of k and v (device, the cache's dtype, Hkv heads of d dense
+ * elements, rows k_stride and v_stride elements apart) as token
+ * slots[r] % page_size of page slots[r] / page_size.  A row whose slot lies
+ * outside [0, n_pages * page_size) is skipped (padding rows have -1); the
+ * slots of the other rows must differ (of two rows with one slot, either may
+ * be stored, or parts of both).  Row strides are multiples of 8 elements and
+ * k, v 16-byte aligned; k and v must not overlap the cache. */
+LCA_API lca_status lca_paged_write(const void* k, const void* v, int64_t k_stride, int64_t v_stride,
+                                   const int32_t* slots, int32_t n_rows, const lca_paged_cache* cache, void* stream);
+
+typedef struct {
+  int32_t Tq, Hq, n_seq;
+  int32_t max_pages;    /* entries of a table row                            */
+  int64_t table_stride; /* entries between table rows, >= max_pages          */
+  int64_t q_stride;     /* elements between rows of q, >= Hq * d, multiple of 8 */
+  int32_t max_q_len;    /* no request has more new tokens than this; 0: not
+                           known.  Chooses kernels, never results.           */
+  float scale;          /* softmax scale; 0 selects 1/sqrt(d)                */
+} lca_paged_shape;
+
+/* Attention of new tokens over the cache: row q_start[i] + t of q is new
+ * token t of request i, at position ie = t + k_len[i] - (q_start[i + 1] -
+ * q_start[i]) of its k_len[i] tokens, and attends those keys that the mask
+ * keeps (positions as in lca_mask_kind, the request being the segment; the
+ * new tokens' own keys must be in the cache already).  A request with one new
+ * token is a decode step, one with many a prompt or a chunk of one; a batch
+ * may mix them.  Masks: FULL, CAUSAL, SLIDING, CAUSAL_SLIDING, DOC,
+ * CAUSAL_DOC, GLOBAL_SLIDING, CAUSAL_BLOCKWISE, PREFIX_LM_CAUSAL and
+ * BLOCK_CAUSAL_DOC (LCA_ERR_UNSUPPORTED for the others).
+ * q: device, the cache's dtype, [Tq] rows of Hq * d dense elements, q_stride
+ * apart, 16-byte aligned.  block_table: int32, device.  q_start: int32
+ * [n_seq + 1], k_len: int32 [n_seq], device.  o: [Tq][Hq][d] dense, the
+ * cache's dtype, 16-byte aligned; lse: float [Hq][Tq], natural log, as
+ * lca_attn_fwd writes it and lca_attn_merge reads it.  Rows that attend
+ * nothing, and rows outside every request, get o = 0, lse = -inf.
+ * Nothing that lies in the cache behind a request's last key, or in keys
+ * that the mask hides from all of its new tokens, reaches a result (infinities
+ * and NaN included).  A table entry outside [0, n_pages) that a row needs
+ * reads as zeros; q_start that decreases or leaves [0, Tq] and k_len outside
+ * [0, max_pages * page_size] are clamped; each sets LCA_ERR_DEVICE_ARG in the
+ * status word (lca_read_status). */
+LCA_API lca_status lca_attn_paged(const void* q, const lca_paged_cache* cache, const int32_t* block_table,
+                                  const int32_t* q_start, const int32_t* k_len, void* o, float* lse,
+                                  const lca_paged_shape* shape, const lca_mask_desc* mask, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+/* Bytes of workspace that lca_attn_paged needs (256-byte aligned).  Host
+ * only; no CUDA call.  Two calls that may run at once need a workspace each. */
+LCA_API lca_status lca_attn_paged_workspace_size(const lca_paged_shape* shape, const lca_paged_cache* cache,
+                                                 const lca_mask_desc* mask, size_t* bytes);
+
 /* Test hook: writes the mask of one segment and query head, evaluated by the
  * same device predicate the attention kernels apply, as bytes (1 = attend)
  * into `out` (device, q_len*k_len, row-major). */
@@ -350,7 +460,8 @@ LCA_API const char* lca_status_string(lca_status status);
 /* Library revision, 100 + n; n grows whenever an entry point's behaviour
  * changes (102: lca_mask_tile_classes reports the empty-half flags; 103:
  * outputs may be mapped host memory, and every pointer's kind is checked;
- * 104: device pointers of another device than the current one are refused). */
+ * 104: device pointers of another device than the current one are refused;
+ * 105: the paged cache). */
 LCA_API int32_t lca_version(void);
 
 #ifdef __cplusplus

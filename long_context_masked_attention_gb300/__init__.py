@@ -13,6 +13,8 @@ from .binding import (  # noqa: F401
     attn_bwd,
     attn_fwd,
     attn_merge,
+    attn_paged,
+    attn_paged_workspace_size,
     cad_plan,
     CadPlan,
     load,
@@ -20,6 +22,9 @@ from .binding import (  # noqa: F401
     mask_materialize,
     mask_nnz,
     mask_tile_classes,
+    PagedPlan,
+    paged_plan,
+    paged_write,
     probe_wait_timeout,
     read_status,
     workspace_size,

@@ -26,7 +26,8 @@ STATUS = {0: "LCA_OK", 1: "LCA_ERR_INVALID_ARG", 2: "LCA_ERR_UNSUPPORTED", 3: "L
 EXPORTED = ("lca_workspace_size", "lca_attn_fwd", "lca_attn_bwd", "lca_mask_materialize", "lca_mask_tile_classes",
             "lca_mask_nnz", "lca_read_status", "lca_probe_wait_timeout", "lca_set_kernel_events", "lca_launch_count",
             "lca_last_error_detail", "lca_attn_fwd_static_workspace", "lca_status_string", "lca_version",
-            "lca_attn_merge", "lca_cad_plan", "lca_attn_fwd_dropout", "lca_attn_bwd_dropout", "lca_set_cta_profile")
+            "lca_attn_merge", "lca_cad_plan", "lca_attn_fwd_dropout", "lca_attn_bwd_dropout", "lca_set_cta_profile",
+            "lca_paged_plan", "lca_paged_write", "lca_attn_paged", "lca_attn_paged_workspace_size")
 PHASES = ("fwd_plan", "fwd", "d_prepass", "dkv_plan", "dkv", "dq_plan", "dq")
 
 
@@ -69,6 +70,17 @@ class Dropout_t(C.Structure):
     _fields_ = [("p", C.c_float), ("seed", C.c_uint64)]
 
 
+class PagedCache_t(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("n_pages", C.c_int32), ("page_size", C.c_int32),
+                ("Hkv", C.c_int32), ("d", C.c_int32), ("dtype", C.c_int32), ("page_stride", C.c_int64),
+                ("token_stride", C.c_int64), ("head_stride", C.c_int64)]
+
+
+class PagedShape_t(C.Structure):
+    _fields_ = [("Tq", C.c_int32), ("Hq", C.c_int32), ("n_seq", C.c_int32), ("max_pages", C.c_int32),
+                ("table_stride", C.c_int64), ("q_stride", C.c_int64), ("max_q_len", C.c_int32), ("scale", C.c_float)]
+
+
 _lib = None
 
 
@@ -98,6 +110,13 @@ def load(path: str = LIB_PATH):
     lib.lca_probe_wait_timeout.argtypes = [vp, C.c_size_t, C.c_int32, vp]
     lib.lca_set_kernel_events.argtypes = [C.POINTER(C.c_void_p), C.c_int32, C.POINTER(C.c_int32)]
     lib.lca_set_cta_profile.argtypes = [vp, C.c_size_t]
+    i32, i64 = C.c_int32, C.c_int64
+    lib.lca_paged_plan.argtypes = [vp, vp, i32, vp, i32, vp, vp, i64, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp]
+    lib.lca_paged_write.argtypes = [vp, vp, i64, i64, vp, i32, C.POINTER(PagedCache_t), vp]
+    lib.lca_attn_paged.argtypes = [vp, C.POINTER(PagedCache_t), vp, vp, vp, vp, vp, C.POINTER(PagedShape_t),
+                                   C.POINTER(MaskDesc_t), vp, C.c_size_t, vp]
+    lib.lca_attn_paged_workspace_size.argtypes = [C.POINTER(PagedShape_t), C.POINTER(PagedCache_t),
+                                                  C.POINTER(MaskDesc_t), C.POINTER(C.c_size_t)]
     lib.lca_launch_count.restype = C.c_uint64
     lib.lca_launch_count.argtypes = []
     lib.lca_attn_fwd_static_workspace.argtypes = [vp, vp, vp, vp, vp, C.POINTER(Shape_t), C.POINTER(MaskDesc_t), vp]
@@ -427,6 +446,268 @@ def attn_bwd(do, q, k, v, o, lse, segments, mask, scale=0.0, dq=None, dk=None, d
         else:
             _check(load().lca_attn_bwd_dropout(*args, C.byref(drop), *tail), "lca_attn_bwd_dropout")
     return dq, dk, dv
+
+
+# ------------------------------------------------------------------ paged cache
+@dataclass
+class PagedPlan:
+    """A batch's rows: first row of each request, its keys, and for each row
+    its slot in the cache and its position (see lca_paged_plan)."""
+    q_start: object
+    k_len: object
+    slots: object
+    positions: object
+    state: object
+
+
+class _On:
+    """The stream of a call that may allocate: tensors made with empty() belong
+    to the given stream (the current one when none is given), and use() keeps
+    the caller's tensors from being reused while that stream reads them."""
+
+    def __init__(self, stream, device):
+        import torch
+
+        self.side = None
+        if stream is not None and device.type == "cuda":
+            s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(
+                int(getattr(stream, "cuda_stream", stream)), device)
+            if s != torch.cuda.current_stream(device):
+                self.side = s
+        self.device = device
+
+    def empty(self, shape, dtype):
+        import torch
+
+        if self.side is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        with torch.cuda.stream(self.side):
+            t = torch.empty(shape, dtype=dtype, device=self.device)
+        t.record_stream(torch.cuda.current_stream(self.device))
+        return t
+
+    def use(self, *tensors):
+        if self.side is not None:
+            for t in tensors:
+                t.record_stream(self.side)
+
+
+def _paged_cache(k, v):
+    import torch
+
+    for name, t in (("k_cache", k), ("v_cache", v)):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+        if t.device.type != "cuda":
+            raise ValueError(f"{name}: must be a CUDA tensor (got {t.device})")
+        if t.dim() != 4:
+            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [n_pages, page_size, Hkv, d]")
+    if v.shape != k.shape or v.dtype != k.dtype or v.device != k.device:
+        raise ValueError(f"v_cache: {tuple(v.shape)} {v.dtype} on {v.device}, expected {tuple(k.shape)} {k.dtype} "
+                         f"on {k.device} as k_cache")
+    if k.dtype == torch.bfloat16:
+        dtype = 0
+    elif k.dtype == torch.float16:
+        dtype = 1
+    else:
+        raise ValueError(f"k_cache: dtype {k.dtype}, expected torch.bfloat16 or torch.float16")
+    n, page, Hkv, d = k.shape
+    strides = []
+    for t in (k, v):
+        a, b, c, e = t.stride()
+        if e != 1 and d > 1 and n:
+            raise ValueError("k_cache, v_cache: the last dimension must be contiguous")
+        # the stride of an axis of length one moves nothing
+        strides.append((a if n > 1 else d, b if n and page > 1 else d, c if n and Hkv > 1 else d))
+    if strides[0] != strides[1]:
+        raise ValueError(f"v_cache: strides {strides[1]}, expected {strides[0]} as k_cache")
+    return PagedCache_t(k.data_ptr(), v.data_ptr(), n, page, Hkv, d, dtype, *strides[0])
+
+
+def _rows(t, name, heads, d, dtype, device):
+    """[T, heads, d] CUDA tensor whose rows are dense; returns its row stride."""
+    import torch
+
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, expected {device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if t.dim() != 3 or t.shape[2] != d or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [T, {'H' if heads is None else heads}, {d}]")
+    T, H, _ = t.shape
+    a, b, c = t.stride()
+    if T and ((c != 1 and d > 1) or (H > 1 and b != d)):
+        raise ValueError(f"{name}: each row's heads must be contiguous")
+    return a if T > 1 else H * d
+
+
+def _ints(t, name, shape, device):
+    import torch
+
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name}: must be a CUDA tensor (got {t.device})")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name}: on {t.device}, expected {device}")
+    if t.dtype != torch.int32:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected torch.int32")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    return t.data_ptr()
+
+
+def _table(t, n_seq, device):
+    """Block table [n_seq, max_pages] with dense rows -> (pointer, entries per row, row stride)."""
+    import torch
+
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"block_table: expected a torch.Tensor, got {type(t).__name__}")
+    if t.device != device:
+        raise ValueError(f"block_table: on {t.device}, expected {device}")
+    if t.dtype != torch.int32:
+        raise ValueError(f"block_table: dtype {t.dtype}, expected torch.int32")
+    if t.dim() != 2 or t.shape[0] != n_seq:
+        raise ValueError(f"block_table: shape {tuple(t.shape)}, expected [{n_seq}, max_pages]")
+    width = t.shape[1]
+    a, b = t.stride()
+    if (n_seq and b != 1 and width > 1) or (n_seq > 1 and a < width):
+        raise ValueError("block_table: each row must be contiguous, and rows must not overlap")
+    return t.data_ptr(), width, a if n_seq > 1 else width
+
+
+def paged_plan(ctx_len, new_len, free_pages, taken, block_table, page_size, n_pages, n_rows, q_start=None, k_len=None,
+               slots=None, positions=None, state=None, stream=None) -> PagedPlan:
+    """The bookkeeping of a batch over a paged cache, on the GPU: gives the new
+    tokens' pages from free_pages[taken:] to the requests' rows of block_table
+    (in place) and returns where every row goes.  ctx_len, new_len [n_seq],
+    free_pages [n], taken [1]: int32 CUDA tensors; block_table [n_seq,
+    max_pages] int32; n_rows: rows of the packed batch, those behind the last
+    request get slot -1.  state holds {free pages used so far, pages missing,
+    requests with unusable lengths, new tokens}; state[:1] is the next call's
+    `taken`."""
+    import torch
+
+    if not isinstance(ctx_len, torch.Tensor):
+        raise TypeError(f"ctx_len: expected a torch.Tensor, got {type(ctx_len).__name__}")
+    n_seq, dev, n_rows = ctx_len.numel(), ctx_len.device, int(n_rows)
+    if n_rows < 0:
+        raise ValueError(f"n_rows: {n_rows}, expected 0 or more")
+    args = [_ints(ctx_len, "ctx_len", (n_seq,), None), _ints(new_len, "new_len", (n_seq,), dev), n_seq]
+    if not isinstance(free_pages, torch.Tensor):
+        raise TypeError(f"free_pages: expected a torch.Tensor, got {type(free_pages).__name__}")
+    args += [_ints(free_pages, "free_pages", (free_pages.numel(),), dev), free_pages.numel(),
+             _ints(taken, "taken", (1,), dev)]
+    tp, width, tstride = _table(block_table, n_seq, dev)
+    on = _On(stream, dev)
+    outs = []
+    for t, name, n in ((q_start, "q_start", n_seq + 1), (k_len, "k_len", n_seq), (slots, "slots", n_rows),
+                       (positions, "positions", n_rows), (state, "state", 4)):
+        if t is None:
+            t = on.empty((n,), torch.int32)
+        else:
+            _ints(t, name, (n,), dev)
+            on.use(t)
+        outs.append(t)
+    on.use(ctx_len, new_len, free_pages, taken, block_table)
+    with _on_device(dev):
+        _check(load().lca_paged_plan(*args, tp, tstride, width, int(page_size), int(n_pages), n_rows,
+                                     *[t.data_ptr() for t in outs], _stream(stream, dev)), "lca_paged_plan")
+    return PagedPlan(*outs)
+
+
+def paged_write(k, v, k_cache, v_cache, slots, stream=None):
+    """Stores rows k, v [T, Hkv, 128] (row stride free) at slots [T] int32 of
+    the cache [n_pages, page_size, Hkv, 128] (strides free, bf16 or fp16), in
+    place; rows whose slot is outside the cache (-1) are skipped."""
+    cache = _paged_cache(k_cache, v_cache)
+    dev = k_cache.device
+    ks = _rows(k, "k", cache.Hkv, cache.d, k_cache.dtype, dev)
+    vs = _rows(v, "v", cache.Hkv, cache.d, k_cache.dtype, dev)
+    T = k.shape[0]
+    if v.shape[0] != T:
+        raise ValueError(f"v: {v.shape[0]} rows, expected {T} as k")
+    sp = _ints(slots, "slots", (T,), dev)
+    _On(stream, dev).use(k, v, k_cache, v_cache, slots)
+    with _on_device(dev):
+        _check(load().lca_paged_write(k.data_ptr(), v.data_ptr(), ks, vs, sp, T, C.byref(cache), _stream(stream, dev)),
+               "lca_paged_write")
+
+
+def _paged_mask(mask):
+    md = MaskDesc_t()
+    md.kind = mask.kind if isinstance(mask.kind, int) else MASK_KINDS.index(mask.kind)
+    for name in ("window_left", "window_right", "num_global", "prefix_len", "block"):
+        setattr(md, name, int(getattr(mask, name, 0) or 0))
+    return md
+
+
+def attn_paged_workspace_size(q, k_cache, v_cache, block_table, mask, scale=0.0, max_q_len=0) -> int:
+    """Bytes of workspace that attn_paged needs for these tensors."""
+    cache = _paged_cache(k_cache, v_cache)
+    return _paged_size(_paged_shape(q, cache, k_cache, block_table, scale, max_q_len)[0], cache, _paged_mask(mask))
+
+
+def _paged_shape(q, cache, k_cache, block_table, scale, max_q_len):
+    qs = _rows(q, "q", None, cache.d, k_cache.dtype, k_cache.device)
+    n_seq = block_table.shape[0]
+    tp, width, tstride = _table(block_table, n_seq, k_cache.device)
+    return PagedShape_t(q.shape[0], q.shape[1], n_seq, width, tstride, qs, int(max_q_len), float(scale)), tp
+
+
+def _paged_size(shape, cache, md):
+    n = C.c_size_t(0)
+    _check(load().lca_attn_paged_workspace_size(C.byref(shape), C.byref(cache), C.byref(md), C.byref(n)),
+           "lca_attn_paged_workspace_size")
+    return n.value
+
+
+def attn_paged(q, k_cache, v_cache, block_table, q_start, k_len, mask, scale=0.0, max_q_len=0, out=None, lse=None,
+               workspace=None, stream=None):
+    """Attention of packed new tokens q [T, Hq, 128] (row stride free) over a
+    paged cache [n_pages, page_size, Hkv, 128] (strides free), bf16 or fp16 ->
+    (o [T, Hq, 128], lse [Hq, T]).  Request i owns rows q_start[i] to
+    q_start[i + 1] and the first k_len[i] tokens of the pages in
+    block_table[i]; its new tokens are the last of them.  q_start, k_len and
+    block_table are int32 CUDA tensors read when the kernels run.  mask: any
+    interval family (see lca_attn_paged).  max_q_len: no request has more new
+    tokens (0: unknown).  After a synchronize, read_status(workspace) tells
+    whether a table entry or a length was out of range."""
+    import torch
+
+    cache = _paged_cache(k_cache, v_cache)
+    if not isinstance(block_table, torch.Tensor):
+        raise TypeError(f"block_table: expected a torch.Tensor, got {type(block_table).__name__}")
+    dev = k_cache.device
+    shape, tp = _paged_shape(q, cache, k_cache, block_table, scale, max_q_len)
+    md = _paged_mask(mask)
+    qsp = _ints(q_start, "q_start", (shape.n_seq + 1,), dev)
+    klp = _ints(k_len, "k_len", (shape.n_seq,), dev)
+    need = _paged_size(shape, cache, md)
+    on = _On(stream, dev)
+    size, lsize = tuple(q.shape), (shape.Hq, shape.Tq)
+    if out is None:
+        out = on.empty(size, q.dtype)
+    else:
+        on.use(_require(out, "out", size, q.dtype, dev))
+    if lse is None:
+        lse = on.empty(lsize, torch.float32)
+    else:
+        on.use(_require(lse, "lse", lsize, torch.float32, dev))
+    if workspace is None:
+        workspace = on.empty((need,), torch.uint8)
+    else:
+        on.use(_require(workspace, "workspace", (workspace.numel(),), torch.uint8, dev))
+    on.use(q, k_cache, v_cache, block_table, q_start, k_len)
+    with _on_device(dev):
+        _check(load().lca_attn_paged(q.data_ptr(), C.byref(cache), tp, qsp, klp, out.data_ptr(), lse.data_ptr(),
+                                     C.byref(shape), C.byref(md), workspace.data_ptr(), workspace.numel(),
+                                     _stream(stream, dev)), "lca_attn_paged")
+    return out, lse
 
 
 def mask_materialize(call: Call, head: int, seg: int, q_len: int, k_len: int, device="cuda", stream=None):

@@ -17,6 +17,7 @@
 #include <vector>
 
 #include "../../include/lca_attn.h"
+#include "lca_host.h"
 #include "lca_internal.h"
 
 namespace lca {
@@ -24,14 +25,18 @@ namespace lca {
 static std::atomic<unsigned long long> g_launches{0};
 void note_launches(int n) { g_launches.fetch_add(static_cast<unsigned long long>(n), std::memory_order_relaxed); }
 
-namespace {
-
-thread_local char g_err_detail[256] = "";
+static thread_local char g_err_detail[256] = "";
 
 lca_status cuda_fail(const char* what, cudaError_t e) {
   snprintf(g_err_detail, sizeof(g_err_detail), "%s: %s", what, cudaGetErrorString(e));
   return LCA_ERR_CUDA;
 }
+lca_status driver_fail(const char* what, int code) {
+  snprintf(g_err_detail, sizeof(g_err_detail), "%s: CUresult %d", what, code);
+  return LCA_ERR_CUDA;
+}
+
+namespace {
 
 // Profiling ring (lca_set_kernel_events).
 struct EventRing {
@@ -74,10 +79,7 @@ void phase_end(int p, cudaStream_t st) {
     (void)cudaGetLastError();
 }
 
-constexpr size_t kAlign = 256;
 constexpr size_t kMaxPartialSlots = 512;  // 64 MiB of f32 dK/dV partial sums at most
-size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
-long long cdiv(long long a, long long b) { return (a + b - 1) / b; }
 
 // ------------------------------------------------------------------ host plan
 struct HostPlan {
@@ -484,6 +486,8 @@ PlanView make_view(const HostPlan& P, const Layout& L, uint8_t* ws) {
   return v;
 }
 
+}  // namespace
+
 // ------------------------------------------------------------------ CUDA helpers
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
@@ -496,6 +500,8 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   }
   return fn;
 }
+
+namespace {
 
 // [rows][heads * 128] bf16, 64-column x box_rows boxes, 128-byte swizzle.
 bool make_map(CUtensorMap* m, const void* ptr, int rows, int heads, int box_rows) {
@@ -517,6 +523,8 @@ bool make_map(CUtensorMap* m, const void* ptr, int rows, int heads, int box_rows
   return r == CUDA_SUCCESS;
 }
 
+}  // namespace
+
 int num_sms() {
   int dev = 0, n = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -527,6 +535,8 @@ int num_sms() {
   }
   return n;
 }
+
+namespace {
 
 // The backward's dK/dV work runs on a library-owned stream of the highest
 // priority, forked from and joined back to the caller's stream by events, so
@@ -561,6 +571,8 @@ cudaStream_t side_stream(lca_status& err) {
   return streams[dev];
 }
 
+}  // namespace
+
 unsigned long long wait_limit_ns() {
   static unsigned long long v = 0;
   if (!v) {
@@ -570,8 +582,6 @@ unsigned long long wait_limit_ns() {
   }
   return v;
 }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Inputs are read through TMA tensor maps and must be device (or managed)
 // memory.  Outputs are written with plain stores only, so they may also be
@@ -585,7 +595,7 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 // buffer, or nullptr for memory they must not write (another device's,
 // pageable host memory, an unknown pointer), which the call refuses before
 // launching.
-int current_device() {
+static int current_device() {
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess) {
     (void)cudaGetLastError();
@@ -617,12 +627,7 @@ void* output_address(void* p) {
   return nullptr;
 }
 
-
-#define LCA_CUDA(x)                                  \
-  do {                                               \
-    const cudaError_t e_ = (x);                      \
-    if (e_ != cudaSuccess) return cuda_fail(#x, e_); \
-  } while (0)
+namespace {
 
 // Common preamble of every entry point that launches: validate, lay out,
 // check the workspace, clear the control block, upload the plan and build
@@ -727,7 +732,7 @@ const char* lca_status_string(lca_status s) {
   return "unknown status";
 }
 
-int32_t lca_version(void) { return 104; }
+int32_t lca_version(void) { return 105; }
 
 lca_status lca_set_kernel_events(void* const* events, int32_t n_events, int32_t* phases) {
   if (events && (n_events < 2 || (n_events & 1))) return LCA_ERR_INVALID_ARG;

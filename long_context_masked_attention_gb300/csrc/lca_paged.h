@@ -1,0 +1,53 @@
+// lca_paged.h — what the paged-cache entry points (lca_paged_api.cu) and
+// their kernels share.
+#pragma once
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <cstdint>
+
+#include "lca_common.cuh"
+
+namespace lca {
+
+void note_launches(int n);
+
+struct PagedPlanArgs {
+  const int *ctx_len, *new_len, *free_pages, *taken;
+  int* block_table;
+  long long table_stride;
+  int n_seq, n_free, max_pages, page_size, n_pages, n_rows;
+  int *q_start, *k_len, *slots, *positions, *state;
+};
+void launch_paged_plan(const PagedPlanArgs& a, int num_sms, cudaStream_t st);
+
+// Strides in 16-byte units.
+struct PagedWriteArgs {
+  const uint4 *k, *v;
+  uint4 *kc, *vc;
+  long long k_stride, v_stride, page_stride, token_stride, head_stride;
+  const int* slots;
+  int n_rows, Hkv, page_size, n_slots;
+};
+void launch_paged_write(const PagedWriteArgs& a, int num_sms, cudaStream_t st);
+
+// A request as the kernels see it: lengths clamped to what the tensors hold.
+struct PagedSeq {
+  int q_off, q_len, k_len, pad;
+};
+
+struct PagedAttnArgs {
+  MaskCtx mask;
+  const void* q;
+  const void *kc, *vc;
+  long long q_stride, page_stride, token_stride, head_stride, table_stride;  // elements
+  const int *table, *q_start, *k_len;
+  void* o;
+  float* lse;
+  int* status;
+  PagedSeq* seqs;
+  int Tq, Hq, Hkv, G, n_seq, max_pages, page_size, n_pages;
+  float scale_log2;
+};
+void launch_paged_attn(const PagedAttnArgs& a, bool fp16, int num_sms, cudaStream_t st);
+
+}  // namespace lca
