@@ -174,73 +174,599 @@ __global__ void __launch_bounds__(256) paged_write_kernel(const PagedWriteArgs a
   }
 }
 
-// ------------------------------------------------------------------ attention
-__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
-__device__ __forceinline__ void from_f(__nv_bfloat16& y, float x) { y = __float2bfloat16_rn(x); }
-__device__ __forceinline__ void from_f(__half& y, float x) { y = __float2half_rn(x); }
+// ------------------------------------------------------------------ attention, few rows
+// Attention is bound here by reading K and V once: with G query heads per KV
+// head and t new tokens a request has G t rows per KV head, and 16 of them
+// take part in every product, so a key costs 512 bytes from HBM and little
+// arithmetic.  The work is a line of units of 64 keys (request, KV head, row
+// tile, unit) cut into equal spans, one per CTA, two CTAs per SM, whatever
+// the lengths; a piece of an item that spans more CTAs leaves unnormalised
+// sums (O, running maximum, sum of exponentials) in the workspace, and the
+// CTA that finishes an item's last piece joins them in the order of the
+// keys.  Each CTA finds its span itself from the lengths, so there is no
+// planning launch.  Within a CTA each of 4 warps owns 16 of a unit's 64 keys,
+// copies them asynchronously into its own ring of shared memory (keys that no
+// row attends are filled with zeros, not read) and keeps its own running
+// maximum and sums; the warps meet once per piece.  16 rows cannot fill a
+// tcgen05 tile of 128, so the products are warp-wide m16n8k16 ones, whose
+// score accumulators are already the A operand of the product with V.
+constexpr int kUnit = 64;                     // keys per unit
+constexpr int kRows = 16;                     // rows per item
+constexpr int kDecWarps = 4;
+constexpr int kDecThreads = 32 * kDecWarps;
+constexpr int kSlice = kUnit / kDecWarps;     // keys per warp and unit
+constexpr int kDecStages = 3;
+constexpr int kSliceBytes = kSlice * 256;     // of K or V
+constexpr int kWarpBytes = kDecStages * 2 * kSliceBytes;
+constexpr int kDecSmem = kDecWarps * kWarpBytes;
+constexpr int kMinUnits = 2;                  // a CTA's share, where there is that much
+constexpr int kSeqTile = 4 * kDecThreads;     // requests whose places on the line are in shared memory at once
+constexpr int kPartFloats = kRows * (kHeadDim + 2);
+static_assert(kSlice == 16, "a slice is one k16 step of the product with V");
+static_assert(kPartFloats == kPagedPartFloats, "workspace layout");
 
-// Clamps the requests' lengths to what the tensors hold and flags those that
-// needed it.
-__global__ void paged_seqs_kernel(const PagedAttnArgs a) {
-  const int i = blockIdx.x * blockDim.x + threadIdx.x;
-  if (i >= a.n_seq) return;
-  const int r0 = a.q_start[i], r1 = a.q_start[i + 1], kl = a.k_len[i];
-  const long long room = static_cast<long long>(a.max_pages) * a.page_size;
-  PagedSeq s{};
-  s.q_off = min(max(r0, 0), a.Tq);
-  s.q_len = min(max(r1, s.q_off), a.Tq) - s.q_off;
-  s.k_len = static_cast<int>(min(static_cast<long long>(max(kl, 0)), room));
-  if (r0 < 0 || r1 < r0 || r1 > a.Tq || kl < 0 || kl > room) raise_status(a.status, kStatusDeviceArg, 50);
-  a.seqs[i] = s;
+template <typename T>
+struct Half2;
+template <>
+struct Half2<__nv_bfloat16> {
+  // p is at most 1, and bf16 has the exponents of fp32
+  static constexpr float kBias = 0.f;
+  static __device__ __forceinline__ uint32_t pack(float lo, float hi) { return pack_bf16x2(lo, hi); }
+  static __device__ __forceinline__ bool not_finite(uint32_t x) {
+    return (x & 0x7F80u) == 0x7F80u || (x & 0x7F800000u) == 0x7F800000u;
+  }
+  static __device__ __forceinline__ float2 unpack(uint32_t x) {
+    return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xFFFF0000u));
+  }
+  static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  }
+};
+template <>
+struct Half2<__half> {
+  // fp16 holds nothing below 2^-24: p is kept times 2^12, so that keys down
+  // to 2^-36 of the largest still count; O, l and their partial sums carry
+  // the factor, the quotient and the LSE do not
+  static constexpr float kBias = 12.f;
+  static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+  }
+  static __device__ __forceinline__ bool not_finite(uint32_t x) {
+    return (x & 0x7C00u) == 0x7C00u || (x & 0x7C000000u) == 0x7C000000u;
+  }
+  static __device__ __forceinline__ float2 unpack(uint32_t x) {
+    return __half22float2(*reinterpret_cast<const __half2*>(&x));
+  }
+  static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  }
+};
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+// 16 bytes, of which those past `bytes` (0 or 16) are zero
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// One warp per (row, query head), one key at a time, online softmax in base 2.
-template <typename T>
-__global__ void __launch_bounds__(256) paged_rows_kernel(const PagedAttnArgs a) {
-  const long long w = blockIdx.x * 8LL + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (w >= static_cast<long long>(a.Tq) * a.Hq) return;
-  const int head = static_cast<int>(w % a.Hq), row = static_cast<int>(w / a.Hq);
-  float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-  int lo = 0, hi = a.n_seq;  // the last request that starts at or before the row
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (a.seqs[mid].q_off <= row) lo = mid; else hi = mid;
-  }
-  const PagedSeq sq = a.n_seq > 0 ? a.seqs[lo] : PagedSeq{};
-  if (row >= sq.q_off && row < sq.q_off + sq.q_len) {
-    SegInfo sg{};
-    sg.q_len = sq.q_len;
-    sg.k_len = sq.k_len;
-    const Span sp = row_span(a.mask, sg, row - sq.q_off);
-    const T* q = static_cast<const T*>(a.q) + row * a.q_stride + head * kHeadDim + lane * 4;
-    float qf[4];
-    for (int k = 0; k < 4; ++k) qf[k] = to_f(q[k]) * a.scale_log2;
-    const int j0 = sp.a1 < sp.b1 ? min(sp.a0 < sp.b0 ? sp.a0 : sp.a1, sp.a1) : sp.a0;
-    const int j1 = max(sp.a0 < sp.b0 ? sp.b0 : 0, sp.a1 < sp.b1 ? sp.b1 : 0);
-    for (int j = j0; j < j1; ++j) {
-      if (!((j >= sp.a0 && j < sp.b0) || (j >= sp.a1 && j < sp.b1))) continue;
-      const int page = a.table[lo * a.table_stride + j / a.page_size];
-      const bool ok = page >= 0 && page < a.n_pages;
-      if (!ok && lane == 0) raise_status(a.status, kStatusDeviceArg, 51);
-      const long long at = (ok ? page : 0) * a.page_stride + j % a.page_size * a.token_stride +
-                           head / a.G * a.head_stride + lane * 4;
-      const T *kr = static_cast<const T*>(a.kc) + at, *vr = static_cast<const T*>(a.vc) + at;
-      float s = 0.f;
-      for (int k = 0; k < 4; ++k) s += ok ? qf[k] * to_f(kr[k]) : 0.f;
-      for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(~0u, s, d);
-      const float mn = fmaxf(m, s), f = exp2f(m - mn), p = exp2f(s - mn);
-      l = l * f + p;
-      for (int k = 0; k < 4; ++k) acc[k] = acc[k] * f + (ok ? p * to_f(vr[k]) : 0.f);
-      m = mn;
+__device__ __forceinline__ bool in_span(const Span& s, int j) {
+  return (j >= s.a0 && j < s.b0) || (j >= s.a1 && j < s.b1);
+}
+
+// Request i with its lengths clamped to what the tensors hold; `flag` reports
+// those that needed it.
+__device__ __forceinline__ SegInfo paged_seg(const PagedAttnArgs& a, int i, bool flag) {
+  const int r0 = a.q_start[i], r1 = a.q_start[i + 1], kl = a.k_len[i];
+  const int room = a.max_pages * a.page_size;
+  if (flag && (r0 < 0 || r1 < r0 || r1 > a.Tq || kl < 0 || kl > room)) raise_status(a.status, kStatusDeviceArg, 50);
+  SegInfo s{};
+  s.q_off = min(max(r0, 0), a.Tq);
+  s.q_len = min(max(r1, s.q_off), a.Tq) - s.q_off;
+  s.k_len = min(max(kl, 0), room);
+  return s;
+}
+
+// Keys that some of the tokens [i0, i1) of a request attends: in every family
+// the bounds of a row's intervals do not decrease from token to token, but
+// for the first lower bound, which may fall to 0 at the last rows, and for
+// GLOBAL_SLIDING's first rows, whose one interval holds all keys; so the two
+// outer rows give the hull.
+__device__ __forceinline__ Span hull(const MaskCtx& m, const SegInfo& sg, int i0, int i1) {
+  const Span s = row_span(m, sg, i0), t = row_span(m, sg, i1 - 1);
+  Span h;
+  h.a0 = min(s.a0, t.a0);
+  h.b0 = max(max(s.b0, t.b0), h.a0);
+  h.a1 = h.b1 = h.b0;
+  if (t.a1 < t.b1) {
+    h.a1 = s.a1 < s.b1 ? min(s.a1, t.a1) : t.a1;
+    h.b1 = max(t.b1, h.b0);
+    if (h.a1 <= h.b0) {  // they touch
+      h.b0 = h.b1;
+      h.a1 = h.b1;
     }
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  T* o = static_cast<T*>(a.o) + w * kHeadDim + lane * 4;
-  for (int k = 0; k < 4; ++k) from_f(o[k], acc[k] * inv);
-  if (lane == 0)
-    a.lse[static_cast<long long>(head) * a.Tq + row] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+  return h;
+}
+
+// The units of a hull: n0 from t0 on, then n1 from t1 on.
+struct Units {
+  int t0, n0, t1, n1;
+  __device__ __forceinline__ int first_key(int u) const { return (u < n0 ? t0 + u : t1 + u - n0) * kUnit; }
+};
+__device__ __forceinline__ Units units_of(const Span& h) {
+  Units u;
+  u.t0 = h.a0 / kUnit;
+  u.n0 = h.b0 > h.a0 ? (h.b0 + kUnit - 1) / kUnit - u.t0 : 0;
+  u.t1 = max(h.a1 / kUnit, u.n0 > 0 ? u.t0 + u.n0 : 0);
+  u.n1 = h.b1 > h.a1 ? max((h.b1 + kUnit - 1) / kUnit - u.t1, 0) : 0;
+  return u;
+}
+
+__device__ __forceinline__ int row_tiles(const PagedAttnArgs& a, int q_len) {
+  return static_cast<int>((static_cast<long long>(q_len) * a.G + kRows - 1) / kRows);
+}
+
+// Units of request i on the line: every (row tile, KV head) has those of the
+// whole request's hull, at least one, so that rows without keys are written.
+__device__ __forceinline__ long long line_units(const PagedAttnArgs& a, int i, bool flag) {
+  const SegInfo sg = paged_seg(a, i, flag);
+  if (sg.q_len == 0) return 0;
+  const Units u = units_of(hull(a.mask, sg, 0, sg.q_len));
+  return static_cast<long long>(row_tiles(a, sg.q_len)) * a.Hkv * max(u.n0 + u.n1, 1);
+}
+
+struct DecodeShared {
+  long long start[kSeqTile + 1];  // first unit of each request of the tile, relative to the tile's
+  long long sums[kDecWarps];
+  float m[kDecWarps][kRows], l[kDecWarps][kRows];
+  int last;
+};
+
+// Places of the requests [base, base + kSeqTile) on the line; returns their units.
+__device__ __forceinline__ long long place_requests(const PagedAttnArgs& a, DecodeShared& sh, int base, bool flag) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  long long n[4], mine = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int i = base + 4 * tid + k;
+    n[k] = i < a.n_seq ? line_units(a, i, flag) : 0;
+    mine += n[k];
+  }
+  long long inc = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long x = __shfl_up_sync(~0u, inc, d);
+    if (lane >= d) inc += x;
+  }
+  __syncthreads();  // earlier readers of start and sums
+  if (lane == 31) sh.sums[warp] = inc;
+  __syncthreads();
+  long long at = inc - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < kDecWarps; ++w) {
+    if (w < warp) at += sh.sums[w];
+    total += sh.sums[w];
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    sh.start[4 * tid + k] = at;
+    at += n[k];
+  }
+  if (tid == kDecThreads - 1) sh.start[kSeqTile] = at;
+  __syncthreads();
+  return total;
+}
+
+// One warp's share of a piece: units [u0, u0 + n) of an item, keys
+// [16 warp, 16 warp + 16) of each.
+template <typename T>
+struct WarpState {
+  float o[16][4];  // rows lane / 4 and lane / 4 + 8, columns 8 t + 2 (lane % 4), + 1
+  float m[2], l[2];
+};
+
+template <typename T>
+__device__ __forceinline__ void decode_warp(const PagedAttnArgs& a, uint32_t ring, int seq, const SegInfo& sg,
+                                            const Units& un, int tile, int head, int u0, int n, WarpState<T>& st) {
+  using H = Half2<T>;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int rows = min(static_cast<int>(min(static_cast<long long>(sg.q_len) * a.G - tile * kRows, 16LL)), kRows);
+  const int r_first = tile * kRows, r_last = r_first + rows - 1;
+  const Span hl = hull(a.mask, sg, r_first / a.G, r_last / a.G + 1);
+  // the two rows of this lane (a row past the last one repeats it, unused)
+  const int ra = min(r_first + (lane >> 2), r_last), rb = min(r_first + (lane >> 2) + 8, r_last);
+  const Span sa = row_span(a.mask, sg, ra / a.G), sb = row_span(a.mask, sg, rb / a.G);
+
+  // offsets of 8-key groups: lane 2 t + g holds group g of unit t of a batch of 16
+  const int* table = a.table + seq * a.table_stride;
+  auto entry = [&](int batch) -> int {  // page of this lane's group, -1 where none is needed or it is no page
+    const int u = batch * 16 + (lane >> 1);
+    if (u >= n) return -1;
+    const int j = un.first_key(u0 + u) + warp * kSlice + (lane & 1) * 8;
+    if (!span_hits(hl, j, j + 8)) return -1;
+    const int p = __ldg(table + j / a.page_size);
+    if (p < 0 || p >= a.n_pages) {
+      raise_status(a.status, kStatusDeviceArg, 51);
+      return -1;
+    }
+    return p;
+  };
+  auto offset = [&](int batch, int page) -> long long {
+    if (page < 0) return -1;
+    const int j = un.first_key(u0 + batch * 16 + (lane >> 1)) + warp * kSlice + (lane & 1) * 8;
+    return page * a.page_stride + j % a.page_size * a.token_stride;
+  };
+  const long long lane_off = head * a.head_stride + (lane >> 4) * a.token_stride + (lane & 15) * 8;
+  const T *kc = static_cast<const T*>(a.kc), *vc = static_cast<const T*>(a.vc);
+  int page_next = entry(0);
+  long long off = 0;
+  // copies the warp's keys of unit u into stage u % 3
+  auto issue = [&](int u) {
+    if (u < n) {
+      if ((u & 15) == 0) {
+        off = offset(u >> 4, page_next);
+        page_next = entry((u >> 4) + 1);
+      }
+      const int j0 = un.first_key(u0 + u) + warp * kSlice;
+      if (span_hits(hl, j0, j0 + kSlice)) {
+        const uint32_t dst = ring + (u % kDecStages) * 2 * kSliceBytes;
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          const long long base = __shfl_sync(~0u, off, 2 * (u & 15) + g);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int key = 8 * g + 2 * i + (lane >> 4);
+            const bool ok = base >= 0 && in_span(hl, j0 + key);
+            const long long at = ok ? base + lane_off + 2 * i * a.token_stride : 0;
+            const uint32_t d = dst + key * 256 + (((lane & 15) ^ (key & 7)) << 4);
+            cp_async_16(d, kc + at, ok ? 16u : 0u);
+            cp_async_16(d + kSliceBytes, vc + at, ok ? 16u : 0u);
+          }
+        }
+      }
+    }
+    cp_async_commit();
+  };
+  issue(0);
+  issue(1);
+
+  // Q as A operands, straight from global memory
+  uint32_t q[8][4];
+  {
+    const T* q0 = static_cast<const T*>(a.q);
+    const T* pa = q0 + (sg.q_off + ra / a.G) * a.q_stride + (head * a.G + ra % a.G) * kHeadDim + 2 * (lane & 3);
+    const T* pb = q0 + (sg.q_off + rb / a.G) * a.q_stride + (head * a.G + rb % a.G) * kHeadDim + 2 * (lane & 3);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      q[c][0] = __ldg(reinterpret_cast<const uint32_t*>(pa + 16 * c));
+      q[c][1] = __ldg(reinterpret_cast<const uint32_t*>(pb + 16 * c));
+      q[c][2] = __ldg(reinterpret_cast<const uint32_t*>(pa + 16 * c + 8));
+      q[c][3] = __ldg(reinterpret_cast<const uint32_t*>(pb + 16 * c + 8));
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < 16; ++t) st.o[t][0] = st.o[t][1] = st.o[t][2] = st.o[t][3] = 0.f;
+  st.m[0] = st.m[1] = -INFINITY;
+  st.l[0] = st.l[1] = 0.f;
+
+  // this lane's row and 16-byte column of the four 8x8 matrices of ldmatrix
+  const int kkey = (lane & 7) + ((lane >> 4) << 3), kcol = (lane >> 3) & 1;   // K: (keys 0-7, 8-15) x (d 0-7, 8-15)
+  const int vkey = (lane & 7) + (((lane >> 3) & 1) << 3), vcol = lane >> 4;   // V, transposed
+  for (int u = 0; u < n; ++u) {
+    issue(u + 2);
+    cp_async_wait<2>();
+    __syncwarp();
+    const int j0 = un.first_key(u0 + u) + warp * kSlice;
+    if (!span_hits(hl, j0, j0 + kSlice)) continue;
+    const uint32_t sk = ring + (u % kDecStages) * 2 * kSliceBytes, sv = sk + kSliceBytes;
+    float s[2][4] = {};
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      uint32_t b[4];
+      ldsm4(b, sk + kkey * 256 + (((2 * c + kcol) ^ (kkey & 7)) << 4));
+      H::mma(s[0], q[c], b[0], b[1]);
+      H::mma(s[1], q[c], b[2], b[3]);
+    }
+    const bool part = !__all_sync(~0u, span_covers(sa, j0, j0 + kSlice) && span_covers(sb, j0, j0 + kSlice));
+    if (part) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int j = j0 + 8 * t + 2 * (lane & 3) + (e & 1);
+          if (!in_span(e < 2 ? sa : sb, j)) s[t][e] = -INFINITY;
+        }
+    }
+    float mx[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      mx[r] = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1])) * a.scale_log2;
+      mx[r] = fmaxf(mx[r], __shfl_xor_sync(~0u, mx[r], 1));
+      mx[r] = fmaxf(mx[r], __shfl_xor_sync(~0u, mx[r], 2));
+      mx[r] = fmaxf(mx[r], st.m[r]);
+    }
+    if (__any_sync(~0u, mx[0] > st.m[0] || mx[1] > st.m[1])) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const float f = mx[r] > st.m[r] ? ex2_approx(st.m[r] - mx[r]) : 1.f;
+        st.m[r] = mx[r];
+        st.l[r] *= f;
+#pragma unroll
+        for (int t = 0; t < 16; ++t) {
+          st.o[t][2 * r] *= f;
+          st.o[t][2 * r + 1] *= f;
+        }
+      }
+    }
+    uint32_t p[4];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const float base = (st.m[r] == -INFINITY ? 0.f : st.m[r]) - H::kBias;
+      float e[4];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        e[2 * t] = ex2_approx(fmaf(s[t][2 * r], a.scale_log2, -base));
+        e[2 * t + 1] = ex2_approx(fmaf(s[t][2 * r + 1], a.scale_log2, -base));
+      }
+      st.l[r] += (e[0] + e[1]) + (e[2] + e[3]);
+      p[r] = H::pack(e[0], e[1]);
+      p[2 + r] = H::pack(e[2], e[3]);
+    }
+    uint32_t bad = 0;
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+      uint32_t b[4];
+      ldsm4t(b, sv + vkey * 256 + (((2 * t + vcol) ^ (vkey & 7)) << 4));
+      if (part) bad |= H::not_finite(b[0]) || H::not_finite(b[1]) || H::not_finite(b[2]) || H::not_finite(b[3]);
+      if (!part) {
+        H::mma(st.o[2 * t], p, b[0], b[1]);
+        H::mma(st.o[2 * t + 1], p, b[2], b[3]);
+      }
+    }
+    if (part) {
+      if (!__any_sync(~0u, bad)) {
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+          uint32_t b[4];
+          ldsm4t(b, sv + vkey * 256 + (((2 * t + vcol) ^ (vkey & 7)) << 4));
+          H::mma(st.o[2 * t], p, b[0], b[1]);
+          H::mma(st.o[2 * t + 1], p, b[2], b[3]);
+        }
+      } else {
+        // a value that is not finite, in keys that some row does not attend:
+        // 0 times it would be NaN there, so each row adds its own keys only
+#pragma unroll 1
+        for (int k = 0; k < kSlice; ++k) {
+          const int from = (lane & ~3) | ((k & 7) >> 1);
+          const float2 x0 = H::unpack(__shfl_sync(~0u, k < 8 ? p[0] : p[2], from));
+          const float2 x1 = H::unpack(__shfl_sync(~0u, k < 8 ? p[1] : p[3], from));
+          const float pa = (k & 1) ? x0.y : x0.x, pb = (k & 1) ? x1.y : x1.x;
+          const bool ta = in_span(sa, j0 + k), tb = in_span(sb, j0 + k);
+#pragma unroll
+          for (int t = 0; t < 16; ++t) {
+            uint32_t w;
+            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(sv + k * 256 + ((t ^ (k & 7)) << 4) + 4 * (lane & 3)));
+            const float2 vv = H::unpack(w);
+            if (ta) {
+              st.o[t][0] = fmaf(pa, vv.x, st.o[t][0]);
+              st.o[t][1] = fmaf(pa, vv.y, st.o[t][1]);
+            }
+            if (tb) {
+              st.o[t][2] = fmaf(pb, vv.x, st.o[t][2]);
+              st.o[t][3] = fmaf(pb, vv.y, st.o[t][3]);
+            }
+          }
+        }
+      }
+    }
+    __syncwarp();  // the stage is refilled by the next issue
+  }
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    st.l[r] += __shfl_xor_sync(~0u, st.l[r], 1);
+    st.l[r] += __shfl_xor_sync(~0u, st.l[r], 2);
+  }
+}
+
+__device__ __forceinline__ void st_row16(__nv_bfloat16* dst, const float (&x)[16]) {
+  uint32_t w[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) w[k] = Half2<__nv_bfloat16>::pack(x[2 * k], x[2 * k + 1]);
+  *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+  *reinterpret_cast<uint4*>(dst + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+}
+__device__ __forceinline__ void st_row16(__half* dst, const float (&x)[16]) {
+  uint32_t w[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) w[k] = Half2<__half>::pack(x[2 * k], x[2 * k + 1]);
+  *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+  *reinterpret_cast<uint4*>(dst + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kDecThreads, 2) paged_decode_kernel(const PagedAttnArgs a) {
+  extern __shared__ __align__(1024) uint8_t ring[];
+  __shared__ DecodeShared sh;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr float kBias = Half2<T>::kBias;
+
+  // rows that no request owns
+  {
+    const SegInfo s0 = a.n_seq > 0 ? paged_seg(a, 0, false) : SegInfo{};
+    const SegInfo s1 = a.n_seq > 0 ? paged_seg(a, a.n_seq - 1, false) : SegInfo{};
+    const int lo = s0.q_off, hi = s1.q_off + s1.q_len;  // rows [0, lo) and [hi, Tq)
+    const long long n = static_cast<long long>(lo + max(a.Tq - hi, 0)) * a.Hq * 16;
+    for (long long t = blockIdx.x * static_cast<long long>(kDecThreads) + tid; t < n;
+         t += gridDim.x * static_cast<long long>(kDecThreads)) {
+      const long long rh = t >> 4;
+      long long row = rh / a.Hq;
+      if (row >= lo) row += hi - lo;
+      const int h = static_cast<int>(rh % a.Hq);
+      reinterpret_cast<uint4*>(a.o)[(row * a.Hq + h) * 16 + (t & 15)] = make_uint4(0, 0, 0, 0);
+      if ((t & 15) == 0) a.lse[static_cast<long long>(h) * a.Tq + row] = -INFINITY;
+    }
+  }
+
+  // requests whose rows do not overlap make fewer than 2^52 units; a q_start
+  // that lets them overlap may make more, and is reported and not served then
+  constexpr long long kMost = 1LL << 52;
+  long long total = 0;
+  for (int base = 0; base < a.n_seq; base += kSeqTile)
+    total = min(total + place_requests(a, sh, base, blockIdx.x == 0), kMost);
+  if (total == 0 || total == kMost) return;
+  const long long ctas = min(static_cast<long long>(gridDim.x), max(total / kMinUnits, 1LL));
+  if (blockIdx.x >= ctas) return;
+  auto span_start = [&](long long c) { return c * total / ctas; };
+  auto cta_of = [&](long long p) { return ((p + 1) * ctas - 1) / total; };
+  long long pos = span_start(blockIdx.x);
+  const long long end = span_start(blockIdx.x + 1);
+  int base = a.n_seq > kSeqTile ? -kSeqTile : 0;      // requests in sh.start begin at base
+  long long tile0 = 0, tile1 = a.n_seq > kSeqTile ? 0 : total;  // their units
+  while (pos < end) {
+    while (pos >= tile1) {
+      base += kSeqTile;
+      if (base >= a.n_seq) return;  // only if the lengths changed meanwhile
+      tile0 = tile1;
+      tile1 += place_requests(a, sh, base, false);
+    }
+    int lo = 0, hi = kSeqTile;  // the last request that starts at or before pos
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (sh.start[mid] <= pos - tile0) lo = mid; else hi = mid;
+    }
+    const int seq = base + lo;
+    const SegInfo sg = paged_seg(a, seq, false);
+    const Units un = units_of(hull(a.mask, sg, 0, sg.q_len));
+    const int nu = max(un.n0 + un.n1, 1);
+    const long long local = pos - tile0 - sh.start[lo];
+    const long long item = local / nu;
+    const int u0 = static_cast<int>(local - item * nu);
+    const int n = static_cast<int>(min(static_cast<long long>(nu - u0), end - pos));
+    const int tiles = row_tiles(a, sg.q_len);
+    const int head = static_cast<int>(item / tiles), tile = static_cast<int>(item % tiles);
+
+    uint8_t* mine = ring + warp * kWarpBytes;
+    {
+      WarpState<T> st;
+      // an item without keys has one unit that holds none
+      decode_warp<T>(a, smem_u32(mine), seq, sg, un, tile, head, u0, un.n0 + un.n1 > 0 ? n : 0, st);
+      cp_async_wait<0>();
+      __syncwarp();
+      float* po = reinterpret_cast<float*>(mine);  // [16][132]
+      const int r = lane >> 2, c = 2 * (lane & 3);
+#pragma unroll
+      for (int t = 0; t < 16; ++t) {
+        *reinterpret_cast<float2*>(po + r * 132 + 8 * t + c) = make_float2(st.o[t][0], st.o[t][1]);
+        *reinterpret_cast<float2*>(po + (r + 8) * 132 + 8 * t + c) = make_float2(st.o[t][2], st.o[t][3]);
+      }
+      if ((lane & 3) == 0) {
+        sh.m[warp][r] = st.m[0];
+        sh.m[warp][r + 8] = st.m[1];
+        sh.l[warp][r] = st.l[0];
+        sh.l[warp][r + 8] = st.l[1];
+      }
+    }
+    __syncthreads();
+    // the four warps' sums; thread: row tid / 8, columns 16 (tid % 8)
+    const int row = tid >> 3, col = (tid & 7) * 16;
+    float m = -INFINITY, l = 0.f, x[16] = {};
+#pragma unroll
+    for (int w = 0; w < kDecWarps; ++w) m = fmaxf(m, sh.m[w][row]);
+#pragma unroll
+    for (int w = 0; w < kDecWarps; ++w) {
+      const float f = sh.l[w][row] != 0.f ? ex2_approx(sh.m[w][row] - m) : 0.f;
+      l += f * sh.l[w][row];
+      const float* po = reinterpret_cast<const float*>(ring + w * kWarpBytes) + row * 132 + col;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float4 y = *reinterpret_cast<const float4*>(po + 4 * k);
+        x[4 * k] = fmaf(f, y.x, x[4 * k]);
+        x[4 * k + 1] = fmaf(f, y.y, x[4 * k + 1]);
+        x[4 * k + 2] = fmaf(f, y.z, x[4 * k + 2]);
+        x[4 * k + 3] = fmaf(f, y.w, x[4 * k + 3]);
+      }
+    }
+    bool write = true;
+    if (n < nu) {
+      // first and last CTA of the item; a CTA keeps its span's first piece in
+      // slot 2 c and a later, unfinished one in slot 2 c + 1
+      const long long i0 = pos - u0, c0 = cta_of(i0), c1 = cta_of(i0 + nu - 1);
+      auto slot = [&](long long c) { return a.parts + (2 * c + (c == c0 && span_start(c) < i0 ? 1 : 0)) * kPartFloats; };
+      float* part = slot(blockIdx.x);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        __stcg(reinterpret_cast<float4*>(part + row * kHeadDim + col) + k,
+               make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]));
+      if ((tid & 7) == 0) {
+        __stcg(part + kRows * kHeadDim + row, m);
+        __stcg(part + kRows * kHeadDim + kRows + row, l);
+      }
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) sh.last = atomicAdd(a.arrived + c0, 1) == static_cast<int>(c1 - c0);
+      __syncthreads();
+      write = sh.last != 0;
+      if (write) {
+        __threadfence();
+        m = -INFINITY;
+        for (long long c = c0; c <= c1; ++c) m = fmaxf(m, __ldcg(slot(c) + kRows * kHeadDim + row));
+        l = 0.f;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) x[k] = 0.f;
+        for (long long c = c0; c <= c1; ++c) {
+          const float* y = slot(c);
+          const float lc = __ldcg(y + kRows * kHeadDim + kRows + row);
+          const float f = lc != 0.f ? ex2_approx(__ldcg(y + kRows * kHeadDim + row) - m) : 0.f;
+          l = fmaf(f, lc, l);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float4 z = __ldcg(reinterpret_cast<const float4*>(y + row * kHeadDim + col) + k);
+            x[4 * k] = fmaf(f, z.x, x[4 * k]);
+            x[4 * k + 1] = fmaf(f, z.y, x[4 * k + 1]);
+            x[4 * k + 2] = fmaf(f, z.z, x[4 * k + 2]);
+            x[4 * k + 3] = fmaf(f, z.w, x[4 * k + 3]);
+          }
+        }
+      }
+    }
+    const long long r = static_cast<long long>(tile) * kRows + row;
+    if (write && r < static_cast<long long>(sg.q_len) * a.G) {
+      const long long token = sg.q_off + r / a.G;
+      const int h = head * a.G + static_cast<int>(r % a.G);
+      const float inv = l == 0.f ? 0.f : 1.f / l;  // a NaN stays one
+#pragma unroll
+      for (int k = 0; k < 16; ++k) x[k] *= inv;
+      st_row16(static_cast<T*>(a.o) + (token * a.Hq + h) * kHeadDim + col, x);
+      if ((tid & 7) == 0)
+        a.lse[static_cast<long long>(h) * a.Tq + token] =
+            l == 0.f ? -INFINITY : (m + log2f(l) - kBias) * 0.6931471805599453f;
+    }
+    pos += n;
+    __syncthreads();  // the ring is refilled
+  }
 }
 
 }  // namespace
@@ -260,17 +786,19 @@ void launch_paged_write(const PagedWriteArgs& a, int num_sms, cudaStream_t st) {
   paged_write_kernel<<<static_cast<int>(std::min<long long>(n, num_sms * 8LL)), 256, 0, st>>>(a);
 }
 
-void launch_paged_attn(const PagedAttnArgs& a, bool fp16, int, cudaStream_t st) {
-  if (a.n_seq > 0) {
-    note_launches(1);
-    paged_seqs_kernel<<<(a.n_seq + 255) / 256, 256, 0, st>>>(a);
-  }
-  const int grid = static_cast<int>((static_cast<long long>(a.Tq) * a.Hq + 7) / 8);
+template <typename T>
+void launch_decode(const PagedAttnArgs& a, int num_sms, cudaStream_t st) {
+  // set on every launch: the attribute belongs to the current device
+  cudaFuncSetAttribute(paged_decode_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kDecSmem);
   note_launches(1);
+  paged_decode_kernel<T><<<std::min(2 * num_sms, kPagedMaxCtas), kDecThreads, kDecSmem, st>>>(a);
+}
+
+void launch_paged_attn(const PagedAttnArgs& a, bool fp16, int num_sms, cudaStream_t st) {
   if (fp16)
-    paged_rows_kernel<__half><<<grid, 256, 0, st>>>(a);
+    launch_decode<__half>(a, num_sms, st);
   else
-    paged_rows_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(a);
+    launch_decode<__nv_bfloat16>(a, num_sms, st);
 }
 
 }  // namespace lca

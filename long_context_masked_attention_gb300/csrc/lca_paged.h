@@ -30,10 +30,10 @@ struct PagedWriteArgs {
 };
 void launch_paged_write(const PagedWriteArgs& a, int num_sms, cudaStream_t st);
 
-// A request as the kernels see it: lengths clamped to what the tensors hold.
-struct PagedSeq {
-  int q_off, q_len, k_len, pad;
-};
+// Attention over few rows: at most this many CTAs, each with two workspace
+// slots for unfinished sums (16 rows of O, maximum and sum).
+constexpr int kPagedMaxCtas = 512;
+constexpr int kPagedPartFloats = 16 * (kHeadDim + 2);
 
 struct PagedAttnArgs {
   MaskCtx mask;
@@ -44,7 +44,8 @@ struct PagedAttnArgs {
   void* o;
   float* lse;
   int* status;
-  PagedSeq* seqs;
+  int* arrived;  // [kPagedMaxCtas] pieces finished of the split item that starts in a CTA's span
+  float* parts;  // [kPagedMaxCtas][2][kPagedPartFloats]
   int Tq, Hq, Hkv, G, n_seq, max_pages, page_size, n_pages;
   float scale_log2;
 };

@@ -43,10 +43,10 @@ bool cache_memory(const lca_paged_cache* c) {
 }
 
 struct PagedLayout {
-  size_t status = 0, seqs = 0, total = 0;
+  size_t status = 0, arrived = 0, parts = 0, total = 0;
 };
 
-PagedLayout paged_layout(const lca_paged_shape* sh) {
+PagedLayout paged_layout() {
   PagedLayout L;
   size_t o = 0;
   auto take = [&](size_t bytes) {
@@ -55,7 +55,8 @@ PagedLayout paged_layout(const lca_paged_shape* sh) {
     return at;
   };
   L.status = take(16);
-  L.seqs = take(sizeof(PagedSeq) * static_cast<size_t>(sh->n_seq));
+  L.arrived = take(sizeof(int) * kPagedMaxCtas);
+  L.parts = take(sizeof(float) * 2 * kPagedMaxCtas * kPagedPartFloats);
   L.total = o;
   return L;
 }
@@ -198,7 +199,7 @@ lca_status lca_attn_paged_workspace_size(const lca_paged_shape* shape, const lca
   MaskCtx m;
   const lca_status r = check_attn(shape, cache, mask, m);
   if (r != LCA_OK) return r;
-  *bytes = paged_layout(shape).total;
+  *bytes = paged_layout().total;
   return LCA_OK;
 }
 
@@ -209,7 +210,7 @@ lca_status lca_attn_paged(const void* q, const lca_paged_cache* cache, const int
   PagedAttnArgs a{};
   const lca_status r = check_attn(shape, cache, mask, a.mask);
   if (r != LCA_OK) return r;
-  const PagedLayout L = paged_layout(shape);
+  const PagedLayout L = paged_layout();
   if (!workspace || reinterpret_cast<uintptr_t>(workspace) % kAlign != 0 || workspace_bytes < L.total ||
       !device_input(workspace))
     return LCA_ERR_WORKSPACE;
@@ -240,7 +241,8 @@ lca_status lca_attn_paged(const void* q, const lca_paged_cache* cache, const int
   a.o = o;
   a.lse = lse;
   a.status = reinterpret_cast<int*>(ws + L.status);
-  a.seqs = reinterpret_cast<PagedSeq*>(ws + L.seqs);
+  a.arrived = reinterpret_cast<int*>(ws + L.arrived);
+  a.parts = reinterpret_cast<float*>(ws + L.parts);
   a.Tq = shape->Tq;
   a.Hq = shape->Hq;
   a.Hkv = cache->Hkv;
@@ -252,7 +254,7 @@ lca_status lca_attn_paged(const void* q, const lca_paged_cache* cache, const int
   const float scale = shape->scale > 0.f ? shape->scale : 1.0f / std::sqrt(static_cast<float>(kHeadDim));
   a.scale_log2 = scale * 1.4426950408889634f;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  LCA_CUDA(cudaMemsetAsync(a.status, 0, 16, st));
+  LCA_CUDA(cudaMemsetAsync(ws, 0, L.parts, st));  // status and counts
   if (shape->Tq > 0) launch_paged_attn(a, cache->dtype == LCA_F16, sms, st);
   LCA_CUDA(cudaGetLastError());
   return LCA_OK;
