@@ -6,6 +6,7 @@
 
 #include <algorithm>
 
+#include "lca_paged.cuh"
 #include "lca_paged.h"
 #include "sm103.cuh"
 
@@ -205,50 +206,28 @@ constexpr int kPartFloats = kRows * (kHeadDim + 2);
 static_assert(kSlice == 16, "a slice is one k16 step of the product with V");
 static_assert(kPartFloats == kPagedPartFloats, "workspace layout");
 
+// bf16 has the exponents of fp32.  fp16 holds nothing below 2^-24: p, at most
+// 1, is kept times 2^12, so that keys down to 2^-36 of the largest still
+// count; O, l and their partial sums carry the factor, the quotient and the
+// LSE do not.
 template <typename T>
-struct Half2;
+constexpr float kBias = 0.f;
 template <>
-struct Half2<__nv_bfloat16> {
-  // p is at most 1, and bf16 has the exponents of fp32
-  static constexpr float kBias = 0.f;
-  static __device__ __forceinline__ uint32_t pack(float lo, float hi) { return pack_bf16x2(lo, hi); }
-  static __device__ __forceinline__ bool not_finite(uint32_t x) {
-    return (x & 0x7F80u) == 0x7F80u || (x & 0x7F800000u) == 0x7F800000u;
-  }
-  static __device__ __forceinline__ float2 unpack(uint32_t x) {
-    return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xFFFF0000u));
-  }
-  static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-                 "{%0, %1, %2, %3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  }
-};
-template <>
-struct Half2<__half> {
-  // fp16 holds nothing below 2^-24: p is kept times 2^12, so that keys down
-  // to 2^-36 of the largest still count; O, l and their partial sums carry
-  // the factor, the quotient and the LSE do not
-  static constexpr float kBias = 12.f;
-  static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-  }
-  static __device__ __forceinline__ bool not_finite(uint32_t x) {
-    return (x & 0x7C00u) == 0x7C00u || (x & 0x7C000000u) == 0x7C000000u;
-  }
-  static __device__ __forceinline__ float2 unpack(uint32_t x) {
-    return __half22float2(*reinterpret_cast<const __half2*>(&x));
-  }
-  static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-                 "{%0, %1, %2, %3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  }
-};
+constexpr float kBias<__half> = 12.f;
+
+__device__ __forceinline__ void warp_mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1,
+                                         __nv_bfloat16) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+               "{%0, %1, %2, %3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void warp_mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, __half) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+               "{%0, %1, %2, %3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -270,45 +249,6 @@ __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commi
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-__device__ __forceinline__ bool in_span(const Span& s, int j) {
-  return (j >= s.a0 && j < s.b0) || (j >= s.a1 && j < s.b1);
-}
-
-// Request i with its lengths clamped to what the tensors hold; `flag` reports
-// those that needed it.
-__device__ __forceinline__ SegInfo paged_seg(const PagedAttnArgs& a, int i, bool flag) {
-  const int r0 = a.q_start[i], r1 = a.q_start[i + 1], kl = a.k_len[i];
-  const int room = a.max_pages * a.page_size;
-  if (flag && (r0 < 0 || r1 < r0 || r1 > a.Tq || kl < 0 || kl > room)) raise_status(a.status, kStatusDeviceArg, 50);
-  SegInfo s{};
-  s.q_off = min(max(r0, 0), a.Tq);
-  s.q_len = min(max(r1, s.q_off), a.Tq) - s.q_off;
-  s.k_len = min(max(kl, 0), room);
-  return s;
-}
-
-// Keys that some of the tokens [i0, i1) of a request attends: in every family
-// the bounds of a row's intervals do not decrease from token to token, but
-// for the first lower bound, which may fall to 0 at the last rows, and for
-// GLOBAL_SLIDING's first rows, whose one interval holds all keys; so the two
-// outer rows give the hull.
-__device__ __forceinline__ Span hull(const MaskCtx& m, const SegInfo& sg, int i0, int i1) {
-  const Span s = row_span(m, sg, i0), t = row_span(m, sg, i1 - 1);
-  Span h;
-  h.a0 = min(s.a0, t.a0);
-  h.b0 = max(max(s.b0, t.b0), h.a0);
-  h.a1 = h.b1 = h.b0;
-  if (t.a1 < t.b1) {
-    h.a1 = s.a1 < s.b1 ? min(s.a1, t.a1) : t.a1;
-    h.b1 = max(t.b1, h.b0);
-    if (h.a1 <= h.b0) {  // they touch
-      h.b0 = h.b1;
-      h.a1 = h.b1;
-    }
-  }
-  return h;
 }
 
 // The units of a hull: n0 from t0 on, then n1 from t1 on.
@@ -333,7 +273,7 @@ __device__ __forceinline__ int row_tiles(const PagedAttnArgs& a, int q_len) {
 // whole request's hull, at least one, so that rows without keys are written.
 __device__ __forceinline__ long long line_units(const PagedAttnArgs& a, int i, bool flag) {
   const SegInfo sg = paged_seg(a, i, flag);
-  if (sg.q_len == 0) return 0;
+  if (sg.q_len == 0 || !few_rows(a, sg.q_len)) return 0;
   const Units u = units_of(hull(a.mask, sg, 0, sg.q_len));
   return static_cast<long long>(row_tiles(a, sg.q_len)) * a.Hkv * max(u.n0 + u.n1, 1);
 }
@@ -487,8 +427,8 @@ __device__ __forceinline__ void decode_warp(const PagedAttnArgs& a, uint32_t rin
     for (int c = 0; c < 8; ++c) {
       uint32_t b[4];
       ldsm4(b, sk + kkey * 256 + (((2 * c + kcol) ^ (kkey & 7)) << 4));
-      H::mma(s[0], q[c], b[0], b[1]);
-      H::mma(s[1], q[c], b[2], b[3]);
+      warp_mma(s[0], q[c], b[0], b[1], T());
+      warp_mma(s[1], q[c], b[2], b[3], T());
     }
     const bool part = !__all_sync(~0u, span_covers(sa, j0, j0 + kSlice) && span_covers(sb, j0, j0 + kSlice));
     if (part) {
@@ -524,7 +464,7 @@ __device__ __forceinline__ void decode_warp(const PagedAttnArgs& a, uint32_t rin
     uint32_t p[4];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      const float base = (st.m[r] == -INFINITY ? 0.f : st.m[r]) - H::kBias;
+      const float base = (st.m[r] == -INFINITY ? 0.f : st.m[r]) - kBias<T>;
       float e[4];
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
@@ -542,8 +482,8 @@ __device__ __forceinline__ void decode_warp(const PagedAttnArgs& a, uint32_t rin
       ldsm4t(b, sv + vkey * 256 + (((2 * t + vcol) ^ (vkey & 7)) << 4));
       if (part) bad |= H::not_finite(b[0]) || H::not_finite(b[1]) || H::not_finite(b[2]) || H::not_finite(b[3]);
       if (!part) {
-        H::mma(st.o[2 * t], p, b[0], b[1]);
-        H::mma(st.o[2 * t + 1], p, b[2], b[3]);
+        warp_mma(st.o[2 * t], p, b[0], b[1], T());
+        warp_mma(st.o[2 * t + 1], p, b[2], b[3], T());
       }
     }
     if (part) {
@@ -552,8 +492,8 @@ __device__ __forceinline__ void decode_warp(const PagedAttnArgs& a, uint32_t rin
         for (int t = 0; t < 8; ++t) {
           uint32_t b[4];
           ldsm4t(b, sv + vkey * 256 + (((2 * t + vcol) ^ (vkey & 7)) << 4));
-          H::mma(st.o[2 * t], p, b[0], b[1]);
-          H::mma(st.o[2 * t + 1], p, b[2], b[3]);
+          warp_mma(st.o[2 * t], p, b[0], b[1], T());
+          warp_mma(st.o[2 * t + 1], p, b[2], b[3], T());
         }
       } else {
         // a value that is not finite, in keys that some row does not attend:
@@ -591,17 +531,11 @@ __device__ __forceinline__ void decode_warp(const PagedAttnArgs& a, uint32_t rin
   }
 }
 
-__device__ __forceinline__ void st_row16(__nv_bfloat16* dst, const float (&x)[16]) {
+template <typename T>
+__device__ __forceinline__ void st_row16(T* dst, const float (&x)[16]) {
   uint32_t w[8];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) w[k] = Half2<__nv_bfloat16>::pack(x[2 * k], x[2 * k + 1]);
-  *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-  *reinterpret_cast<uint4*>(dst + 8) = make_uint4(w[4], w[5], w[6], w[7]);
-}
-__device__ __forceinline__ void st_row16(__half* dst, const float (&x)[16]) {
-  uint32_t w[8];
-#pragma unroll
-  for (int k = 0; k < 8; ++k) w[k] = Half2<__half>::pack(x[2 * k], x[2 * k + 1]);
+  for (int k = 0; k < 8; ++k) w[k] = Half2<T>::pack(x[2 * k], x[2 * k + 1]);
   *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
   *reinterpret_cast<uint4*>(dst + 8) = make_uint4(w[4], w[5], w[6], w[7]);
 }
@@ -611,7 +545,6 @@ __global__ void __launch_bounds__(kDecThreads, 2) paged_decode_kernel(const Page
   extern __shared__ __align__(1024) uint8_t ring[];
   __shared__ DecodeShared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  constexpr float kBias = Half2<T>::kBias;
 
   // rows that no request owns
   {
@@ -762,7 +695,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) paged_decode_kernel(const Page
       st_row16(static_cast<T*>(a.o) + (token * a.Hq + h) * kHeadDim + col, x);
       if ((tid & 7) == 0)
         a.lse[static_cast<long long>(h) * a.Tq + token] =
-            l == 0.f ? -INFINITY : (m + log2f(l) - kBias) * 0.6931471805599453f;
+            l == 0.f ? -INFINITY : (m + log2f(l) - kBias<T>) * 0.6931471805599453f;
     }
     pos += n;
     __syncthreads();  // the ring is refilled
@@ -794,7 +727,7 @@ void launch_decode(const PagedAttnArgs& a, int num_sms, cudaStream_t st) {
   paged_decode_kernel<T><<<std::min(2 * num_sms, kPagedMaxCtas), kDecThreads, kDecSmem, st>>>(a);
 }
 
-void launch_paged_attn(const PagedAttnArgs& a, bool fp16, int num_sms, cudaStream_t st) {
+void launch_paged_decode(const PagedAttnArgs& a, bool fp16, int num_sms, cudaStream_t st) {
   if (fp16)
     launch_decode<__half>(a, num_sms, st);
   else

@@ -34,6 +34,12 @@ void launch_paged_write(const PagedWriteArgs& a, int num_sms, cudaStream_t st);
 // slots for unfinished sums (16 rows of O, maximum and sum).
 constexpr int kPagedMaxCtas = 512;
 constexpr int kPagedPartFloats = 16 * (kHeadDim + 2);
+// Over many rows: the same with 256 rows.
+constexpr int kPagedMaxChunkCtas = 256;
+constexpr int kPagedChunkPartFloats = 256 * (kHeadDim + 2);
+// Requests with up to this many rows (new tokens x query heads of a group)
+// per KV head go to the kernel for few rows when both kernels run.
+constexpr int kPagedFewRows = 16;
 
 struct PagedAttnArgs {
   MaskCtx mask;
@@ -48,7 +54,21 @@ struct PagedAttnArgs {
   float* parts;  // [kPagedMaxCtas][2][kPagedPartFloats]
   int Tq, Hq, Hkv, G, n_seq, max_pages, page_size, n_pages;
   float scale_log2;
+  int few;  // rows per KV head up to which the kernel for few rows serves a request
+  // the kernel for many rows
+  int tpt;       // tokens of a 128-row sub-tile: floor(128 / G)
+  int box_rows;  // keys of one TMA box: gcd(page_size, 128)
+  int max_blocks;
+  int* block0;        // [n_seq + 1] row blocks before each request
+  long long* line;    // [max_blocks + 1] key tiles before each row block
+  float* chunk_parts; // [kPagedMaxChunkCtas][2][kPagedChunkPartFloats]
+  int out_v8;         // o is 32-byte aligned
+  unsigned long long wait_limit_ns;
 };
-void launch_paged_attn(const PagedAttnArgs& a, bool fp16, int num_sms, cudaStream_t st);
+void launch_paged_decode(const PagedAttnArgs& a, bool fp16, int num_sms, cudaStream_t st);
+// Queries as boxes of tpt tokens x G heads x 64, keys and values as boxes of
+// box_rows tokens of one page and head x 64, 128-byte swizzled.
+void launch_paged_chunk(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttnArgs& a,
+                        bool fp16, int num_sms, cudaStream_t st);
 
 }  // namespace lca

@@ -42,11 +42,23 @@ bool cache_memory(const lca_paged_cache* c) {
   return c->k && c->v && aligned16(c->k) && aligned16(c->v) && device_input(c->k) && device_input(c->v);
 }
 
+// Whether the kernel for many rows takes part: some request may have more
+// rows per KV head than the other one's tile, a token's heads fit a tile, and
+// there is a cache to map.
+bool many_rows(const lca_paged_shape* sh, const lca_paged_cache* c) {
+  const long long G = sh->Hq / c->Hkv;
+  const long long most = sh->max_q_len > 0 && sh->max_q_len < sh->Tq ? sh->max_q_len : sh->Tq;
+  return most * G > kPagedFewRows && G <= kTile && c->n_pages > 0;
+}
+
+int tokens_per_tile(const lca_paged_shape* sh, const lca_paged_cache* c) { return kTile / (sh->Hq / c->Hkv); }
+
 struct PagedLayout {
-  size_t status = 0, arrived = 0, parts = 0, total = 0;
+  size_t status = 0, arrived = 0, parts = 0, block0 = 0, line = 0, chunk_parts = 0, total = 0;
+  int max_blocks = 0;
 };
 
-PagedLayout paged_layout() {
+PagedLayout paged_layout(const lca_paged_shape* sh, const lca_paged_cache* c) {
   PagedLayout L;
   size_t o = 0;
   auto take = [&](size_t bytes) {
@@ -57,6 +69,12 @@ PagedLayout paged_layout() {
   L.status = take(16);
   L.arrived = take(sizeof(int) * kPagedMaxCtas);
   L.parts = take(sizeof(float) * 2 * kPagedMaxCtas * kPagedPartFloats);
+  if (many_rows(sh, c)) {
+    L.max_blocks = sh->Tq / (2 * tokens_per_tile(sh, c)) + sh->n_seq;
+    L.block0 = take(sizeof(int) * (sh->n_seq + 1LL));
+    L.line = take(sizeof(long long) * (L.max_blocks + 1LL));
+    L.chunk_parts = take(sizeof(float) * 2 * kPagedMaxChunkCtas * kPagedChunkPartFloats);
+  }
   L.total = o;
   return L;
 }
@@ -117,6 +135,32 @@ lca_status check_attn(const lca_paged_shape* sh, const lca_paged_cache* c, const
   m.wr = m.wr < kFar ? m.wr : kFar;
   m.block = m.block < kFar ? m.block : kFar;
   return LCA_OK;
+}
+
+bool encode(CUtensorMap* m, const void* p, int dtype, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+            const cuuint32_t* box) {
+  const auto fn = encode_fn();
+  if (!fn) {
+    driver_fail("cuTensorMapEncodeTiled entry point", 0);
+    return false;
+  }
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUresult r = fn(m, dtype == LCA_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank,
+                        const_cast<void*>(p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) driver_fail("cuTensorMapEncodeTiled", static_cast<int>(r));
+  return r == CUDA_SUCCESS;
+}
+
+bool cache_map(CUtensorMap* m, const void* p, const lca_paged_cache* c, int box_rows) {
+  const cuuint64_t dims[4] = {kHeadDim, static_cast<cuuint64_t>(c->page_size), static_cast<cuuint64_t>(c->Hkv),
+                              static_cast<cuuint64_t>(c->n_pages)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(c->token_stride) * 2,
+                                 static_cast<cuuint64_t>(c->head_stride) * 2,
+                                 static_cast<cuuint64_t>(c->page_stride) * 2};
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box_rows), 1, 1};
+  return encode(m, p, c->dtype, 4, dims, strides, box);
 }
 
 }  // namespace
@@ -199,7 +243,7 @@ lca_status lca_attn_paged_workspace_size(const lca_paged_shape* shape, const lca
   MaskCtx m;
   const lca_status r = check_attn(shape, cache, mask, m);
   if (r != LCA_OK) return r;
-  *bytes = paged_layout().total;
+  *bytes = paged_layout(shape, cache).total;
   return LCA_OK;
 }
 
@@ -210,7 +254,7 @@ lca_status lca_attn_paged(const void* q, const lca_paged_cache* cache, const int
   PagedAttnArgs a{};
   const lca_status r = check_attn(shape, cache, mask, a.mask);
   if (r != LCA_OK) return r;
-  const PagedLayout L = paged_layout();
+  const PagedLayout L = paged_layout(shape, cache);
   if (!workspace || reinterpret_cast<uintptr_t>(workspace) % kAlign != 0 || workspace_bytes < L.total ||
       !device_input(workspace))
     return LCA_ERR_WORKSPACE;
@@ -253,9 +297,31 @@ lca_status lca_attn_paged(const void* q, const lca_paged_cache* cache, const int
   a.n_pages = cache->n_pages;
   const float scale = shape->scale > 0.f ? shape->scale : 1.0f / std::sqrt(static_cast<float>(kHeadDim));
   a.scale_log2 = scale * 1.4426950408889634f;
+  if (cache->n_pages == 0) a.kc = a.vc = q;  // no key is read; the address is only given
+  const bool many = many_rows(shape, cache) && shape->n_seq > 0;
+  a.few = many ? kPagedFewRows : 0x7FFFFFFF;
+  CUtensorMap tq, tk, tv;
+  if (many) {
+    a.tpt = tokens_per_tile(shape, cache);
+    a.box_rows = kTile;
+    while (cache->page_size % a.box_rows != 0) a.box_rows /= 2;
+    a.max_blocks = L.max_blocks;
+    a.block0 = reinterpret_cast<int*>(ws + L.block0);
+    a.line = reinterpret_cast<long long*>(ws + L.line);
+    a.chunk_parts = reinterpret_cast<float*>(ws + L.chunk_parts);
+    a.out_v8 = (reinterpret_cast<uintptr_t>(o) & 31u) == 0;
+    a.wait_limit_ns = wait_limit_ns();
+    const cuuint64_t dims[3] = {kHeadDim, static_cast<cuuint64_t>(a.Hq), static_cast<cuuint64_t>(a.Tq)};
+    const cuuint64_t strides[2] = {kHeadDim * 2, static_cast<cuuint64_t>(a.q_stride) * 2};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(a.G), static_cast<cuuint32_t>(a.tpt)};
+    if (!encode(&tq, q, cache->dtype, 3, dims, strides, box) || !cache_map(&tk, cache->k, cache, a.box_rows) ||
+        !cache_map(&tv, cache->v, cache, a.box_rows))
+      return LCA_ERR_CUDA;
+  }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   LCA_CUDA(cudaMemsetAsync(ws, 0, L.parts, st));  // status and counts
-  if (shape->Tq > 0) launch_paged_attn(a, cache->dtype == LCA_F16, sms, st);
+  if (many) launch_paged_chunk(tq, tk, tv, a, cache->dtype == LCA_F16, sms, st);
+  if (shape->Tq > 0) launch_paged_decode(a, cache->dtype == LCA_F16, sms, st);
   LCA_CUDA(cudaGetLastError());
   return LCA_OK;
 }

@@ -1,0 +1,910 @@
+// lca_paged_chunk.cu — attention of many rows over a paged cache for sm_103a
+// (tcgen05 + TMEM + TMA): prompts, chunks of prompts, drafts to verify.
+//
+// The rows of a request that share a KV head are packed: row t G + g of a
+// head's block is new token t, query head g of the group, so the G query
+// heads read every key once and a block of few tokens still fills a tile.  A
+// sub-tile of 128 rows holds tpt = floor(128 / G) tokens; an item is two
+// sub-tiles of one (request, KV head).  Queries come by TMA as boxes of
+// [token][head of the group][64], keys and values as boxes of the rows of one
+// page: gcd(page_size, 128) rows, so that no box leaves its page and a
+// 128-key tile is a whole number of them whatever the page size.  Table
+// entries are read by the producer's lanes one tile ahead; keys that no row
+// attends are not read (a box outside the array is filled with zeros).
+//
+// The products bound the work (4 d operations per attended pair); per key
+// tile and item 1024 keys' rows pass the tensor core against 64 KB of K and V
+// from L2.  Roles as in the packed forward: warp 9 loads, warp 8 issues
+// S = Q K^T and O += P V, warps 0-7 are two softmax warpgroups, each thread
+// one row.  The tiles of all items form one line that is cut into equal spans,
+// one per CTA (paged_items_kernel places the items on it), so that batches of
+// any mixture of lengths end together; the items that a cut divides leave
+// their sums in the workspace and paged_join_kernel joins them in the order
+// of the keys.  An item of one sub-tile (a narrow one: at most 128 rows)
+// gives both score buffers to that sub-tile, so that the product with the
+// next keys runs while the first warpgroup works on the present ones.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "lca_paged.cuh"
+#include "lca_paged.h"
+#include "sm103.cuh"
+
+namespace lca {
+namespace {
+
+constexpr int kThreads = 320;
+constexpr int kStages = 5;
+constexpr uint32_t kTileBytes = 32768;   // 128 rows x 128 values
+constexpr uint32_t kChunkBytes = 16384;  // 128 rows x 64 values, 128-byte swizzled
+constexpr int kOffQ = 0;
+constexpr int kOffKV = 2 * kTileBytes;
+constexpr int kOffCtl = kOffKV + kStages * kTileBytes;
+constexpr int kSmemBytes = kOffCtl + 1024 + 1024;
+constexpr int kMinTiles = 4;  // a CTA's share, where there is that much
+
+enum : int {
+  B_QFULL = 0,
+  B_QEMPTY = 1,
+  B_KVFULL = 2,
+  B_KVEMPTY = B_KVFULL + kStages,
+  B_SFULL = B_KVEMPTY + kStages,
+  B_PFULL = B_SFULL + 2,
+  B_OFULL = B_PFULL + 2,
+  B_ITFULL = B_OFULL + 2,
+  B_ITEMPTY = B_ITFULL + 2,
+  B_DRAIN = B_ITEMPTY + 2,
+  B_COUNT = B_DRAIN + 1
+};
+
+// What the producer tells the other roles about a piece of an item.
+struct Item {
+  int valid, narrow;
+  int n, u0;              // its tiles: u0 .. u0 + n - 1 of the item's
+  int head, tok0;         // KV head; first token, inside the request
+  int part;               // workspace slot of its sums, -1 when it is the whole item
+  int seq;
+  int q_off, q_len, k_len;
+  int t0, n0, t1;         // the item's tiles: n0 from t0 on, then from t1 on
+  int pad[2];
+  Span hull[2], full[2];  // per sub-tile: keys that some, and that all, of its rows attend
+  Span all;               // keys that some row of the item attends
+  __device__ __forceinline__ int tile(int t) const { return u0 + t < n0 ? t0 + u0 + t : t1 + u0 + t - n0; }
+  __device__ __forceinline__ uint32_t cls(int x, int kt) const {
+    const int j0 = kt * kTile;
+    if (!span_hits(hull[x], j0, j0 + kTile)) return kTileEmpty;
+    return span_covers(full[x], j0, j0 + kTile) ? kTileFull : kTilePartial;
+  }
+};
+static_assert(sizeof(Item) == 144, "two items fit between the barriers and the TMEM slot");
+
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kRescaleThreshold = 8.0f;  // log2 units
+
+// fp16 holds nothing below 2^-24 and p reaches 2^8 between rescalings, so p
+// is kept times 2^7: at most 2^15, and keys down to 2^-31 of the largest count.
+template <typename T>
+constexpr float kBias = 0.f;
+template <>
+constexpr float kBias<__half> = 7.f;
+
+template <typename T>
+constexpr uint32_t kAbFormat = 0;  // fields of A and B format that idesc_bf16_f32 sets and T clears
+template <>
+constexpr uint32_t kAbFormat<__half> = (1u << 7) | (1u << 10);
+template <typename T>
+__host__ __device__ constexpr uint32_t idesc(bool b_mn_major) {
+  return idesc_bf16_f32(128, 128, false, b_mn_major) & ~kAbFormat<T>;
+}
+
+__device__ __forceinline__ bool waitw(uint64_t* bar, uint32_t parity, const PagedAttnArgs& a, int where) {
+  const bool ok = mbar_wait(bar, parity, a.status, a.wait_limit_ns, kStatusTimeout, where);
+  return __all_sync(0xFFFFFFFFu, ok);
+}
+
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z,
+                                            int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
+      : "memory");
+}
+
+// ------------------------------------------------------------------ items
+// Keys that all of the tokens [i0, i1) of a request attend (some of them: the
+// intersection first interval by first, second by second).  Bounds move with
+// the position in one direction (see hull), so the outer rows decide, with
+// two exceptions that are looked at as well: GLOBAL_SLIDING's first row past
+// the global ones, and CAUSAL_BLOCKWISE's last row before the last block.
+__device__ __forceinline__ Span common(const MaskCtx& m, const SegInfo& sg, int i0, int i1) {
+  int mid = i0;
+  const int shift = sg.k_len - sg.q_len;
+  if (m.kind == kGlobalSliding) mid = m.ng - shift;
+  if (m.kind == kCausalBlockwise) mid = (sg.k_len - 1) / m.block * m.block - 1 - shift;
+  const int at[3] = {i0, min(max(mid, i0), i1 - 1), i1 - 1};
+  Span c{0, 0x7FFFFFFF, 0, 0x7FFFFFFF};
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    Span s = row_span(m, sg, at[k]);
+    if (s.a1 >= s.b1) s.a1 = s.a0, s.b1 = s.b0;  // one interval counts as both
+    c.a0 = max(c.a0, s.a0);
+    c.b0 = min(c.b0, s.b0);
+    c.a1 = max(c.a1, s.a1);
+    c.b1 = min(c.b1, s.b1);
+  }
+  return c;
+}
+
+// Key tiles of a hull: n0 from t0 on, then n1 from t1 on.
+struct Tiles {
+  int t0, n0, t1, n1;
+};
+__device__ __forceinline__ Tiles tiles_of(const Span& h) {
+  Tiles u;
+  u.t0 = h.a0 / kTile;
+  u.n0 = h.b0 > h.a0 ? (h.b0 + kTile - 1) / kTile - u.t0 : 0;
+  u.t1 = max(h.a1 / kTile, u.n0 > 0 ? u.t0 + u.n0 : 0);
+  u.n1 = h.b1 > h.a1 ? max((h.b1 + kTile - 1) / kTile - u.t1, 0) : 0;
+  return u;
+}
+
+// Row blocks (two sub-tiles) of request i; none when the other kernel serves it.
+__device__ __forceinline__ int row_blocks(const PagedAttnArgs& a, int q_len) {
+  return few_rows(a, q_len) ? 0 : (q_len + 2 * a.tpt - 1) / (2 * a.tpt);
+}
+
+// Sums over the requests and their row blocks: block0[i] = row blocks of the
+// requests before i, line[b] = key tiles of the row blocks before b (one head;
+// at least one per block, so that rows without keys are written).
+__global__ void __launch_bounds__(1024) paged_items_kernel(const PagedAttnArgs a) {
+  __shared__ long long part[32];
+  const int tid = threadIdx.x;
+  long long at = 0;
+  for (int base = 0; base < a.n_seq; base += 1024) {
+    const int i = base + tid;
+    const long long n = i < a.n_seq ? row_blocks(a, paged_seg(a, i, true).q_len) : 0;
+    long long total;
+    const long long inc = block_scan(n, part, total);
+    // rows that overlap (a bad q_start) can make more blocks than there is room for
+    if (i < a.n_seq) a.block0[i] = static_cast<int>(min(at + inc - n, static_cast<long long>(a.max_blocks)));
+    at += total;
+  }
+  const int blocks = static_cast<int>(min(at, static_cast<long long>(a.max_blocks)));
+  if (tid == 0) a.block0[a.n_seq] = blocks;
+  __syncthreads();
+  at = 0;
+  for (int base = 0; base < blocks; base += 1024) {
+    const int b = base + tid;
+    long long n = 0;
+    if (b < blocks) {
+      int i = 0;  // the last request whose blocks start at or before b
+      for (int hi = a.n_seq; hi - i > 1;) {
+        const int mid = (i + hi) >> 1;
+        if (a.block0[mid] <= b) i = mid; else hi = mid;
+      }
+      const SegInfo sg = paged_seg(a, i, false);
+      const int tok = (b - a.block0[i]) * 2 * a.tpt;
+      if (tok < sg.q_len) {
+        const Tiles t = tiles_of(hull(a.mask, sg, tok, min(tok + 2 * a.tpt, sg.q_len)));
+        n = max(t.n0 + t.n1, 1);
+      }
+    }
+    long long total;
+    const long long inc = block_scan(n, part, total);
+    if (b < blocks) a.line[b] = at + inc - n;
+    at += total;
+  }
+  if (tid == 0) a.line[blocks] = at;
+}
+
+// The line of tiles: request by request, head by head, block by block.
+struct Line {
+  long long total, ctas;
+  __device__ __forceinline__ Line(const PagedAttnArgs& a, int grid) {
+    total = a.line[a.block0[a.n_seq]] * a.Hkv;
+    ctas = min(static_cast<long long>(grid), max(total / kMinTiles, 1LL));
+  }
+  __device__ __forceinline__ long long start(long long c) const { return c * total / ctas; }
+  __device__ __forceinline__ long long cta_of(long long p) const { return ((p + 1) * ctas - 1) / total; }
+};
+
+struct Place {
+  int seq, head, block;  // block: inside the request
+  long long first;       // of the item on the line
+  int tiles;
+};
+__device__ __forceinline__ Place locate(const PagedAttnArgs& a, long long pos) {
+  int lo = 0, hi = a.n_seq;  // the last request that starts at or before pos
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (a.line[a.block0[mid]] * a.Hkv <= pos) lo = mid; else hi = mid;
+  }
+  Place p;
+  p.seq = lo;
+  const int b0 = a.block0[lo], b1 = a.block0[lo + 1];
+  const long long l0 = a.line[b0], per = a.line[b1] - l0;  // tiles of one head
+  const long long rel = pos - l0 * a.Hkv;
+  p.head = static_cast<int>(rel / per);
+  const long long in = rel - p.head * per + l0;
+  lo = b0, hi = b1;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (a.line[mid] <= in) lo = mid; else hi = mid;
+  }
+  p.block = lo - b0;
+  p.first = pos - (in - a.line[lo]);
+  p.tiles = static_cast<int>(a.line[lo + 1] - a.line[lo]);
+  return p;
+}
+
+// Slot of CTA c's sums of the item that starts at `first`: 2 c when it is the
+// first piece of its span, 2 c + 1 for a later one.
+__device__ __forceinline__ long long slot_of(const Line& ln, long long c, long long first) {
+  return 2 * c + (ln.start(c) < first ? 1 : 0);
+}
+
+// ------------------------------------------------------------------ producer
+__device__ __forceinline__ void producer(const PagedAttnArgs& a, const Line& ln, const CUtensorMap* tq,
+                                         const CUtensorMap* tk, const CUtensorMap* tv, uint8_t* sQ, uint8_t* sKV,
+                                         uint64_t* bar, Item* items) {
+  const int lane = threadIdx.x & 31;
+  const int boxes = kTile / a.box_rows;  // per tile and half
+  const int box = lane % boxes, half = lane / boxes;
+  const uint32_t q_bytes = static_cast<uint32_t>(a.tpt * a.G) * 128;  // of one 64-value half of a sub-tile
+  long long pos = ln.start(blockIdx.x);
+  const long long end = ln.start(blockIdx.x + 1);
+  uint32_t kv_iter = 0, issued = 0;
+  int q_issued = 0;
+  for (int it = 0;; ++it) {
+    const int slot = it & 1;
+    if (it >= 2 && !waitw(&bar[B_ITEMPTY + slot], ((it >> 1) - 1) & 1, a, 60)) break;
+    Item inf;
+    inf.valid = pos < end;
+    if (!inf.valid) {
+      if (lane == 0) {
+        items[slot].valid = 0;
+        mbar_arrive(&bar[B_ITFULL + slot]);
+      }
+      return;
+    }
+    const Place p = locate(a, pos);
+    const SegInfo sg = paged_seg(a, p.seq, false);
+    inf.seq = p.seq;
+    inf.head = p.head;
+    inf.tok0 = p.block * 2 * a.tpt;
+    inf.q_off = sg.q_off;
+    inf.q_len = sg.q_len;
+    inf.k_len = sg.k_len;
+    const int toks = min(2 * a.tpt, sg.q_len - inf.tok0);
+    inf.narrow = toks <= a.tpt;
+    inf.all = hull(a.mask, sg, inf.tok0, inf.tok0 + toks);
+    const Tiles tl = tiles_of(inf.all);
+    inf.t0 = tl.t0;
+    inf.n0 = tl.n0;
+    inf.t1 = tl.t1;
+    inf.u0 = static_cast<int>(pos - p.first);
+    const int take = static_cast<int>(min(static_cast<long long>(p.tiles - inf.u0), end - pos));
+    inf.n = tl.n0 + tl.n1 > 0 ? take : 0;
+    inf.part = take < p.tiles ? static_cast<int>(slot_of(ln, blockIdx.x, p.first)) : -1;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int i0 = inf.tok0 + (inf.narrow ? 0 : x * a.tpt), i1 = min(i0 + a.tpt, sg.q_len);
+      inf.hull[x] = hull(a.mask, sg, i0, i1);
+      inf.full[x] = common(a.mask, sg, i0, i1);
+    }
+    pos += take;
+    if (lane == 0) {
+      items[slot] = inf;
+      mbar_arrive(&bar[B_ITFULL + slot]);
+    }
+
+    if (it >= 1 && !waitw(&bar[B_QEMPTY], (it - 1) & 1, a, 61)) break;
+    if (lane == 0) {
+      const int subs = inf.narrow ? 1 : 2;
+      mbar_arrive_expect_tx(&bar[B_QFULL], 2 * subs * q_bytes);
+      for (int x = 0; x < subs; ++x)
+        for (int c = 0; c < 2; ++c)
+          tma_load_3d(sQ + x * kTileBytes + c * kChunkBytes, tq, &bar[B_QFULL], c * 64, inf.head * a.G,
+                      inf.q_off + inf.tok0 + x * a.tpt);
+    }
+    q_issued = it + 1;
+
+    const int* table = a.table + inf.seq * a.table_stride;
+    // page of this lane's box of tile t (n_pages, past the array, where none is
+    // needed or the entry is no page: that box is filled with zeros)
+    auto entry = [&](int t) -> int {
+      const int j = inf.tile(t) * kTile + box * a.box_rows;
+      if (!span_hits(inf.all, j, j + a.box_rows)) return a.n_pages;
+      const int pg = __ldg(table + j / a.page_size);
+      if (pg < 0 || pg >= a.n_pages) {
+        raise_status(a.status, kStatusDeviceArg, 51);
+        return a.n_pages;
+      }
+      return pg;
+    };
+    int next = inf.n > 0 ? entry(0) : 0;
+    bool ok = true;
+    for (int t = 0; t < inf.n && ok; ++t) {
+      const int page = next;
+      const int y = (inf.tile(t) * kTile + box * a.box_rows) % a.page_size;
+      if (t + 1 < inf.n) next = entry(t + 1);
+#pragma unroll
+      for (int which = 0; which < 2; ++which) {  // K(t) then V(t)
+        const uint32_t idx = kv_iter + 2 * t + which;
+        const int stg = idx % kStages;
+        if (idx >= kStages && !waitw(&bar[B_KVEMPTY + stg], ((idx / kStages) - 1) & 1, a, 62)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) mbar_arrive_expect_tx(&bar[B_KVFULL + stg], kTileBytes);
+        __syncwarp();
+        if (half < 2)
+          tma_load_4d(sKV + stg * kTileBytes + half * kChunkBytes + box * a.box_rows * 128, which ? tv : tk,
+                      &bar[B_KVFULL + stg], half * 64, y, inf.head, page);
+        issued = idx + 1;
+      }
+    }
+    if (!ok) break;
+    kv_iter += 2 * inf.n;
+  }
+  // a wait ran out: let the copies already issued land before the CTA leaves
+  for (uint32_t d = 0; d < kStages && d < issued; ++d) {
+    const uint32_t idx = issued - 1 - d;
+    mbar_wait(&bar[B_KVFULL + idx % kStages], (idx / kStages) & 1, nullptr, 100000000ull, 0, 0);
+  }
+  if (q_issued >= 1) mbar_wait(&bar[B_QFULL], (q_issued - 1) & 1, nullptr, 100000000ull, 0, 0);
+}
+
+// ------------------------------------------------------------------ MMA issuer
+template <typename T>
+__device__ __forceinline__ void mma_issuer(const PagedAttnArgs& a, uint8_t* sQ, uint8_t* sKV, uint64_t* bar,
+                                           const Item* items, uint32_t tbase) {
+  constexpr uint32_t kIdescS = idesc<T>(false);  // S = Q K^T (both K-major)
+  constexpr uint32_t kIdescO = idesc<T>(true);   // O += P V (P in TMEM, V N-major)
+  const uint64_t dQ0 = sdesc_sw128(smem_u32(sQ), 16, 1024);
+  const uint64_t dK0 = sdesc_sw128(smem_u32(sKV), 16, 1024);
+  const uint64_t dV0 = sdesc_sw128(smem_u32(sKV), kChunkBytes, 1024);
+  uint32_t kv_iter = 0;
+  uint32_t p_iss[2] = {0, 0};
+  auto scores = [&](int buf, int sub, int kst) {
+    const uint64_t dK = desc_add(dK0, kst * kTileBytes), dQ = desc_add(dQ0, sub * kTileBytes);
+    tc_fence_after();
+#pragma unroll
+    for (int ks = 0; ks < 8; ++ks) {
+      const uint32_t off = (ks >> 2) * kChunkBytes + (ks & 3) * 32;
+      umma_ss(tbase + 128 * buf, desc_add(dQ, off), desc_add(dK, off), kIdescS, ks > 0 ? 1u : 0u);
+    }
+    umma_commit(&bar[B_SFULL + buf]);
+  };
+  auto values = [&](int buf, int sub, int vst, bool first) {
+    const uint64_t dV = desc_add(dV0, vst * kTileBytes);
+    tc_fence_after();
+#pragma unroll
+    for (int ks = 0; ks < 8; ++ks)
+      umma_ts(tbase + 256 + 128 * sub, tbase + 128 * buf + 8 * ks, desc_add(dV, ks * 2048), kIdescO,
+              ks > 0 || !first ? 1u : 0u);
+    umma_commit(&bar[B_OFULL + sub]);
+  };
+  for (int it = 0;; ++it) {
+    const int slot = it & 1;
+    if (!waitw(&bar[B_ITFULL + slot], (it >> 1) & 1, a, 70)) goto abort;
+    {
+      const Item& inf = items[slot];
+      if (!inf.valid) return;
+      const int n = inf.n;
+      if (!waitw(&bar[B_QFULL], it & 1, a, 71)) goto abort;
+      auto kv_full = [&](uint32_t idx) { return waitw(&bar[B_KVFULL + idx % kStages], (idx / kStages) & 1, a, 72); };
+      if (inf.narrow) {
+        // S(0), S(1), PV(0), S(2), PV(1), ...: tile t in score buffer t & 1
+        for (int t = 0; t <= n; ++t) {
+          if (t < n) {
+            const uint32_t kidx = kv_iter + 2 * t;
+            if (!kv_full(kidx)) goto abort;
+            scores(t & 1, 0, kidx % kStages);
+            umma_commit(&bar[B_KVEMPTY + kidx % kStages]);
+            if (t == n - 1) umma_commit(&bar[B_QEMPTY]);
+          }
+          if (t >= 1) {
+            const uint32_t vidx = kv_iter + 2 * (t - 1) + 1;
+            const int buf = (t - 1) & 1;
+            if (!kv_full(vidx)) goto abort;
+            if (!waitw(&bar[B_PFULL + buf], p_iss[buf] & 1, a, 73)) goto abort;
+            ++p_iss[buf];
+            values(buf, 0, vidx % kStages, t == 1);
+            umma_commit(&bar[B_KVEMPTY + vidx % kStages]);
+          }
+        }
+      } else {
+        bool first[2] = {true, true};
+        uint32_t prev[2] = {kTileEmpty, kTileEmpty};
+        for (int t = 0; t <= n; ++t) {
+          const uint32_t vidx = kv_iter + 2 * (t - 1) + 1, kidx = kv_iter + 2 * t;
+          const int kt = t < n ? inf.tile(t) : 0;
+          bool v_ready = false, k_ready = false;
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (prev[x] != kTileEmpty) {  // O_x += P_x(t-1) V(t-1), before S_x(t) overwrites P_x
+              if (!v_ready && !kv_full(vidx)) goto abort;
+              v_ready = true;
+              if (!waitw(&bar[B_PFULL + x], p_iss[x] & 1, a, 74)) goto abort;
+              ++p_iss[x];
+              values(x, x, vidx % kStages, first[x]);
+              first[x] = false;
+            }
+            prev[x] = t < n ? inf.cls(x, kt) : kTileEmpty;
+            if (prev[x] != kTileEmpty) {
+              if (!k_ready && !kv_full(kidx)) goto abort;
+              k_ready = true;
+              scores(x, x, kidx % kStages);
+            }
+          }
+          if (t >= 1) {
+            if (!v_ready && !kv_full(vidx)) goto abort;  // released only once it has landed
+            umma_commit(&bar[B_KVEMPTY + vidx % kStages]);
+          }
+          if (t < n) {
+            if (!k_ready && !kv_full(kidx)) goto abort;
+            umma_commit(&bar[B_KVEMPTY + kidx % kStages]);
+            if (t == n - 1) umma_commit(&bar[B_QEMPTY]);
+          }
+        }
+      }
+      if (n == 0) umma_commit(&bar[B_QEMPTY]);
+      kv_iter += 2 * n;
+      __syncwarp();
+      if ((threadIdx.x & 31) == 0) mbar_arrive(&bar[B_ITEMPTY + slot]);
+    }
+  }
+abort:
+  umma_commit(&bar[B_DRAIN]);
+  mbar_wait(&bar[B_DRAIN], 0, nullptr, 100000000ull, 0, 0);
+}
+
+// ------------------------------------------------------------------ softmax warpgroup
+template <bool kMasked>
+__device__ __forceinline__ float score(uint32_t raw, uint32_t bits, int k) {
+  return (!kMasked || ((bits >> k) & 1u)) ? __uint_as_float(raw) : -INFINITY;
+}
+
+// Maximum of the thread's 128 scores, 64 columns at a time.  Masked tiles run
+// a rolled loop (smaller code), others an unrolled one.
+template <bool kMasked>
+__device__ __forceinline__ void max_half(float (&mp)[8], uint32_t tS, int h, uint32_t m0, uint32_t m1) {
+  uint32_t r0[32], r1[32];
+  tmem_ld32(tS + 64 * h, r0);
+  tmem_ld32(tS + 64 * h + 32, r1);
+  tmem_ld_wait();
+#pragma unroll
+  for (int g = 0; g < 2; ++g)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      mp[j] = fmax3(mp[j], score<kMasked>(r0[16 * g + j], m0, 16 * g + j),
+                    score<kMasked>(r0[16 * g + 8 + j], m0, 16 * g + 8 + j));
+      mp[j] = fmax3(mp[j], score<kMasked>(r1[16 * g + j], m1, 16 * g + j),
+                    score<kMasked>(r1[16 * g + 8 + j], m1, 16 * g + 8 + j));
+    }
+}
+template <bool kMasked>
+__device__ __forceinline__ float row_max(uint32_t tS, const uint32_t (&mb)[4]) {
+  float mp[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) mp[j] = -INFINITY;
+  if constexpr (kMasked) {
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) max_half<true>(mp, tS, h, h ? mb[2] : mb[0], h ? mb[3] : mb[1]);
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) max_half<false>(mp, tS, h, 0u, 0u);
+  }
+  return fmax3(fmax3(mp[0], mp[1], mp[2]), fmax3(mp[3], mp[4], mp[5]), fmaxf(mp[6], mp[7]));
+}
+
+// p = 2^(s scale log2(e) - base) of 32 columns, written as pairs over the
+// columns of S read before; the next 32 are requested meanwhile.
+template <typename T, bool kMasked>
+__device__ __forceinline__ void exp_chunk(uint32_t tS, int c, const uint32_t (&cur)[32], uint32_t (&nxt)[32],
+                                          uint32_t bits, uint64_t sl2x2, uint64_t nb2, uint64_t (&acc)[4]) {
+  tmem_ld_wait();
+  if (c + 1 < 4) tmem_ld32(tS + 32 * (c + 1), nxt);
+  uint32_t pk[16];
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    const uint64_t sv = f2(score<kMasked>(cur[2 * k], bits, 2 * k), score<kMasked>(cur[2 * k + 1], bits, 2 * k + 1));
+    const uint64_t xx = ffma2(sv, sl2x2, nb2);
+    const uint64_t pp = f2(ex2_approx(f2lo(xx)), ex2_approx(f2hi(xx)));
+    acc[k & 3] = fadd2(acc[k & 3], pp);
+    pk[k] = Half2<T>::pack(f2lo(pp), f2hi(pp));
+  }
+  tmem_st16(tS + 16 * c, pk);
+}
+template <typename T, bool kMasked>
+__device__ __forceinline__ float row_exp(uint32_t tS, const uint32_t (&mb)[4], float sl2, float base) {
+  const uint64_t sl2x2 = f2(sl2, sl2), nb2 = f2(-base, -base);
+  uint64_t acc[4] = {0, 0, 0, 0};
+  uint32_t ra[32], rb[32];
+  tmem_ld32(tS, ra);
+  if constexpr (kMasked) {
+#pragma unroll 1
+    for (int c = 0; c < 4; c += 2) {
+      exp_chunk<T, true>(tS, c, ra, rb, c ? mb[2] : mb[0], sl2x2, nb2, acc);
+      exp_chunk<T, true>(tS, c + 1, rb, ra, c ? mb[3] : mb[1], sl2x2, nb2, acc);
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < 4; c += 2) {
+      exp_chunk<T, false>(tS, c, ra, rb, ~0u, sl2x2, nb2, acc);
+      exp_chunk<T, false>(tS, c + 1, rb, ra, ~0u, sl2x2, nb2, acc);
+    }
+  }
+  const uint64_t t = fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3]));
+  return f2lo(t) + f2hi(t);
+}
+
+// Row `key` of the V tile (one thread per key): zeros where no row of the
+// item attends it (nothing of what lies there may meet a p of 0), else
+// whether it holds a value that is not finite.
+template <typename T>
+__device__ __forceinline__ bool clean_v_row(uint8_t* v, int key, bool used) {
+  bool bad = false;
+#pragma unroll
+  for (int c = 0; c < 2; ++c)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      uint4* p = reinterpret_cast<uint4*>(v + c * kChunkBytes + key * 128 + ((i ^ (key & 7)) << 4));
+      if (!used) {
+        *p = make_uint4(0, 0, 0, 0);
+      } else {
+        const uint4 w = *p;
+        bad |= Half2<T>::not_finite(w.x) || Half2<T>::not_finite(w.y) || Half2<T>::not_finite(w.z) ||
+               Half2<T>::not_finite(w.w);
+      }
+    }
+  return bad;
+}
+
+// One row over the piece's keys without products of hidden values, by a whole
+// warp: lane k has values 4 k .. 4 k + 3.  For the rare rows that share a
+// partly masked tile with a value that is not finite.
+template <typename T>
+__device__ __noinline__ void row_alone(const PagedAttnArgs& a, const Item& inf, int token, int head, float& m_out,
+                                       float& l_out, float (&o)[4]) {
+  const int lane = threadIdx.x & 31;
+  SegInfo sg{};
+  sg.q_len = inf.q_len;
+  sg.k_len = inf.k_len;
+  const Span sp = row_span(a.mask, sg, token);
+  const T* q = static_cast<const T*>(a.q) + (inf.q_off + token) * a.q_stride + head * kHeadDim + 4 * lane;
+  const int* table = a.table + inf.seq * a.table_stride;
+  float m = -INFINITY, l = 0.f;
+  o[0] = o[1] = o[2] = o[3] = 0.f;
+  for (int t = 0; t < inf.n; ++t)
+    for (int j = inf.tile(t) * kTile, e = j + kTile; j < e; ++j) {
+      if (!((j >= sp.a0 && j < sp.b0) || (j >= sp.a1 && j < sp.b1))) continue;
+      const int page = __ldg(table + j / a.page_size);
+      const bool ok = page >= 0 && page < a.n_pages;
+      const long long at = (ok ? page : 0) * a.page_stride + j % a.page_size * a.token_stride +
+                           inf.head * a.head_stride + 4 * lane;
+      float s = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
+      if (ok)
+        for (int k = 0; k < 4; ++k) {
+          s += static_cast<float>(q[k]) * static_cast<float>(static_cast<const T*>(a.kc)[at + k]);
+          v[k] = static_cast<float>(static_cast<const T*>(a.vc)[at + k]);
+        }
+      for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(~0u, s, d);
+      s *= a.scale_log2;
+      const float mn = fmaxf(m, s), f = ex2_approx(m - mn), p = ex2_approx(s - mn + kBias<T>);
+      l = (l == 0.f ? 0.f : l * f) + p;
+      for (int k = 0; k < 4; ++k) o[k] = (m == -INFINITY ? 0.f : o[k] * f) + p * v[k];
+      m = mn;
+    }
+  m_out = m;
+  l_out = l;
+}
+
+template <typename T>
+__device__ __forceinline__ void softmax_wg(const PagedAttnArgs& a, int x, uint64_t* bar, const Item* items,
+                                           uint8_t* sKV, volatile int* bad_item, uint32_t tbase) {
+  const int wq = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
+  const int row = wq * 32 + lane;  // TMEM lane = row of the sub-tile
+  const uint32_t tl = static_cast<uint32_t>(wq * 32) << 16;
+  const uint32_t tO = tbase + tl + 256 + 128 * x;
+  const float sl2 = a.scale_log2;
+  uint32_t s_cnt[2] = {0, 0};  // tiles of each score buffer so far
+  uint32_t o_cnt = 0;          // products into this sub-tile's O so far
+  uint32_t kv_iter = 0;
+  for (int it = 0;; ++it) {
+    const int slot = it & 1;
+    if (!waitw(&bar[B_ITFULL + slot], (it >> 1) & 1, a, 80 + x)) return;
+    const Item& inf = items[slot];
+    if (!inf.valid) return;
+    const bool narrow = inf.narrow != 0;
+    const int n = inf.n;
+    if (narrow && x == 1) {  // the other warpgroup's item
+      s_cnt[0] += (n + 1) / 2;
+      s_cnt[1] += n / 2;
+      kv_iter += 2 * n;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar[B_ITEMPTY + slot]);
+      continue;
+    }
+    SegInfo sg{};
+    sg.q_len = inf.q_len;
+    sg.k_len = inf.k_len;
+    const int tok_in = row / a.G;
+    const int token = inf.tok0 + x * a.tpt + tok_in;
+    const int head = inf.head * a.G + row - tok_in * a.G;
+    const bool valid = tok_in < a.tpt && token < inf.q_len;
+    const Span sp = row_span(a.mask, sg, min(token, inf.q_len - 1));
+    float m = -INFINITY, l = 0.f;
+    bool any = false;
+    for (int t = 0; t < n; ++t) {
+      const int kt = inf.tile(t);
+      int buf = t & 1;
+      const uint32_t cls = inf.cls(x, kt);
+      if (!narrow) {
+        buf = x;
+        if (inf.cls(1 - x, kt) != kTileEmpty) ++s_cnt[1 - x];
+        if (cls == kTileEmpty) continue;
+      }
+      const uint32_t tS = tbase + tl + 128 * buf;
+      uint32_t mb[4];
+      if (cls != kTileFull) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) mb[c] = span_bits(sp, kt * kTile + 32 * c);
+        const uint32_t vidx = kv_iter + 2 * t + 1;
+        if (!waitw(&bar[B_KVFULL + vidx % kStages], (vidx / kStages) & 1, a, 88 + x)) return;
+        const int j = kt * kTile + row;
+        if (clean_v_row<T>(sKV + (vidx % kStages) * kTileBytes, row,
+                           (j >= inf.all.a0 && j < inf.all.b0) || (j >= inf.all.a1 && j < inf.all.b1)))
+          *bad_item = it + 1;
+        fence_proxy_async_smem();
+      }
+      if (!waitw(&bar[B_SFULL + buf], s_cnt[buf] & 1, a, 82 + x)) return;
+      ++s_cnt[buf];
+      tc_fence_after();
+      const float mx = cls == kTileFull ? row_max<false>(tS, mb) : row_max<true>(tS, mb);
+      const float m_new = fmaxf(m, mx * sl2);
+      float factor = 1.f;
+      bool need = false;
+      if (!any) {
+        m = m_new;
+      } else if (m_new > m + kRescaleThreshold) {
+        factor = ex2_approx(m - m_new);
+        need = true;
+        m = m_new;
+      }
+      const float base = (m == -INFINITY ? 0.f : m) - kBias<T>;
+      const float sum = cls == kTileFull ? row_exp<T, false>(tS, mb, sl2, base) : row_exp<T, true>(tS, mb, sl2, base);
+      l = l * factor + sum;
+      if (__any_sync(0xFFFFFFFFu, need)) {
+        // the product before this one must have finished before O is rescaled
+        if (!waitw(&bar[B_OFULL + x], (o_cnt - 1) & 1, a, 84 + x)) return;
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t r[32];
+          tmem_ld32(tO + 32 * c, r);
+          tmem_ld_wait();
+#pragma unroll
+          for (int k = 0; k < 32; ++k) r[k] = __float_as_uint(__uint_as_float(r[k]) * factor);
+          tmem_st32(tO + 32 * c, r);
+        }
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar[B_PFULL + buf]);
+      ++o_cnt;
+      any = true;
+    }
+    kv_iter += 2 * n;
+    if (any) {
+      // a narrow item's last two products may both be under way, and a wait
+      // for the last alone would take the one before the last but one for it
+      if (narrow && n >= 2 && !waitw(&bar[B_OFULL + x], o_cnt & 1, a, 86 + x)) return;
+      if (!waitw(&bar[B_OFULL + x], (o_cnt - 1) & 1, a, 86 + x)) return;
+      tc_fence_after();
+    }
+    T* orow = static_cast<T*>(a.o) + (static_cast<long long>(inf.q_off + (valid ? token : 0)) * a.Hq + head) * kHeadDim;
+    float* part = inf.part < 0 ? nullptr : a.chunk_parts + inf.part * static_cast<long long>(kPagedChunkPartFloats);
+    if (any && *bad_item == it + 1) {
+      // row by row, the warp together
+#pragma unroll 1
+      for (int r = 0; r < 32; ++r) {
+        const int tok = __shfl_sync(~0u, token, r), h = __shfl_sync(~0u, head, r);
+        if (!__shfl_sync(~0u, valid ? 1 : 0, r)) continue;
+        float mr, lr, o[4];
+        row_alone<T>(a, inf, tok, h, mr, lr, o);
+        if (part) {
+          *reinterpret_cast<float4*>(part + (x * 128 + wq * 32 + r) * kHeadDim + 4 * lane) =
+              make_float4(o[0], o[1], o[2], o[3]);
+        } else {
+          const float inv = lr == 0.f ? 0.f : 1.f / lr;
+          T* dst = static_cast<T*>(a.o) + (static_cast<long long>(inf.q_off + tok) * a.Hq + h) * kHeadDim + 4 * lane;
+          *reinterpret_cast<uint2*>(dst) =
+              make_uint2(Half2<T>::pack(o[0] * inv, o[1] * inv), Half2<T>::pack(o[2] * inv, o[3] * inv));
+        }
+        if (lane == r) m = mr, l = lr;
+      }
+    } else if (any) {
+      const float inv = part ? 1.f : l == 0.f ? 0.f : 1.f / l;
+      uint32_t r[2][32];
+      tmem_ld32(tO, r[0]);
+      tmem_ld_wait();
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        if (c < 3) tmem_ld32(tO + 32 * (c + 1), r[(c + 1) & 1]);
+        if (valid && part) {
+          float* dst = part + (x * 128 + row) * kHeadDim + 32 * c;
+#pragma unroll
+          for (int u = 0; u < 4; ++u) st_global_v8(dst + 8 * u, &r[c & 1][8 * u]);
+        } else if (valid) {
+          uint32_t w[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k)
+            w[k] = Half2<T>::pack(__uint_as_float(r[c & 1][2 * k]) * inv, __uint_as_float(r[c & 1][2 * k + 1]) * inv);
+          if (a.out_v8) {
+            st_global_v8(orow + 32 * c, w);
+            st_global_v8(orow + 32 * c + 16, w + 8);
+          } else {
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              *reinterpret_cast<uint4*>(orow + 32 * c + 8 * u) =
+                  make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
+          }
+        }
+        if (c < 3) tmem_ld_wait();
+      }
+    } else if (valid && !part) {
+#pragma unroll
+      for (int u = 0; u < 16; ++u) *reinterpret_cast<uint4*>(orow + 8 * u) = make_uint4(0, 0, 0, 0);
+    }
+    if (valid && part) {
+      part[256 * kHeadDim + x * 128 + row] = m;
+      part[256 * kHeadDim + 256 + x * 128 + row] = any ? l : 0.f;
+    } else if (valid) {
+      a.lse[static_cast<long long>(head) * a.Tq + inf.q_off + token] =
+          !any || l == 0.f ? -INFINITY : (m + log2f(l) - kBias<T>) * kLn2;
+    }
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bar[B_ITEMPTY + slot]);
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                       const __grid_constant__ CUtensorMap tmV, const PagedAttnArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  const Line ln(a, gridDim.x);
+  if (blockIdx.x >= ln.ctas || ln.total == 0) return;
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sQ = sm + kOffQ;
+  uint8_t* sKV = sm + kOffKV;
+  uint64_t* bar = reinterpret_cast<uint64_t*>(sm + kOffCtl);
+  Item* items = reinterpret_cast<Item*>(sm + kOffCtl + 512);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + kOffCtl + 896);
+  int* bad_item = reinterpret_cast<int*>(sm + kOffCtl + 904);  // per sub-tile
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp == 8) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  if (threadIdx.x == 0) {
+    for (int b = 0; b < B_COUNT; ++b) mbar_init(&bar[b], 1);
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&bar[B_PFULL + x], 4);    // one arrival per softmax warp
+      mbar_init(&bar[B_ITEMPTY + x], 9);  // eight softmax warps and the MMA warp
+      bad_item[x] = 0;
+    }
+    fence_mbar_init();
+  }
+  if (warp == 9 && lane == 0) {
+    tma_prefetch_map(&tmQ);
+    tma_prefetch_map(&tmK);
+    tma_prefetch_map(&tmV);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = *tmem_slot;
+  if (warp == 9)
+    producer(a, ln, &tmQ, &tmK, &tmV, sQ, sKV, bar, items);
+  else if (warp == 8)
+    mma_issuer<T>(a, sQ, sKV, bar, items, tbase);
+  else
+    softmax_wg<T>(a, warp >> 2, bar, items, sKV, bad_item + (warp >> 2), tbase);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tbase, 512);
+  }
+}
+
+// Joins the pieces of the item that starts in CTA blockIdx.x's span and ends
+// in a later one's: 32 rows per block, a warp per row, lane k the values
+// 4 k .. 4 k + 3.
+template <typename T>
+__global__ void __launch_bounds__(256) paged_join_kernel(const PagedAttnArgs a, int grid) {
+  const Line ln(a, grid);
+  const long long c0 = blockIdx.x;
+  if (c0 >= ln.ctas || ln.total == 0) return;
+  const Place p = locate(a, ln.start(c0 + 1) - 1);
+  const long long last = p.first + p.tiles;
+  if (p.first < ln.start(c0) || last <= ln.start(c0 + 1)) return;
+  const long long c1 = ln.cta_of(last - 1);
+  const SegInfo sg = paged_seg(a, p.seq, false);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int k = 0; k < 4; ++k) {
+    const int row = blockIdx.y * 32 + warp * 4 + k;  // of the item's two sub-tiles
+    const int sub = row >> 7, in = (row & 127) / a.G;
+    const int token = p.block * 2 * a.tpt + sub * a.tpt + in;
+    if (in >= a.tpt || token >= sg.q_len) continue;
+    const int head = p.head * a.G + (row & 127) - in * a.G;
+    auto part = [&](long long c) {
+      return a.chunk_parts + slot_of(ln, c, c == c0 ? p.first : ln.start(c)) * kPagedChunkPartFloats;
+    };
+    // each lane the maximum and sum of some pieces
+    float m = -INFINITY;
+    for (long long c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, part(c)[256 * kHeadDim + row]);
+    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
+    float l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (long long c = c0; c <= c1; ++c) {
+      const float* y = part(c);
+      const float4 z = *reinterpret_cast<const float4*>(y + row * kHeadDim + 4 * lane);
+      const float lc = y[256 * kHeadDim + 256 + row];
+      if (lc != 0.f) {  // a piece without keys leaves its values unwritten
+        const float f = ex2_approx(y[256 * kHeadDim + row] - m);
+        l = fmaf(f, lc, l);
+        o[0] = fmaf(f, z.x, o[0]);
+        o[1] = fmaf(f, z.y, o[1]);
+        o[2] = fmaf(f, z.z, o[2]);
+        o[3] = fmaf(f, z.w, o[3]);
+      }
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    T* dst = static_cast<T*>(a.o) + (static_cast<long long>(sg.q_off + token) * a.Hq + head) * kHeadDim + 4 * lane;
+    *reinterpret_cast<uint2*>(dst) =
+        make_uint2(Half2<T>::pack(o[0] * inv, o[1] * inv), Half2<T>::pack(o[2] * inv, o[3] * inv));
+    if (lane == 0)
+      a.lse[static_cast<long long>(head) * a.Tq + sg.q_off + token] =
+          l == 0.f ? -INFINITY : (m + log2f(l) - kBias<T>) * kLn2;
+  }
+}
+
+template <typename T>
+void launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttnArgs& a, int num_sms,
+            cudaStream_t st) {
+  cudaFuncSetAttribute(paged_chunk_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  const int grid = std::min(num_sms, kPagedMaxChunkCtas);
+  note_launches(3);
+  paged_items_kernel<<<1, 1024, 0, st>>>(a);
+  paged_chunk_kernel<T><<<grid, kThreads, kSmemBytes, st>>>(tq, tk, tv, a);
+  paged_join_kernel<T><<<dim3(grid, 8), 256, 0, st>>>(a, grid);
+}
+
+}  // namespace
+
+void launch_paged_chunk(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttnArgs& a,
+                        bool fp16, int num_sms, cudaStream_t st) {
+  if (fp16)
+    launch<__half>(tq, tk, tv, a, num_sms, st);
+  else
+    launch<__nv_bfloat16>(tq, tk, tv, a, num_sms, st);
+}
+
+}  // namespace lca
