@@ -200,7 +200,7 @@ constexpr int kDecStages = 3;
 constexpr int kSliceBytes = kSlice * 256;     // of K or V
 constexpr int kWarpBytes = kDecStages * 2 * kSliceBytes;
 constexpr int kDecSmem = kDecWarps * kWarpBytes;
-constexpr int kMinUnits = 2;                  // a CTA's share, where there is that much
+constexpr int kMinUnits = 4;                  // a CTA's share, where there is that much
 constexpr int kSeqTile = 4 * kDecThreads;     // requests whose places on the line are in shared memory at once
 constexpr int kPartFloats = kRows * (kHeadDim + 2);
 static_assert(kSlice == 16, "a slice is one k16 step of the product with V");
@@ -271,10 +271,10 @@ __device__ __forceinline__ int row_tiles(const PagedAttnArgs& a, int q_len) {
 
 // Units of request i on the line: every (row tile, KV head) has those of the
 // whole request's hull, at least one, so that rows without keys are written.
-__device__ __forceinline__ long long line_units(const PagedAttnArgs& a, int i, bool flag) {
-  const SegInfo sg = paged_seg(a, i, flag);
+__device__ __forceinline__ long long line_units(const PagedAttnArgs& a, int i) {
+  const SegInfo sg = paged_seg(a, i);
   if (sg.q_len == 0 || !few_rows(a, sg.q_len)) return 0;
-  const Units u = units_of(hull(a.mask, sg, 0, sg.q_len));
+  const Units u = units_of(hull(a, sg.q_len, sg.k_len, 0, sg.q_len));
   return static_cast<long long>(row_tiles(a, sg.q_len)) * a.Hkv * max(u.n0 + u.n1, 1);
 }
 
@@ -286,14 +286,16 @@ struct DecodeShared {
 };
 
 // Places of the requests [base, base + kSeqTile) on the line; returns their units.
-__device__ __forceinline__ long long place_requests(const PagedAttnArgs& a, DecodeShared& sh, int base, bool flag) {
+__device__ __forceinline__ long long place_requests(const PagedAttnArgs& a, DecodeShared& sh, int base) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  long long n[4], mine = 0;
-#pragma unroll
+  __syncthreads();  // earlier readers of start and sums
+  long long mine = 0;
+#pragma unroll 1
   for (int k = 0; k < 4; ++k) {
     const int i = base + 4 * tid + k;
-    n[k] = i < a.n_seq ? line_units(a, i, flag) : 0;
-    mine += n[k];
+    const long long n = i < a.n_seq ? line_units(a, i) : 0;
+    sh.start[4 * tid + k] = n;
+    mine += n;
   }
   long long inc = mine;
 #pragma unroll
@@ -301,7 +303,6 @@ __device__ __forceinline__ long long place_requests(const PagedAttnArgs& a, Deco
     const long long x = __shfl_up_sync(~0u, inc, d);
     if (lane >= d) inc += x;
   }
-  __syncthreads();  // earlier readers of start and sums
   if (lane == 31) sh.sums[warp] = inc;
   __syncthreads();
   long long at = inc - mine, total = 0;
@@ -312,8 +313,9 @@ __device__ __forceinline__ long long place_requests(const PagedAttnArgs& a, Deco
   }
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
+    const long long n = sh.start[4 * tid + k];
     sh.start[4 * tid + k] = at;
-    at += n[k];
+    at += n;
   }
   if (tid == kDecThreads - 1) sh.start[kSeqTile] = at;
   __syncthreads();
@@ -335,10 +337,10 @@ __device__ __forceinline__ void decode_warp(const PagedAttnArgs& a, uint32_t rin
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rows = min(static_cast<int>(min(static_cast<long long>(sg.q_len) * a.G - tile * kRows, 16LL)), kRows);
   const int r_first = tile * kRows, r_last = r_first + rows - 1;
-  const Span hl = hull(a.mask, sg, r_first / a.G, r_last / a.G + 1);
+  const Span hl = hull(a, sg.q_len, sg.k_len, r_first / a.G, r_last / a.G + 1);
   // the two rows of this lane (a row past the last one repeats it, unused)
   const int ra = min(r_first + (lane >> 2), r_last), rb = min(r_first + (lane >> 2) + 8, r_last);
-  const Span sa = row_span(a.mask, sg, ra / a.G), sb = row_span(a.mask, sg, rb / a.G);
+  const Span sa = paged_span(a, sg.q_len, sg.k_len, ra / a.G), sb = paged_span(a, sg.q_len, sg.k_len, rb / a.G);
 
   // offsets of 8-key groups: lane 2 t + g holds group g of unit t of a batch of 16
   const int* table = a.table + seq * a.table_stride;
@@ -390,9 +392,6 @@ __device__ __forceinline__ void decode_warp(const PagedAttnArgs& a, uint32_t rin
     }
     cp_async_commit();
   };
-  issue(0);
-  issue(1);
-
   // Q as A operands, straight from global memory
   uint32_t q[8][4];
   {
@@ -415,8 +414,10 @@ __device__ __forceinline__ void decode_warp(const PagedAttnArgs& a, uint32_t rin
   // this lane's row and 16-byte column of the four 8x8 matrices of ldmatrix
   const int kkey = (lane & 7) + ((lane >> 4) << 3), kcol = (lane >> 3) & 1;   // K: (keys 0-7, 8-15) x (d 0-7, 8-15)
   const int vkey = (lane & 7) + (((lane >> 3) & 1) << 3), vcol = lane >> 4;   // V, transposed
-  for (int u = 0; u < n; ++u) {
-    issue(u + 2);
+#pragma unroll 1
+  for (int u = -2; u < n; ++u) {
+    issue(u + 2);  // two units ahead
+    if (u < 0) continue;
     cp_async_wait<2>();
     __syncwarp();
     const int j0 = un.first_key(u0 + u) + warp * kSlice;
@@ -475,49 +476,47 @@ __device__ __forceinline__ void decode_warp(const PagedAttnArgs& a, uint32_t rin
       p[r] = H::pack(e[0], e[1]);
       p[2 + r] = H::pack(e[2], e[3]);
     }
-    uint32_t bad = 0;
+    bool alone = false;
+    if (part) {
+      // a value that is not finite, in keys that some row does not attend?
+      uint32_t bad = 0;
+#pragma unroll 1
+      for (int t = 0; t < 8; ++t) {
+        uint32_t b[4];
+        ldsm4t(b, sv + vkey * 256 + (((2 * t + vcol) ^ (vkey & 7)) << 4));
+        bad |= H::not_finite(b[0]) || H::not_finite(b[1]) || H::not_finite(b[2]) || H::not_finite(b[3]);
+      }
+      alone = __any_sync(~0u, bad);
+    }
+    if (!alone) {
 #pragma unroll
-    for (int t = 0; t < 8; ++t) {
-      uint32_t b[4];
-      ldsm4t(b, sv + vkey * 256 + (((2 * t + vcol) ^ (vkey & 7)) << 4));
-      if (part) bad |= H::not_finite(b[0]) || H::not_finite(b[1]) || H::not_finite(b[2]) || H::not_finite(b[3]);
-      if (!part) {
+      for (int t = 0; t < 8; ++t) {
+        uint32_t b[4];
+        ldsm4t(b, sv + vkey * 256 + (((2 * t + vcol) ^ (vkey & 7)) << 4));
         warp_mma(st.o[2 * t], p, b[0], b[1], T());
         warp_mma(st.o[2 * t + 1], p, b[2], b[3], T());
       }
-    }
-    if (part) {
-      if (!__any_sync(~0u, bad)) {
-#pragma unroll
-        for (int t = 0; t < 8; ++t) {
-          uint32_t b[4];
-          ldsm4t(b, sv + vkey * 256 + (((2 * t + vcol) ^ (vkey & 7)) << 4));
-          warp_mma(st.o[2 * t], p, b[0], b[1], T());
-          warp_mma(st.o[2 * t + 1], p, b[2], b[3], T());
-        }
-      } else {
-        // a value that is not finite, in keys that some row does not attend:
-        // 0 times it would be NaN there, so each row adds its own keys only
+    } else {
+      // 0 times such a value would be NaN: each row adds its own keys only
 #pragma unroll 1
-        for (int k = 0; k < kSlice; ++k) {
-          const int from = (lane & ~3) | ((k & 7) >> 1);
-          const float2 x0 = H::unpack(__shfl_sync(~0u, k < 8 ? p[0] : p[2], from));
-          const float2 x1 = H::unpack(__shfl_sync(~0u, k < 8 ? p[1] : p[3], from));
-          const float pa = (k & 1) ? x0.y : x0.x, pb = (k & 1) ? x1.y : x1.x;
-          const bool ta = in_span(sa, j0 + k), tb = in_span(sb, j0 + k);
+      for (int k = 0; k < kSlice; ++k) {
+        const int from = (lane & ~3) | ((k & 7) >> 1);
+        const float2 x0 = H::unpack(__shfl_sync(~0u, k < 8 ? p[0] : p[2], from));
+        const float2 x1 = H::unpack(__shfl_sync(~0u, k < 8 ? p[1] : p[3], from));
+        const float pa = (k & 1) ? x0.y : x0.x, pb = (k & 1) ? x1.y : x1.x;
+        const bool ta = in_span(sa, j0 + k), tb = in_span(sb, j0 + k);
 #pragma unroll
-          for (int t = 0; t < 16; ++t) {
-            uint32_t w;
-            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(sv + k * 256 + ((t ^ (k & 7)) << 4) + 4 * (lane & 3)));
-            const float2 vv = H::unpack(w);
-            if (ta) {
-              st.o[t][0] = fmaf(pa, vv.x, st.o[t][0]);
-              st.o[t][1] = fmaf(pa, vv.y, st.o[t][1]);
-            }
-            if (tb) {
-              st.o[t][2] = fmaf(pb, vv.x, st.o[t][2]);
-              st.o[t][3] = fmaf(pb, vv.y, st.o[t][3]);
-            }
+        for (int t = 0; t < 16; ++t) {
+          uint32_t w;
+          asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(sv + k * 256 + ((t ^ (k & 7)) << 4) + 4 * (lane & 3)));
+          const float2 vv = H::unpack(w);
+          if (ta) {
+            st.o[t][0] = fmaf(pa, vv.x, st.o[t][0]);
+            st.o[t][1] = fmaf(pa, vv.y, st.o[t][1]);
+          }
+          if (tb) {
+            st.o[t][2] = fmaf(pb, vv.x, st.o[t][2]);
+            st.o[t][3] = fmaf(pb, vv.y, st.o[t][3]);
           }
         }
       }
@@ -540,40 +539,42 @@ __device__ __forceinline__ void st_row16(T* dst, const float (&x)[16]) {
   *reinterpret_cast<uint4*>(dst + 8) = make_uint4(w[4], w[5], w[6], w[7]);
 }
 
+// o = 0, lse = -inf in rows that no request owns: [0, lo) and [hi, Tq).
+__device__ __noinline__ void clear_unowned_rows(const PagedAttnArgs& a) {
+  const SegInfo s0 = a.n_seq > 0 ? paged_seg(a, 0) : SegInfo{};
+  const SegInfo s1 = a.n_seq > 0 ? paged_seg(a, a.n_seq - 1) : SegInfo{};
+  const int lo = s0.q_off, hi = s1.q_off + s1.q_len;
+  const long long n = static_cast<long long>(lo + max(a.Tq - hi, 0)) * a.Hq * 16;
+  for (long long t = threadIdx.x; t < n; t += kDecThreads) {
+    const long long rh = t >> 4;
+    long long row = rh / a.Hq;
+    if (row >= lo) row += hi - lo;
+    const int h = static_cast<int>(rh % a.Hq);
+    reinterpret_cast<uint4*>(a.o)[(row * a.Hq + h) * 16 + (t & 15)] = make_uint4(0, 0, 0, 0);
+    if ((t & 15) == 0) a.lse[static_cast<long long>(h) * a.Tq + row] = -INFINITY;
+  }
+}
+
 template <typename T>
-__global__ void __launch_bounds__(kDecThreads, 2) paged_decode_kernel(const PagedAttnArgs a) {
+__global__ void __launch_bounds__(kDecThreads, 2) paged_decode_kernel(const __grid_constant__ PagedAttnArgs a) {
   extern __shared__ __align__(1024) uint8_t ring[];
   __shared__ DecodeShared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
-  // rows that no request owns
-  {
-    const SegInfo s0 = a.n_seq > 0 ? paged_seg(a, 0, false) : SegInfo{};
-    const SegInfo s1 = a.n_seq > 0 ? paged_seg(a, a.n_seq - 1, false) : SegInfo{};
-    const int lo = s0.q_off, hi = s1.q_off + s1.q_len;  // rows [0, lo) and [hi, Tq)
-    const long long n = static_cast<long long>(lo + max(a.Tq - hi, 0)) * a.Hq * 16;
-    for (long long t = blockIdx.x * static_cast<long long>(kDecThreads) + tid; t < n;
-         t += gridDim.x * static_cast<long long>(kDecThreads)) {
-      const long long rh = t >> 4;
-      long long row = rh / a.Hq;
-      if (row >= lo) row += hi - lo;
-      const int h = static_cast<int>(rh % a.Hq);
-      reinterpret_cast<uint4*>(a.o)[(row * a.Hq + h) * 16 + (t & 15)] = make_uint4(0, 0, 0, 0);
-      if ((t & 15) == 0) a.lse[static_cast<long long>(h) * a.Tq + row] = -INFINITY;
-    }
-  }
-
+  launch_dependents();
   // requests whose rows do not overlap make fewer than 2^52 units; a q_start
   // that lets them overlap may make more, and is reported and not served then
   constexpr long long kMost = 1LL << 52;
   long long total = 0;
   for (int base = 0; base < a.n_seq; base += kSeqTile)
-    total = min(total + place_requests(a, sh, base, blockIdx.x == 0), kMost);
+    total = min(total + place_requests(a, sh, base), kMost);
+  grid_wait();  // counts and status are cleared
+  if (blockIdx.x == gridDim.x - 1) clear_unowned_rows(a);
   if (total == 0 || total == kMost) return;
   const long long ctas = min(static_cast<long long>(gridDim.x), max(total / kMinUnits, 1LL));
   if (blockIdx.x >= ctas) return;
-  auto span_start = [&](long long c) { return c * total / ctas; };
-  auto cta_of = [&](long long p) { return ((p + 1) * ctas - 1) / total; };
+  auto span_start = [&](long long c) { return line_div(c * total, ctas); };
+  auto cta_of = [&](long long p) { return line_div((p + 1) * ctas - 1, total); };
   long long pos = span_start(blockIdx.x);
   const long long end = span_start(blockIdx.x + 1);
   int base = a.n_seq > kSeqTile ? -kSeqTile : 0;      // requests in sh.start begin at base
@@ -583,32 +584,33 @@ __global__ void __launch_bounds__(kDecThreads, 2) paged_decode_kernel(const Page
       base += kSeqTile;
       if (base >= a.n_seq) return;  // only if the lengths changed meanwhile
       tile0 = tile1;
-      tile1 += place_requests(a, sh, base, false);
+      tile1 += place_requests(a, sh, base);
     }
-    int lo = 0, hi = kSeqTile;  // the last request that starts at or before pos
+    int lo = 0, hi = min(kSeqTile, a.n_seq - base);  // the last request that starts at or before pos
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (sh.start[mid] <= pos - tile0) lo = mid; else hi = mid;
     }
     const int seq = base + lo;
-    const SegInfo sg = paged_seg(a, seq, false);
-    const Units un = units_of(hull(a.mask, sg, 0, sg.q_len));
+    const SegInfo sg = paged_seg(a, seq);
+    const Units un = units_of(hull(a, sg.q_len, sg.k_len, 0, sg.q_len));
     const int nu = max(un.n0 + un.n1, 1);
     const long long local = pos - tile0 - sh.start[lo];
-    const long long item = local / nu;
+    const long long item = line_div(local, nu);
     const int u0 = static_cast<int>(local - item * nu);
     const int n = static_cast<int>(min(static_cast<long long>(nu - u0), end - pos));
     const int tiles = row_tiles(a, sg.q_len);
-    const int head = static_cast<int>(item / tiles), tile = static_cast<int>(item % tiles);
+    const int head = static_cast<int>(line_div(item, tiles)), tile = static_cast<int>(item - static_cast<long long>(head) * tiles);
 
-    uint8_t* mine = ring + warp * kWarpBytes;
+    const int rows = static_cast<int>(min(static_cast<long long>(sg.q_len) * a.G - static_cast<long long>(tile) * kRows,
+                                          static_cast<long long>(kRows)));
+    float* po = reinterpret_cast<float*>(ring + warp * kWarpBytes);  // [16][132], once the ring is empty
     {
       WarpState<T> st;
       // an item without keys has one unit that holds none
-      decode_warp<T>(a, smem_u32(mine), seq, sg, un, tile, head, u0, un.n0 + un.n1 > 0 ? n : 0, st);
+      decode_warp<T>(a, smem_u32(po), seq, sg, un, tile, head, u0, un.n0 + un.n1 > 0 ? n : 0, st);
       cp_async_wait<0>();
       __syncwarp();
-      float* po = reinterpret_cast<float*>(mine);  // [16][132]
       const int r = lane >> 2, c = 2 * (lane & 3);
 #pragma unroll
       for (int t = 0; t < 16; ++t) {
@@ -623,75 +625,75 @@ __global__ void __launch_bounds__(kDecThreads, 2) paged_decode_kernel(const Page
       }
     }
     __syncthreads();
-    // the four warps' sums; thread: row tid / 8, columns 16 (tid % 8)
     const int row = tid >> 3, col = (tid & 7) * 16;
+    // the four warps' sums of row `row`, columns col .. col + 15
     float m = -INFINITY, l = 0.f, x[16] = {};
 #pragma unroll
     for (int w = 0; w < kDecWarps; ++w) m = fmaxf(m, sh.m[w][row]);
 #pragma unroll
     for (int w = 0; w < kDecWarps; ++w) {
       const float f = sh.l[w][row] != 0.f ? ex2_approx(sh.m[w][row] - m) : 0.f;
-      l += f * sh.l[w][row];
-      const float* po = reinterpret_cast<const float*>(ring + w * kWarpBytes) + row * 132 + col;
+      l = fmaf(f, sh.l[w][row], l);
+      const float* pw = reinterpret_cast<const float*>(ring + w * kWarpBytes) + row * 132 + col;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const float4 y = *reinterpret_cast<const float4*>(po + 4 * k);
+        const float4 y = *reinterpret_cast<const float4*>(pw + 4 * k);
         x[4 * k] = fmaf(f, y.x, x[4 * k]);
         x[4 * k + 1] = fmaf(f, y.y, x[4 * k + 1]);
         x[4 * k + 2] = fmaf(f, y.z, x[4 * k + 2]);
         x[4 * k + 3] = fmaf(f, y.w, x[4 * k + 3]);
       }
     }
-    bool write = true;
     if (n < nu) {
       // first and last CTA of the item; a CTA keeps its span's first piece in
       // slot 2 c and a later, unfinished one in slot 2 c + 1
-      const long long i0 = pos - u0, c0 = cta_of(i0), c1 = cta_of(i0 + nu - 1);
-      auto slot = [&](long long c) { return a.parts + (2 * c + (c == c0 && span_start(c) < i0 ? 1 : 0)) * kPartFloats; };
+      const long long i0 = pos - u0;
+      const int c0 = static_cast<int>(cta_of(i0)), c1 = static_cast<int>(cta_of(i0 + nu - 1));
+      const int late = span_start(c0) < i0 ? 1 : 0;
+      auto slot = [&](int c) { return a.parts + (2 * c + (c == c0 ? late : 0)) * static_cast<long long>(kPartFloats); };
       float* part = slot(blockIdx.x);
+      if (row < rows) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        __stcg(reinterpret_cast<float4*>(part + row * kHeadDim + col) + k,
-               make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]));
-      if ((tid & 7) == 0) {
-        __stcg(part + kRows * kHeadDim + row, m);
-        __stcg(part + kRows * kHeadDim + kRows + row, l);
+        for (int k = 0; k < 4; ++k)
+          __stcg(reinterpret_cast<float4*>(part + row * kHeadDim + col) + k,
+                 make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]));
+        if ((tid & 7) == 0) {
+          __stcg(part + kRows * kHeadDim + row, m);
+          __stcg(part + kRows * kHeadDim + kRows + row, l);
+        }
       }
       __threadfence();
       __syncthreads();
-      if (tid == 0) sh.last = atomicAdd(a.arrived + c0, 1) == static_cast<int>(c1 - c0);
+      if (tid == 0) sh.last = atomicAdd(a.arrived + c0, 1) == c1 - c0;
       __syncthreads();
-      write = sh.last != 0;
-      if (write) {
+      if (sh.last) {
         __threadfence();
-        m = -INFINITY;
-        for (long long c = c0; c <= c1; ++c) m = fmaxf(m, __ldcg(slot(c) + kRows * kHeadDim + row));
-        l = 0.f;
-#pragma unroll
-        for (int k = 0; k < 16; ++k) x[k] = 0.f;
-        for (long long c = c0; c <= c1; ++c) {
-          const float* y = slot(c);
-          const float lc = __ldcg(y + kRows * kHeadDim + kRows + row);
-          const float f = lc != 0.f ? ex2_approx(__ldcg(y + kRows * kHeadDim + row) - m) : 0.f;
-          l = fmaf(f, lc, l);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float4 z = __ldcg(reinterpret_cast<const float4*>(y + row * kHeadDim + col) + k);
-            x[4 * k] = fmaf(f, z.x, x[4 * k]);
-            x[4 * k + 1] = fmaf(f, z.y, x[4 * k + 1]);
-            x[4 * k + 2] = fmaf(f, z.z, x[4 * k + 2]);
-            x[4 * k + 3] = fmaf(f, z.w, x[4 * k + 3]);
-          }
+#pragma unroll 1
+        for (int i = warp; i < rows; i += kDecWarps) {
+          auto at = [&](int k) {
+            return a.parts + (2 * (c0 + k) + (k == 0 ? late : 0)) * static_cast<long long>(kPartFloats) + i * kHeadDim;
+          };
+          auto stat = [&](int k) { return at(k) + kRows * kHeadDim - i * (kHeadDim - 1); };
+          float mr, lr, y[4];
+          join_row(c1 - c0 + 1, at, stat, kRows, mr, lr, y);
+          const long long r = static_cast<long long>(tile) * kRows + i;
+          const long long token = sg.q_off + r / a.G;
+          const int h = head * a.G + static_cast<int>(r % a.G);
+          const float inv = lr == 0.f ? 0.f : 1.f / lr;
+          *reinterpret_cast<uint2*>(static_cast<T*>(a.o) + (token * a.Hq + h) * kHeadDim + 4 * lane) =
+              make_uint2(Half2<T>::pack(y[0] * inv, y[1] * inv), Half2<T>::pack(y[2] * inv, y[3] * inv));
+          if (lane == 0)
+            a.lse[static_cast<long long>(h) * a.Tq + token] =
+                lr == 0.f ? -INFINITY : (mr + log2f(lr) - kBias<T>) * 0.6931471805599453f;
         }
       }
-    }
-    const long long r = static_cast<long long>(tile) * kRows + row;
-    if (write && r < static_cast<long long>(sg.q_len) * a.G) {
-      const long long token = sg.q_off + r / a.G;
-      const int h = head * a.G + static_cast<int>(r % a.G);
+    } else if (row < rows) {
       const float inv = l == 0.f ? 0.f : 1.f / l;  // a NaN stays one
 #pragma unroll
       for (int k = 0; k < 16; ++k) x[k] *= inv;
+      const long long r = static_cast<long long>(tile) * kRows + row;
+      const long long token = sg.q_off + r / a.G;
+      const int h = head * a.G + static_cast<int>(r % a.G);
       st_row16(static_cast<T*>(a.o) + (token * a.Hq + h) * kHeadDim + col, x);
       if ((tid & 7) == 0)
         a.lse[static_cast<long long>(h) * a.Tq + token] =
@@ -720,18 +722,17 @@ void launch_paged_write(const PagedWriteArgs& a, int num_sms, cudaStream_t st) {
 }
 
 template <typename T>
-void launch_decode(const PagedAttnArgs& a, int num_sms, cudaStream_t st) {
+cudaError_t launch_decode(const PagedAttnArgs& a, int num_sms, cudaStream_t st) {
   // set on every launch: the attribute belongs to the current device
-  cudaFuncSetAttribute(paged_decode_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kDecSmem);
+  const cudaError_t e =
+      cudaFuncSetAttribute(paged_decode_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kDecSmem);
+  if (e != cudaSuccess) return e;
   note_launches(1);
-  paged_decode_kernel<T><<<std::min(2 * num_sms, kPagedMaxCtas), kDecThreads, kDecSmem, st>>>(a);
+  return launch_after(paged_decode_kernel<T>, dim3(std::min(2 * num_sms, kPagedMaxCtas)), kDecThreads, kDecSmem, st, a);
 }
 
-void launch_paged_decode(const PagedAttnArgs& a, bool fp16, int num_sms, cudaStream_t st) {
-  if (fp16)
-    launch_decode<__half>(a, num_sms, st);
-  else
-    launch_decode<__nv_bfloat16>(a, num_sms, st);
+cudaError_t launch_paged_decode(const PagedAttnArgs& a, bool fp16, int num_sms, cudaStream_t st) {
+  return fp16 ? launch_decode<__half>(a, num_sms, st) : launch_decode<__nv_bfloat16>(a, num_sms, st);
 }
 
 }  // namespace lca

@@ -41,6 +41,13 @@ constexpr int kPagedChunkPartFloats = 256 * (kHeadDim + 2);
 // per KV head go to the kernel for few rows when both kernels run.
 constexpr int kPagedFewRows = 16;
 
+// An item of many rows that goes on past the span of the CTA it starts in.
+struct PagedCut {
+  int seq, head, block;
+  int last;  // CTA of its last piece
+  int late;  // its first piece is not the first of its CTA's span
+};
+
 struct PagedAttnArgs {
   MaskCtx mask;
   const void* q;
@@ -62,13 +69,35 @@ struct PagedAttnArgs {
   int* block0;        // [n_seq + 1] row blocks before each request
   long long* line;    // [max_blocks + 1] key tiles before each row block
   float* chunk_parts; // [kPagedMaxChunkCtas][2][kPagedChunkPartFloats]
+  PagedCut* cuts;     // [kPagedMaxChunkCtas] seq < 0: none starts in this CTA's span
   int out_v8;         // o is 32-byte aligned
   unsigned long long wait_limit_ns;
 };
-void launch_paged_decode(const PagedAttnArgs& a, bool fp16, int num_sms, cudaStream_t st);
+// A call is paged_begin, then paged_decode, then, where some request may have
+// many rows, paged_chunk: each later kernel is launched while the one before
+// it runs, and waits for it.
+cudaError_t launch_paged_begin(const PagedAttnArgs& a, bool many, cudaStream_t st);
+cudaError_t launch_paged_decode(const PagedAttnArgs& a, bool fp16, int num_sms, cudaStream_t st);
 // Queries as boxes of tpt tokens x G heads x 64, keys and values as boxes of
 // box_rows tokens of one page and head x 64, 128-byte swizzled.
-void launch_paged_chunk(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttnArgs& a,
-                        bool fp16, int num_sms, cudaStream_t st);
+cudaError_t launch_paged_chunk(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                               const PagedAttnArgs& a, bool fp16, int num_sms, cudaStream_t st);
+
+// Launches `kernel` so that it may start before the kernel in front of it on
+// `st` has ended (it calls grid_wait before it touches what that one wrote).
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, const A&... args) {
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
 
 }  // namespace lca

@@ -54,7 +54,7 @@ bool many_rows(const lca_paged_shape* sh, const lca_paged_cache* c) {
 int tokens_per_tile(const lca_paged_shape* sh, const lca_paged_cache* c) { return kTile / (sh->Hq / c->Hkv); }
 
 struct PagedLayout {
-  size_t status = 0, arrived = 0, parts = 0, block0 = 0, line = 0, chunk_parts = 0, total = 0;
+  size_t status = 0, arrived = 0, parts = 0, block0 = 0, line = 0, cuts = 0, chunk_parts = 0, total = 0;
   int max_blocks = 0;
 };
 
@@ -73,6 +73,7 @@ PagedLayout paged_layout(const lca_paged_shape* sh, const lca_paged_cache* c) {
     L.max_blocks = sh->Tq / (2 * tokens_per_tile(sh, c)) + sh->n_seq;
     L.block0 = take(sizeof(int) * (sh->n_seq + 1LL));
     L.line = take(sizeof(long long) * (L.max_blocks + 1LL));
+    L.cuts = take(sizeof(PagedCut) * kPagedMaxChunkCtas);
     L.chunk_parts = take(sizeof(float) * 2 * kPagedMaxChunkCtas * kPagedChunkPartFloats);
   }
   L.total = o;
@@ -308,6 +309,7 @@ lca_status lca_attn_paged(const void* q, const lca_paged_cache* cache, const int
     a.max_blocks = L.max_blocks;
     a.block0 = reinterpret_cast<int*>(ws + L.block0);
     a.line = reinterpret_cast<long long*>(ws + L.line);
+    a.cuts = reinterpret_cast<PagedCut*>(ws + L.cuts);
     a.chunk_parts = reinterpret_cast<float*>(ws + L.chunk_parts);
     a.out_v8 = (reinterpret_cast<uintptr_t>(o) & 31u) == 0;
     a.wait_limit_ns = wait_limit_ns();
@@ -319,10 +321,10 @@ lca_status lca_attn_paged(const void* q, const lca_paged_cache* cache, const int
       return LCA_ERR_CUDA;
   }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  LCA_CUDA(cudaMemsetAsync(ws, 0, L.parts, st));  // status and counts
-  if (many) launch_paged_chunk(tq, tk, tv, a, cache->dtype == LCA_F16, sms, st);
-  if (shape->Tq > 0) launch_paged_decode(a, cache->dtype == LCA_F16, sms, st);
-  LCA_CUDA(cudaGetLastError());
+  const bool fp16 = cache->dtype == LCA_F16;
+  LCA_CUDA(launch_paged_begin(a, many, st));
+  if (shape->Tq > 0) LCA_CUDA(launch_paged_decode(a, fp16, sms, st));
+  if (many) LCA_CUDA(launch_paged_chunk(tq, tk, tv, a, fp16, sms, st));
   return LCA_OK;
 }
 

@@ -16,8 +16,8 @@
 // tile and item 1024 keys' rows pass the tensor core against 64 KB of K and V
 // from L2.  Roles as in the packed forward: warp 9 loads, warp 8 issues
 // S = Q K^T and O += P V, warps 0-7 are two softmax warpgroups, each thread
-// one row.  The tiles of all items form one line that is cut into equal spans,
-// one per CTA (paged_items_kernel places the items on it), so that batches of
+// one row; warp 10 finds the next items and their key ranges ahead of them.  The tiles of all items form one line that is cut into equal spans,
+// one per CTA (paged_begin_kernel places the items on it), so that batches of
 // any mixture of lengths end together; the items that a cut divides leave
 // their sums in the workspace and paged_join_kernel joins them in the order
 // of the keys.  An item of one sub-tile (a narrow one: at most 128 rows)
@@ -36,7 +36,7 @@
 namespace lca {
 namespace {
 
-constexpr int kThreads = 320;
+constexpr int kThreads = 352;
 constexpr int kStages = 5;
 constexpr uint32_t kTileBytes = 32768;   // 128 rows x 128 values
 constexpr uint32_t kChunkBytes = 16384;  // 128 rows x 64 values, 128-byte swizzled
@@ -44,23 +44,30 @@ constexpr int kOffQ = 0;
 constexpr int kOffKV = 2 * kTileBytes;
 constexpr int kOffCtl = kOffKV + kStages * kTileBytes;
 constexpr int kSmemBytes = kOffCtl + 1024 + 1024;
+constexpr int kItemSlots = 3;
 constexpr int kMinTiles = 4;  // a CTA's share, where there is that much
+constexpr int kItemCost = 3;  // what an item costs beside its tiles, in tiles
 
+// Scores and probabilities have three barriers each: those of sub-tiles 0 and
+// 1, and one for the odd tiles of a narrow item, which go through sub-tile
+// 1's columns to the first warpgroup.  So each barrier has one waiting
+// warpgroup, which sees all of its phases: a wait by parity must not be two
+// phases behind.
 enum : int {
   B_QFULL = 0,
   B_QEMPTY = 1,
   B_KVFULL = 2,
   B_KVEMPTY = B_KVFULL + kStages,
   B_SFULL = B_KVEMPTY + kStages,
-  B_PFULL = B_SFULL + 2,
-  B_OFULL = B_PFULL + 2,
+  B_PFULL = B_SFULL + 3,
+  B_OFULL = B_PFULL + 3,
   B_ITFULL = B_OFULL + 2,
-  B_ITEMPTY = B_ITFULL + 2,
-  B_DRAIN = B_ITEMPTY + 2,
+  B_ITEMPTY = B_ITFULL + kItemSlots,
+  B_DRAIN = B_ITEMPTY + kItemSlots,
   B_COUNT = B_DRAIN + 1
 };
 
-// What the producer tells the other roles about a piece of an item.
+// What the scheduler tells the other roles about a piece of an item.
 struct Item {
   int valid, narrow;
   int n, u0;              // its tiles: u0 .. u0 + n - 1 of the item's
@@ -79,7 +86,8 @@ struct Item {
     return span_covers(full[x], j0, j0 + kTile) ? kTileFull : kTilePartial;
   }
 };
-static_assert(sizeof(Item) == 144, "two items fit between the barriers and the TMEM slot");
+static_assert(sizeof(Item) == 144 && 8 * B_COUNT <= 256 && kItemSlots * sizeof(Item) <= 640,
+              "the items lie between the barriers and the TMEM slot");
 
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
@@ -100,9 +108,14 @@ __host__ __device__ constexpr uint32_t idesc(bool b_mn_major) {
   return idesc_bf16_f32(128, 128, false, b_mn_major) & ~kAbFormat<T>;
 }
 
-__device__ __forceinline__ bool waitw(uint64_t* bar, uint32_t parity, const PagedAttnArgs& a, int where) {
+// Warp-uniform wait; what follows the first test is a call, one copy of it.
+__device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, const PagedAttnArgs& a, int where) {
   const bool ok = mbar_wait(bar, parity, a.status, a.wait_limit_ns, kStatusTimeout, where);
   return __all_sync(0xFFFFFFFFu, ok);
+}
+__device__ __forceinline__ bool waitw(uint64_t* bar, uint32_t parity, const PagedAttnArgs& a, int where) {
+  if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
+  return wait_on(bar, parity, a, where);
 }
 
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z) {
@@ -127,16 +140,15 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, u
 // the position in one direction (see hull), so the outer rows decide, with
 // two exceptions that are looked at as well: GLOBAL_SLIDING's first row past
 // the global ones, and CAUSAL_BLOCKWISE's last row before the last block.
-__device__ __forceinline__ Span common(const MaskCtx& m, const SegInfo& sg, int i0, int i1) {
+__device__ __noinline__ Span common(const PagedAttnArgs& a, int q_len, int k_len, int i0, int i1) {
   int mid = i0;
-  const int shift = sg.k_len - sg.q_len;
-  if (m.kind == kGlobalSliding) mid = m.ng - shift;
-  if (m.kind == kCausalBlockwise) mid = (sg.k_len - 1) / m.block * m.block - 1 - shift;
-  const int at[3] = {i0, min(max(mid, i0), i1 - 1), i1 - 1};
+  const int shift = k_len - q_len;
+  if (a.mask.kind == kGlobalSliding) mid = a.mask.ng - shift;
+  if (a.mask.kind == kCausalBlockwise) mid = (k_len - 1) / a.mask.block * a.mask.block - 1 - shift;
   Span c{0, 0x7FFFFFFF, 0, 0x7FFFFFFF};
-#pragma unroll
+#pragma unroll 1
   for (int k = 0; k < 3; ++k) {
-    Span s = row_span(m, sg, at[k]);
+    Span s = paged_span(a, q_len, k_len, k == 0 ? i0 : k == 1 ? min(max(mid, i0), i1 - 1) : i1 - 1);
     if (s.a1 >= s.b1) s.a1 = s.a0, s.b1 = s.b0;  // one interval counts as both
     c.a0 = max(c.a0, s.a0);
     c.b0 = min(c.b0, s.b0);
@@ -166,14 +178,15 @@ __device__ __forceinline__ int row_blocks(const PagedAttnArgs& a, int q_len) {
 
 // Sums over the requests and their row blocks: block0[i] = row blocks of the
 // requests before i, line[b] = key tiles of the row blocks before b (one head;
-// at least one per block, so that rows without keys are written).
-__global__ void __launch_bounds__(1024) paged_items_kernel(const PagedAttnArgs a) {
+// at least one per block, so that rows without keys are written) and
+// kItemCost more for each block.
+__device__ void place_items(const PagedAttnArgs& a) {
   __shared__ long long part[32];
   const int tid = threadIdx.x;
   long long at = 0;
   for (int base = 0; base < a.n_seq; base += 1024) {
     const int i = base + tid;
-    const long long n = i < a.n_seq ? row_blocks(a, paged_seg(a, i, true).q_len) : 0;
+    const long long n = i < a.n_seq ? row_blocks(a, paged_seg(a, i).q_len) : 0;
     long long total;
     const long long inc = block_scan(n, part, total);
     // rows that overlap (a bad q_start) can make more blocks than there is room for
@@ -193,11 +206,11 @@ __global__ void __launch_bounds__(1024) paged_items_kernel(const PagedAttnArgs a
         const int mid = (i + hi) >> 1;
         if (a.block0[mid] <= b) i = mid; else hi = mid;
       }
-      const SegInfo sg = paged_seg(a, i, false);
+      const SegInfo sg = paged_seg(a, i);
       const int tok = (b - a.block0[i]) * 2 * a.tpt;
       if (tok < sg.q_len) {
-        const Tiles t = tiles_of(hull(a.mask, sg, tok, min(tok + 2 * a.tpt, sg.q_len)));
-        n = max(t.n0 + t.n1, 1);
+        const Tiles t = tiles_of(hull(a, sg.q_len, sg.k_len, tok, min(tok + 2 * a.tpt, sg.q_len)));
+        n = max(t.n0 + t.n1, 1) + kItemCost;
       }
     }
     long long total;
@@ -208,23 +221,43 @@ __global__ void __launch_bounds__(1024) paged_items_kernel(const PagedAttnArgs a
   if (tid == 0) a.line[blocks] = at;
 }
 
-// The line of tiles: request by request, head by head, block by block.
+// First kernel of a call: clears the status and the counts, reports lengths
+// that the tensors do not hold, and places the items of many rows.
+__global__ void __launch_bounds__(1024) paged_begin_kernel(const __grid_constant__ PagedAttnArgs a, bool many) {
+  launch_dependents();
+  for (int i = threadIdx.x; i < kPagedMaxCtas; i += 1024) a.arrived[i] = 0;
+  if (many && threadIdx.x < kPagedMaxChunkCtas) a.cuts[threadIdx.x].seq = -1;
+  if (threadIdx.x < 4) a.status[threadIdx.x] = 0;
+  __syncthreads();
+  const int room = a.max_pages * a.page_size;
+  for (int i = threadIdx.x; i < a.n_seq; i += 1024) {
+    const int r0 = a.q_start[i], r1 = a.q_start[i + 1], kl = a.k_len[i];
+    if (r0 < 0 || r1 < r0 || r1 > a.Tq || kl < 0 || kl > room) raise_status(a.status, kStatusDeviceArg, 50);
+  }
+  if (many) place_items(a);
+}
+
+// The line of tiles: request by request, head by head, block by block.  An
+// item's kItemCost come before its tiles; a span that ends within them has
+// no piece of it.
 struct Line {
   long long total, ctas;
   __device__ __forceinline__ Line(const PagedAttnArgs& a, int grid) {
     total = a.line[a.block0[a.n_seq]] * a.Hkv;
     ctas = min(static_cast<long long>(grid), max(total / kMinTiles, 1LL));
   }
-  __device__ __forceinline__ long long start(long long c) const { return c * total / ctas; }
-  __device__ __forceinline__ long long cta_of(long long p) const { return ((p + 1) * ctas - 1) / total; }
+  __device__ __forceinline__ long long start(long long c) const { return line_div(c * total, ctas); }
+  __device__ __forceinline__ long long cta_of(long long p) const {
+    return line_div((p + 1) * ctas - 1, total);
+  }
 };
 
 struct Place {
   int seq, head, block;  // block: inside the request
-  long long first;       // of the item on the line
+  long long first;       // of the item's tiles on the line
   int tiles;
 };
-__device__ __forceinline__ Place locate(const PagedAttnArgs& a, long long pos) {
+__device__ __noinline__ Place locate(const PagedAttnArgs& a, long long pos) {
   int lo = 0, hi = a.n_seq;  // the last request that starts at or before pos
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -235,7 +268,7 @@ __device__ __forceinline__ Place locate(const PagedAttnArgs& a, long long pos) {
   const int b0 = a.block0[lo], b1 = a.block0[lo + 1];
   const long long l0 = a.line[b0], per = a.line[b1] - l0;  // tiles of one head
   const long long rel = pos - l0 * a.Hkv;
-  p.head = static_cast<int>(rel / per);
+  p.head = static_cast<int>(line_div(rel, per));
   const long long in = rel - p.head * per + l0;
   lo = b0, hi = b1;
   while (hi - lo > 1) {
@@ -243,73 +276,121 @@ __device__ __forceinline__ Place locate(const PagedAttnArgs& a, long long pos) {
     if (a.line[mid] <= in) lo = mid; else hi = mid;
   }
   p.block = lo - b0;
-  p.first = pos - (in - a.line[lo]);
-  p.tiles = static_cast<int>(a.line[lo + 1] - a.line[lo]);
+  p.first = pos - (in - a.line[lo]) + kItemCost;
+  p.tiles = static_cast<int>(a.line[lo + 1] - a.line[lo]) - kItemCost;
   return p;
 }
 
-// Slot of CTA c's sums of the item that starts at `first`: 2 c when it is the
-// first piece of its span, 2 c + 1 for a later one.
+// Slot of CTA c's sums of the item whose tiles start at `first`: 2 c when it
+// is the first piece of its span, 2 c + 1 for a later one.
 __device__ __forceinline__ long long slot_of(const Line& ln, long long c, long long first) {
-  return 2 * c + (ln.start(c) < first ? 1 : 0);
+  return 2 * c + (ln.start(c) < first - kItemCost ? 1 : 0);
 }
 
-// ------------------------------------------------------------------ producer
-__device__ __forceinline__ void producer(const PagedAttnArgs& a, const Line& ln, const CUtensorMap* tq,
-                                         const CUtensorMap* tk, const CUtensorMap* tv, uint8_t* sQ, uint8_t* sKV,
-                                         uint64_t* bar, Item* items) {
+// ------------------------------------------------------------------ scheduler
+__device__ __forceinline__ void scheduler(const PagedAttnArgs& a, const Line& ln, uint64_t* bar, Item* items) {
   const int lane = threadIdx.x & 31;
-  const int boxes = kTile / a.box_rows;  // per tile and half
-  const int box = lane % boxes, half = lane / boxes;
-  const uint32_t q_bytes = static_cast<uint32_t>(a.tpt * a.G) * 128;  // of one 64-value half of a sub-tile
   long long pos = ln.start(blockIdx.x);
   const long long end = ln.start(blockIdx.x + 1);
-  uint32_t kv_iter = 0, issued = 0;
-  int q_issued = 0;
-  for (int it = 0;; ++it) {
-    const int slot = it & 1;
-    if (it >= 2 && !waitw(&bar[B_ITEMPTY + slot], ((it >> 1) - 1) & 1, a, 60)) break;
-    Item inf;
-    inf.valid = pos < end;
-    if (!inf.valid) {
+  Place p{};
+  SegInfo sg{};
+  int b0 = 0, b1 = 0;  // the request's row blocks
+  bool begun = false;
+  for (int it = 0;;) {
+    const int slot = it % kItemSlots;
+    if (pos >= end) {
+      if (it >= kItemSlots && !waitw(&bar[B_ITEMPTY + slot], (it / kItemSlots - 1) & 1, a, 60)) return;
       if (lane == 0) {
         items[slot].valid = 0;
         mbar_arrive(&bar[B_ITFULL + slot]);
       }
       return;
     }
-    const Place p = locate(a, pos);
-    const SegInfo sg = paged_seg(a, p.seq, false);
-    inf.seq = p.seq;
-    inf.head = p.head;
-    inf.tok0 = p.block * 2 * a.tpt;
-    inf.q_off = sg.q_off;
-    inf.q_len = sg.q_len;
-    inf.k_len = sg.k_len;
-    const int toks = min(2 * a.tpt, sg.q_len - inf.tok0);
-    inf.narrow = toks <= a.tpt;
-    inf.all = hull(a.mask, sg, inf.tok0, inf.tok0 + toks);
-    const Tiles tl = tiles_of(inf.all);
-    inf.t0 = tl.t0;
-    inf.n0 = tl.n0;
-    inf.t1 = tl.t1;
-    inf.u0 = static_cast<int>(pos - p.first);
-    const int take = static_cast<int>(min(static_cast<long long>(p.tiles - inf.u0), end - pos));
-    inf.n = tl.n0 + tl.n1 > 0 ? take : 0;
-    inf.part = take < p.tiles ? static_cast<int>(slot_of(ln, blockIdx.x, p.first)) : -1;
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int i0 = inf.tok0 + (inf.narrow ? 0 : x * a.tpt), i1 = min(i0 + a.tpt, sg.q_len);
-      inf.hull[x] = hull(a.mask, sg, i0, i1);
-      inf.full[x] = common(a.mask, sg, i0, i1);
+    if (!begun) {
+      begun = true;
+      p = locate(a, pos);
+      sg = paged_seg(a, p.seq);
+      b0 = a.block0[p.seq];
+      b1 = a.block0[p.seq + 1];
+    } else {  // the next block, head or request
+      p.first = pos + kItemCost;
+      if (++p.block == b1 - b0) {
+        p.block = 0;
+        if (++p.head == a.Hkv) {
+          p.head = 0;
+          do {
+            ++p.seq;
+            b0 = b1;
+            b1 = a.block0[p.seq + 1];
+          } while (b1 == b0 && p.seq + 1 < a.n_seq);
+          sg = paged_seg(a, p.seq);
+        }
+      }
+      p.tiles = static_cast<int>(a.line[b0 + p.block + 1] - a.line[b0 + p.block]) - kItemCost;
     }
-    pos += take;
+    const long long from = max(pos, p.first), to = min(p.first + p.tiles, end);
+    pos = min(p.first + p.tiles, end);
+    if (from >= to) continue;
+    const int tok0 = p.block * 2 * a.tpt, toks = min(2 * a.tpt, sg.q_len - tok0);
+    const bool narrow = toks <= a.tpt;
+    const int u0 = static_cast<int>(from - p.first), take = static_cast<int>(to - from);
+    // lanes 0 and 1: a sub-tile's ranges; the others the item's
+    const int x = lane < 2 && !narrow ? lane : 0;
+    const int i0 = tok0 + (lane < 2 ? x * a.tpt : 0), i1 = lane < 2 ? min(i0 + a.tpt, sg.q_len) : tok0 + toks;
+    const Span h = hull(a, sg.q_len, sg.k_len, i0, i1), f = common(a, sg.q_len, sg.k_len, i0, i1);
+    if (it >= kItemSlots && !waitw(&bar[B_ITEMPTY + slot], (it / kItemSlots - 1) & 1, a, 60)) return;
+    Item& inf = items[slot];
+    if (lane < 2) {
+      inf.hull[lane] = h;
+      inf.full[lane] = f;
+    } else if (lane == 2) {
+      const Tiles tl = tiles_of(h);
+      inf.all = h;
+      inf.valid = 1;
+      inf.narrow = narrow;
+      inf.n = tl.n0 + tl.n1 > 0 ? take : 0;
+      inf.u0 = u0;
+      inf.head = p.head;
+      inf.tok0 = tok0;
+      inf.part = take < p.tiles ? static_cast<int>(slot_of(ln, blockIdx.x, p.first)) : -1;
+      inf.seq = p.seq;
+      inf.q_off = sg.q_off;
+      inf.q_len = sg.q_len;
+      inf.k_len = sg.k_len;
+      inf.t0 = tl.t0;
+      inf.n0 = tl.n0;
+      inf.t1 = tl.t1;
+    }
+    __syncwarp();
     if (lane == 0) {
-      items[slot] = inf;
       mbar_arrive(&bar[B_ITFULL + slot]);
+      // an item that starts here and goes on in later spans, for the join
+      if (u0 == 0 && take < p.tiles)
+        a.cuts[blockIdx.x] = PagedCut{p.seq, p.head, p.block, static_cast<int>(ln.cta_of(p.first + p.tiles - 1)),
+                                      static_cast<int>(slot_of(ln, blockIdx.x, p.first) & 1)};
     }
+    ++it;
+  }
+}
 
-    if (it >= 1 && !waitw(&bar[B_QEMPTY], (it - 1) & 1, a, 61)) break;
+// ------------------------------------------------------------------ producer
+__device__ __forceinline__ void producer(const PagedAttnArgs& a, const CUtensorMap* tq, const CUtensorMap* tk,
+                                         const CUtensorMap* tv, uint8_t* sQ, uint8_t* sKV, uint64_t* bar,
+                                         const Item* items) {
+  const int lane = threadIdx.x & 31;
+  const int boxes = kTile / a.box_rows;  // per tile and half
+  const int box = lane % boxes, half = lane / boxes;
+  const uint32_t q_bytes = static_cast<uint32_t>(a.tpt * a.G) * 128;  // of one 64-value half of a sub-tile
+  uint32_t kv_iter = 0, issued = 0;
+  int q_issued = 0;
+  for (int it = 0;; ++it) {
+    const int slot = it % kItemSlots;
+    if (!waitw(&bar[B_ITFULL + slot], (it / kItemSlots) & 1, a, 61)) break;
+    const Item inf = items[slot];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bar[B_ITEMPTY + slot]);
+    if (!inf.valid) return;
+    if (it >= 1 && !waitw(&bar[B_QEMPTY], (it - 1) & 1, a, 63)) break;
     if (lane == 0) {
       const int subs = inf.narrow ? 1 : 2;
       mbar_arrive_expect_tx(&bar[B_QFULL], 2 * subs * q_bytes);
@@ -376,8 +457,8 @@ __device__ __forceinline__ void mma_issuer(const PagedAttnArgs& a, uint8_t* sQ, 
   const uint64_t dK0 = sdesc_sw128(smem_u32(sKV), 16, 1024);
   const uint64_t dV0 = sdesc_sw128(smem_u32(sKV), kChunkBytes, 1024);
   uint32_t kv_iter = 0;
-  uint32_t p_iss[2] = {0, 0};
-  auto scores = [&](int buf, int sub, int kst) {
+  uint32_t p_iss[3] = {0, 0, 0};
+  auto scores = [&](int buf, int sub, int kst, int full) {
     const uint64_t dK = desc_add(dK0, kst * kTileBytes), dQ = desc_add(dQ0, sub * kTileBytes);
     tc_fence_after();
 #pragma unroll
@@ -385,7 +466,7 @@ __device__ __forceinline__ void mma_issuer(const PagedAttnArgs& a, uint8_t* sQ, 
       const uint32_t off = (ks >> 2) * kChunkBytes + (ks & 3) * 32;
       umma_ss(tbase + 128 * buf, desc_add(dQ, off), desc_add(dK, off), kIdescS, ks > 0 ? 1u : 0u);
     }
-    umma_commit(&bar[B_SFULL + buf]);
+    umma_commit(&bar[B_SFULL + full]);
   };
   auto values = [&](int buf, int sub, int vst, bool first) {
     const uint64_t dV = desc_add(dV0, vst * kTileBytes);
@@ -397,8 +478,8 @@ __device__ __forceinline__ void mma_issuer(const PagedAttnArgs& a, uint8_t* sQ, 
     umma_commit(&bar[B_OFULL + sub]);
   };
   for (int it = 0;; ++it) {
-    const int slot = it & 1;
-    if (!waitw(&bar[B_ITFULL + slot], (it >> 1) & 1, a, 70)) goto abort;
+    const int slot = it % kItemSlots;
+    if (!waitw(&bar[B_ITFULL + slot], (it / kItemSlots) & 1, a, 70)) goto abort;
     {
       const Item& inf = items[slot];
       if (!inf.valid) return;
@@ -411,17 +492,17 @@ __device__ __forceinline__ void mma_issuer(const PagedAttnArgs& a, uint8_t* sQ, 
           if (t < n) {
             const uint32_t kidx = kv_iter + 2 * t;
             if (!kv_full(kidx)) goto abort;
-            scores(t & 1, 0, kidx % kStages);
+            scores(t & 1, 0, kidx % kStages, (t & 1) ? 2 : 0);
             umma_commit(&bar[B_KVEMPTY + kidx % kStages]);
             if (t == n - 1) umma_commit(&bar[B_QEMPTY]);
           }
           if (t >= 1) {
             const uint32_t vidx = kv_iter + 2 * (t - 1) + 1;
-            const int buf = (t - 1) & 1;
+            const int odd = (t - 1) & 1, full = odd ? 2 : 0;
             if (!kv_full(vidx)) goto abort;
-            if (!waitw(&bar[B_PFULL + buf], p_iss[buf] & 1, a, 73)) goto abort;
-            ++p_iss[buf];
-            values(buf, 0, vidx % kStages, t == 1);
+            if (!waitw(&bar[B_PFULL + full], (odd ? p_iss[2] : p_iss[0]) & 1, a, 73)) goto abort;
+            if (odd) ++p_iss[2]; else ++p_iss[0];
+            values(odd, 0, vidx % kStages, t == 1);
             umma_commit(&bar[B_KVEMPTY + vidx % kStages]);
           }
         }
@@ -446,7 +527,7 @@ __device__ __forceinline__ void mma_issuer(const PagedAttnArgs& a, uint8_t* sQ, 
             if (prev[x] != kTileEmpty) {
               if (!k_ready && !kv_full(kidx)) goto abort;
               k_ready = true;
-              scores(x, x, kidx % kStages);
+              scores(x, x, kidx % kStages, x);
             }
           }
           if (t >= 1) {
@@ -557,9 +638,9 @@ __device__ __forceinline__ float row_exp(uint32_t tS, const uint32_t (&mb)[4], f
 template <typename T>
 __device__ __forceinline__ bool clean_v_row(uint8_t* v, int key, bool used) {
   bool bad = false;
-#pragma unroll
+#pragma unroll 1
   for (int c = 0; c < 2; ++c)
-#pragma unroll
+#pragma unroll 4
     for (int i = 0; i < 8; ++i) {
       uint4* p = reinterpret_cast<uint4*>(v + c * kChunkBytes + key * 128 + ((i ^ (key & 7)) << 4));
       if (!used) {
@@ -580,10 +661,7 @@ template <typename T>
 __device__ __noinline__ void row_alone(const PagedAttnArgs& a, const Item& inf, int token, int head, float& m_out,
                                        float& l_out, float (&o)[4]) {
   const int lane = threadIdx.x & 31;
-  SegInfo sg{};
-  sg.q_len = inf.q_len;
-  sg.k_len = inf.k_len;
-  const Span sp = row_span(a.mask, sg, token);
+  const Span sp = paged_span(a, inf.q_len, inf.k_len, token);
   const T* q = static_cast<const T*>(a.q) + (inf.q_off + token) * a.q_stride + head * kHeadDim + 4 * lane;
   const int* table = a.table + inf.seq * a.table_stride;
   float m = -INFINITY, l = 0.f;
@@ -620,48 +698,47 @@ __device__ __forceinline__ void softmax_wg(const PagedAttnArgs& a, int x, uint64
   const uint32_t tl = static_cast<uint32_t>(wq * 32) << 16;
   const uint32_t tO = tbase + tl + 256 + 128 * x;
   const float sl2 = a.scale_log2;
-  uint32_t s_cnt[2] = {0, 0};  // tiles of each score buffer so far
+  uint32_t s_cnt = 0, s_odd = 0;  // phases of the score barriers so far
   uint32_t o_cnt = 0;          // products into this sub-tile's O so far
   uint32_t kv_iter = 0;
   for (int it = 0;; ++it) {
-    const int slot = it & 1;
-    if (!waitw(&bar[B_ITFULL + slot], (it >> 1) & 1, a, 80 + x)) return;
+    const int slot = it % kItemSlots;
+    if (!waitw(&bar[B_ITFULL + slot], (it / kItemSlots) & 1, a, 80 + x)) return;
     const Item& inf = items[slot];
     if (!inf.valid) return;
     const bool narrow = inf.narrow != 0;
     const int n = inf.n;
     if (narrow && x == 1) {  // the other warpgroup's item
-      s_cnt[0] += (n + 1) / 2;
-      s_cnt[1] += n / 2;
       kv_iter += 2 * n;
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar[B_ITEMPTY + slot]);
       continue;
     }
-    SegInfo sg{};
-    sg.q_len = inf.q_len;
-    sg.k_len = inf.k_len;
     const int tok_in = row / a.G;
     const int token = inf.tok0 + x * a.tpt + tok_in;
     const int head = inf.head * a.G + row - tok_in * a.G;
     const bool valid = tok_in < a.tpt && token < inf.q_len;
-    const Span sp = row_span(a.mask, sg, min(token, inf.q_len - 1));
+    const Span sp = paged_span(a, inf.q_len, inf.k_len, min(token, inf.q_len - 1));
     float m = -INFINITY, l = 0.f;
     bool any = false;
     for (int t = 0; t < n; ++t) {
       const int kt = inf.tile(t);
-      int buf = t & 1;
       const uint32_t cls = inf.cls(x, kt);
-      if (!narrow) {
-        buf = x;
-        if (inf.cls(1 - x, kt) != kTileEmpty) ++s_cnt[1 - x];
-        if (cls == kTileEmpty) continue;
-      }
+      if (!narrow && cls == kTileEmpty) continue;
+      const bool odd = narrow && (t & 1);  // an odd tile of a narrow item
+      const int buf = odd ? 1 : x, full = odd ? 2 : x;
       const uint32_t tS = tbase + tl + 128 * buf;
       uint32_t mb[4];
       if (cls != kTileFull) {
 #pragma unroll
         for (int c = 0; c < 4; ++c) mb[c] = span_bits(sp, kt * kTile + 32 * c);
+      }
+      if (!waitw(&bar[B_SFULL + full], (odd ? s_odd : s_cnt) & 1, a, 82 + x)) return;
+      if (odd) ++s_odd; else ++s_cnt;
+      tc_fence_after();
+      if (cls != kTileFull) {
+        // only now: a warpgroup that skipped a narrow item runs ahead of the
+        // loads, and the scores show that the ring has come to this tile
         const uint32_t vidx = kv_iter + 2 * t + 1;
         if (!waitw(&bar[B_KVFULL + vidx % kStages], (vidx / kStages) & 1, a, 88 + x)) return;
         const int j = kt * kTile + row;
@@ -670,9 +747,6 @@ __device__ __forceinline__ void softmax_wg(const PagedAttnArgs& a, int x, uint64
           *bad_item = it + 1;
         fence_proxy_async_smem();
       }
-      if (!waitw(&bar[B_SFULL + buf], s_cnt[buf] & 1, a, 82 + x)) return;
-      ++s_cnt[buf];
-      tc_fence_after();
       const float mx = cls == kTileFull ? row_max<false>(tS, mb) : row_max<true>(tS, mb);
       const float m_new = fmaxf(m, mx * sl2);
       float factor = 1.f;
@@ -691,7 +765,7 @@ __device__ __forceinline__ void softmax_wg(const PagedAttnArgs& a, int x, uint64
         // the product before this one must have finished before O is rescaled
         if (!waitw(&bar[B_OFULL + x], (o_cnt - 1) & 1, a, 84 + x)) return;
         tc_fence_after();
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < 4; ++c) {
           uint32_t r[32];
           tmem_ld32(tO + 32 * c, r);
@@ -704,7 +778,7 @@ __device__ __forceinline__ void softmax_wg(const PagedAttnArgs& a, int x, uint64
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bar[B_PFULL + buf]);
+      if (lane == 0) mbar_arrive(&bar[B_PFULL + full]);
       ++o_cnt;
       any = true;
     }
@@ -739,21 +813,20 @@ __device__ __forceinline__ void softmax_wg(const PagedAttnArgs& a, int x, uint64
       }
     } else if (any) {
       const float inv = part ? 1.f : l == 0.f ? 0.f : 1.f / l;
-      uint32_t r[2][32];
-      tmem_ld32(tO, r[0]);
-      tmem_ld_wait();
-#pragma unroll
+#pragma unroll 1
       for (int c = 0; c < 4; ++c) {
-        if (c < 3) tmem_ld32(tO + 32 * (c + 1), r[(c + 1) & 1]);
+        uint32_t r[32];
+        tmem_ld32(tO + 32 * c, r);
+        tmem_ld_wait();
         if (valid && part) {
           float* dst = part + (x * 128 + row) * kHeadDim + 32 * c;
 #pragma unroll
-          for (int u = 0; u < 4; ++u) st_global_v8(dst + 8 * u, &r[c & 1][8 * u]);
+          for (int u = 0; u < 4; ++u) st_global_v8(dst + 8 * u, &r[8 * u]);
         } else if (valid) {
           uint32_t w[16];
 #pragma unroll
           for (int k = 0; k < 16; ++k)
-            w[k] = Half2<T>::pack(__uint_as_float(r[c & 1][2 * k]) * inv, __uint_as_float(r[c & 1][2 * k + 1]) * inv);
+            w[k] = Half2<T>::pack(__uint_as_float(r[2 * k]) * inv, __uint_as_float(r[2 * k + 1]) * inv);
           if (a.out_v8) {
             st_global_v8(orow + 32 * c, w);
             st_global_v8(orow + 32 * c + 16, w + 8);
@@ -764,7 +837,6 @@ __device__ __forceinline__ void softmax_wg(const PagedAttnArgs& a, int x, uint64
                   make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
           }
         }
-        if (c < 3) tmem_ld_wait();
       }
     } else if (valid && !part) {
 #pragma unroll
@@ -786,15 +858,17 @@ __device__ __forceinline__ void softmax_wg(const PagedAttnArgs& a, int x, uint64
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                       const __grid_constant__ CUtensorMap tmV, const PagedAttnArgs a) {
+                       const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PagedAttnArgs a) {
   extern __shared__ uint8_t smem_raw[];
+  launch_dependents();
+  grid_wait();  // the items' places on the line
   const Line ln(a, gridDim.x);
   if (blockIdx.x >= ln.ctas || ln.total == 0) return;
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = sm + kOffQ;
   uint8_t* sKV = sm + kOffKV;
   uint64_t* bar = reinterpret_cast<uint64_t*>(sm + kOffCtl);
-  Item* items = reinterpret_cast<Item*>(sm + kOffCtl + 512);
+  Item* items = reinterpret_cast<Item*>(sm + kOffCtl + 256);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + kOffCtl + 896);
   int* bad_item = reinterpret_cast<int*>(sm + kOffCtl + 904);  // per sub-tile
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -804,11 +878,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (threadIdx.x == 0) {
     for (int b = 0; b < B_COUNT; ++b) mbar_init(&bar[b], 1);
-    for (int x = 0; x < 2; ++x) {
-      mbar_init(&bar[B_PFULL + x], 4);    // one arrival per softmax warp
-      mbar_init(&bar[B_ITEMPTY + x], 9);  // eight softmax warps and the MMA warp
-      bad_item[x] = 0;
-    }
+    for (int x = 0; x < 3; ++x) mbar_init(&bar[B_PFULL + x], 4);  // one arrival per softmax warp
+    bad_item[0] = bad_item[1] = 0;
+    for (int x = 0; x < kItemSlots; ++x) mbar_init(&bar[B_ITEMPTY + x], 10);  // softmax, MMA and producer warps
     fence_mbar_init();
   }
   if (warp == 9 && lane == 0) {
@@ -820,8 +892,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
-  if (warp == 9)
-    producer(a, ln, &tmQ, &tmK, &tmV, sQ, sKV, bar, items);
+  if (warp == 10)
+    scheduler(a, ln, bar, items);
+  else if (warp == 9)
+    producer(a, &tmQ, &tmK, &tmV, sQ, sKV, bar, items);
   else if (warp == 8)
     mma_issuer<T>(a, sQ, sKV, bar, items, tbase);
   else
@@ -835,76 +909,65 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the pieces of the item that starts in CTA blockIdx.x's span and ends
-// in a later one's: 32 rows per block, a warp per row, lane k the values
+// in a later one's: 8 rows per block, a warp per row, lane k the values
 // 4 k .. 4 k + 3.
+constexpr int kJoinRows = 8;
 template <typename T>
-__global__ void __launch_bounds__(256) paged_join_kernel(const PagedAttnArgs a, int grid) {
-  const Line ln(a, grid);
-  const long long c0 = blockIdx.x;
-  if (c0 >= ln.ctas || ln.total == 0) return;
-  const Place p = locate(a, ln.start(c0 + 1) - 1);
-  const long long last = p.first + p.tiles;
-  if (p.first < ln.start(c0) || last <= ln.start(c0 + 1)) return;
-  const long long c1 = ln.cta_of(last - 1);
-  const SegInfo sg = paged_seg(a, p.seq, false);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int k = 0; k < 4; ++k) {
-    const int row = blockIdx.y * 32 + warp * 4 + k;  // of the item's two sub-tiles
-    const int sub = row >> 7, in = (row & 127) / a.G;
-    const int token = p.block * 2 * a.tpt + sub * a.tpt + in;
-    if (in >= a.tpt || token >= sg.q_len) continue;
-    const int head = p.head * a.G + (row & 127) - in * a.G;
-    auto part = [&](long long c) {
-      return a.chunk_parts + slot_of(ln, c, c == c0 ? p.first : ln.start(c)) * kPagedChunkPartFloats;
-    };
-    // each lane the maximum and sum of some pieces
-    float m = -INFINITY;
-    for (long long c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, part(c)[256 * kHeadDim + row]);
-    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
-    float l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-    for (long long c = c0; c <= c1; ++c) {
-      const float* y = part(c);
-      const float4 z = *reinterpret_cast<const float4*>(y + row * kHeadDim + 4 * lane);
-      const float lc = y[256 * kHeadDim + 256 + row];
-      if (lc != 0.f) {  // a piece without keys leaves its values unwritten
-        const float f = ex2_approx(y[256 * kHeadDim + row] - m);
-        l = fmaf(f, lc, l);
-        o[0] = fmaf(f, z.x, o[0]);
-        o[1] = fmaf(f, z.y, o[1]);
-        o[2] = fmaf(f, z.z, o[2]);
-        o[3] = fmaf(f, z.w, o[3]);
-      }
-    }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    T* dst = static_cast<T*>(a.o) + (static_cast<long long>(sg.q_off + token) * a.Hq + head) * kHeadDim + 4 * lane;
-    *reinterpret_cast<uint2*>(dst) =
-        make_uint2(Half2<T>::pack(o[0] * inv, o[1] * inv), Half2<T>::pack(o[2] * inv, o[3] * inv));
-    if (lane == 0)
-      a.lse[static_cast<long long>(head) * a.Tq + sg.q_off + token] =
-          l == 0.f ? -INFINITY : (m + log2f(l) - kBias<T>) * kLn2;
-  }
+__global__ void __launch_bounds__(32 * kJoinRows, 4) paged_join_kernel(const __grid_constant__ PagedAttnArgs a) {
+  launch_dependents();
+  grid_wait();
+  const int c0 = blockIdx.x;
+  const PagedCut cut = a.cuts[c0];
+  if (cut.seq < 0) return;
+  const int lane = threadIdx.x & 31;
+  const int row = blockIdx.y * kJoinRows + (threadIdx.x >> 5);  // of the item's two sub-tiles
+  const int sub = row >> 7, in = (row & 127) / a.G;
+  const int token = cut.block * 2 * a.tpt + sub * a.tpt + in;
+  const SegInfo sg = paged_seg(a, cut.seq);
+  if (in >= a.tpt || token >= sg.q_len) return;
+  const int head = cut.head * a.G + (row & 127) - in * a.G;
+  auto at = [&](int k) {
+    return a.chunk_parts + (2 * (c0 + k) + (k == 0 ? cut.late : 0)) * static_cast<long long>(kPagedChunkPartFloats) +
+           row * kHeadDim;
+  };
+  auto stat = [&](int k) { return at(k) + 256 * kHeadDim - row * (kHeadDim - 1); };
+  float m, l, o[4];
+  join_row(cut.last - c0 + 1, at, stat, 256, m, l, o);
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  T* dst = static_cast<T*>(a.o) + (static_cast<long long>(sg.q_off + token) * a.Hq + head) * kHeadDim + 4 * lane;
+  *reinterpret_cast<uint2*>(dst) =
+      make_uint2(Half2<T>::pack(o[0] * inv, o[1] * inv), Half2<T>::pack(o[2] * inv, o[3] * inv));
+  if (lane == 0)
+    a.lse[static_cast<long long>(head) * a.Tq + sg.q_off + token] =
+        l == 0.f ? -INFINITY : (m + log2f(l) - kBias<T>) * kLn2;
 }
 
 template <typename T>
-void launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttnArgs& a, int num_sms,
-            cudaStream_t st) {
-  cudaFuncSetAttribute(paged_chunk_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttnArgs& a,
+                   int num_sms, cudaStream_t st) {
   const int grid = std::min(num_sms, kPagedMaxChunkCtas);
-  note_launches(3);
-  paged_items_kernel<<<1, 1024, 0, st>>>(a);
-  paged_chunk_kernel<T><<<grid, kThreads, kSmemBytes, st>>>(tq, tk, tv, a);
-  paged_join_kernel<T><<<dim3(grid, 8), 256, 0, st>>>(a, grid);
+  // set on every launch: the attribute belongs to the current device
+  cudaError_t e =
+      cudaFuncSetAttribute(paged_chunk_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  if (e == cudaSuccess)
+    e = launch_after(paged_chunk_kernel<T>, dim3(grid), kThreads, kSmemBytes, st, tq, tk, tv, a);
+  if (e == cudaSuccess)
+    e = launch_after(paged_join_kernel<T>, dim3(grid, 256 / kJoinRows), 32 * kJoinRows, 0, st, a);
+  note_launches(2);
+  return e;
 }
 
 }  // namespace
 
-void launch_paged_chunk(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttnArgs& a,
-                        bool fp16, int num_sms, cudaStream_t st) {
-  if (fp16)
-    launch<__half>(tq, tk, tv, a, num_sms, st);
-  else
-    launch<__nv_bfloat16>(tq, tk, tv, a, num_sms, st);
+cudaError_t launch_paged_begin(const PagedAttnArgs& a, bool many, cudaStream_t st) {
+  note_launches(1);
+  paged_begin_kernel<<<1, 1024, 0, st>>>(a, many);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_paged_chunk(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                               const PagedAttnArgs& a, bool fp16, int num_sms, cudaStream_t st) {
+  return fp16 ? launch<__half>(tq, tk, tv, a, num_sms, st) : launch<__nv_bfloat16>(tq, tk, tv, a, num_sms, st);
 }
 
 }  // namespace lca
