@@ -545,31 +545,27 @@ __device__ __noinline__ void clear_unowned_rows(const PagedAttnArgs& a) {
   const SegInfo s1 = a.n_seq > 0 ? paged_seg(a, a.n_seq - 1) : SegInfo{};
   const int lo = s0.q_off, hi = s1.q_off + s1.q_len;
   const long long n = static_cast<long long>(lo + max(a.Tq - hi, 0)) * a.Hq * 16;
-  for (long long t = threadIdx.x; t < n; t += kDecThreads) {
-    const long long rh = t >> 4;
+  for (long long t = blockIdx.x * static_cast<long long>(kDecThreads) + threadIdx.x; t < n;
+       t += gridDim.x * static_cast<long long>(kDecThreads)) {
+    const unsigned rh = static_cast<unsigned>(t >> 4);  // Tq Hq < 2^31
+    const unsigned h = rh % a.Hq;
     long long row = rh / a.Hq;
     if (row >= lo) row += hi - lo;
-    const int h = static_cast<int>(rh % a.Hq);
     reinterpret_cast<uint4*>(a.o)[(row * a.Hq + h) * 16 + (t & 15)] = make_uint4(0, 0, 0, 0);
     if ((t & 15) == 0) a.lse[static_cast<long long>(h) * a.Tq + row] = -INFINITY;
   }
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kDecThreads, 2) paged_decode_kernel(const __grid_constant__ PagedAttnArgs a) {
-  extern __shared__ __align__(1024) uint8_t ring[];
-  __shared__ DecodeShared sh;
+__device__ __forceinline__ void decode_span(const PagedAttnArgs& a, DecodeShared& sh, uint8_t* ring, bool behind) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-
-  launch_dependents();
   // requests whose rows do not overlap make fewer than 2^52 units; a q_start
   // that lets them overlap may make more, and is reported and not served then
   constexpr long long kMost = 1LL << 52;
   long long total = 0;
   for (int base = 0; base < a.n_seq; base += kSeqTile)
     total = min(total + place_requests(a, sh, base), kMost);
-  grid_wait();  // counts and status are cleared
-  if (blockIdx.x == gridDim.x - 1) clear_unowned_rows(a);
+  if (!behind) grid_wait();  // counts and status are cleared
   if (total == 0 || total == kMost) return;
   const long long ctas = min(static_cast<long long>(gridDim.x), max(total / kMinUnits, 1LL));
   if (blockIdx.x >= ctas) return;
@@ -704,6 +700,21 @@ __global__ void __launch_bounds__(kDecThreads, 2) paged_decode_kernel(const __gr
   }
 }
 
+// behind: launched under the kernel for many rows, which lets this one start
+// once the call's first kernel has ended; this one's CTAs then take the SMs
+// that the other leaves, and end only after it, so that what follows them in
+// the stream waits for both.
+template <typename T>
+__global__ void __launch_bounds__(kDecThreads, 2)
+    paged_decode_kernel(const __grid_constant__ PagedAttnArgs a, bool behind) {
+  extern __shared__ __align__(1024) uint8_t ring[];
+  __shared__ DecodeShared sh;
+  launch_dependents();
+  decode_span<T>(a, sh, ring, behind);
+  clear_unowned_rows(a);
+  if (behind) grid_wait();
+}
+
 }  // namespace
 
 void launch_paged_plan(const PagedPlanArgs& a, int num_sms, cudaStream_t st) {
@@ -722,17 +733,18 @@ void launch_paged_write(const PagedWriteArgs& a, int num_sms, cudaStream_t st) {
 }
 
 template <typename T>
-cudaError_t launch_decode(const PagedAttnArgs& a, int num_sms, cudaStream_t st) {
+cudaError_t launch_decode(const PagedAttnArgs& a, bool behind, int num_sms, cudaStream_t st) {
   // set on every launch: the attribute belongs to the current device
   const cudaError_t e =
       cudaFuncSetAttribute(paged_decode_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kDecSmem);
   if (e != cudaSuccess) return e;
   note_launches(1);
-  return launch_after(paged_decode_kernel<T>, dim3(std::min(2 * num_sms, kPagedMaxCtas)), kDecThreads, kDecSmem, st, a);
+  return launch_after(paged_decode_kernel<T>, dim3(std::min(2 * num_sms, kPagedMaxCtas)), kDecThreads, kDecSmem, st, a,
+                      behind);
 }
 
-cudaError_t launch_paged_decode(const PagedAttnArgs& a, bool fp16, int num_sms, cudaStream_t st) {
-  return fp16 ? launch_decode<__half>(a, num_sms, st) : launch_decode<__nv_bfloat16>(a, num_sms, st);
+cudaError_t launch_paged_decode(const PagedAttnArgs& a, bool behind, bool fp16, int num_sms, cudaStream_t st) {
+  return fp16 ? launch_decode<__half>(a, behind, num_sms, st) : launch_decode<__nv_bfloat16>(a, behind, num_sms, st);
 }
 
 }  // namespace lca

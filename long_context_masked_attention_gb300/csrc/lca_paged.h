@@ -73,15 +73,16 @@ struct PagedAttnArgs {
   int out_v8;         // o is 32-byte aligned
   unsigned long long wait_limit_ns;
 };
-// A call is paged_begin, then paged_decode, then, where some request may have
-// many rows, paged_chunk: each later kernel is launched while the one before
-// it runs, and waits for it.
+// A call is begin and decode or, where some request may have many rows,
+// begin, chunk, decode (behind), join.  Each later kernel is launched while
+// the one before it runs.
 cudaError_t launch_paged_begin(const PagedAttnArgs& a, bool many, cudaStream_t st);
-cudaError_t launch_paged_decode(const PagedAttnArgs& a, bool fp16, int num_sms, cudaStream_t st);
+cudaError_t launch_paged_decode(const PagedAttnArgs& a, bool behind, bool fp16, int num_sms, cudaStream_t st);
 // Queries as boxes of tpt tokens x G heads x 64, keys and values as boxes of
 // box_rows tokens of one page and head x 64, 128-byte swizzled.
 cudaError_t launch_paged_chunk(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                                const PagedAttnArgs& a, bool fp16, int num_sms, cudaStream_t st);
+cudaError_t launch_paged_join(const PagedAttnArgs& a, bool fp16, int num_sms, cudaStream_t st);
 
 // Launches `kernel` so that it may start before the kernel in front of it on
 // `st` has ended (it calls grid_wait before it touches what that one wrote).

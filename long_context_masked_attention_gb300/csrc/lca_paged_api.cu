@@ -323,8 +323,9 @@ lca_status lca_attn_paged(const void* q, const lca_paged_cache* cache, const int
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool fp16 = cache->dtype == LCA_F16;
   LCA_CUDA(launch_paged_begin(a, many, st));
-  if (shape->Tq > 0) LCA_CUDA(launch_paged_decode(a, fp16, sms, st));
   if (many) LCA_CUDA(launch_paged_chunk(tq, tk, tv, a, fp16, sms, st));
+  if (shape->Tq > 0) LCA_CUDA(launch_paged_decode(a, many, fp16, sms, st));
+  if (many) LCA_CUDA(launch_paged_join(a, fp16, sms, st));
   return LCA_OK;
 }
 

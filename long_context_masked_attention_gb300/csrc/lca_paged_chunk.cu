@@ -246,7 +246,7 @@ struct Line {
     total = a.line[a.block0[a.n_seq]] * a.Hkv;
     ctas = min(static_cast<long long>(grid), max(total / kMinTiles, 1LL));
   }
-  __device__ __forceinline__ long long start(long long c) const { return line_div(c * total, ctas); }
+  __device__ __forceinline__ long long start(long long c) const { return line_div(min(c, ctas) * total, ctas); }
   __device__ __forceinline__ long long cta_of(long long p) const {
     return line_div((p + 1) * ctas - 1, total);
   }
@@ -860,10 +860,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                        const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PagedAttnArgs a) {
   extern __shared__ uint8_t smem_raw[];
-  launch_dependents();
-  grid_wait();  // the items' places on the line
-  const Line ln(a, gridDim.x);
-  if (blockIdx.x >= ln.ctas || ln.total == 0) return;
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = sm + kOffQ;
   uint8_t* sKV = sm + kOffKV;
@@ -892,6 +888,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
+  grid_wait();          // the items have their places on the line
+  launch_dependents();  // and what follows this kernel need not wait for the one before it
+  const Line ln(a, gridDim.x);
+  // a CTA without a span finds no item
   if (warp == 10)
     scheduler(a, ln, bar, items);
   else if (warp == 9)
@@ -945,16 +945,13 @@ __global__ void __launch_bounds__(32 * kJoinRows, 4) paged_join_kernel(const __g
 template <typename T>
 cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttnArgs& a,
                    int num_sms, cudaStream_t st) {
-  const int grid = std::min(num_sms, kPagedMaxChunkCtas);
   // set on every launch: the attribute belongs to the current device
-  cudaError_t e =
+  const cudaError_t e =
       cudaFuncSetAttribute(paged_chunk_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-  if (e == cudaSuccess)
-    e = launch_after(paged_chunk_kernel<T>, dim3(grid), kThreads, kSmemBytes, st, tq, tk, tv, a);
-  if (e == cudaSuccess)
-    e = launch_after(paged_join_kernel<T>, dim3(grid, 256 / kJoinRows), 32 * kJoinRows, 0, st, a);
-  note_launches(2);
-  return e;
+  if (e != cudaSuccess) return e;
+  note_launches(1);
+  return launch_after(paged_chunk_kernel<T>, dim3(std::min(num_sms, kPagedMaxChunkCtas)), kThreads, kSmemBytes, st, tq,
+                      tk, tv, a);
 }
 
 }  // namespace
@@ -968,6 +965,13 @@ cudaError_t launch_paged_begin(const PagedAttnArgs& a, bool many, cudaStream_t s
 cudaError_t launch_paged_chunk(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                                const PagedAttnArgs& a, bool fp16, int num_sms, cudaStream_t st) {
   return fp16 ? launch<__half>(tq, tk, tv, a, num_sms, st) : launch<__nv_bfloat16>(tq, tk, tv, a, num_sms, st);
+}
+
+cudaError_t launch_paged_join(const PagedAttnArgs& a, bool fp16, int num_sms, cudaStream_t st) {
+  const dim3 grid(std::min(num_sms, kPagedMaxChunkCtas), 256 / kJoinRows);
+  note_launches(1);
+  return launch_after(fp16 ? paged_join_kernel<__half> : paged_join_kernel<__nv_bfloat16>, grid, 32 * kJoinRows, 0, st,
+                      a);
 }
 
 }  // namespace lca
