@@ -460,68 +460,110 @@ class PagedPlan:
     state: object
 
 
-class _On:
-    """The stream of a call that may allocate: tensors made with empty() belong
-    to the given stream (the current one when none is given), and use() keeps
-    the caller's tensors from being reused while that stream reads them."""
+def _side_stream(stream, device):
+    """The torch stream of a call given another stream than the current one,
+    else None."""
+    import torch
 
-    def __init__(self, stream, device):
+    if stream is None:
+        return None
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(
+        int(getattr(stream, "cuda_stream", stream)), device)
+    return None if s == torch.cuda.current_stream(device) else s
+
+
+def _empty(shape, dtype, device, side):
+    """A tensor that belongs to the call's stream, so that its memory is not
+    handed on while that stream uses it."""
+    import torch
+
+    if side is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(side):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
+def _call(fn, name, device, side, *args):
+    """fn(*args, stream) on the tensors' device: the current stream of that
+    device, or the side stream.  What these calls cost is mostly this side of
+    them, so the common case, that device being current, takes no context."""
+    from torch import _C
+
+    index = device.index
+    raw = _C._cuda_getCurrentRawStream(index) if side is None else side.cuda_stream
+    if _C._cuda_getDevice() == index:
+        code = fn(*args, raw)
+    else:
         import torch
 
-        self.side = None
-        if stream is not None and device.type == "cuda":
-            s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(
-                int(getattr(stream, "cuda_stream", stream)), device)
-            if s != torch.cuda.current_stream(device):
-                self.side = s
-        self.device = device
+        with torch.cuda.device(device):
+            code = fn(*args, raw)
+    if code:
+        _check(code, name)
 
-    def empty(self, shape, dtype):
-        import torch
 
-        if self.side is None:
-            return torch.empty(shape, dtype=dtype, device=self.device)
-        with torch.cuda.stream(self.side):
-            t = torch.empty(shape, dtype=dtype, device=self.device)
-        t.record_stream(torch.cuda.current_stream(self.device))
-        return t
+def _refuse(t, name, dtype, shape, device):
+    """Why tensor t is not what an entry point reads."""
+    import torch
 
-    def use(self, *tensors):
-        if self.side is not None:
-            for t in tensors:
-                t.record_stream(self.side)
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name}: must be a CUDA tensor (got {t.device})")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name}: on {t.device}, expected {device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    raise ValueError(f"{name}: shape {tuple(t.shape)}, strides {t.stride()}, expected a contiguous {tuple(shape)}")
+
+
+def _ptr(t, name, dtype, shape, device):
+    """Address of a dense CUDA tensor of this dtype, shape and device."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.device == device and t.is_cuda and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(t, name, dtype, shape, device)
 
 
 def _paged_cache(k, v):
+    """lca_paged_cache of two [n_pages, page_size, Hkv, d] tensors."""
     import torch
 
     for name, t in (("k_cache", k), ("v_cache", v)):
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
-        if t.device.type != "cuda":
+        if not t.is_cuda:
             raise ValueError(f"{name}: must be a CUDA tensor (got {t.device})")
-        if t.dim() != 4:
-            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [n_pages, page_size, Hkv, d]")
-    if v.shape != k.shape or v.dtype != k.dtype or v.device != k.device:
-        raise ValueError(f"v_cache: {tuple(v.shape)} {v.dtype} on {v.device}, expected {tuple(k.shape)} {k.dtype} "
-                         f"on {k.device} as k_cache")
-    if k.dtype == torch.bfloat16:
-        dtype = 0
-    elif k.dtype == torch.float16:
-        dtype = 1
+    shape, dt = k.shape, k.dtype
+    if len(shape) != 4:
+        raise ValueError(f"k_cache: shape {tuple(shape)}, expected [n_pages, page_size, Hkv, d]")
+    if v.shape != shape or v.dtype is not dt or v.device != k.device:
+        raise ValueError(f"v_cache: {tuple(v.shape)} {v.dtype} on {v.device}, expected {tuple(shape)} {dt} on {k.device} "
+                         "as k_cache")
+    if dt is torch.bfloat16:
+        code = 0
+    elif dt is torch.float16:
+        code = 1
     else:
-        raise ValueError(f"k_cache: dtype {k.dtype}, expected torch.bfloat16 or torch.float16")
-    n, page, Hkv, d = k.shape
-    strides = []
-    for t in (k, v):
-        a, b, c, e = t.stride()
-        if e != 1 and d > 1 and n:
-            raise ValueError("k_cache, v_cache: the last dimension must be contiguous")
-        # the stride of an axis of length one moves nothing
-        strides.append((a if n > 1 else d, b if n and page > 1 else d, c if n and Hkv > 1 else d))
-    if strides[0] != strides[1]:
-        raise ValueError(f"v_cache: strides {strides[1]}, expected {strides[0]} as k_cache")
-    return PagedCache_t(k.data_ptr(), v.data_ptr(), n, page, Hkv, d, dtype, *strides[0])
+        raise ValueError(f"k_cache: dtype {dt}, expected torch.bfloat16 or torch.float16")
+    n, page, Hkv, d = shape
+    ks, vs = k.stride(), v.stride()
+    if n <= 1 or page == 1 or Hkv == 1 or d == 1:
+        # the stride of an axis of length one (or of an empty cache) moves nothing
+        def moves(st):
+            return (st[0] if n > 1 else d, st[1] if n and page > 1 else d, st[2] if n and Hkv > 1 else d,
+                    st[3] if n and d > 1 else 1)
+
+        ks, vs = moves(ks), moves(vs)
+    if ks != vs:
+        raise ValueError(f"v_cache: strides {vs}, expected {ks} as k_cache")
+    if ks[3] != 1:
+        raise ValueError("k_cache, v_cache: the last dimension must be contiguous")
+    return PagedCache_t(k.data_ptr(), v.data_ptr(), n, page, Hkv, d, code, ks[0], ks[1], ks[2])
 
 
 def _rows(t, name, heads, d, dtype, device):
@@ -532,33 +574,16 @@ def _rows(t, name, heads, d, dtype, device):
         raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
     if t.device != device:
         raise ValueError(f"{name}: on {t.device}, expected {device}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
-    if t.dim() != 3 or t.shape[2] != d or (heads is not None and t.shape[1] != heads):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [T, {'H' if heads is None else heads}, {d}]")
-    T, H, _ = t.shape
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != d or (heads is not None and shape[1] != heads):
+        raise ValueError(f"{name}: shape {tuple(shape)}, expected [T, {'H' if heads is None else heads}, {d}]")
+    T, H, _ = shape
     a, b, c = t.stride()
     if T and ((c != 1 and d > 1) or (H > 1 and b != d)):
         raise ValueError(f"{name}: each row's heads must be contiguous")
     return a if T > 1 else H * d
-
-
-def _ints(t, name, shape, device):
-    import torch
-
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
-    if t.device.type != "cuda":
-        raise ValueError(f"{name}: must be a CUDA tensor (got {t.device})")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name}: on {t.device}, expected {device}")
-    if t.dtype != torch.int32:
-        raise ValueError(f"{name}: dtype {t.dtype}, expected torch.int32")
-    if t.shape != shape:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: must be contiguous")
-    return t.data_ptr()
 
 
 def _table(t, n_seq, device):
@@ -569,11 +594,12 @@ def _table(t, n_seq, device):
         raise TypeError(f"block_table: expected a torch.Tensor, got {type(t).__name__}")
     if t.device != device:
         raise ValueError(f"block_table: on {t.device}, expected {device}")
-    if t.dtype != torch.int32:
+    if t.dtype is not torch.int32:
         raise ValueError(f"block_table: dtype {t.dtype}, expected torch.int32")
-    if t.dim() != 2 or t.shape[0] != n_seq:
-        raise ValueError(f"block_table: shape {tuple(t.shape)}, expected [{n_seq}, max_pages]")
-    width = t.shape[1]
+    shape = t.shape
+    if len(shape) != 2 or (n_seq is not None and shape[0] != n_seq):
+        raise ValueError(f"block_table: shape {tuple(shape)}, expected [{'n_seq' if n_seq is None else n_seq}, max_pages]")
+    n_seq, width = shape
     a, b = t.stride()
     if (n_seq and b != 1 and width > 1) or (n_seq > 1 and a < width):
         raise ValueError("block_table: each row must be contiguous, and rows must not overlap")
@@ -589,34 +615,36 @@ def paged_plan(ctx_len, new_len, free_pages, taken, block_table, page_size, n_pa
     max_pages] int32; n_rows: rows of the packed batch, those behind the last
     request get slot -1.  state holds {free pages used so far, pages missing,
     requests with unusable lengths, new tokens}; state[:1] is the next call's
-    `taken`."""
+    `taken`.  Outputs that are not given are parts of one new tensor."""
     import torch
 
-    if not isinstance(ctx_len, torch.Tensor):
-        raise TypeError(f"ctx_len: expected a torch.Tensor, got {type(ctx_len).__name__}")
-    n_seq, dev, n_rows = ctx_len.numel(), ctx_len.device, int(n_rows)
+    for name, t in (("ctx_len", ctx_len), ("free_pages", free_pages)):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+    n_seq, n_free, dev, i32, n_rows = ctx_len.numel(), free_pages.numel(), ctx_len.device, torch.int32, int(n_rows)
     if n_rows < 0:
         raise ValueError(f"n_rows: {n_rows}, expected 0 or more")
-    args = [_ints(ctx_len, "ctx_len", (n_seq,), None), _ints(new_len, "new_len", (n_seq,), dev), n_seq]
-    if not isinstance(free_pages, torch.Tensor):
-        raise TypeError(f"free_pages: expected a torch.Tensor, got {type(free_pages).__name__}")
-    args += [_ints(free_pages, "free_pages", (free_pages.numel(),), dev), free_pages.numel(),
-             _ints(taken, "taken", (1,), dev)]
+    ins = (_ptr(ctx_len, "ctx_len", i32, (n_seq,), dev), _ptr(new_len, "new_len", i32, (n_seq,), dev), n_seq,
+           _ptr(free_pages, "free_pages", i32, (n_free,), dev), n_free, _ptr(taken, "taken", i32, (1,), dev))
     tp, width, tstride = _table(block_table, n_seq, dev)
-    on = _On(stream, dev)
-    outs = []
-    for t, name, n in ((q_start, "q_start", n_seq + 1), (k_len, "k_len", n_seq), (slots, "slots", n_rows),
-                       (positions, "positions", n_rows), (state, "state", 4)):
-        if t is None:
-            t = on.empty((n,), torch.int32)
+    side = _side_stream(stream, dev)
+    outs = [q_start, k_len, slots, positions, state]
+    sizes = [n_seq + 1, n_seq, n_rows, n_rows, 4]
+    new = [n if t is None else 0 for t, n in zip(outs, sizes)]
+    buf = _empty((sum(new),), i32, dev, side)
+    parts, at, ptrs = torch.split_with_sizes(buf, new), buf.data_ptr(), []
+    for i, name in enumerate(("q_start", "k_len", "slots", "positions", "state")):
+        if outs[i] is None:
+            outs[i] = parts[i]
+            ptrs.append(at)
+            at += 4 * sizes[i]
         else:
-            _ints(t, name, (n,), dev)
-            on.use(t)
-        outs.append(t)
-    on.use(ctx_len, new_len, free_pages, taken, block_table)
-    with _on_device(dev):
-        _check(load().lca_paged_plan(*args, tp, tstride, width, int(page_size), int(n_pages), n_rows,
-                                     *[t.data_ptr() for t in outs], _stream(stream, dev)), "lca_paged_plan")
+            ptrs.append(_ptr(outs[i], name, i32, (sizes[i],), dev))
+    if side is not None:
+        for t in (ctx_len, new_len, free_pages, taken, block_table, *outs):
+            t.record_stream(side)
+    _call(load().lca_paged_plan, "lca_paged_plan", dev, side, *ins, tp, tstride, width, int(page_size), int(n_pages),
+          n_rows, *ptrs)
     return PagedPlan(*outs)
 
 
@@ -624,39 +652,45 @@ def paged_write(k, v, k_cache, v_cache, slots, stream=None):
     """Stores rows k, v [T, Hkv, 128] (row stride free) at slots [T] int32 of
     the cache [n_pages, page_size, Hkv, 128] (strides free, bf16 or fp16), in
     place; rows whose slot is outside the cache (-1) are skipped."""
+    import torch
+
     cache = _paged_cache(k_cache, v_cache)
-    dev = k_cache.device
-    ks = _rows(k, "k", cache.Hkv, cache.d, k_cache.dtype, dev)
-    vs = _rows(v, "v", cache.Hkv, cache.d, k_cache.dtype, dev)
+    dev, dt = k_cache.device, k_cache.dtype
+    ks = _rows(k, "k", cache.Hkv, cache.d, dt, dev)
+    vs = _rows(v, "v", cache.Hkv, cache.d, dt, dev)
     T = k.shape[0]
     if v.shape[0] != T:
         raise ValueError(f"v: {v.shape[0]} rows, expected {T} as k")
-    sp = _ints(slots, "slots", (T,), dev)
-    _On(stream, dev).use(k, v, k_cache, v_cache, slots)
-    with _on_device(dev):
-        _check(load().lca_paged_write(k.data_ptr(), v.data_ptr(), ks, vs, sp, T, C.byref(cache), _stream(stream, dev)),
-               "lca_paged_write")
+    sp = _ptr(slots, "slots", torch.int32, (T,), dev)
+    side = _side_stream(stream, dev)
+    if side is not None:
+        for t in (k, v, k_cache, v_cache, slots):
+            t.record_stream(side)
+    _call(load().lca_paged_write, "lca_paged_write", dev, side, k.data_ptr(), v.data_ptr(), ks, vs, sp, T,
+          C.byref(cache))
 
 
 def _paged_mask(mask):
-    md = MaskDesc_t()
-    md.kind = mask.kind if isinstance(mask.kind, int) else MASK_KINDS.index(mask.kind)
-    for name in ("window_left", "window_right", "num_global", "prefix_len", "block"):
-        setattr(md, name, int(getattr(mask, name, 0) or 0))
+    kind = mask.kind
+    if not isinstance(kind, int):
+        kind = MASK_KINDS.index(kind)
+    md = MaskDesc_t(kind)
+    if kind not in _PLAIN_KINDS:
+        for name in ("window_left", "window_right", "num_global", "prefix_len", "block"):
+            setattr(md, name, int(getattr(mask, name, 0) or 0))
     return md
 
 
-def attn_paged_workspace_size(q, k_cache, v_cache, block_table, mask, scale=0.0, max_q_len=0) -> int:
-    """Bytes of workspace that attn_paged needs for these tensors."""
-    cache = _paged_cache(k_cache, v_cache)
-    return _paged_size(_paged_shape(q, cache, k_cache, block_table, scale, max_q_len)[0], cache, _paged_mask(mask))
+_SIZES: dict = {}  # workspace bytes of attn_paged by shape
+_PLAIN_KINDS = tuple(MASK_KINDS.index(k) for k in ("FULL", "CAUSAL", "DOC", "CAUSAL_DOC"))  # no parameters
 
 
 def _paged_shape(q, cache, k_cache, block_table, scale, max_q_len):
-    qs = _rows(q, "q", None, cache.d, k_cache.dtype, k_cache.device)
-    n_seq = block_table.shape[0]
-    tp, width, tstride = _table(block_table, n_seq, k_cache.device)
-    return PagedShape_t(q.shape[0], q.shape[1], n_seq, width, tstride, qs, int(max_q_len), float(scale)), tp
+    dev = k_cache.device
+    qs = _rows(q, "q", None, cache.d, k_cache.dtype, dev)
+    tp, width, tstride = _table(block_table, None, dev)
+    shape = q.shape
+    return PagedShape_t(shape[0], shape[1], block_table.shape[0], width, tstride, qs, max_q_len, scale), tp
 
 
 def _paged_size(shape, cache, md):
@@ -664,6 +698,12 @@ def _paged_size(shape, cache, md):
     _check(load().lca_attn_paged_workspace_size(C.byref(shape), C.byref(cache), C.byref(md), C.byref(n)),
            "lca_attn_paged_workspace_size")
     return n.value
+
+
+def attn_paged_workspace_size(q, k_cache, v_cache, block_table, mask, scale=0.0, max_q_len=0) -> int:
+    """Bytes of workspace that attn_paged needs for these tensors."""
+    cache = _paged_cache(k_cache, v_cache)
+    return _paged_size(_paged_shape(q, cache, k_cache, block_table, scale, max_q_len)[0], cache, _paged_mask(mask))
 
 
 def attn_paged(q, k_cache, v_cache, block_table, q_start, k_len, mask, scale=0.0, max_q_len=0, out=None, lse=None,
@@ -680,33 +720,40 @@ def attn_paged(q, k_cache, v_cache, block_table, q_start, k_len, mask, scale=0.0
     import torch
 
     cache = _paged_cache(k_cache, v_cache)
-    if not isinstance(block_table, torch.Tensor):
-        raise TypeError(f"block_table: expected a torch.Tensor, got {type(block_table).__name__}")
-    dev = k_cache.device
+    dev, dt = k_cache.device, q.dtype
     shape, tp = _paged_shape(q, cache, k_cache, block_table, scale, max_q_len)
     md = _paged_mask(mask)
-    qsp = _ints(q_start, "q_start", (shape.n_seq + 1,), dev)
-    klp = _ints(k_len, "k_len", (shape.n_seq,), dev)
-    need = _paged_size(shape, cache, md)
-    on = _On(stream, dev)
-    size, lsize = tuple(q.shape), (shape.Hq, shape.Tq)
+    n_seq = shape.n_seq
+    qsp = _ptr(q_start, "q_start", torch.int32, (n_seq + 1,), dev)
+    klp = _ptr(k_len, "k_len", torch.int32, (n_seq,), dev)
+    side = _side_stream(stream, dev)
+    size, lsize = q.shape, (shape.Hq, shape.Tq)
     if out is None:
-        out = on.empty(size, q.dtype)
+        out = _empty(size, dt, dev, side)
+        op = out.data_ptr()
     else:
-        on.use(_require(out, "out", size, q.dtype, dev))
+        op = _ptr(out, "out", dt, size, dev)
     if lse is None:
-        lse = on.empty(lsize, torch.float32)
+        lse = _empty(lsize, torch.float32, dev, side)
+        lp = lse.data_ptr()
     else:
-        on.use(_require(lse, "lse", lsize, torch.float32, dev))
+        lp = _ptr(lse, "lse", torch.float32, lsize, dev)
     if workspace is None:
-        workspace = on.empty((need,), torch.uint8)
+        # the size depends on these alone
+        key = (shape.Tq, shape.Hq, n_seq, shape.max_q_len, cache.Hkv, cache.n_pages > 0)
+        need = _SIZES.get(key)
+        if need is None:
+            if len(_SIZES) >= 4096:
+                _SIZES.clear()
+            need = _SIZES[key] = _paged_size(shape, cache, md)
+        workspace = _empty((need,), torch.uint8, dev, side)
     else:
-        on.use(_require(workspace, "workspace", (workspace.numel(),), torch.uint8, dev))
-    on.use(q, k_cache, v_cache, block_table, q_start, k_len)
-    with _on_device(dev):
-        _check(load().lca_attn_paged(q.data_ptr(), C.byref(cache), tp, qsp, klp, out.data_ptr(), lse.data_ptr(),
-                                     C.byref(shape), C.byref(md), workspace.data_ptr(), workspace.numel(),
-                                     _stream(stream, dev)), "lca_attn_paged")
+        _ptr(workspace, "workspace", torch.uint8, (workspace.numel(),), dev)
+    if side is not None:
+        for t in (q, k_cache, v_cache, block_table, q_start, k_len, out, lse, workspace):
+            t.record_stream(side)
+    _call(load().lca_attn_paged, "lca_attn_paged", dev, side, q.data_ptr(), C.byref(cache), tp, qsp, klp, op, lp,
+          C.byref(shape), C.byref(md), workspace.data_ptr(), workspace.numel())
     return out, lse
 
 

@@ -664,23 +664,28 @@ __device__ __forceinline__ void decode_span(const PagedAttnArgs& a, DecodeShared
       __syncthreads();
       if (sh.last) {
         __threadfence();
+        auto piece = [&](int k) {
+          return a.parts + (2 * (c0 + k) + (k == 0 ? late : 0)) * static_cast<long long>(kPartFloats);
+        };
 #pragma unroll 1
-        for (int i = warp; i < rows; i += kDecWarps) {
-          auto at = [&](int k) {
-            return a.parts + (2 * (c0 + k) + (k == 0 ? late : 0)) * static_cast<long long>(kPartFloats) + i * kHeadDim;
-          };
-          auto stat = [&](int k) { return at(k) + kRows * kHeadDim - i * (kHeadDim - 1); };
-          float mr, lr, y[4];
-          join_row(c1 - c0 + 1, at, stat, kRows, mr, lr, y);
-          const long long r = static_cast<long long>(tile) * kRows + i;
-          const long long token = sg.q_off + r / a.G;
-          const int h = head * a.G + static_cast<int>(r % a.G);
-          const float inv = lr == 0.f ? 0.f : 1.f / lr;
-          *reinterpret_cast<uint2*>(static_cast<T*>(a.o) + (token * a.Hq + h) * kHeadDim + 4 * lane) =
-              make_uint2(Half2<T>::pack(y[0] * inv, y[1] * inv), Half2<T>::pack(y[2] * inv, y[3] * inv));
-          if (lane == 0)
-            a.lse[static_cast<long long>(h) * a.Tq + token] =
-                lr == 0.f ? -INFINITY : (mr + log2f(lr) - kBias<T>) * 0.6931471805599453f;
+        for (int i = 2 * warp; i < rows; i += 2 * kDecWarps) {
+          float mr, lr, y[2][4];
+          join_rows<kRows, 2, 8>(c1 - c0 + 1, piece, i, mr, lr, y);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const float mk = __shfl_sync(~0u, mr, 16 * k), lk = __shfl_sync(~0u, lr, 16 * k);
+            if (i + k < rows) {
+              const long long r = static_cast<long long>(tile) * kRows + i + k;
+              const long long token = sg.q_off + r / a.G;
+              const int h = head * a.G + static_cast<int>(r % a.G);
+              const float inv = lk == 0.f ? 0.f : 1.f / lk;
+              *reinterpret_cast<uint2*>(static_cast<T*>(a.o) + (token * a.Hq + h) * kHeadDim + 4 * lane) =
+                  make_uint2(Half2<T>::pack(y[k][0] * inv, y[k][1] * inv), Half2<T>::pack(y[k][2] * inv, y[k][3] * inv));
+              if (lane == 0)
+                a.lse[static_cast<long long>(h) * a.Tq + token] =
+                    lk == 0.f ? -INFINITY : (mk + log2f(lk) - kBias<T>) * 0.6931471805599453f;
+            }
+          }
         }
       }
     } else if (row < rows) {
@@ -734,9 +739,8 @@ void launch_paged_write(const PagedWriteArgs& a, int num_sms, cudaStream_t st) {
 
 template <typename T>
 cudaError_t launch_decode(const PagedAttnArgs& a, bool behind, int num_sms, cudaStream_t st) {
-  // set on every launch: the attribute belongs to the current device
-  const cudaError_t e =
-      cudaFuncSetAttribute(paged_decode_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kDecSmem);
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem(paged_decode_kernel<T>, kDecSmem, done);
   if (e != cudaSuccess) return e;
   note_launches(1);
   return launch_after(paged_decode_kernel<T>, dim3(std::min(2 * num_sms, kPagedMaxCtas)), kDecThreads, kDecSmem, st, a,

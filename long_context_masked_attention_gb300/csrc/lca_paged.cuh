@@ -89,50 +89,59 @@ __device__ __forceinline__ bool few_rows(const PagedAttnArgs& a, int q_len) {
   return static_cast<long long>(q_len) * a.G <= a.few;
 }
 
-// Sums of one row over pieces that hold it unnormalised, by a whole warp:
-// piece k has its values (128) at at(k), its maximum at stat(k)[0] and its sum
-// of exponentials at stat(k)[gap].  Lane j gets values 4 j .. 4 j + 3.  All
-// loads of eight pieces are under way at once: a trip to L2 is what this costs.
-template <typename At, typename Stat>
-__device__ __forceinline__ void join_row(int n, At at, Stat stat, int gap, float& m, float& l, float (&o)[4]) {
-  const int lane = threadIdx.x & 31;
-  // lane k: piece k of the first 32
-  const float m0 = lane < n ? __ldcg(stat(lane)) : -INFINITY, l0 = lane < n ? __ldcg(stat(lane) + gap) : 0.f;
+// Sums of R rows over n pieces that hold them unnormalised, by a whole warp:
+// piece(k) has kRowsOf x 128 values, the rows' maxima, then their sums of
+// exponentials.  Lane j gets values 4 j .. 4 j + 3 of the rows row0 .. row0 +
+// R - 1, and the maximum and sum of row row0 + j / (32 / R).  The loads of P
+// pieces of all rows are under way at once: a trip to L2 is what this costs.
+template <int kRowsOf, int R, int P, typename Piece>
+__device__ __forceinline__ void join_rows(int n, Piece piece, int row0, float& m, float& l, float (&o)[R][4]) {
+  constexpr int W = 32 / R;  // pieces whose factors are in lanes at once
+  const int lane = threadIdx.x & 31, p = lane % W, stat = kRowsOf * kHeadDim + row0 + lane / W;
+  const float m0 = p < n ? __ldcg(piece(p) + stat) : -INFINITY;
+  const float l0 = p < n ? __ldcg(piece(p) + stat + kRowsOf) : 0.f;
   m = m0;
-  for (int k = lane + 32; k < n; k += 32) m = fmaxf(m, __ldcg(stat(k)));
+  for (int k = p + W; k < n; k += W) m = fmaxf(m, __ldcg(piece(k) + stat));
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
+  for (int d = W / 2; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
   l = 0.f;
-  o[0] = o[1] = o[2] = o[3] = 0.f;
+#pragma unroll
+  for (int r = 0; r < R; ++r) o[r][0] = o[r][1] = o[r][2] = o[r][3] = 0.f;
 #pragma unroll 1
-  for (int b = 0; b < n; b += 32) {
+  for (int b = 0; b < n; b += W) {
     float mk = m0, lk = l0;
     if (b > 0) {
-      mk = b + lane < n ? __ldcg(stat(b + lane)) : -INFINITY;
-      lk = b + lane < n ? __ldcg(stat(b + lane) + gap) : 0.f;
+      mk = b + p < n ? __ldcg(piece(b + p) + stat) : -INFINITY;
+      lk = b + p < n ? __ldcg(piece(b + p) + stat + kRowsOf) : 0.f;
     }
     const float f = lk != 0.f ? ex2_approx(mk - m) : 0.f;
     l = fmaf(f, lk, l);
-    const int here = min(32, n - b);
+    const int here = min(W, n - b);
 #pragma unroll 1
-    for (int k = 0; k < here; k += 8) {
-      float4 z[8];
+    for (int k = 0; k < here; k += P) {
+      float4 z[P][R];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) z[u] = __ldcg(reinterpret_cast<const float4*>(at(b + min(k + u, here - 1))) + lane);
+      for (int u = 0; u < P; ++u) {
+        const float* y = piece(b + min(k + u, here - 1)) + row0 * kHeadDim;
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const float fk = __shfl_sync(~0u, f, min(k + u, 31));
-        if (k + u < here && fk != 0.f) {  // a piece without keys leaves its values unwritten
-          o[0] = fmaf(fk, z[u].x, o[0]);
-          o[1] = fmaf(fk, z[u].y, o[1]);
-          o[2] = fmaf(fk, z[u].z, o[2]);
-          o[3] = fmaf(fk, z[u].w, o[3]);
-        }
+        for (int r = 0; r < R; ++r) z[u][r] = __ldcg(reinterpret_cast<const float4*>(y + r * kHeadDim) + lane);
       }
+#pragma unroll
+      for (int u = 0; u < P; ++u)
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const float fk = __shfl_sync(~0u, f, r * W + min(k + u, W - 1));
+          if (k + u < here && fk != 0.f) {  // a piece without keys leaves its values unwritten
+            o[r][0] = fmaf(fk, z[u][r].x, o[r][0]);
+            o[r][1] = fmaf(fk, z[u][r].y, o[r][1]);
+            o[r][2] = fmaf(fk, z[u][r].z, o[r][2]);
+            o[r][3] = fmaf(fk, z[u][r].w, o[r][3]);
+          }
+        }
     }
   }
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(~0u, l, d);
+  for (int d = W / 2; d > 0; d >>= 1) l += __shfl_xor_sync(~0u, l, d);
 }
 
 // a / b of the line's positions, once in code

@@ -3,6 +3,7 @@
 #pragma once
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <atomic>
 #include <cstdint>
 
 #include "lca_common.cuh"
@@ -42,10 +43,10 @@ constexpr int kPagedChunkPartFloats = 256 * (kHeadDim + 2);
 constexpr int kPagedFewRows = 16;
 
 // An item of many rows that goes on past the span of the CTA it starts in.
-struct PagedCut {
-  int seq, head, block;
-  int last;  // CTA of its last piece
+struct alignas(32) PagedCut {
+  int last;  // CTA of its last piece, -1: no such item
   int late;  // its first piece is not the first of its CTA's span
+  int head, tok0, q_off, q_len, pad[2];
 };
 
 struct PagedAttnArgs {
@@ -69,7 +70,7 @@ struct PagedAttnArgs {
   int* block0;        // [n_seq + 1] row blocks before each request
   long long* line;    // [max_blocks + 1] key tiles before each row block
   float* chunk_parts; // [kPagedMaxChunkCtas][2][kPagedChunkPartFloats]
-  PagedCut* cuts;     // [kPagedMaxChunkCtas] seq < 0: none starts in this CTA's span
+  PagedCut* cuts;     // [kPagedMaxChunkCtas], by the CTA it starts in
   int out_v8;         // o is 32-byte aligned
   unsigned long long wait_limit_ns;
 };
@@ -83,6 +84,20 @@ cudaError_t launch_paged_decode(const PagedAttnArgs& a, bool behind, bool fp16, 
 cudaError_t launch_paged_chunk(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                                const PagedAttnArgs& a, bool fp16, int num_sms, cudaStream_t st);
 cudaError_t launch_paged_join(const PagedAttnArgs& a, bool fp16, int num_sms, cudaStream_t st);
+
+// Lets `kernel` use `bytes` of dynamic shared memory on the current device;
+// asks CUDA once per device.  One `done` per kernel, bit d for device d.
+template <typename K>
+cudaError_t allow_smem(K* kernel, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t{1} << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
 
 // Launches `kernel` so that it may start before the kernel in front of it on
 // `st` has ended (it calls grid_wait before it touches what that one wrote).

@@ -226,7 +226,7 @@ __device__ void place_items(const PagedAttnArgs& a) {
 __global__ void __launch_bounds__(1024) paged_begin_kernel(const __grid_constant__ PagedAttnArgs a, bool many) {
   launch_dependents();
   for (int i = threadIdx.x; i < kPagedMaxCtas; i += 1024) a.arrived[i] = 0;
-  if (many && threadIdx.x < kPagedMaxChunkCtas) a.cuts[threadIdx.x].seq = -1;
+  if (many && threadIdx.x < kPagedMaxChunkCtas) a.cuts[threadIdx.x].last = -1;
   if (threadIdx.x < 4) a.status[threadIdx.x] = 0;
   __syncthreads();
   const int room = a.max_pages * a.page_size;
@@ -366,8 +366,13 @@ __device__ __forceinline__ void scheduler(const PagedAttnArgs& a, const Line& ln
       mbar_arrive(&bar[B_ITFULL + slot]);
       // an item that starts here and goes on in later spans, for the join
       if (u0 == 0 && take < p.tiles)
-        a.cuts[blockIdx.x] = PagedCut{p.seq, p.head, p.block, static_cast<int>(ln.cta_of(p.first + p.tiles - 1)),
-                                      static_cast<int>(slot_of(ln, blockIdx.x, p.first) & 1)};
+        a.cuts[blockIdx.x] = PagedCut{static_cast<int>(ln.cta_of(p.first + p.tiles - 1)),
+                                      static_cast<int>(slot_of(ln, blockIdx.x, p.first) & 1),
+                                      p.head,
+                                      tok0,
+                                      sg.q_off,
+                                      sg.q_len,
+                                      {0, 0}};
     }
     ++it;
   }
@@ -909,45 +914,45 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the pieces of the item that starts in CTA blockIdx.x's span and ends
-// in a later one's: 8 rows per block, a warp per row, lane k the values
-// 4 k .. 4 k + 3.
-constexpr int kJoinRows = 8;
+// in a later one's: 32 rows per block, four rows per warp.
+constexpr int kJoinRows = 32;
 template <typename T>
-__global__ void __launch_bounds__(32 * kJoinRows, 4) paged_join_kernel(const __grid_constant__ PagedAttnArgs a) {
+__global__ void __launch_bounds__(8 * kJoinRows, 3) paged_join_kernel(const __grid_constant__ PagedAttnArgs a) {
   launch_dependents();
   grid_wait();
   const int c0 = blockIdx.x;
   const PagedCut cut = a.cuts[c0];
-  if (cut.seq < 0) return;
+  if (cut.last < 0) return;
   const int lane = threadIdx.x & 31;
-  const int row = blockIdx.y * kJoinRows + (threadIdx.x >> 5);  // of the item's two sub-tiles
-  const int sub = row >> 7, in = (row & 127) / a.G;
-  const int token = cut.block * 2 * a.tpt + sub * a.tpt + in;
-  const SegInfo sg = paged_seg(a, cut.seq);
-  if (in >= a.tpt || token >= sg.q_len) return;
-  const int head = cut.head * a.G + (row & 127) - in * a.G;
-  auto at = [&](int k) {
-    return a.chunk_parts + (2 * (c0 + k) + (k == 0 ? cut.late : 0)) * static_cast<long long>(kPagedChunkPartFloats) +
-           row * kHeadDim;
+  const int row0 = blockIdx.y * kJoinRows + (threadIdx.x >> 5) * 4;  // of the item's two sub-tiles
+  auto token_of = [&](int row) { return cut.tok0 + (row >> 7) * a.tpt + (row & 127) / a.G; };
+  if (token_of(row0) >= cut.q_len || (row0 & 127) >= a.tpt * a.G) return;  // nor do the three after it have a token
+  auto piece = [&](int k) {
+    return a.chunk_parts + (2 * (c0 + k) + (k == 0 ? cut.late : 0)) * static_cast<long long>(kPagedChunkPartFloats);
   };
-  auto stat = [&](int k) { return at(k) + 256 * kHeadDim - row * (kHeadDim - 1); };
-  float m, l, o[4];
-  join_row(cut.last - c0 + 1, at, stat, 256, m, l, o);
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  T* dst = static_cast<T*>(a.o) + (static_cast<long long>(sg.q_off + token) * a.Hq + head) * kHeadDim + 4 * lane;
-  *reinterpret_cast<uint2*>(dst) =
-      make_uint2(Half2<T>::pack(o[0] * inv, o[1] * inv), Half2<T>::pack(o[2] * inv, o[3] * inv));
-  if (lane == 0)
-    a.lse[static_cast<long long>(head) * a.Tq + sg.q_off + token] =
-        l == 0.f ? -INFINITY : (m + log2f(l) - kBias<T>) * kLn2;
+  float m, l, o[4][4];
+  join_rows<256, 4, 2>(cut.last - c0 + 1, piece, row0, m, l, o);
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const float mr = __shfl_sync(~0u, m, 8 * r), lr = __shfl_sync(~0u, l, 8 * r);
+    const int row = row0 + r, token = token_of(row);
+    if (token >= cut.q_len || (row & 127) >= a.tpt * a.G) continue;
+    const int head = cut.head * a.G + (row & 127) % a.G;
+    const float inv = lr == 0.f ? 0.f : 1.f / lr;
+    T* dst = static_cast<T*>(a.o) + (static_cast<long long>(cut.q_off + token) * a.Hq + head) * kHeadDim + 4 * lane;
+    *reinterpret_cast<uint2*>(dst) =
+        make_uint2(Half2<T>::pack(o[r][0] * inv, o[r][1] * inv), Half2<T>::pack(o[r][2] * inv, o[r][3] * inv));
+    if (lane == 0)
+      a.lse[static_cast<long long>(head) * a.Tq + cut.q_off + token] =
+          lr == 0.f ? -INFINITY : (mr + log2f(lr) - kBias<T>) * kLn2;
+  }
 }
 
 template <typename T>
 cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttnArgs& a,
                    int num_sms, cudaStream_t st) {
-  // set on every launch: the attribute belongs to the current device
-  const cudaError_t e =
-      cudaFuncSetAttribute(paged_chunk_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem(paged_chunk_kernel<T>, kSmemBytes, done);
   if (e != cudaSuccess) return e;
   note_launches(1);
   return launch_after(paged_chunk_kernel<T>, dim3(std::min(num_sms, kPagedMaxChunkCtas)), kThreads, kSmemBytes, st, tq,
@@ -970,7 +975,7 @@ cudaError_t launch_paged_chunk(const CUtensorMap& tq, const CUtensorMap& tk, con
 cudaError_t launch_paged_join(const PagedAttnArgs& a, bool fp16, int num_sms, cudaStream_t st) {
   const dim3 grid(std::min(num_sms, kPagedMaxChunkCtas), 256 / kJoinRows);
   note_launches(1);
-  return launch_after(fp16 ? paged_join_kernel<__half> : paged_join_kernel<__nv_bfloat16>, grid, 32 * kJoinRows, 0, st,
+  return launch_after(fp16 ? paged_join_kernel<__half> : paged_join_kernel<__nv_bfloat16>, grid, 8 * kJoinRows, 0, st,
                       a);
 }
 
