@@ -181,10 +181,11 @@ __global__ void __launch_bounds__(256) paged_write_kernel(const PagedWriteArgs a
 // take part in every product, so a key costs 512 bytes from HBM and little
 // arithmetic.  The work is a line of units of 64 keys (request, KV head, row
 // tile, unit) cut into equal spans, one per CTA, two CTAs per SM, whatever
-// the lengths; a piece of an item that spans more CTAs leaves unnormalised
-// sums (O, running maximum, sum of exponentials) in the workspace, and the
-// CTA that finishes an item's last piece joins them in the order of the
-// keys.  Each CTA finds its span itself from the lengths, so there is no
+// the lengths; of a long line the last part is cut finer and claimed by the
+// CTAs that are done first, since SMs differ in what they get of HBM.  A
+// piece of an item that goes on in another span leaves unnormalised sums (O,
+// running maximum, sum of exponentials) in the workspace, and the CTA that
+// finishes an item's last piece joins them in the order of the keys.  Each CTA finds its span itself from the lengths, so there is no
 // planning launch.  Within a CTA each of 4 warps owns 16 of a unit's 64 keys,
 // copies them asynchronously into its own ring of shared memory (keys that no
 // row attends are filled with zeros, not read) and keeps its own running
@@ -200,8 +201,9 @@ constexpr int kDecStages = 3;
 constexpr int kSliceBytes = kSlice * 256;     // of K or V
 constexpr int kWarpBytes = kDecStages * 2 * kSliceBytes;
 constexpr int kDecSmem = kDecWarps * kWarpBytes;
+constexpr int kLongShare = 64;                // units per CTA from which on the last part is claimed
 constexpr int kMinUnits = 4;                  // a CTA's share, where there is that much
-constexpr int kSeqTile = 4 * kDecThreads;     // requests whose places on the line are in shared memory at once
+constexpr int kSeqTile = 2 * kDecThreads;     // requests whose places on the line are in shared memory at once
 constexpr int kPartFloats = kRows * (kHeadDim + 2);
 static_assert(kSlice == 16, "a slice is one k16 step of the product with V");
 static_assert(kPartFloats == kPagedPartFloats, "workspace layout");
@@ -269,33 +271,37 @@ __device__ __forceinline__ int row_tiles(const PagedAttnArgs& a, int q_len) {
   return static_cast<int>((static_cast<long long>(q_len) * a.G + kRows - 1) / kRows);
 }
 
-// Units of request i on the line: every (row tile, KV head) has those of the
+// A request as the line has it: every (row tile, KV head) has the units of the
 // whole request's hull, at least one, so that rows without keys are written.
-__device__ __forceinline__ long long line_units(const PagedAttnArgs& a, int i) {
-  const SegInfo sg = paged_seg(a, i);
-  if (sg.q_len == 0 || !few_rows(a, sg.q_len)) return 0;
-  const Units u = units_of(hull(a, sg.q_len, sg.k_len, 0, sg.q_len));
-  return static_cast<long long>(row_tiles(a, sg.q_len)) * a.Hkv * max(u.n0 + u.n1, 1);
-}
+struct Request {
+  int q_off, q_len, k_len;
+  Units un;
+};
 
 struct DecodeShared {
   long long start[kSeqTile + 1];  // first unit of each request of the tile, relative to the tile's
+  Request req[kSeqTile];
   long long sums[kDecWarps];
   float m[kDecWarps][kRows], l[kDecWarps][kRows];
-  int last;
+  int last, next;
 };
 
 // Places of the requests [base, base + kSeqTile) on the line; returns their units.
 __device__ __forceinline__ long long place_requests(const PagedAttnArgs& a, DecodeShared& sh, int base) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  __syncthreads();  // earlier readers of start and sums
-  long long mine = 0;
+  __syncthreads();  // earlier readers
+  long long n0 = 0, mine = 0;
 #pragma unroll 1
-  for (int k = 0; k < 4; ++k) {
-    const int i = base + 4 * tid + k;
-    const long long n = i < a.n_seq ? line_units(a, i) : 0;
-    sh.start[4 * tid + k] = n;
-    mine += n;
+  for (int k = 0; k < 2; ++k) {
+    const int i = base + 2 * tid + k;
+    if (i >= a.n_seq) break;
+    const SegInfo sg = paged_seg(a, i);
+    if (sg.q_len > 0 && few_rows(a, sg.q_len)) {
+      const Units u = units_of(hull(a, sg.q_len, sg.k_len, 0, sg.q_len));
+      mine += static_cast<long long>(row_tiles(a, sg.q_len)) * a.Hkv * max(u.n0 + u.n1, 1);
+      sh.req[2 * tid + k] = Request{sg.q_off, sg.q_len, sg.k_len, u};
+    }
+    if (k == 0) n0 = mine;
   }
   long long inc = mine;
 #pragma unroll
@@ -311,16 +317,31 @@ __device__ __forceinline__ long long place_requests(const PagedAttnArgs& a, Deco
     if (w < warp) at += sh.sums[w];
     total += sh.sums[w];
   }
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const long long n = sh.start[4 * tid + k];
-    sh.start[4 * tid + k] = at;
-    at += n;
-  }
-  if (tid == kDecThreads - 1) sh.start[kSeqTile] = at;
+  sh.start[2 * tid] = at;
+  sh.start[2 * tid + 1] = at + n0;
+  if (tid == kDecThreads - 1) sh.start[kSeqTile] = total;
   __syncthreads();
   return total;
 }
+
+// The line's spans: one per CTA over its first `big` units and, where a CTA's
+// share is long, two more per CTA over the rest.
+struct Spans {
+  long long total, big;
+  int first, rest;
+  __device__ __forceinline__ Spans(long long t, int grid) : total(t) {
+    first = static_cast<int>(min(static_cast<long long>(grid), max(total / kMinUnits, 1LL)));
+    rest = total / first >= kLongShare ? 2 * first : 0;
+    big = rest > 0 ? total - total / 8 : total;
+  }
+  __device__ __forceinline__ long long start(int c) const {
+    return c <= first ? line_div(c * big, first) : big + line_div((c - first) * (total - big), rest);
+  }
+  __device__ __forceinline__ int of(long long p) const {
+    return static_cast<int>(p < big ? line_div((p + 1) * first - 1, big)
+                                    : first + line_div((p - big + 1) * rest - 1, total - big));
+  }
+};
 
 // One warp's share of a piece: units [u0, u0 + n) of an item, keys
 // [16 warp, 16 warp + 16) of each.
@@ -331,16 +352,21 @@ struct WarpState {
 };
 
 template <typename T>
-__device__ __forceinline__ void decode_warp(const PagedAttnArgs& a, uint32_t ring, int seq, const SegInfo& sg,
+__device__ __forceinline__ void decode_warp(const PagedAttnArgs& a, uint32_t ring, int seq, const Request& sg,
                                             const Units& un, int tile, int head, int u0, int n, WarpState<T>& st) {
   using H = Half2<T>;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rows = min(static_cast<int>(min(static_cast<long long>(sg.q_len) * a.G - tile * kRows, 16LL)), kRows);
   const int r_first = tile * kRows, r_last = r_first + rows - 1;
-  const Span hl = hull(a, sg.q_len, sg.k_len, r_first / a.G, r_last / a.G + 1);
   // the two rows of this lane (a row past the last one repeats it, unused)
   const int ra = min(r_first + (lane >> 2), r_last), rb = min(r_first + (lane >> 2) + 8, r_last);
-  const Span sa = paged_span(a, sg.q_len, sg.k_len, ra / a.G), sb = paged_span(a, sg.q_len, sg.k_len, rb / a.G);
+  // lane r finds row r's keys; hl: what some row attends
+  const Span own = paged_span(a, sg.q_len, sg.k_len, min(r_first + (lane & 15), r_last) / a.G);
+  auto row_of = [&](int r) {
+    return Span{__shfl_sync(~0u, own.a0, r), __shfl_sync(~0u, own.b0, r), __shfl_sync(~0u, own.a1, r),
+                __shfl_sync(~0u, own.b1, r)};
+  };
+  const Span sa = row_of(lane >> 2), sb = row_of((lane >> 2) + 8), hl = hull_of(row_of(0), row_of(15));
 
   // offsets of 8-key groups: lane 2 t + g holds group g of unit t of a batch of 16
   const int* table = a.table + seq * a.table_stride;
@@ -361,8 +387,15 @@ __device__ __forceinline__ void decode_warp(const PagedAttnArgs& a, uint32_t rin
     const int j = un.first_key(u0 + batch * 16 + (lane >> 1)) + warp * kSlice + (lane & 1) * 8;
     return page * a.page_stride + j % a.page_size * a.token_stride;
   };
-  const long long lane_off = head * a.head_stride + (lane >> 4) * a.token_stride + (lane & 15) * 8;
-  const T *kc = static_cast<const T*>(a.kc), *vc = static_cast<const T*>(a.vc);
+  // a lane copies 16 bytes of every second key of a group: its first key's
+  // address, the step to the next, the places in the stage
+  const T* const k_lane =
+      static_cast<const T*>(a.kc) + head * a.head_stride + (lane >> 4) * a.token_stride + (lane & 15) * 8;
+  const long long to_v = static_cast<const char*>(a.vc) - static_cast<const char*>(a.kc), step = 2 * a.token_stride;
+  uint32_t place[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    place[i] = (2 * i + (lane >> 4)) * 256 + (((lane & 15) ^ (2 * i + (lane >> 4))) << 4);
   int page_next = entry(0);
   long long off = 0;
   // copies the warp's keys of unit u into stage u % 3
@@ -373,19 +406,19 @@ __device__ __forceinline__ void decode_warp(const PagedAttnArgs& a, uint32_t rin
         page_next = entry((u >> 4) + 1);
       }
       const int j0 = un.first_key(u0 + u) + warp * kSlice;
-      if (span_hits(hl, j0, j0 + kSlice)) {
+      const bool all = span_covers(hl, j0, j0 + kSlice);  // no key to leave out
+      if (all || span_hits(hl, j0, j0 + kSlice)) {
         const uint32_t dst = ring + (u % kDecStages) * 2 * kSliceBytes;
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
           const long long base = __shfl_sync(~0u, off, 2 * (u & 15) + g);
+          const T* src = k_lane + max(base, 0LL);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int key = 8 * g + 2 * i + (lane >> 4);
-            const bool ok = base >= 0 && in_span(hl, j0 + key);
-            const long long at = ok ? base + lane_off + 2 * i * a.token_stride : 0;
-            const uint32_t d = dst + key * 256 + (((lane & 15) ^ (key & 7)) << 4);
-            cp_async_16(d, kc + at, ok ? 16u : 0u);
-            cp_async_16(d + kSliceBytes, vc + at, ok ? 16u : 0u);
+            const uint32_t bytes = base >= 0 && (all || in_span(hl, j0 + 8 * g + 2 * i + (lane >> 4))) ? 16u : 0u;
+            cp_async_16(dst + g * 2048 + place[i], src, bytes);
+            cp_async_16(dst + g * 2048 + place[i] + kSliceBytes, reinterpret_cast<const char*>(src) + to_v, bytes);
+            src += step;
           }
         }
       }
@@ -567,15 +600,24 @@ __device__ __forceinline__ void decode_span(const PagedAttnArgs& a, DecodeShared
     total = min(total + place_requests(a, sh, base), kMost);
   if (!behind) grid_wait();  // counts and status are cleared
   if (total == 0 || total == kMost) return;
-  const long long ctas = min(static_cast<long long>(gridDim.x), max(total / kMinUnits, 1LL));
-  if (blockIdx.x >= ctas) return;
-  auto span_start = [&](long long c) { return line_div(c * total, ctas); };
-  auto cta_of = [&](long long p) { return line_div((p + 1) * ctas - 1, total); };
-  long long pos = span_start(blockIdx.x);
-  const long long end = span_start(blockIdx.x + 1);
+  const Spans sp(total, gridDim.x);
+  if (blockIdx.x >= sp.first) return;
   int base = a.n_seq > kSeqTile ? -kSeqTile : 0;      // requests in sh.start begin at base
   long long tile0 = 0, tile1 = a.n_seq > kSeqTile ? 0 : total;  // their units
-  while (pos < end) {
+  int span = blockIdx.x;
+  long long pos = sp.start(span), end = sp.start(span + 1);
+  for (;;) {
+    if (pos == end) {  // the next span that nobody has; spans are claimed in order, so it lies further on
+      if (sp.rest == 0) return;
+      if (tid == 0) sh.next = sp.first + atomicAdd(a.claims, 1);
+      __syncthreads();
+      span = sh.next;
+      if (span >= sp.first + sp.rest) return;
+      pos = sp.start(span);
+      end = sp.start(span + 1);
+      __syncthreads();  // next is written again only after all have read it
+      if (pos == end) continue;
+    }
     while (pos >= tile1) {
       base += kSeqTile;
       if (base >= a.n_seq) return;  // only if the lengths changed meanwhile
@@ -588,15 +630,16 @@ __device__ __forceinline__ void decode_span(const PagedAttnArgs& a, DecodeShared
       if (sh.start[mid] <= pos - tile0) lo = mid; else hi = mid;
     }
     const int seq = base + lo;
-    const SegInfo sg = paged_seg(a, seq);
-    const Units un = units_of(hull(a, sg.q_len, sg.k_len, 0, sg.q_len));
+    const Request sg = sh.req[lo];
+    const Units un = sg.un;
     const int nu = max(un.n0 + un.n1, 1);
     const long long local = pos - tile0 - sh.start[lo];
     const long long item = line_div(local, nu);
     const int u0 = static_cast<int>(local - item * nu);
     const int n = static_cast<int>(min(static_cast<long long>(nu - u0), end - pos));
     const int tiles = row_tiles(a, sg.q_len);
-    const int head = static_cast<int>(line_div(item, tiles)), tile = static_cast<int>(item - static_cast<long long>(head) * tiles);
+    const int head = static_cast<int>(line_div(item, tiles));
+    const int tile = static_cast<int>(item - static_cast<long long>(head) * tiles);
 
     const int rows = static_cast<int>(min(static_cast<long long>(sg.q_len) * a.G - static_cast<long long>(tile) * kRows,
                                           static_cast<long long>(kRows)));
@@ -641,13 +684,13 @@ __device__ __forceinline__ void decode_span(const PagedAttnArgs& a, DecodeShared
       }
     }
     if (n < nu) {
-      // first and last CTA of the item; a CTA keeps its span's first piece in
-      // slot 2 c and a later, unfinished one in slot 2 c + 1
+      // first and last span of the item; span c's first piece is in slot 2 c
+      // and a later, unfinished one in slot 2 c + 1
       const long long i0 = pos - u0;
-      const int c0 = static_cast<int>(cta_of(i0)), c1 = static_cast<int>(cta_of(i0 + nu - 1));
-      const int late = span_start(c0) < i0 ? 1 : 0;
+      const int c0 = sp.of(i0), c1 = sp.of(i0 + nu - 1);
+      const int late = sp.start(c0) < i0 ? 1 : 0;
       auto slot = [&](int c) { return a.parts + (2 * c + (c == c0 ? late : 0)) * static_cast<long long>(kPartFloats); };
-      float* part = slot(blockIdx.x);
+      float* part = slot(span);
       if (row < rows) {
 #pragma unroll
         for (int k = 0; k < 4; ++k)
@@ -658,12 +701,14 @@ __device__ __forceinline__ void decode_span(const PagedAttnArgs& a, DecodeShared
           __stcg(part + kRows * kHeadDim + kRows + row, l);
         }
       }
-      __threadfence();
       __syncthreads();
-      if (tid == 0) sh.last = atomicAdd(a.arrived + c0, 1) == c1 - c0;
+      if (tid == 0) {  // its fences cover what the barrier has ordered before and after them
+        __threadfence();
+        sh.last = atomicAdd(a.arrived + c0, 1) == c1 - c0;
+        __threadfence();
+      }
       __syncthreads();
       if (sh.last) {
-        __threadfence();
         auto piece = [&](int k) {
           return a.parts + (2 * (c0 + k) + (k == 0 ? late : 0)) * static_cast<long long>(kPartFloats);
         };

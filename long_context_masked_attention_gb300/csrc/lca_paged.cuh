@@ -67,8 +67,7 @@ static __device__ __noinline__ Span paged_span(const PagedAttnArgs& a, int q_len
 // for the first lower bound, which may fall to 0 at the last rows, and for
 // GLOBAL_SLIDING's first rows, whose one interval holds all keys; so the two
 // outer rows give the hull.
-static __device__ __noinline__ Span hull(const PagedAttnArgs& a, int q_len, int k_len, int i0, int i1) {
-  const Span s = paged_span(a, q_len, k_len, i0), t = paged_span(a, q_len, k_len, i1 - 1);
+__device__ __forceinline__ Span hull_of(const Span& s, const Span& t) {
   Span h;
   h.a0 = min(s.a0, t.a0);
   h.b0 = max(max(s.b0, t.b0), h.a0);
@@ -82,6 +81,11 @@ static __device__ __noinline__ Span hull(const PagedAttnArgs& a, int q_len, int 
     }
   }
   return h;
+}
+
+static __device__ __noinline__ Span hull(const PagedAttnArgs& a, int q_len, int k_len, int i0, int i1) {
+  const Span s = paged_span(a, q_len, k_len, i0);
+  return hull_of(s, i1 - 1 > i0 ? paged_span(a, q_len, k_len, i1 - 1) : s);
 }
 
 // Whether the kernel for few rows serves a request with q_len new tokens.
@@ -100,6 +104,16 @@ __device__ __forceinline__ void join_rows(int n, Piece piece, int row0, float& m
   const int lane = threadIdx.x & 31, p = lane % W, stat = kRowsOf * kHeadDim + row0 + lane / W;
   const float m0 = p < n ? __ldcg(piece(p) + stat) : -INFINITY;
   const float l0 = p < n ? __ldcg(piece(p) + stat + kRowsOf) : 0.f;
+  float4 z[P][R];
+  auto load = [&](int k) {
+#pragma unroll
+    for (int u = 0; u < P; ++u) {
+      const float* y = piece(min(k + u, n - 1)) + row0 * kHeadDim;
+#pragma unroll
+      for (int r = 0; r < R; ++r) z[u][r] = __ldcg(reinterpret_cast<const float4*>(y + r * kHeadDim) + lane);
+    }
+  };
+  load(0);
   m = m0;
   for (int k = p + W; k < n; k += W) m = fmaxf(m, __ldcg(piece(k) + stat));
 #pragma unroll
@@ -119,13 +133,7 @@ __device__ __forceinline__ void join_rows(int n, Piece piece, int row0, float& m
     const int here = min(W, n - b);
 #pragma unroll 1
     for (int k = 0; k < here; k += P) {
-      float4 z[P][R];
-#pragma unroll
-      for (int u = 0; u < P; ++u) {
-        const float* y = piece(b + min(k + u, here - 1)) + row0 * kHeadDim;
-#pragma unroll
-        for (int r = 0; r < R; ++r) z[u][r] = __ldcg(reinterpret_cast<const float4*>(y + r * kHeadDim) + lane);
-      }
+      if (b + k > 0) load(b + k);
 #pragma unroll
       for (int u = 0; u < P; ++u)
 #pragma unroll

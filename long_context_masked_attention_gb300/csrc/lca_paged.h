@@ -31,9 +31,10 @@ struct PagedWriteArgs {
 };
 void launch_paged_write(const PagedWriteArgs& a, int num_sms, cudaStream_t st);
 
-// Attention over few rows: at most this many CTAs, each with two workspace
-// slots for unfinished sums (16 rows of O, maximum and sum).
+// Attention over few rows: at most this many CTAs and spans of work, each span
+// with two workspace slots for unfinished sums (16 rows of O, maximum, sum).
 constexpr int kPagedMaxCtas = 512;
+constexpr int kPagedMaxSpans = 3 * kPagedMaxCtas;
 constexpr int kPagedPartFloats = 16 * (kHeadDim + 2);
 // Over many rows: the same with 256 rows.
 constexpr int kPagedMaxChunkCtas = 256;
@@ -58,8 +59,9 @@ struct PagedAttnArgs {
   void* o;
   float* lse;
   int* status;
-  int* arrived;  // [kPagedMaxCtas] pieces finished of the split item that starts in a CTA's span
-  float* parts;  // [kPagedMaxCtas][2][kPagedPartFloats]
+  int* arrived;  // [kPagedMaxSpans] pieces finished of the split item that starts in a span
+  int* claims;   // [1] spans claimed past the CTAs' first ones
+  float* parts;  // [kPagedMaxSpans][2][kPagedPartFloats]
   int Tq, Hq, Hkv, G, n_seq, max_pages, page_size, n_pages;
   float scale_log2;
   int few;  // rows per KV head up to which the kernel for few rows serves a request

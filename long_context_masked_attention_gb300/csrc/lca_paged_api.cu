@@ -67,8 +67,8 @@ PagedLayout paged_layout(const lca_paged_shape* sh, const lca_paged_cache* c) {
     return at;
   };
   L.status = take(16);
-  L.arrived = take(sizeof(int) * kPagedMaxCtas);
-  L.parts = take(sizeof(float) * 2 * kPagedMaxCtas * kPagedPartFloats);
+  L.arrived = take(sizeof(int) * (kPagedMaxSpans + 1));
+  L.parts = take(sizeof(float) * 2 * kPagedMaxSpans * kPagedPartFloats);
   if (many_rows(sh, c)) {
     L.max_blocks = sh->Tq / (2 * tokens_per_tile(sh, c)) + sh->n_seq;
     L.block0 = take(sizeof(int) * (sh->n_seq + 1LL));
@@ -287,6 +287,7 @@ lca_status lca_attn_paged(const void* q, const lca_paged_cache* cache, const int
   a.lse = lse;
   a.status = reinterpret_cast<int*>(ws + L.status);
   a.arrived = reinterpret_cast<int*>(ws + L.arrived);
+  a.claims = a.arrived + kPagedMaxSpans;
   a.parts = reinterpret_cast<float*>(ws + L.parts);
   a.Tq = shape->Tq;
   a.Hq = shape->Hq;

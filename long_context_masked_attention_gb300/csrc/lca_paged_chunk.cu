@@ -225,7 +225,7 @@ __device__ void place_items(const PagedAttnArgs& a) {
 // that the tensors do not hold, and places the items of many rows.
 __global__ void __launch_bounds__(1024) paged_begin_kernel(const __grid_constant__ PagedAttnArgs a, bool many) {
   launch_dependents();
-  for (int i = threadIdx.x; i < kPagedMaxCtas; i += 1024) a.arrived[i] = 0;
+  for (int i = threadIdx.x; i <= kPagedMaxSpans; i += 1024) a.arrived[i] = 0;  // and the claims behind them
   if (many && threadIdx.x < kPagedMaxChunkCtas) a.cuts[threadIdx.x].last = -1;
   if (threadIdx.x < 4) a.status[threadIdx.x] = 0;
   __syncthreads();
