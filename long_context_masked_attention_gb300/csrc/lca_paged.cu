@@ -517,9 +517,9 @@ __device__ __forceinline__ void decode_warp(const PagedAttnArgs& a, uint32_t rin
       for (int t = 0; t < 8; ++t) {
         uint32_t b[4];
         ldsm4t(b, sv + vkey * 256 + (((2 * t + vcol) ^ (vkey & 7)) << 4));
-        bad |= H::not_finite(b[0]) || H::not_finite(b[1]) || H::not_finite(b[2]) || H::not_finite(b[3]);
+        bad |= H::not_finite(b[0]) | H::not_finite(b[1]) | H::not_finite(b[2]) | H::not_finite(b[3]);
       }
-      alone = __any_sync(~0u, bad);
+      alone = __any_sync(~0u, bad & 0x80008000u);
     }
     if (!alone) {
 #pragma unroll

@@ -14,9 +14,9 @@ struct Half2;
 template <>
 struct Half2<__nv_bfloat16> {
   static __device__ __forceinline__ uint32_t pack(float lo, float hi) { return pack_bf16x2(lo, hi); }
-  static __device__ __forceinline__ bool not_finite(uint32_t x) {
-    return (x & 0x7F80u) == 0x7F80u || (x & 0x7F800000u) == 0x7F800000u;
-  }
+  // sign bits set where the exponent is all ones (infinities, NaN); the other
+  // bits say nothing
+  static __device__ __forceinline__ uint32_t not_finite(uint32_t x) { return (x & 0x7FFF7FFFu) + 0x00800080u; }
   static __device__ __forceinline__ float2 unpack(uint32_t x) {
     return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xFFFF0000u));
   }
@@ -28,9 +28,7 @@ struct Half2<__half> {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
   }
-  static __device__ __forceinline__ bool not_finite(uint32_t x) {
-    return (x & 0x7C00u) == 0x7C00u || (x & 0x7C000000u) == 0x7C000000u;
-  }
+  static __device__ __forceinline__ uint32_t not_finite(uint32_t x) { return (x & 0x7FFF7FFFu) + 0x04000400u; }
   static __device__ __forceinline__ float2 unpack(uint32_t x) {
     return __half22float2(*reinterpret_cast<const __half2*>(&x));
   }

@@ -558,105 +558,94 @@ abort:
 }
 
 // ------------------------------------------------------------------ softmax warpgroup
-template <bool kMasked>
-__device__ __forceinline__ float score(uint32_t raw, uint32_t bits, int k) {
-  return (!kMasked || ((bits >> k) & 1u)) ? __uint_as_float(raw) : -INFINITY;
+// A partly masked tile: -inf over the scores whose bit is clear, in TMEM, so
+// that one copy of what follows serves every tile.
+__device__ __forceinline__ void mask_scores(uint32_t tS, const Span& sp, int j0) {
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    const uint32_t bits = span_bits(sp, j0 + 32 * c);
+    uint32_t r[32];
+    tmem_ld32(tS + 32 * c, r);
+    tmem_ld_wait();
+#pragma unroll
+    for (int k = 0; k < 32; ++k) r[k] = ((bits >> k) & 1u) ? r[k] : 0xFF800000u;
+    tmem_st32(tS + 32 * c, r);
+  }
+  tmem_st_wait();
 }
 
-// Maximum of the thread's 128 scores, 64 columns at a time.  Masked tiles run
-// a rolled loop (smaller code), others an unrolled one.
-template <bool kMasked>
-__device__ __forceinline__ void max_half(float (&mp)[8], uint32_t tS, int h, uint32_t m0, uint32_t m1) {
-  uint32_t r0[32], r1[32];
-  tmem_ld32(tS + 64 * h, r0);
-  tmem_ld32(tS + 64 * h + 32, r1);
-  tmem_ld_wait();
-#pragma unroll
-  for (int g = 0; g < 2; ++g)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      mp[j] = fmax3(mp[j], score<kMasked>(r0[16 * g + j], m0, 16 * g + j),
-                    score<kMasked>(r0[16 * g + 8 + j], m0, 16 * g + 8 + j));
-      mp[j] = fmax3(mp[j], score<kMasked>(r1[16 * g + j], m1, 16 * g + j),
-                    score<kMasked>(r1[16 * g + 8 + j], m1, 16 * g + 8 + j));
-    }
-}
-template <bool kMasked>
-__device__ __forceinline__ float row_max(uint32_t tS, const uint32_t (&mb)[4]) {
+// Maximum of the thread's 128 scores, 64 columns at a time: eight independent
+// partial maxima, so that the row is not one dependency chain.
+__device__ __forceinline__ float row_max(uint32_t tS) {
   float mp[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) mp[j] = -INFINITY;
-  if constexpr (kMasked) {
-#pragma unroll 1
-    for (int h = 0; h < 2; ++h) max_half<true>(mp, tS, h, h ? mb[2] : mb[0], h ? mb[3] : mb[1]);
-  } else {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) max_half<false>(mp, tS, h, 0u, 0u);
+  for (int h = 0; h < 2; ++h) {
+    uint32_t r0[32], r1[32];
+    tmem_ld32(tS + 64 * h, r0);
+    tmem_ld32(tS + 64 * h + 32, r1);
+    tmem_ld_wait();
+#pragma unroll
+    for (int g = 0; g < 2; ++g)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        mp[j] = fmax3(mp[j], __uint_as_float(r0[16 * g + j]), __uint_as_float(r0[16 * g + 8 + j]));
+        mp[j] = fmax3(mp[j], __uint_as_float(r1[16 * g + j]), __uint_as_float(r1[16 * g + 8 + j]));
+      }
   }
   return fmax3(fmax3(mp[0], mp[1], mp[2]), fmax3(mp[3], mp[4], mp[5]), fmaxf(mp[6], mp[7]));
 }
 
 // p = 2^(s scale log2(e) - base) of 32 columns, written as pairs over the
 // columns of S read before; the next 32 are requested meanwhile.
-template <typename T, bool kMasked>
+template <typename T>
 __device__ __forceinline__ void exp_chunk(uint32_t tS, int c, const uint32_t (&cur)[32], uint32_t (&nxt)[32],
-                                          uint32_t bits, uint64_t sl2x2, uint64_t nb2, uint64_t (&acc)[4]) {
+                                          uint64_t sl2x2, uint64_t nb2, uint64_t (&acc)[4]) {
   tmem_ld_wait();
   if (c + 1 < 4) tmem_ld32(tS + 32 * (c + 1), nxt);
   uint32_t pk[16];
 #pragma unroll
   for (int k = 0; k < 16; ++k) {
-    const uint64_t sv = f2(score<kMasked>(cur[2 * k], bits, 2 * k), score<kMasked>(cur[2 * k + 1], bits, 2 * k + 1));
-    const uint64_t xx = ffma2(sv, sl2x2, nb2);
+    const uint64_t xx = ffma2(f2(__uint_as_float(cur[2 * k]), __uint_as_float(cur[2 * k + 1])), sl2x2, nb2);
     const uint64_t pp = f2(ex2_approx(f2lo(xx)), ex2_approx(f2hi(xx)));
     acc[k & 3] = fadd2(acc[k & 3], pp);
     pk[k] = Half2<T>::pack(f2lo(pp), f2hi(pp));
   }
   tmem_st16(tS + 16 * c, pk);
 }
-template <typename T, bool kMasked>
-__device__ __forceinline__ float row_exp(uint32_t tS, const uint32_t (&mb)[4], float sl2, float base) {
+template <typename T>
+__device__ __forceinline__ float row_exp(uint32_t tS, float sl2, float base) {
   const uint64_t sl2x2 = f2(sl2, sl2), nb2 = f2(-base, -base);
   uint64_t acc[4] = {0, 0, 0, 0};
   uint32_t ra[32], rb[32];
   tmem_ld32(tS, ra);
-  if constexpr (kMasked) {
-#pragma unroll 1
-    for (int c = 0; c < 4; c += 2) {
-      exp_chunk<T, true>(tS, c, ra, rb, c ? mb[2] : mb[0], sl2x2, nb2, acc);
-      exp_chunk<T, true>(tS, c + 1, rb, ra, c ? mb[3] : mb[1], sl2x2, nb2, acc);
-    }
-  } else {
 #pragma unroll
-    for (int c = 0; c < 4; c += 2) {
-      exp_chunk<T, false>(tS, c, ra, rb, ~0u, sl2x2, nb2, acc);
-      exp_chunk<T, false>(tS, c + 1, rb, ra, ~0u, sl2x2, nb2, acc);
-    }
+  for (int c = 0; c < 4; c += 2) {
+    exp_chunk<T>(tS, c, ra, rb, sl2x2, nb2, acc);
+    exp_chunk<T>(tS, c + 1, rb, ra, sl2x2, nb2, acc);
   }
   const uint64_t t = fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3]));
   return f2lo(t) + f2hi(t);
 }
 
-// Row `key` of the V tile (one thread per key): zeros where no row of the
-// item attends it (nothing of what lies there may meet a p of 0), else
-// whether it holds a value that is not finite.
-template <typename T>
-__device__ __forceinline__ bool clean_v_row(uint8_t* v, int key, bool used) {
-  bool bad = false;
+// Row `key` of the V tile (one thread per key): zeros where no row of the item
+// attends it (nothing of what lies there may meet a p of 0) ...
+__device__ __forceinline__ void clear_v_row(uint8_t* v, int key) {
 #pragma unroll 1
-  for (int c = 0; c < 2; ++c)
+  for (int i = 0; i < 16; ++i)
+    *reinterpret_cast<uint4*>(v + (i >> 3) * kChunkBytes + key * 128 + (((i ^ key) & 7) << 4)) = make_uint4(0, 0, 0, 0);
+}
+// ... or whether it holds a value that is not finite.
+template <typename T>
+__device__ __forceinline__ bool bad_v_row(const uint8_t* v, int key) {
+  uint32_t bad = 0;
 #pragma unroll 4
-    for (int i = 0; i < 8; ++i) {
-      uint4* p = reinterpret_cast<uint4*>(v + c * kChunkBytes + key * 128 + ((i ^ (key & 7)) << 4));
-      if (!used) {
-        *p = make_uint4(0, 0, 0, 0);
-      } else {
-        const uint4 w = *p;
-        bad |= Half2<T>::not_finite(w.x) || Half2<T>::not_finite(w.y) || Half2<T>::not_finite(w.z) ||
-               Half2<T>::not_finite(w.w);
-      }
-    }
-  return bad;
+  for (int i = 0; i < 16; ++i) {
+    const uint4 w = *reinterpret_cast<const uint4*>(v + (i >> 3) * kChunkBytes + key * 128 + (((i ^ key) & 7) << 4));
+    bad |= Half2<T>::not_finite(w.x) | Half2<T>::not_finite(w.y) | Half2<T>::not_finite(w.z) | Half2<T>::not_finite(w.w);
+  }
+  return (bad & 0x80008000u) != 0;
 }
 
 // One row over the piece's keys without products of hidden values, by a whole
@@ -733,11 +722,6 @@ __device__ __forceinline__ void softmax_wg(const PagedAttnArgs& a, int x, uint64
       const bool odd = narrow && (t & 1);  // an odd tile of a narrow item
       const int buf = odd ? 1 : x, full = odd ? 2 : x;
       const uint32_t tS = tbase + tl + 128 * buf;
-      uint32_t mb[4];
-      if (cls != kTileFull) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) mb[c] = span_bits(sp, kt * kTile + 32 * c);
-      }
       if (!waitw(&bar[B_SFULL + full], (odd ? s_odd : s_cnt) & 1, a, 82 + x)) return;
       if (odd) ++s_odd; else ++s_cnt;
       tc_fence_after();
@@ -747,12 +731,15 @@ __device__ __forceinline__ void softmax_wg(const PagedAttnArgs& a, int x, uint64
         const uint32_t vidx = kv_iter + 2 * t + 1;
         if (!waitw(&bar[B_KVFULL + vidx % kStages], (vidx / kStages) & 1, a, 88 + x)) return;
         const int j = kt * kTile + row;
-        if (clean_v_row<T>(sKV + (vidx % kStages) * kTileBytes, row,
-                           (j >= inf.all.a0 && j < inf.all.b0) || (j >= inf.all.a1 && j < inf.all.b1)))
+        uint8_t* v = sKV + (vidx % kStages) * kTileBytes;
+        if (!in_span(inf.all, j))
+          clear_v_row(v, row);
+        else if (!in_span(inf.full[x], j) && bad_v_row<T>(v, row))  // a key of all rows is nobody's hidden one
           *bad_item = it + 1;
         fence_proxy_async_smem();
+        mask_scores(tS, sp, kt * kTile);
       }
-      const float mx = cls == kTileFull ? row_max<false>(tS, mb) : row_max<true>(tS, mb);
+      const float mx = row_max(tS);
       const float m_new = fmaxf(m, mx * sl2);
       float factor = 1.f;
       bool need = false;
@@ -764,7 +751,7 @@ __device__ __forceinline__ void softmax_wg(const PagedAttnArgs& a, int x, uint64
         m = m_new;
       }
       const float base = (m == -INFINITY ? 0.f : m) - kBias<T>;
-      const float sum = cls == kTileFull ? row_exp<T, false>(tS, mb, sl2, base) : row_exp<T, true>(tS, mb, sl2, base);
+      const float sum = row_exp<T>(tS, sl2, base);
       l = l * factor + sum;
       if (__any_sync(0xFFFFFFFFu, need)) {
         // the product before this one must have finished before O is rescaled
