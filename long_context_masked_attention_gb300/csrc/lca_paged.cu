@@ -56,7 +56,8 @@ __device__ __forceinline__ int bisect(const long long* start, int n, long long x
   return lo;
 }
 
-__device__ __forceinline__ int pages_of(long long tokens, int page_size) {
+// tokens and page_size below 2^31
+__device__ __forceinline__ int pages_of(unsigned tokens, unsigned page_size) {
   return static_cast<int>((tokens + page_size - 1) / page_size);
 }
 
@@ -66,6 +67,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedPla
   __shared__ int ctx_s[kPlanThreads];
   const int tid = threadIdx.x;
   const long long room = static_cast<long long>(a.max_pages) * a.page_size;
+  const unsigned page_size = a.page_size;
   const int taken = min(max(a.taken[0], 0), a.n_free);
   long long rows = 0, pages = 0;  // sums before the tile
   int bad = 0;
@@ -79,7 +81,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedPla
       ctx = min(static_cast<long long>(max(c, 0)), room);
       want_len = min(ctx + nw, room);
       wrong = c < 0 || w < 0 || c > room || ctx + nw > room;
-      fresh = max(pages_of(want_len, a.page_size) - pages_of(ctx, a.page_size), 0);
+      fresh = max(pages_of(static_cast<unsigned>(want_len), page_size) - pages_of(static_cast<unsigned>(ctx), page_size), 0);
     }
     long long ir = nw, ip = fresh;
     block_scan2(ir, ip, part);
@@ -107,22 +109,23 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedPla
       const long long r = s * kPlanShare + in;
       if (r < rows || r >= r_end) continue;
       const int i = bisect(row0, n, r);
-      const long long pos = ctx_s[i] + (r - row0[i]);
+      const long long at = ctx_s[i] + (r - row0[i]);
+      const unsigned pos = static_cast<unsigned>(min(at, 0x7FFFFFFFLL));
       int slot = -1;
-      if (pos < room) {
-        const int c = static_cast<int>(pos / a.page_size);
-        const int have = pages_of(ctx_s[i], a.page_size);
+      if (at < room) {  // room < 2^31
+        const unsigned c = pos / page_size;
+        const int have = pages_of(ctx_s[i], page_size);
         int page;
-        if (c < have) {
+        if (static_cast<int>(c) < have) {
           page = a.block_table[(base + i) * a.table_stride + c];
         } else {
-          const long long f = taken + page0[i] + (c - have);
+          const long long f = taken + page0[i] + (static_cast<int>(c) - have);
           page = f < a.n_free ? a.free_pages[f] : -1;
         }
-        if (page >= 0 && page < a.n_pages) slot = page * a.page_size + static_cast<int>(pos % a.page_size);
+        if (page >= 0 && page < a.n_pages) slot = page * a.page_size + static_cast<int>(pos - c * page_size);
       }
       a.slots[r] = slot;
-      a.positions[r] = static_cast<int>(min(pos, 0x7FFFFFFFLL));
+      a.positions[r] = static_cast<int>(pos);
     }
     // and of its fresh pages
     for (long long s = pages / kPlanShare + (me - pages / kPlanShare % step + step) % step; s * kPlanShare < page0[n];
@@ -130,7 +133,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedPla
       const long long f = s * kPlanShare + in;
       if (f < pages || f >= page0[n]) continue;
       const int i = bisect(page0, n, f);
-      const int have = pages_of(ctx_s[i], a.page_size);
+      const int have = pages_of(ctx_s[i], page_size);
       int page = taken + f < a.n_free ? a.free_pages[taken + f] : -1;
       if (page < 0 || page >= a.n_pages) page = -1;
       a.block_table[(base + i) * a.table_stride + have + (f - page0[i])] = page;
@@ -201,7 +204,8 @@ constexpr int kDecStages = 3;
 constexpr int kSliceBytes = kSlice * 256;     // of K or V
 constexpr int kWarpBytes = kDecStages * 2 * kSliceBytes;
 constexpr int kDecSmem = kDecWarps * kWarpBytes;
-constexpr int kLongShare = 64;                // units per CTA from which on the last part is claimed
+constexpr int kLongShare = 160;               // units per CTA from which on the last part is claimed
+constexpr int kItemUnits = 4;                 // what an item costs beside its units, in units
 constexpr int kMinUnits = 4;                  // a CTA's share, where there is that much
 constexpr int kSeqTile = 2 * kDecThreads;     // requests whose places on the line are in shared memory at once
 constexpr int kPartFloats = kRows * (kHeadDim + 2);
@@ -271,8 +275,9 @@ __device__ __forceinline__ int row_tiles(const PagedAttnArgs& a, int q_len) {
   return static_cast<int>((static_cast<long long>(q_len) * a.G + kRows - 1) / kRows);
 }
 
-// A request as the line has it: every (row tile, KV head) has the units of the
-// whole request's hull, at least one, so that rows without keys are written.
+// A request as the line has it: every (row tile, KV head) has kItemUnits and
+// then the units of the whole request's hull, at least one, so that rows
+// without keys are written.
 struct Request {
   int q_off, q_len, k_len;
   Units un;
@@ -298,7 +303,7 @@ __device__ __forceinline__ long long place_requests(const PagedAttnArgs& a, Deco
     const SegInfo sg = paged_seg(a, i);
     if (sg.q_len > 0 && few_rows(a, sg.q_len)) {
       const Units u = units_of(hull(a, sg.q_len, sg.k_len, 0, sg.q_len));
-      mine += static_cast<long long>(row_tiles(a, sg.q_len)) * a.Hkv * max(u.n0 + u.n1, 1);
+      mine += static_cast<long long>(row_tiles(a, sg.q_len)) * a.Hkv * (max(u.n0 + u.n1, 1) + kItemUnits);
       sh.req[2 * tid + k] = Request{sg.q_off, sg.q_len, sg.k_len, u};
     }
     if (k == 0) n0 = mine;
@@ -634,9 +639,14 @@ __device__ __forceinline__ void decode_span(const PagedAttnArgs& a, DecodeShared
     const Units un = sg.un;
     const int nu = max(un.n0 + un.n1, 1);
     const long long local = pos - tile0 - sh.start[lo];
-    const long long item = line_div(local, nu);
-    const int u0 = static_cast<int>(local - item * nu);
-    const int n = static_cast<int>(min(static_cast<long long>(nu - u0), end - pos));
+    const long long item = line_div(local, nu + kItemUnits);
+    // the span has the item's places [from, to), of which the first kItemUnits hold no keys
+    const int from = static_cast<int>(local - item * (nu + kItemUnits));
+    const int to = from + static_cast<int>(min(static_cast<long long>(nu + kItemUnits - from), end - pos));
+    const long long i0 = pos - from + kItemUnits;  // the item's first unit
+    pos += to - from;
+    const int u0 = max(from - kItemUnits, 0), n = to - kItemUnits - u0;
+    if (n <= 0) continue;
     const int tiles = row_tiles(a, sg.q_len);
     const int head = static_cast<int>(line_div(item, tiles));
     const int tile = static_cast<int>(item - static_cast<long long>(head) * tiles);
@@ -686,9 +696,8 @@ __device__ __forceinline__ void decode_span(const PagedAttnArgs& a, DecodeShared
     if (n < nu) {
       // first and last span of the item; span c's first piece is in slot 2 c
       // and a later, unfinished one in slot 2 c + 1
-      const long long i0 = pos - u0;
       const int c0 = sp.of(i0), c1 = sp.of(i0 + nu - 1);
-      const int late = sp.start(c0) < i0 ? 1 : 0;
+      const int late = sp.start(c0) < i0 - kItemUnits ? 1 : 0;
       auto slot = [&](int c) { return a.parts + (2 * c + (c == c0 ? late : 0)) * static_cast<long long>(kPartFloats); };
       float* part = slot(span);
       if (row < rows) {
@@ -745,7 +754,6 @@ __device__ __forceinline__ void decode_span(const PagedAttnArgs& a, DecodeShared
         a.lse[static_cast<long long>(h) * a.Tq + token] =
             l == 0.f ? -INFINITY : (m + log2f(l) - kBias<T>) * 0.6931471805599453f;
     }
-    pos += n;
     __syncthreads();  // the ring is refilled
   }
 }
@@ -768,9 +776,9 @@ __global__ void __launch_bounds__(kDecThreads, 2)
 }  // namespace
 
 void launch_paged_plan(const PagedPlanArgs& a, int num_sms, cudaStream_t st) {
-  // a block per 4096 rows: below that, one block's own writes cost less than
-  // the sums each further block would repeat
-  const int grid = std::max(1, std::min(num_sms, static_cast<int>((static_cast<long long>(a.n_rows) + 4095) / 4096)));
+  // a block per 1024 rows, one each for its threads: the sums are the same
+  // work for one block or for all of them at once
+  const int grid = std::max(1, std::min(num_sms, static_cast<int>((static_cast<long long>(a.n_rows) + 1023) / 1024)));
   note_launches(1);
   paged_plan_kernel<<<grid, kPlanThreads, 0, st>>>(a);
 }
