@@ -344,7 +344,9 @@ typedef struct {
  * apart, 16-byte aligned.  block_table: int32, device.  q_start: int32
  * [n_seq + 1], k_len: int32 [n_seq], device.  o: [Tq][Hq][d] dense, the
  * cache's dtype, 16-byte aligned; lse: float [Hq][Tq], natural log, as
- * lca_attn_fwd writes it and lca_attn_merge reads it.  Rows that attend
+ * lca_attn_fwd writes it and lca_attn_merge reads it.  o, lse and the
+ * workspace must not overlap one another or an input (LCA_ERR_INVALID_ARG;
+ * the cache counts from its first to its last element).  Rows that attend
  * nothing, and rows outside every request, get o = 0, lse = -inf.
  * Nothing that lies in the cache behind a request's last key, or in keys
  * that the mask hides from all of its new tokens, reaches a result (infinities

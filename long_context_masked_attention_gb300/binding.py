@@ -740,7 +740,8 @@ def attn_paged(q, k_cache, v_cache, block_table, q_start, k_len, mask, scale=0.0
         lp = _ptr(lse, "lse", torch.float32, lsize, dev)
     if workspace is None:
         # the size depends on these alone
-        key = (shape.Tq, shape.Hq, n_seq, shape.max_q_len, cache.Hkv, cache.n_pages > 0)
+        key = (shape.Tq, shape.Hq, n_seq, shape.max_q_len, cache.Hkv, min(cache.n_pages, 2), cache.page_stride,
+               cache.token_stride, cache.head_stride)
         need = _SIZES.get(key)
         if need is None:
             if len(_SIZES) >= 4096:

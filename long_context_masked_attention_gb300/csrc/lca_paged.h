@@ -68,6 +68,7 @@ struct PagedAttnArgs {
   // the kernel for many rows
   int tpt;       // tokens of a 128-row sub-tile: floor(128 / G)
   int box_rows;  // keys of one TMA box: gcd(page_size, 128)
+  bool head_first;  // the K and V maps' axes: 64 values, head, token, page; else token before head
   int max_blocks;
   int* block0;        // [n_seq + 1] row blocks before each request
   long long* line;    // [max_blocks + 1] key tiles before each row block

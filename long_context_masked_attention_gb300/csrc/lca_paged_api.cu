@@ -42,13 +42,31 @@ bool cache_memory(const lca_paged_cache* c) {
   return c->k && c->v && aligned16(c->k) && aligned16(c->v) && device_input(c->k) && device_input(c->v);
 }
 
+// The cache's strides as a tensor map has them, in ascending order: token and
+// head as they come, the page last.  The stride of an axis of length one moves
+// nothing and is taken as its neighbour's.
+struct MapStrides {
+  int64_t token, head, page;
+  bool head_first, ordered;
+};
+MapStrides map_strides(const lca_paged_cache* c) {
+  MapStrides m;
+  m.token = c->token_stride;
+  m.head = c->Hkv > 1 ? c->head_stride : m.token;
+  m.head_first = m.head < m.token;
+  const int64_t most = m.head_first ? m.token : m.head;
+  m.page = c->n_pages > 1 ? c->page_stride : most;
+  m.ordered = m.page >= most;
+  return m;
+}
+
 // Whether the kernel for many rows takes part: some request may have more
 // rows per KV head than the other one's tile, a token's heads fit a tile, and
-// there is a cache to map.
+// there is a cache to map, its pages further apart than its tokens and heads.
 bool many_rows(const lca_paged_shape* sh, const lca_paged_cache* c) {
   const long long G = sh->Hq / c->Hkv;
   const long long most = sh->max_q_len > 0 && sh->max_q_len < sh->Tq ? sh->max_q_len : sh->Tq;
-  return most * G > kPagedFewRows && G <= kTile && c->n_pages > 0;
+  return most * G > kPagedFewRows && G <= kTile && c->n_pages > 0 && map_strides(c).ordered;
 }
 
 int tokens_per_tile(const lca_paged_shape* sh, const lca_paged_cache* c) { return kTile / (sh->Hq / c->Hkv); }
@@ -155,12 +173,15 @@ bool encode(CUtensorMap* m, const void* p, int dtype, int rank, const cuuint64_t
 }
 
 bool cache_map(CUtensorMap* m, const void* p, const lca_paged_cache* c, int box_rows) {
-  const cuuint64_t dims[4] = {kHeadDim, static_cast<cuuint64_t>(c->page_size), static_cast<cuuint64_t>(c->Hkv),
-                              static_cast<cuuint64_t>(c->n_pages)};
-  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(c->token_stride) * 2,
-                                 static_cast<cuuint64_t>(c->head_stride) * 2,
-                                 static_cast<cuuint64_t>(c->page_stride) * 2};
-  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box_rows), 1, 1};
+  const MapStrides st = map_strides(c);
+  const bool hf = st.head_first;
+  const cuuint64_t tokens = static_cast<cuuint64_t>(c->page_size), heads = static_cast<cuuint64_t>(c->Hkv);
+  const cuuint64_t dims[4] = {kHeadDim, hf ? heads : tokens, hf ? tokens : heads, static_cast<cuuint64_t>(c->n_pages)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(hf ? st.head : st.token) * 2,
+                                 static_cast<cuuint64_t>(hf ? st.token : st.head) * 2,
+                                 static_cast<cuuint64_t>(st.page) * 2};
+  const cuuint32_t rows = static_cast<cuuint32_t>(box_rows);
+  const cuuint32_t box[4] = {64, hf ? 1 : rows, hf ? rows : 1, 1};
   return encode(m, p, c->dtype, 4, dims, strides, box);
 }
 
@@ -269,6 +290,28 @@ lca_status lca_attn_paged(const void* q, const lca_paged_cache* cache, const int
         !device_input(lse))
       return LCA_ERR_INVALID_ARG;
   }
+  if (shape->Tq > 0) {
+    const long long rows = shape->Tq, heads = shape->Hq;
+    const long long extent =
+        cache->n_pages == 0 ? 0
+                            : ((cache->n_pages - 1) * cache->page_stride + (cache->page_size - 1) * cache->token_stride +
+                               (cache->Hkv - 1) * cache->head_stride + kHeadDim) * 2;
+    const struct {
+      const void* p;
+      long long bytes;
+    } t[9] = {{o, rows * heads * kHeadDim * 2},
+              {lse, rows * heads * 4},
+              {workspace, static_cast<long long>(L.total)},
+              {q, ((rows - 1) * shape->q_stride + heads * kHeadDim) * 2},
+              {cache->k, extent},
+              {cache->v, extent},
+              {block_table, 4 * n_table},
+              {q_start, 4 * (shape->n_seq + 1LL)},
+              {k_len, 4LL * shape->n_seq}};
+    for (int i = 0; i < 3; ++i)  // the first three are written
+      for (int j = i + 1; j < 9; ++j)
+        if (overlap(t[i].p, t[i].bytes, t[j].p, t[j].bytes)) return LCA_ERR_INVALID_ARG;
+  }
   const int sms = num_sms();
   if (sms <= 0) return LCA_ERR_CUDA;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -307,6 +350,7 @@ lca_status lca_attn_paged(const void* q, const lca_paged_cache* cache, const int
     a.tpt = tokens_per_tile(shape, cache);
     a.box_rows = kTile;
     while (cache->page_size % a.box_rows != 0) a.box_rows /= 2;
+    a.head_first = map_strides(cache).head_first;
     a.max_blocks = L.max_blocks;
     a.block0 = reinterpret_cast<int*>(ws + L.block0);
     a.line = reinterpret_cast<long long*>(ws + L.line);

@@ -437,7 +437,7 @@ __device__ __forceinline__ void producer(const PagedAttnArgs& a, const CUtensorM
         __syncwarp();
         if (half < 2)
           tma_load_4d(sKV + stg * kTileBytes + half * kChunkBytes + box * a.box_rows * 128, which ? tv : tk,
-                      &bar[B_KVFULL + stg], half * 64, y, inf.head, page);
+                      &bar[B_KVFULL + stg], half * 64, a.head_first ? inf.head : y, a.head_first ? y : inf.head, page);
         issued = idx + 1;
       }
     }
@@ -648,40 +648,81 @@ __device__ __forceinline__ bool bad_v_row(const uint8_t* v, int key) {
   return (bad & 0x80008000u) != 0;
 }
 
-// One row over the piece's keys without products of hidden values, by a whole
-// warp: lane k has values 4 k .. 4 k + 3.  For the rare rows that share a
-// partly masked tile with a value that is not finite.
+// The rows of a warp, one per lane, over the piece's keys without products of
+// hidden values: for the rare items that have a value that is not finite among
+// keys which only some rows attend (0 times it would be NaN).  o: the row's
+// sums, in local memory; all lanes take part.  About a microsecond per key,
+// well inside the limit of what the CTA's other warps wait meanwhile.
 template <typename T>
-__device__ __noinline__ void row_alone(const PagedAttnArgs& a, const Item& inf, int token, int head, float& m_out,
-                                       float& l_out, float (&o)[4]) {
-  const int lane = threadIdx.x & 31;
-  const Span sp = paged_span(a, inf.q_len, inf.k_len, token);
-  const T* q = static_cast<const T*>(a.q) + (inf.q_off + token) * a.q_stride + head * kHeadDim + 4 * lane;
+__device__ __noinline__ void rows_alone(const PagedAttnArgs& a, const Item& inf, Span sp, int row, int head, float* o,
+                                        float& m_out, float& l_out) {
+  const uint4* q = reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + row * a.q_stride + head * kHeadDim);
   const int* table = a.table + inf.seq * a.table_stride;
   float m = -INFINITY, l = 0.f;
-  o[0] = o[1] = o[2] = o[3] = 0.f;
+#pragma unroll 1
+  for (int k = 0; k < kHeadDim; ++k) o[k] = 0.f;
+#pragma unroll 1
   for (int t = 0; t < inf.n; ++t)
+#pragma unroll 1
     for (int j = inf.tile(t) * kTile, e = j + kTile; j < e; ++j) {
-      if (!((j >= sp.a0 && j < sp.b0) || (j >= sp.a1 && j < sp.b1))) continue;
+      const bool mine = in_span(sp, j);
+      if (!__any_sync(0xFFFFFFFFu, mine)) continue;
       const int page = __ldg(table + j / a.page_size);
       const bool ok = page >= 0 && page < a.n_pages;
-      const long long at = (ok ? page : 0) * a.page_stride + j % a.page_size * a.token_stride +
-                           inf.head * a.head_stride + 4 * lane;
-      float s = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
-      if (ok)
-        for (int k = 0; k < 4; ++k) {
-          s += static_cast<float>(q[k]) * static_cast<float>(static_cast<const T*>(a.kc)[at + k]);
-          v[k] = static_cast<float>(static_cast<const T*>(a.vc)[at + k]);
+      const long long at =
+          (ok ? page : 0) * a.page_stride + j % a.page_size * a.token_stride + inf.head * a.head_stride;
+      const uint4* k4 = reinterpret_cast<const uint4*>(static_cast<const T*>(a.kc) + at);
+      const uint4* v4 = reinterpret_cast<const uint4*>(static_cast<const T*>(a.vc) + at);
+      auto pair = [](const uint4& w, int i) { return Half2<T>::unpack(i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w); };
+      float s = 0.f;
+#pragma unroll 2
+      for (int c = 0; c < 16; ++c) {
+        const uint4 x = __ldg(q + c), y = ok ? k4[c] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 u = pair(x, i), w = pair(y, i);
+          s = fmaf(u.x, w.x, fmaf(u.y, w.y, s));
         }
-      for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(~0u, s, d);
-      s *= a.scale_log2;
-      const float mn = fmaxf(m, s), f = ex2_approx(m - mn), p = ex2_approx(s - mn + kBias<T>);
-      l = (l == 0.f ? 0.f : l * f) + p;
-      for (int k = 0; k < 4; ++k) o[k] = (m == -INFINITY ? 0.f : o[k] * f) + p * v[k];
+      }
+      const float mn = mine ? fmaxf(m, s * a.scale_log2) : m;
+      const float f = m == -INFINITY ? 0.f : ex2_approx(m - mn);
+      const float p = mine ? ex2_approx(s * a.scale_log2 - mn + kBias<T>) : 0.f;
+      l = (m == -INFINITY ? 0.f : l * f) + p;
+#pragma unroll 2
+      for (int c = 0; c < 16; ++c) {
+        const uint4 y = ok ? v4[c] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 w = pair(y, i);
+          float* oo = o + 8 * c + 2 * i;
+          oo[0] = m == -INFINITY ? 0.f : oo[0] * f;
+          oo[1] = m == -INFINITY ? 0.f : oo[1] * f;
+          if (mine) {
+            oo[0] = fmaf(p, w.x, oo[0]);
+            oo[1] = fmaf(p, w.y, oo[1]);
+          }
+        }
+      }
       m = mn;
     }
   m_out = m;
   l_out = l;
+}
+
+template <typename T>
+__device__ __noinline__ void write_alone(const PagedAttnArgs& a, const Item& inf, int x, int row, bool valid, int token,
+                                         int head, Span sp, T* orow, float* part, float& m, float& l) {
+  float o[kHeadDim];
+  rows_alone<T>(a, inf, valid ? sp : Span{0, 0, 0, 0}, inf.q_off + (valid ? token : 0), valid ? head : 0, o, m, l);
+  if (!valid) return;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll 1
+  for (int k = 0; k < kHeadDim; k += 2) {
+    if (part)
+      *reinterpret_cast<float2*>(part + (x * 128 + row) * kHeadDim + k) = make_float2(o[k], o[k + 1]);
+    else
+      *reinterpret_cast<uint32_t*>(orow + k) = Half2<T>::pack(o[k] * inv, o[k + 1] * inv);
+  }
 }
 
 template <typename T>
@@ -785,24 +826,7 @@ __device__ __forceinline__ void softmax_wg(const PagedAttnArgs& a, int x, uint64
     T* orow = static_cast<T*>(a.o) + (static_cast<long long>(inf.q_off + (valid ? token : 0)) * a.Hq + head) * kHeadDim;
     float* part = inf.part < 0 ? nullptr : a.chunk_parts + inf.part * static_cast<long long>(kPagedChunkPartFloats);
     if (any && *bad_item == it + 1) {
-      // row by row, the warp together
-#pragma unroll 1
-      for (int r = 0; r < 32; ++r) {
-        const int tok = __shfl_sync(~0u, token, r), h = __shfl_sync(~0u, head, r);
-        if (!__shfl_sync(~0u, valid ? 1 : 0, r)) continue;
-        float mr, lr, o[4];
-        row_alone<T>(a, inf, tok, h, mr, lr, o);
-        if (part) {
-          *reinterpret_cast<float4*>(part + (x * 128 + wq * 32 + r) * kHeadDim + 4 * lane) =
-              make_float4(o[0], o[1], o[2], o[3]);
-        } else {
-          const float inv = lr == 0.f ? 0.f : 1.f / lr;
-          T* dst = static_cast<T*>(a.o) + (static_cast<long long>(inf.q_off + tok) * a.Hq + h) * kHeadDim + 4 * lane;
-          *reinterpret_cast<uint2*>(dst) =
-              make_uint2(Half2<T>::pack(o[0] * inv, o[1] * inv), Half2<T>::pack(o[2] * inv, o[3] * inv));
-        }
-        if (lane == r) m = mr, l = lr;
-      }
+      write_alone<T>(a, inf, x, row, valid, token, head, sp, orow, part, m, l);
     } else if (any) {
       const float inv = part ? 1.f : l == 0.f ? 0.f : 1.f / l;
 #pragma unroll 1
