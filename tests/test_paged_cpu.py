@@ -170,3 +170,45 @@ def test_binding_turns_away_unsuitable_tensors():
     for bad in (tab.t(), tab[:, ::2], tab.expand(2, 9)[:1].expand(2, 9), tab.long()):
         with pytest.raises(ValueError):
             B._table(bad, 2, meta)
+
+
+@pytest.mark.parametrize("current", [0, 1])
+def test_calls_run_on_the_tensors_device(monkeypatch, current):
+    """The library is called with the tensors' device current and that
+    device's stream, whichever device the caller had selected."""
+    log = []
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: current, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 1000 + i, raising=False)
+
+    class On:
+        def __init__(self, device):
+            self.device = device
+
+        def __enter__(self):
+            log.append(("enter", self.device.index))
+
+        def __exit__(self, *a):
+            log.append(("exit", self.device.index))
+
+    monkeypatch.setattr(torch.cuda, "device", On)
+
+    def fn(*args):
+        log.append(args)
+        return 0
+
+    B._call(fn, "f", torch.device("cuda", 1), None, 5, 6)
+    assert log == ([(5, 6, 1001)] if current == 1 else [("enter", 1), (5, 6, 1001), ("exit", 1)])
+    with pytest.raises(lib.LcaError, match="INVALID"):
+        B._call(lambda *a: 1, "f", torch.device("cuda", 1), None)
+
+
+def test_workspace_sizes_of_shapes_that_need_no_tiles_of_many_rows(L):
+    """One new token per request, a group too wide for a tile, no pages, or
+    pages closer together than their tokens: no room for sums of many rows."""
+    many = size(L, shape(Tq=40), cache())[1]
+    few = size(L, shape(Tq=40, max_q_len=1), cache())[1]
+    assert few < many
+    assert size(L, shape(Tq=40, Hq=512, q_stride=512 * 128), cache())[1] == few
+    assert size(L, shape(Tq=40), cache(n_pages=0))[1] == few
+    assert size(L, shape(Tq=40), cache(page_stride=128, token_stride=4096))[1] == few
+    assert size(L, shape(Tq=40), cache(n_pages=1, page_stride=128, token_stride=4096))[1] == many

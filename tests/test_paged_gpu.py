@@ -320,6 +320,140 @@ def cut(p, rows):
     return p
 
 
+def test_infinities_among_a_long_contexts_last_keys(lca):
+    """The rows before such a token are found again without it, in time."""
+    for lens, bad in (([(60000, 40)], 60030), ([(40000, 300)], 40100)):
+        p = make(lens, 64, 4, 1, CAUSAL, "fp16", seed=16, device="cuda")
+        page, at = int(p.table[0, bad // 64]), bad % 64
+        p.vc[page, at, 0, 7] = float("inf")
+        o, lse, st = attend(lca, p)
+        assert st == (0, 0)
+        first = bad - lens[0][0]
+        p.prob.segments[0].q_len = first
+        check(o[:first], lse[:, :first], cut(p, first))
+        assert bool((o[first:, :, 7] == float("inf")).all()) and bool(o[first:, :, :7].isfinite().all())
+
+
+@pytest.mark.parametrize("new", [1, 3, 90])
+def test_pages_between_sinks_and_window_may_be_gone(lca, new):
+    """GLOBAL_SLIDING over a long context: the table has no entry, and the
+    cache NaN, between the first keys and the window of the first new token."""
+    mask = MaskSpec("GLOBAL_SLIDING", window_left=200, window_right=0, num_global=20)
+    p = make([(3000, new), (900, new)], 16, 8, 2, mask, seed=new, device="cuda")
+    ref = reference(p)
+    for i, ctx in enumerate((3000, 900)):
+        for e in range(2, (ctx - 200) // 16):
+            page = int(p.table[i, e])
+            p.kc[page] = float("nan")
+            p.vc[page] = float("nan")
+            p.table[i, e] = -1
+    o, lse, st = attend(lca, p)
+    assert st == (0, 0)
+    check(o, lse, p, ref)
+
+
+@pytest.mark.parametrize("Hq", [64, 100, 128, 136, 260])
+def test_many_heads_of_one_group(lca, Hq):
+    """More heads than rows of a tile among them."""
+    p = make([(200, 1), (0, 5), (130, 3)], 16, Hq, 1, CAUSAL, seed=Hq, device="cuda")
+    o, lse, st = attend(lca, p)
+    check(o, lse, p)
+    assert st == (0, 0)
+
+
+def test_many_requests(lca):
+    """More requests than are placed at once, some without new tokens, some
+    with no keys, short and long ones mixed."""
+    rng = np.random.default_rng(5)
+    lens = [(int(rng.integers(0, 260)), int(rng.choice([0, 1, 1, 1, 2, 5, 40]))) for _ in range(1100)]
+    p = make(lens, 8, 4, 1, CAUSAL, "fp16", pad=9, seed=17, device="cuda")
+    ref = reference(p)
+    for hint in (0, 40):
+        o, lse, st = attend(lca, p, max_q_len=hint)
+        check(o, lse, p, ref)
+        assert st == (0, 0)
+
+
+def test_long_lines_are_claimed(lca):
+    """Enough keys that the last part of the work is claimed by the CTAs that
+    are done first; the results do not depend on who was."""
+    import torch
+
+    p = make([(90000, 1), (70000, 1), (52000, 1), (3, 1)], 128, 16, 16, CAUSAL, seed=18, device="cuda")
+    o, lse, st = attend(lca, p)
+    assert st == (0, 0)
+    check(o, lse, p)
+    for _ in range(4):
+        o2, lse2, _ = attend(lca, p)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+def test_pages_far_apart(lca):
+    """Pages more than 2^31 elements apart, read and written."""
+    import torch
+
+    far = (1 << 31) + 64
+    buf = torch.empty(3 * far + 4096, dtype=torch.bfloat16, device="cuda")
+    for new in (1, 60):
+        p = make([(20, new)], 32, 8, 2, CAUSAL, seed=new, device="cuda")
+        n = p.kc.shape[0]
+        assert n <= 6
+        keep = [int(x) for x in p.table[0] if x >= 0]
+        view = lambda at: buf.as_strided((3, 32, 2, 128), (far, 256, 128, 1), at)  # noqa: E731
+        kc, vc = view(0), view(64 * 256)
+        table = torch.tensor([[2, 0, 1]], dtype=torch.int32, device="cuda")
+        for i, page in enumerate(keep):
+            kc[table[0, i]] = p.kc[page]
+            vc[table[0, i]] = p.vc[page]
+        p.kc, p.vc, p.table = kc, vc, table
+        o, lse, st = attend(lca, p)
+        assert st == (0, 0)
+        check(o, lse, p)
+        # the new tokens' rows again through the write
+        slots = torch.tensor([int(table[0, j // 32]) * 32 + j % 32 for j in range(20, 20 + new)], dtype=torch.int32)
+        before = [kc[int(s) // 32, int(s) % 32].clone() for s in slots]
+        for s in slots:
+            kc[int(s) // 32, int(s) % 32] = 0
+        lca.paged_write(p.k[20:].cuda(), p.v[20:].cuda(), kc, vc, slots.cuda())
+        assert all(torch.equal(b, kc[int(s) // 32, int(s) % 32]) for b, s in zip(before, slots))
+
+
+@pytest.mark.parametrize("order", [(0, 1, 2), (1, 0, 2), (2, 0, 1), (1, 2, 0), (0, 2, 1), (2, 1, 0)], ids=str)
+def test_any_order_of_the_axes(lca, order):
+    """The cache's axes (page, token, head) in every order in memory."""
+    p = make([(40, 1), (10, 90), (70, 4)], 24, 6, 2, CAUSAL, "fp16", seed=3, device="cuda")
+    back = [order.index(i) for i in range(3)] + [3]
+    p.kc, p.vc = (x.permute(*order, 3).contiguous().permute(*back) for x in (p.kc, p.vc))
+    o, lse, st = attend(lca, p)
+    check(o, lse, p)
+    assert st == (0, 0)
+
+
+def test_narrow_items_among_wide_ones_repeat(lca):
+    """Items of one sub-tile between items of two, many times over."""
+    import torch
+
+    p = make(CHUNKS * 3, 32, 8, 1, CAUSAL, "fp16", seed=8, device="cuda")
+    ref = reference(p)
+    a = attend(lca, p)
+    check(a[0], a[1], p, ref)
+    for _ in range(60):
+        b = attend(lca, p)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_overlapping_outputs_are_refused(lca):
+    import torch
+
+    p = make([(40, 3)], 16, 8, 8, CAUSAL, seed=2, device="cuda")
+    call = lambda **kw: lca.attn_paged(p.q, p.kc, p.vc, p.table, p.q_start, p.k_len, CAUSAL, **kw)  # noqa: E731
+    o, lse = call()
+    flat = torch.empty(4096, dtype=torch.float32, device="cuda")
+    for kw in (dict(out=p.q), dict(out=p.kc[0, :3]), dict(out=flat[:1536].view(torch.bfloat16).view(3, 8, 128), lse=flat[1000:1024].view(8, 3))):
+        with pytest.raises(lca.LcaError, match="INVALID"):
+            call(**kw)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 def test_large_scores_and_an_explicit_scale(lca, dtype):
     """Scores of some hundreds (one key takes all), and a scale of the user's own."""
