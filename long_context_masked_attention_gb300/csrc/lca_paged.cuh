@@ -159,8 +159,12 @@ __device__ __forceinline__ void join_rows(int n, Piece piece, int row0, float& m
   for (int d = W / 2; d > 0; d >>= 1) l += __shfl_xor_sync(~0u, l, d);
 }
 
-// a / b of the line's positions, once in code
-static __device__ __noinline__ long long line_div(long long a, long long b) { return a / b; }
+// a / b of the line's positions (not negative), once in code; 32 bits are
+// enough for most calls and a fraction of the work
+static __device__ __noinline__ long long line_div(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
 
 // Inclusive sum over a block of 1024 threads; `total` gets the whole sum.
 // part: shared memory, free again when the call returns on every thread.

@@ -794,10 +794,16 @@ __device__ __forceinline__ void softmax_wg(const PagedAttnArgs& a, int x, uint64
       const float base = (m == -INFINITY ? 0.f : m) - kBias<T>;
       const float sum = row_exp<T>(tS, sl2, base);
       l = l * factor + sum;
-      if (__any_sync(0xFFFFFFFFu, need)) {
-        // the product before this one must have finished before O is rescaled
+      const bool rescale = __any_sync(0xFFFFFFFFu, need);
+      // The product before this one must have finished before O is rescaled.
+      // In a narrow item nothing else tells that it has (the next scores do
+      // not come after it), and it must be known before another one starts: a
+      // wait by parity cannot tell the last phase from the last but two.
+      if (any && (rescale || narrow)) {
         if (!waitw(&bar[B_OFULL + x], (o_cnt - 1) & 1, a, 84 + x)) return;
         tc_fence_after();
+      }
+      if (rescale) {
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
           uint32_t r[32];
@@ -817,9 +823,6 @@ __device__ __forceinline__ void softmax_wg(const PagedAttnArgs& a, int x, uint64
     }
     kv_iter += 2 * n;
     if (any) {
-      // a narrow item's last two products may both be under way, and a wait
-      // for the last alone would take the one before the last but one for it
-      if (narrow && n >= 2 && !waitw(&bar[B_OFULL + x], o_cnt & 1, a, 86 + x)) return;
       if (!waitw(&bar[B_OFULL + x], (o_cnt - 1) & 1, a, 86 + x)) return;
       tc_fence_after();
     }

@@ -442,6 +442,26 @@ def test_narrow_items_among_wide_ones_repeat(lca):
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+def test_narrow_items_never_wait_in_vain(lca):
+    """Many calls of nothing but narrow items with long and short pieces: no
+    wait runs out (a wait that could miss its phase did so once in some
+    thousand items)."""
+    import torch
+
+    p = make([(int(c), 5) for c in np.linspace(200, 5000, 24)], 32, 16, 2, CAUSAL, seed=21, device="cuda")
+    need = lca.attn_paged_workspace_size(p.q, p.kc, p.vc, p.table, CAUSAL)
+    first = None
+    for _ in range(6):
+        spaces = [torch.empty(need, dtype=torch.uint8, device="cuda") for _ in range(50)]
+        outs = [lca.attn_paged(p.q, p.kc, p.vc, p.table, p.q_start, p.k_len, CAUSAL, workspace=w) for w in spaces]
+        torch.cuda.synchronize()
+        first = first or outs[0]
+        for w, (o, lse) in zip(spaces, outs):
+            assert lca.read_status(w) == (0, 0)
+            assert torch.equal(o, first[0]) and torch.equal(lse, first[1])
+    check(first[0], first[1], p)
+
+
 def test_overlapping_outputs_are_refused(lca):
     import torch
 
