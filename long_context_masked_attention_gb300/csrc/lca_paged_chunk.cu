@@ -318,6 +318,10 @@ __device__ __forceinline__ void scheduler(const PagedAttnArgs& a, const Line& ln
         p.block = 0;
         if (++p.head == a.Hkv) {
           p.head = 0;
+          if (p.seq + 1 >= a.n_seq) {  // only if the lengths changed meanwhile
+            pos = end;
+            continue;
+          }
           do {
             ++p.seq;
             b0 = b1;
