@@ -615,7 +615,7 @@ def paged_plan(ctx_len, new_len, free_pages, taken, block_table, page_size, n_pa
     max_pages] int32; n_rows: rows of the packed batch, those behind the last
     request get slot -1.  state holds {free pages used so far, pages missing,
     requests with unusable lengths, new tokens}; state[:1] is the next call's
-    `taken`.  Outputs that are not given are parts of one new tensor."""
+    `taken`."""
     import torch
 
     for name, t in (("ctx_len", ctx_len), ("free_pages", free_pages)):
@@ -628,18 +628,16 @@ def paged_plan(ctx_len, new_len, free_pages, taken, block_table, page_size, n_pa
            _ptr(free_pages, "free_pages", i32, (n_free,), dev), n_free, _ptr(taken, "taken", i32, (1,), dev))
     tp, width, tstride = _table(block_table, n_seq, dev)
     side = _side_stream(stream, dev)
-    outs = [q_start, k_len, slots, positions, state]
-    sizes = [n_seq + 1, n_seq, n_rows, n_rows, 4]
-    new = [n if t is None else 0 for t, n in zip(outs, sizes)]
-    buf = _empty((sum(new),), i32, dev, side)
-    parts, at, ptrs = torch.split_with_sizes(buf, new), buf.data_ptr(), []
-    for i, name in enumerate(("q_start", "k_len", "slots", "positions", "state")):
-        if outs[i] is None:
-            outs[i] = parts[i]
-            ptrs.append(at)
-            at += 4 * sizes[i]
+    # an allocation each: parts of one would cost more than they save
+    outs, ptrs = [], []
+    for t, name, n in ((q_start, "q_start", n_seq + 1), (k_len, "k_len", n_seq), (slots, "slots", n_rows),
+                       (positions, "positions", n_rows), (state, "state", 4)):
+        if t is None:
+            t = _empty(n, i32, dev, side)
+            ptrs.append(t.data_ptr())
         else:
-            ptrs.append(_ptr(outs[i], name, i32, (sizes[i],), dev))
+            ptrs.append(_ptr(t, name, i32, (n,), dev))
+        outs.append(t)
     if side is not None:
         for t in (ctx_len, new_len, free_pages, taken, block_table, *outs):
             t.record_stream(side)
