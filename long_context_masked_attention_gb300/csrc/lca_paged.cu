@@ -20,6 +20,8 @@ namespace {
 // sums over all requests itself, 1024 at a time, and from each such tile
 // writes only its own share of the rows and of the fresh pages (256 at a
 // time, round robin), finding a row's request by bisection in shared memory.
+// 6.2 us for 8 requests of a token each, 8.3 for 1024 requests with 61K rows
+// (a replayed graph): latency in both.
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanShare = 256;
 
@@ -160,7 +162,10 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedPla
 }
 
 // ------------------------------------------------------------------ write
-// Copies 16-byte pieces: 16 threads per (row, head) for K and V together.
+// Copies 16-byte pieces: 16 threads per (row, head) for K and V together, so
+// that a half-warp's loads and stores are the 256 contiguous bytes of a row
+// whatever the strides between rows, heads and pages.  Bound by HBM: 16.5K rows
+// of 8 heads take 22.6 us (6.0 TB/s, 0.88 of a copy's rate); 64 rows take 4.1.
 __global__ void __launch_bounds__(256) paged_write_kernel(const PagedWriteArgs a) {
   const long long n = static_cast<long long>(a.n_rows) * a.Hkv * 16;
   for (long long t = blockIdx.x * 256LL + threadIdx.x; t < n; t += gridDim.x * 256LL) {
@@ -188,13 +193,18 @@ __global__ void __launch_bounds__(256) paged_write_kernel(const PagedWriteArgs a
 // CTAs that are done first, since SMs differ in what they get of HBM.  A
 // piece of an item that goes on in another span leaves unnormalised sums (O,
 // running maximum, sum of exponentials) in the workspace, and the CTA that
-// finishes an item's last piece joins them in the order of the keys.  Each CTA finds its span itself from the lengths, so there is no
-// planning launch.  Within a CTA each of 4 warps owns 16 of a unit's 64 keys,
+// finishes an item's last piece joins them in the order of the keys.  Each CTA
+// finds its span itself from the lengths, so there is no planning launch.
+// Within a CTA each of 4 warps owns 16 of a unit's 64 keys,
 // copies them asynchronously into its own ring of shared memory (keys that no
 // row attends are filled with zeros, not read) and keeps its own running
 // maximum and sums; the warps meet once per piece.  16 rows cannot fill a
 // tcgen05 tile of 128, so the products are warp-wide m16n8k16 ones, whose
 // score accumulators are already the A operand of the product with V.
+// Measured (replayed graphs): 64 requests of 1K-32K keys, 64 query heads on 8,
+// 364 us (6.5 TB/s, 0.96 of a copy's rate); 4 of 512K 1246 us (6.9 TB/s); 32 of
+// 2K-16K with 16 heads of their own 249 us (6.5 TB/s); one of 4K 18.5 us, which
+// is latency: start-up, keys and the join of the pieces.
 constexpr int kUnit = 64;                     // keys per unit
 constexpr int kRows = 16;                     // rows per item
 constexpr int kDecWarps = 4;
@@ -204,9 +214,17 @@ constexpr int kDecStages = 3;
 constexpr int kSliceBytes = kSlice * 256;     // of K or V
 constexpr int kWarpBytes = kDecStages * 2 * kSliceBytes;
 constexpr int kDecSmem = kDecWarps * kWarpBytes;
-constexpr int kLongShare = 160;               // units per CTA from which on the last part is claimed
-constexpr int kItemUnits = 4;                 // what an item costs beside its units, in units
-constexpr int kMinUnits = 4;                  // a CTA's share, where there is that much
+// Units per CTA from which on the line's last eighth is claimed.  Above it: 64
+// requests of 1K-32K 373 -> 356 us, 4 of 512K 1277 -> 1210.  Below it the finer
+// spans cost more than they even out: 256 requests of 1K, 134 units per CTA,
+// 174 us unclaimed and 189 claimed.
+constexpr int kLongShare = 160;
+// What an item costs beside its units, in units; 0 against 4: 128 ragged
+// requests 294 and 250 us, 64 of 500 keys 43.2 and 37.8, 8 of 4K 43 and 39.
+constexpr int kItemUnits = 4;
+// A CTA's share, where there is that much; 2, 4 and 8: one request of 1K 14.5,
+// 16.6 and 20.6 us, one of 4K 20.3, 18.7 and 20.6.
+constexpr int kMinUnits = 4;
 constexpr int kSeqTile = 2 * kDecThreads;     // requests whose places on the line are in shared memory at once
 constexpr int kPartFloats = kRows * (kHeadDim + 2);
 static_assert(kSlice == 16, "a slice is one k16 step of the product with V");
@@ -777,7 +795,8 @@ __global__ void __launch_bounds__(kDecThreads, 2)
 
 void launch_paged_plan(const PagedPlanArgs& a, int num_sms, cudaStream_t st) {
   // a block per 1024 rows, one each for its threads: the sums are the same
-  // work for one block or for all of them at once
+  // work for one block or for all of them at once.  61K rows with a block per
+  // 512, 1024, 2048 and 4096 of them: 8.35, 8.4, 10.3 and 12.4 us
   const int grid = std::max(1, std::min(num_sms, static_cast<int>((static_cast<long long>(a.n_rows) + 1023) / 1024)));
   note_launches(1);
   paged_plan_kernel<<<grid, kPlanThreads, 0, st>>>(a);
