@@ -302,7 +302,7 @@ typedef struct {
  * n_rows are dropped (q_start stops there).
  * ctx_len, new_len [n_seq], free_pages [n_free], taken [1]: int32, device.
  * block_table: int32, device, n_seq rows of max_pages entries, table_stride
- * entries apart (>= max_pages).  n_rows: rows of the packed batch, at least
+ * entries apart (>= max_pages); n_seq below 2^30.  n_rows: rows of the packed batch, at least
  * the new tokens; 0 to 2^31 - 1.  Outputs must not overlap one another or an
  * input (LCA_ERR_INVALID_ARG). */
 LCA_API lca_status lca_paged_plan(const int32_t* ctx_len, const int32_t* new_len, int32_t n_seq,

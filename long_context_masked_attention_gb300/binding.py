@@ -622,8 +622,12 @@ def paged_plan(ctx_len, new_len, free_pages, taken, block_table, page_size, n_pa
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
     n_seq, n_free, dev, i32, n_rows = ctx_len.numel(), free_pages.numel(), ctx_len.device, torch.int32, int(n_rows)
-    if n_rows < 0:
-        raise ValueError(f"n_rows: {n_rows}, expected 0 or more")
+    if not 0 <= n_rows < 1 << 31:  # a C int32 would keep the low bits
+        raise ValueError(f"n_rows: {n_rows}, expected 0 to 2^31 - 1")
+    if not 0 < page_size < 1 << 31:
+        raise ValueError(f"page_size: {page_size}, expected 1 to 2^31 - 1")
+    if not 0 <= n_pages < 1 << 31:
+        raise ValueError(f"n_pages: {n_pages}, expected 0 to 2^31 - 1")
     ins = (_ptr(ctx_len, "ctx_len", i32, (n_seq,), dev), _ptr(new_len, "new_len", i32, (n_seq,), dev), n_seq,
            _ptr(free_pages, "free_pages", i32, (n_free,), dev), n_free, _ptr(taken, "taken", i32, (1,), dev))
     tp, width, tstride = _table(block_table, n_seq, dev)

@@ -26,6 +26,13 @@ bool ints(const int32_t* p, long long n) { return n == 0 || (p && aligned4(p) &&
 constexpr long long kMaxStride = 1LL << 38;  // elements; a TMA map takes byte strides below 2^40
 bool stride_ok(int64_t s) { return s >= 8 && s % 8 == 0 && s <= kMaxStride; }
 
+// Elements from the first of n rows to the last, `stride` apart.  What is
+// longer than any memory is refused before it is multiplied in 64 bits.
+bool fits(long long n, int64_t stride) {
+  return n <= 1 || static_cast<double>(n - 1) * static_cast<double>(stride) <= 1e15;
+}
+constexpr int kMostRequests = 0x3FFFFFFF;  // the kernels' loops over requests stay in 32 bits
+
 lca_status check_cache(const lca_paged_cache* c) {
   if (!c) return LCA_ERR_INVALID_ARG;
   if (c->dtype != LCA_BF16 && c->dtype != LCA_F16) return LCA_ERR_INVALID_ARG;
@@ -33,6 +40,8 @@ lca_status check_cache(const lca_paged_cache* c) {
   if (c->d != kHeadDim || c->page_size % 8 != 0) return LCA_ERR_UNSUPPORTED;
   if (static_cast<long long>(c->n_pages) * c->page_size > 0x7FFFFFFFLL) return LCA_ERR_UNSUPPORTED;
   if (!stride_ok(c->page_stride) || !stride_ok(c->token_stride) || !stride_ok(c->head_stride))
+    return LCA_ERR_INVALID_ARG;
+  if (!fits(c->n_pages, c->page_stride) || !fits(c->page_size, c->token_stride) || !fits(c->Hkv, c->head_stride))
     return LCA_ERR_INVALID_ARG;
   return LCA_OK;
 }
@@ -104,9 +113,12 @@ lca_status check_attn(const lca_paged_shape* sh, const lca_paged_cache* c, const
   if (r != LCA_OK) return r;
   if (sh->Tq < 0 || sh->Hq <= 0 || sh->n_seq < 0 || sh->max_pages < 0 || sh->max_q_len < 0) return LCA_ERR_INVALID_ARG;
   if (sh->Hq % c->Hkv != 0) return LCA_ERR_INVALID_ARG;
-  if (sh->table_stride < sh->max_pages) return LCA_ERR_INVALID_ARG;
-  if (sh->q_stride < static_cast<long long>(sh->Hq) * kHeadDim || !stride_ok(sh->q_stride)) return LCA_ERR_INVALID_ARG;
-  if (!std::isfinite(sh->scale) || sh->scale < 0.f) return LCA_ERR_INVALID_ARG;
+  if (sh->n_seq > kMostRequests) return LCA_ERR_UNSUPPORTED;
+  if (sh->table_stride < sh->max_pages || !fits(sh->n_seq, sh->table_stride)) return LCA_ERR_INVALID_ARG;
+  if (sh->q_stride < static_cast<long long>(sh->Hq) * kHeadDim || !stride_ok(sh->q_stride) ||
+      !fits(sh->Tq, sh->q_stride))
+    return LCA_ERR_INVALID_ARG;
+  if (!std::isfinite(sh->scale * 1.4426950408889634f) || sh->scale < 0.f) return LCA_ERR_INVALID_ARG;
   // sums of two lengths or of a length and a window stay in 32 bits, so do the launch grids
   if (static_cast<long long>(sh->max_pages) * c->page_size > 0x3FFFFF00LL || sh->Tq > 0x3FFFFFFF)
     return LCA_ERR_UNSUPPORTED;
@@ -197,10 +209,10 @@ lca_status lca_paged_plan(const int32_t* ctx_len, const int32_t* new_len, int32_
                           int32_t max_pages, int32_t page_size, int32_t n_pages, int32_t n_rows, int32_t* q_start,
                           int32_t* k_len, int32_t* slots, int32_t* positions, int32_t* state, void* stream) {
   if (n_seq < 0 || n_free < 0 || max_pages < 0 || page_size <= 0 || n_pages < 0 || n_rows < 0 ||
-      table_stride < max_pages)
+      table_stride < max_pages || !fits(n_seq, table_stride))
     return LCA_ERR_INVALID_ARG;
   if (static_cast<long long>(n_pages) * page_size > 0x7FFFFFFFLL ||
-      static_cast<long long>(max_pages) * page_size > 0x7FFFFF00LL || n_seq == 0x7FFFFFFF)
+      static_cast<long long>(max_pages) * page_size > 0x7FFFFF00LL || n_seq > kMostRequests)
     return LCA_ERR_UNSUPPORTED;
   const long long n_table = n_seq > 0 && max_pages > 0 ? (n_seq - 1) * table_stride + max_pages : 0;
   if (!ints(ctx_len, n_seq) || !ints(new_len, n_seq) || !ints(free_pages, n_free) || !ints(taken, 1) ||
@@ -230,7 +242,8 @@ lca_status lca_paged_write(const void* k, const void* v, int64_t k_stride, int64
   const lca_status r = check_cache(cache);
   if (r != LCA_OK) return r;
   const long long row = static_cast<long long>(cache->Hkv) * kHeadDim;
-  if (n_rows < 0 || k_stride < row || v_stride < row || !stride_ok(k_stride) || !stride_ok(v_stride))
+  if (n_rows < 0 || k_stride < row || v_stride < row || !stride_ok(k_stride) || !stride_ok(v_stride) ||
+      !fits(n_rows, k_stride) || !fits(n_rows, v_stride))
     return LCA_ERR_INVALID_ARG;
   if (n_rows == 0) return LCA_OK;
   if (!k || !v || !aligned16(k) || !aligned16(v) || !device_input(k) || !device_input(v) || !ints(slots, n_rows))

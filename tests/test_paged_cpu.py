@@ -212,3 +212,46 @@ def test_workspace_sizes_of_shapes_that_need_no_tiles_of_many_rows(L):
     assert size(L, shape(Tq=40), cache(n_pages=0))[1] == few
     assert size(L, shape(Tq=40), cache(page_stride=128, token_stride=4096))[1] == few
     assert size(L, shape(Tq=40), cache(n_pages=1, page_stride=128, token_stride=4096))[1] == many
+
+
+@pytest.mark.parametrize("over", [dict(page_stride=1 << 38, n_pages=1 << 20), dict(token_stride=1 << 38, page_size=1 << 20),
+                                  dict(head_stride=1 << 38, Hkv=1 << 20)], ids=str)
+def test_a_cache_longer_than_any_memory_is_refused(L, over):
+    """Its last byte's address does not fit 64 bits, nor do the checks for overlaps."""
+    ca = cache(**over)
+    assert size(L, shape(Hq=ca.Hkv, q_stride=ca.Hkv * 128), ca)[0] == INVALID
+    assert size(L, shape(Hq=8), cache(page_stride=1 << 38, n_pages=3))[0] == 0  # long, but possible
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(n_seq=4, table_stride=1 << 62), INVALID), (dict(n_seq=1 << 20, table_stride=1 << 40), INVALID),
+    (dict(Tq=1 << 20, q_stride=1 << 38), INVALID), (dict(scale=3e38), INVALID), (dict(n_seq=1 << 30), UNSUPPORTED),
+    (dict(n_seq=0x7FFFFFFF), UNSUPPORTED), (dict(n_seq=1, table_stride=1 << 62), 0),
+], ids=str)
+def test_shapes_past_64_bits_are_refused(L, over, code):
+    assert size(L, shape(**over), cache())[0] == code
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(stride=1 << 62, n=4), INVALID), (dict(stride=1 << 40, n=1 << 20), INVALID), (dict(n=1 << 30), UNSUPPORTED),
+    (dict(n=0x7FFFFC10), UNSUPPORTED),
+], ids=str)
+def test_plans_past_64_bits_are_refused(L, over, code):
+    assert plan(L, **over) == code
+
+
+def test_numbers_past_32_bits_are_not_cut(monkeypatch):
+    """ctypes would keep the low 32 bits: a page size of 2^32 + 16 as one of 16."""
+    s, t = torch.zeros(3, dtype=torch.int32), torch.zeros(3, 4, dtype=torch.int32)
+    monkeypatch.setattr(B, "_ptr", lambda *a: FAKE)
+    called = []
+    monkeypatch.setattr(B, "_call", lambda *a: called.append(a))
+    monkeypatch.setattr(B, "_side_stream", lambda *a: None)
+    outs = dict(q_start=s, k_len=s, slots=s, positions=s, state=s)
+    for page, pages, rows, name in (((1 << 32) + 16, 4, 3, "page_size"), (16, (1 << 32) + 4, 3, "n_pages"),
+                                    (16, 4, (1 << 32) + 3, "n_rows"), (-(1 << 32) + 16, 4, 3, "page_size")):
+        with pytest.raises(ValueError, match=name):
+            lib.paged_plan(s, s, s, s[:1], t, page, pages, rows, **outs)
+    assert not called
+    lib.paged_plan(s, s, s, s[:1], t, 16, 4, 3, **outs)
+    assert len(called) == 1
