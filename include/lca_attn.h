@@ -317,7 +317,8 @@ LCA_API lca_status lca_paged_plan(const int32_t* ctx_len, const int32_t* new_len
  * outside [0, n_pages * page_size) is skipped (padding rows have -1); the
  * slots of the other rows must differ (of two rows with one slot, either may
  * be stored, or parts of both).  Row strides are multiples of 8 elements and
- * k, v 16-byte aligned; k and v must not overlap the cache. */
+ * k, v 16-byte aligned; k, v and slots must not overlap the cache
+ * (LCA_ERR_INVALID_ARG; it counts from its first to its last element). */
 LCA_API lca_status lca_paged_write(const void* k, const void* v, int64_t k_stride, int64_t v_stride,
                                    const int32_t* slots, int32_t n_rows, const lca_paged_cache* cache, void* stream);
 

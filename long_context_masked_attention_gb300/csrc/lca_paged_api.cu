@@ -51,6 +51,13 @@ bool cache_memory(const lca_paged_cache* c) {
   return c->k && c->v && aligned16(c->k) && aligned16(c->v) && device_input(c->k) && device_input(c->v);
 }
 
+// Bytes from the first to the last element of k, and of v.
+long long cache_extent(const lca_paged_cache* c) {
+  if (c->n_pages == 0) return 0;
+  return ((c->n_pages - 1) * c->page_stride + (c->page_size - 1) * c->token_stride + (c->Hkv - 1) * c->head_stride +
+          kHeadDim) * 2;
+}
+
 // The cache's strides as a tensor map has them, in ascending order: token and
 // head as they come, the page last.  The stride of an axis of length one moves
 // nothing and is taken as its neighbour's.
@@ -250,6 +257,12 @@ lca_status lca_paged_write(const void* k, const void* v, int64_t k_stride, int64
     return LCA_ERR_INVALID_ARG;
   if (cache->n_pages == 0) return LCA_OK;  // every slot lies outside
   if (!cache_memory(cache)) return LCA_ERR_INVALID_ARG;
+  for (const void* c : {cache->k, cache->v}) {
+    const long long n = cache_extent(cache);
+    if (overlap(c, n, k, ((n_rows - 1) * k_stride + row) * 2) || overlap(c, n, v, ((n_rows - 1) * v_stride + row) * 2) ||
+        overlap(c, n, slots, 4LL * n_rows))
+      return LCA_ERR_INVALID_ARG;
+  }
   const int sms = num_sms();
   if (sms <= 0) return LCA_ERR_CUDA;
   PagedWriteArgs a{};
@@ -305,10 +318,7 @@ lca_status lca_attn_paged(const void* q, const lca_paged_cache* cache, const int
   }
   if (shape->Tq > 0) {
     const long long rows = shape->Tq, heads = shape->Hq;
-    const long long extent =
-        cache->n_pages == 0 ? 0
-                            : ((cache->n_pages - 1) * cache->page_stride + (cache->page_size - 1) * cache->token_stride +
-                               (cache->Hkv - 1) * cache->head_stride + kHeadDim) * 2;
+    const long long extent = cache_extent(cache);
     const struct {
       const void* p;
       long long bytes;

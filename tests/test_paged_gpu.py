@@ -174,6 +174,22 @@ def test_write_of_one_slot_twice_stores_rows_of_the_call(lca):
     assert float(flat.sum(1)[[0, 1, 2, 4, 5, 6, 7, 8, 10, 12]].abs().max()) == 0
 
 
+def test_write_from_the_cache_itself_is_refused(lca):
+    """Rows that are read while others are written would be either."""
+    import torch
+
+    kc, vc = (torch.arange(4 * 8 * 2 * 128, device="cuda").view(4, 8, 2, 128).to(torch.bfloat16) for _ in range(2))
+    before = kc.clone(), vc.clone()
+    k = torch.zeros(6, 2, 128, dtype=torch.bfloat16, device="cuda")
+    slots = torch.arange(6, dtype=torch.int32, device="cuda")
+    rows = kc.view(32, 2, 128)
+    inside = vc.view(-1)[:512].view(torch.int32)[:6]
+    for args in ((rows[8:14], k, slots), (k, rows[26:], slots), (k, vc.view(32, 2, 128)[3:9], slots), (k, k, inside)):
+        with pytest.raises(lca.LcaError, match="INVALID"):
+            lca.paged_write(args[0], args[1], kc, vc, args[2])
+    assert torch.equal(kc, before[0]) and torch.equal(vc, before[1])
+
+
 # ------------------------------------------------------------------ attention
 def attend(lca, p: Paged, **kw):
     import torch
