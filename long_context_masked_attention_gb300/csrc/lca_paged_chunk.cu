@@ -255,7 +255,10 @@ __global__ void __launch_bounds__(1024) paged_begin_kernel(const __grid_constant
 struct Line {
   long long total, ctas;
   __device__ __forceinline__ Line(const PagedAttnArgs& a, int grid) {
-    total = a.line[a.block0[a.n_seq]] * a.Hkv;
+    // requests whose rows do not overlap make fewer than 2^52 places; a q_start
+    // that lets them overlap may make more, and is reported and not served then
+    const long long head = a.line[a.block0[a.n_seq]];
+    total = head < (1LL << 52) / a.Hkv ? head * a.Hkv : 0;
     ctas = min(static_cast<long long>(grid), max(total / kMinTiles, 1LL));
   }
   __device__ __forceinline__ long long start(long long c) const { return line_div(min(c, ctas) * total, ctas); }
