@@ -90,7 +90,7 @@ struct Item {
   int t0, n0, t1;         // the item's tiles: n0 from t0 on, then from t1 on
   int pad[2];
   Span hull[2], full[2];  // per sub-tile: keys that some, and that all, of its rows attend
-  Span all;               // keys that some row of the item attends
+  Span all, every;        // keys that some, and that all, of the item's rows attend
   __device__ __forceinline__ int tile(int t) const { return u0 + t < n0 ? t0 + u0 + t : t1 + u0 + t - n0; }
   __device__ __forceinline__ uint32_t cls(int x, int kt) const {
     const int j0 = kt * kTile;
@@ -98,7 +98,7 @@ struct Item {
     return span_covers(full[x], j0, j0 + kTile) ? kTileFull : kTilePartial;
   }
 };
-static_assert(sizeof(Item) == 144 && 8 * B_COUNT <= 256 && kItemSlots * sizeof(Item) <= 640,
+static_assert(sizeof(Item) == 160 && 8 * B_COUNT <= 256 && kItemSlots * sizeof(Item) <= 640,
               "the items lie between the barriers and the TMEM slot");
 
 constexpr float kLn2 = 0.6931471805599453f;
@@ -365,6 +365,7 @@ __device__ __forceinline__ void scheduler(const PagedAttnArgs& a, const Line& ln
     } else if (lane == 2) {
       const Tiles tl = tiles_of(h);
       inf.all = h;
+      inf.every = f;
       inf.valid = 1;
       inf.narrow = narrow;
       inf.n = tl.n0 + tl.n1 > 0 ? take : 0;
@@ -648,14 +649,19 @@ __device__ __forceinline__ float row_exp(uint32_t tS, float sl2, float base) {
   return f2lo(t) + f2hi(t);
 }
 
-// Row `key` of the V tile (one thread per key): zeros where no row of the item
-// attends it (nothing of what lies there may meet a p of 0) ...
-__device__ __forceinline__ void clear_v_row(uint8_t* v, int key) {
-#pragma unroll 1
-  for (int i = 0; i < 16; ++i)
-    *reinterpret_cast<uint4*>(v + (i >> 3) * kChunkBytes + key * 128 + (((i ^ key) & 7) << 4)) = make_uint4(0, 0, 0, 0);
-}
-// ... or whether it holds a value that is not finite.
+// Values that are not finite in keys that only some rows of an item attend
+// must not meet a p of 0.  Before a tile's product they are set to zero in
+// shared memory, value by value, by each warpgroup that has a product with the
+// tile (both write the same); at the end the rows that attend such a key add
+// the values to their sums.  A weight is positive, so whatever it is, its
+// product with an infinity or NaN is that same value, and no score is needed
+// for it.
+//
+// One such value in a chunk of 256 tokens at 131K keys takes the call from 0.82
+// to 0.90 ms; what all calls pay for it is a look at the keys of partial tiles
+// (8 prompts 278 -> 284 us).
+//
+// Row `key` of the V tile (one thread per key): whether it holds such a value,
 template <typename T>
 __device__ __forceinline__ bool bad_v_row(const uint8_t* v, int key) {
   uint32_t bad = 0;
@@ -666,87 +672,93 @@ __device__ __forceinline__ bool bad_v_row(const uint8_t* v, int key) {
   }
   return (bad & 0x80008000u) != 0;
 }
-
-// The rows of a warp, one per lane, over the piece's keys without products of
-// hidden values: for the rare items that have a value that is not finite among
-// keys which only some rows attend (0 times it would be NaN).  o: the row's
-// sums, in local memory; all lanes take part.  About a microsecond per key,
-// well inside the limit of what the CTA's other warps wait meanwhile.
+// and its values without them,
 template <typename T>
-__device__ __noinline__ void rows_alone(const PagedAttnArgs& a, const Item& inf, Span sp, int row, int head, float* o,
-                                        float& m_out, float& l_out) {
-  const uint4* q = reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + row * a.q_stride + head * kHeadDim);
+__device__ __forceinline__ uint32_t finite_part(uint32_t w) {
+  return w & ~(((Half2<T>::not_finite(w) & 0x80008000u) >> 15) * 0xFFFFu);
+}
+template <typename T>
+__device__ __noinline__ void finite_v_row(uint8_t* v, int key) {
+#pragma unroll 1
+  for (int i = 0; i < 16; ++i) {
+    uint4* at = reinterpret_cast<uint4*>(v + (i >> 3) * kChunkBytes + key * 128 + (((i ^ key) & 7) << 4));
+    const uint4 w = *at;
+    *at = make_uint4(finite_part<T>(w.x), finite_part<T>(w.y), finite_part<T>(w.z), finite_part<T>(w.w));
+  }
+}
+// or none at all (no row of the item attends the key, and nothing of
+// what lies there may reach a result).
+__device__ __forceinline__ void clear_v_row(uint8_t* v, int key) {
+#pragma unroll 1
+  for (int i = 0; i < 16; ++i)
+    *reinterpret_cast<uint4*>(v + (i >> 3) * kChunkBytes + key * 128 + (((i ^ key) & 7) << 4)) = make_uint4(0, 0, 0, 0);
+}
+
+// Writes a warp's rows, one per lane, of an item that had such values, adding
+// them from the cache; all lanes take part.  tO: the products' sums.
+template <typename T>
+__device__ __noinline__ void write_hidden(const PagedAttnArgs& a, const Item& inf, int x, uint32_t tO, bool valid,
+                                          Span sp, T* orow, float* part, float l) {
+  const float inv = part ? 1.f : l == 0.f ? 0.f : 1.f / l;
   const int* table = a.table + inf.seq * a.table_stride;
-  float m = -INFINITY, l = 0.f;
+  const T* v = static_cast<const T*>(a.vc) + inf.head * a.head_stride;
+  // place of key j's values in v, -1 where all rows or none attend it or it has no page
+  auto place = [&](int j) -> long long {
+    if (!in_span(inf.all, j) || in_span(inf.every, j)) return -1;
+    const int page = __ldg(table + j / a.page_size);
+    return page < 0 || page >= a.n_pages ? -1 : page * a.page_stride + j % a.page_size * a.token_stride;
+  };
 #pragma unroll 1
-  for (int k = 0; k < kHeadDim; ++k) o[k] = 0.f;
+  for (int c = 0; c < 4; ++c) {
+    uint32_t r[32];
+    __syncwarp();
+    tmem_ld32(tO + 32 * c, r);
+    tmem_ld_wait();
 #pragma unroll 1
-  for (int t = 0; t < inf.n; ++t)
+    for (int t = 0; t < inf.n; ++t) {
+      const int kt = inf.tile(t);
+      if (span_covers(inf.every, kt * kTile, kt * kTile + kTile) || (!inf.narrow && inf.cls(x, kt) == kTileEmpty))
+        continue;
 #pragma unroll 1
-    for (int j = inf.tile(t) * kTile, e = j + kTile; j < e; ++j) {
-      const bool mine = in_span(sp, j);
-      if (!__any_sync(0xFFFFFFFFu, mine)) continue;
-      const int page = __ldg(table + j / a.page_size);
-      const bool ok = page >= 0 && page < a.n_pages;
-      const long long at =
-          (ok ? page : 0) * a.page_stride + j % a.page_size * a.token_stride + inf.head * a.head_stride;
-      const uint4* k4 = reinterpret_cast<const uint4*>(static_cast<const T*>(a.kc) + at);
-      const uint4* v4 = reinterpret_cast<const uint4*>(static_cast<const T*>(a.vc) + at);
-      auto pair = [](const uint4& w, int i) { return Half2<T>::unpack(i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w); };
-      float s = 0.f;
-#pragma unroll 2
-      for (int c = 0; c < 16; ++c) {
-        const uint4 x = __ldg(q + c), y = ok ? k4[c] : make_uint4(0, 0, 0, 0);
+      for (int j0 = kt * kTile; j0 < (kt + 1) * kTile; j0 += 32) {
+        const long long at = place(j0 + (threadIdx.x & 31));
+        uint32_t bad = 0;
+        if (at >= 0)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 u = pair(x, i), w = pair(y, i);
-          s = fmaf(u.x, w.x, fmaf(u.y, w.y, s));
-        }
-      }
-      const float mn = mine ? fmaxf(m, s * a.scale_log2) : m;
-      const float f = m == -INFINITY ? 0.f : ex2_approx(m - mn);
-      const float p = mine ? ex2_approx(s * a.scale_log2 - mn + kBias<T>) : 0.f;
-      l = (m == -INFINITY ? 0.f : l * f) + p;
-#pragma unroll 2
-      for (int c = 0; c < 16; ++c) {
-        const uint4 y = ok ? v4[c] : make_uint4(0, 0, 0, 0);
+          for (int u = 0; u < 4; ++u) {
+            const uint4 w = *reinterpret_cast<const uint4*>(v + at + 32 * c + 8 * u);
+            bad |= Half2<T>::not_finite(w.x) | Half2<T>::not_finite(w.y) | Half2<T>::not_finite(w.z) |
+                   Half2<T>::not_finite(w.w);
+          }
+        for (uint32_t keys = __ballot_sync(0xFFFFFFFFu, bad & 0x80008000u); keys != 0; keys &= keys - 1) {
+          const int j = __ffs(keys) - 1;
+          const T* vj = v + __shfl_sync(0xFFFFFFFFu, at, j) + 32 * c;
+          if (!in_span(sp, j0 + j)) continue;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 w = pair(y, i);
-          float* oo = o + 8 * c + 2 * i;
-          oo[0] = m == -INFINITY ? 0.f : oo[0] * f;
-          oo[1] = m == -INFINITY ? 0.f : oo[1] * f;
-          if (mine) {
-            oo[0] = fmaf(p, w.x, oo[0]);
-            oo[1] = fmaf(p, w.y, oo[1]);
+          for (int u = 0; u < 16; ++u) {
+            const uint32_t w = *reinterpret_cast<const uint32_t*>(vj + 2 * u);
+            const float2 f = Half2<T>::unpack(w ^ finite_part<T>(w));  // zero where it is finite
+            r[2 * u] = __float_as_uint(__uint_as_float(r[2 * u]) + f.x);
+            r[2 * u + 1] = __float_as_uint(__uint_as_float(r[2 * u + 1]) + f.y);
           }
         }
       }
-      m = mn;
     }
-  m_out = m;
-  l_out = l;
-}
-
-template <typename T>
-__device__ __noinline__ void write_alone(const PagedAttnArgs& a, const Item& inf, int x, int row, bool valid, int token,
-                                         int head, Span sp, T* orow, float* part, float& m, float& l) {
-  float o[kHeadDim];
-  rows_alone<T>(a, inf, valid ? sp : Span{0, 0, 0, 0}, inf.q_off + (valid ? token : 0), valid ? head : 0, o, m, l);
-  if (!valid) return;
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll 1
-  for (int k = 0; k < kHeadDim; k += 2) {
-    if (part)
-      *reinterpret_cast<float2*>(part + (x * 128 + row) * kHeadDim + k) = make_float2(o[k], o[k + 1]);
-    else
-      *reinterpret_cast<uint32_t*>(orow + k) = Half2<T>::pack(o[k] * inv, o[k + 1] * inv);
+    if (!valid) continue;
+#pragma unroll
+    for (int k = 0; k < 32; k += 2) {
+      const float y0 = __uint_as_float(r[k]) * inv, y1 = __uint_as_float(r[k + 1]) * inv;
+      if (part)
+        *reinterpret_cast<float2*>(part + 32 * c + k) = make_float2(y0, y1);
+      else
+        *reinterpret_cast<uint32_t*>(orow + 32 * c + k) = Half2<T>::pack(y0, y1);
+    }
   }
 }
 
 template <typename T>
 __device__ __forceinline__ void softmax_wg(const PagedAttnArgs& a, int x, uint64_t* bar, const Item* items,
-                                           uint8_t* sKV, volatile int* bad_item, uint32_t tbase) {
+                                           uint8_t* sKV, volatile int* hidden, uint32_t tbase) {
   const int wq = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
   const int row = wq * 32 + lane;  // TMEM lane = row of the sub-tile
   const uint32_t tl = static_cast<uint32_t>(wq * 32) << 16;
@@ -785,19 +797,23 @@ __device__ __forceinline__ void softmax_wg(const PagedAttnArgs& a, int x, uint64
       if (!waitw(&bar[B_SFULL + full], (odd ? s_odd : s_cnt) & 1, a, 82 + x)) return;
       if (odd) ++s_odd; else ++s_cnt;
       tc_fence_after();
-      if (cls != kTileFull) {
+      if (!span_covers(inf.every, kt * kTile, kt * kTile + kTile)) {
         // only now: a warpgroup that skipped a narrow item runs ahead of the
         // loads, and the scores show that the ring has come to this tile
         const uint32_t vidx = kv_iter + 2 * t + 1;
         if (!waitw(&bar[B_KVFULL + vidx % kStages], (vidx / kStages) & 1, a, 88 + x)) return;
         const int j = kt * kTile + row;
         uint8_t* v = sKV + (vidx % kStages) * kTileBytes;
-        if (!in_span(inf.all, j))
+        if (!in_span(inf.all, j)) {
           clear_v_row(v, row);
-        else if (!in_span(inf.full[x], j) && bad_v_row<T>(v, row))  // a key of all rows is nobody's hidden one
-          *bad_item = it + 1;
+        } else if (!in_span(inf.every, j) && bad_v_row<T>(v, row)) {
+          // the other warpgroup may find the value gone, but then the mark set
+          hidden[slot] = it + 1;
+          __threadfence_block();
+          finite_v_row<T>(v, row);
+        }
         fence_proxy_async_smem();
-        mask_scores(tS, sp, kt * kTile);
+        if (cls != kTileFull) mask_scores(tS, sp, kt * kTile);
       }
       const float mx = row_max(tS);
       const float m_new = fmaxf(m, mx * sl2);
@@ -847,8 +863,8 @@ __device__ __forceinline__ void softmax_wg(const PagedAttnArgs& a, int x, uint64
     }
     T* orow = static_cast<T*>(a.o) + (static_cast<long long>(inf.q_off + (valid ? token : 0)) * a.Hq + head) * kHeadDim;
     float* part = inf.part < 0 ? nullptr : a.chunk_parts + inf.part * static_cast<long long>(kPagedChunkPartFloats);
-    if (any && *bad_item == it + 1) {
-      write_alone<T>(a, inf, x, row, valid, token, head, sp, orow, part, m, l);
+    if (any && hidden[slot] == it + 1) {
+      write_hidden<T>(a, inf, x, tO, valid, sp, orow, part ? part + (x * 128 + row) * kHeadDim : nullptr, l);
     } else if (any) {
       const float inv = part ? 1.f : l == 0.f ? 0.f : 1.f / l;
 #pragma unroll 1
@@ -904,7 +920,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* bar = reinterpret_cast<uint64_t*>(sm + kOffCtl);
   Item* items = reinterpret_cast<Item*>(sm + kOffCtl + 256);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + kOffCtl + 896);
-  int* bad_item = reinterpret_cast<int*>(sm + kOffCtl + 904);  // per sub-tile
+  // per item slot: the last item (from 1) with values that write_hidden adds;
+  // a warp may be that many items ahead of another
+  int* hidden = reinterpret_cast<int*>(sm + kOffCtl + 904);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (warp == 8) {
     tmem_alloc(tmem_slot, 512);
@@ -913,7 +931,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int b = 0; b < B_COUNT; ++b) mbar_init(&bar[b], 1);
     for (int x = 0; x < 3; ++x) mbar_init(&bar[B_PFULL + x], 4);  // one arrival per softmax warp
-    bad_item[0] = bad_item[1] = 0;
+    for (int x = 0; x < kItemSlots; ++x) hidden[x] = 0;
     for (int x = 0; x < kItemSlots; ++x) mbar_init(&bar[B_ITEMPTY + x], 10);  // softmax, MMA and producer warps
     fence_mbar_init();
   }
@@ -937,7 +955,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   else if (warp == 8)
     mma_issuer<T>(a, sQ, sKV, bar, items, tbase);
   else
-    softmax_wg<T>(a, warp >> 2, bar, items, sKV, bad_item + (warp >> 2), tbase);
+    softmax_wg<T>(a, warp >> 2, bar, items, sKV, hidden, tbase);
   tc_fence_before();
   __syncthreads();
   if (warp == 8) {

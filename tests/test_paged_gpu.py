@@ -350,6 +350,68 @@ def test_infinities_among_a_long_contexts_last_keys(lca):
         assert bool((o[first:, :, 7] == float("inf")).all()) and bool(o[first:, :, :7].isfinite().all())
 
 
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+@pytest.mark.parametrize("lens,bads", [
+    ([(0, 100)], [3, 60]),                         # the only tile of its items
+    ([(0, 9), (3, 15), (500, 11)], [4, 6, 505]),   # narrow items, one after another
+    ([(0, 700)], list(range(5, 700, 64))),         # every item, several tiles each
+    ([(1000, 300), (5, 260), (2, 13)], [1000, 1130, 1299, 100, 8]),
+    ([(126, 14), (254, 14)], [127, 128, 255, 256]),  # two tiles of a narrow item in turn
+], ids=str)
+def test_several_tiles_with_infinities(lca, lens, bads, value):
+    """Every row equals the one that a cache without the infinities that it
+    does not attend gives; those that attend one have it in that column only."""
+    import torch
+
+    p = make(lens, 16, 8, 2, CAUSAL, seed=len(bads), device="cuda")
+    ref = reference(p)
+    o0, lse0, _ = attend(lca, p)
+    check(o0, lse0, p, ref)
+    hit = torch.zeros(p.q.shape[0], dtype=torch.bool)
+    row = 0
+    for i, (ctx, new) in enumerate(lens):
+        mine = [b for b in bads if ctx <= b < ctx + new]
+        for b in mine:
+            p.vc[int(p.table[i, b // 16]), b % 16, :, 77] = value
+        if mine:
+            hit[row + min(mine) - ctx:row + new] = True
+        row += new
+    assert bool(hit.any()) and not bool(hit.all())
+    for _ in range(3):
+        o, lse, st = attend(lca, p)
+        assert st == (0, 0)
+        hid = hit.nonzero().flatten().cuda()
+        assert not bool(o[hid][:, :, 77].isfinite().any())
+        o[hid, :, 77] = o0[hid, :, 77]  # all else within its bound
+        check(o, lse, p, ref)
+
+
+def test_infinities_among_a_very_long_contexts_last_keys(lca):
+    """Pieces of hundreds of thousands of keys, with one value that is not
+    finite: what it costs goes by its tile, not by the piece."""
+    import torch
+
+    ctx, new, page, Hkv = 786432, 2048, 64, 8
+    n = (ctx + new) // page
+    g = torch.Generator(device="cuda").manual_seed(3)
+    kc, vc = (torch.rand(n, page, Hkv, 128, device="cuda", generator=g, dtype=torch.bfloat16) - 0.5 for _ in range(2))
+    q = torch.rand(new, 8 * Hkv, 128, device="cuda", generator=g, dtype=torch.bfloat16) - 0.5
+    table = torch.arange(n, dtype=torch.int32, device="cuda")[None]
+    q_start, k_len = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([0, new], [ctx + new]))
+    ws = torch.empty(lca.attn_paged_workspace_size(q, kc, vc, table, CAUSAL), dtype=torch.uint8, device="cuda")
+    call = lambda: lca.attn_paged(q, kc, vc, table, q_start, k_len, CAUSAL, workspace=ws)  # noqa: E731
+    o0, lse0 = call()
+    bad = ctx + 1000
+    vc[bad // page, bad % page, :, 9] = float("inf")
+    o, lse = call()
+    assert lca.read_status(ws) == (0, 0)
+    assert torch.equal(lse, lse0)  # no score changed
+    assert bool((o[1000:, :, 9] == float("inf")).all()) and bool(o[:1000].isfinite().all())
+    o[1000:, :, 9] = o0[1000:, :, 9]
+    # both are roundings of sums whose weights are off by 2^-8 at most, |v| <= 1/2
+    assert float((o.float() - o0.float()).abs().max()) <= 2 * (2.0**-8 * 0.5 + 2.0**-8 * 0.5)
+
+
 @pytest.mark.parametrize("new", [1, 3, 90])
 def test_pages_between_sinks_and_window_may_be_gone(lca, new):
     """GLOBAL_SLIDING over a long context: the table has no entry, and the
