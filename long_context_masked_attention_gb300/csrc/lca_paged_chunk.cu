@@ -867,28 +867,58 @@ __device__ __forceinline__ void softmax_wg(const PagedAttnArgs& a, int x, uint64
       write_hidden<T>(a, inf, x, tO, valid, sp, orow, part ? part + (x * 128 + row) * kHeadDim : nullptr, l);
     } else if (any) {
       const float inv = part ? 1.f : l == 0.f ? 0.f : 1.f / l;
+      if (part) {
 #pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
-        uint32_t r[32];
-        tmem_ld32(tO + 32 * c, r);
-        tmem_ld_wait();
-        if (valid && part) {
-          float* dst = part + (x * 128 + row) * kHeadDim + 32 * c;
+        for (int c = 0; c < 4; ++c) {
+          uint32_t r[32];
+          tmem_ld32(tO + 32 * c, r);
+          tmem_ld_wait();
+          if (valid) {
+            float* dst = part + (x * 128 + row) * kHeadDim + 32 * c;
 #pragma unroll
-          for (int u = 0; u < 4; ++u) st_global_v8(dst + 8 * u, &r[8 * u]);
-        } else if (valid) {
-          uint32_t w[16];
+            for (int u = 0; u < 4; ++u) st_global_v8(dst + 8 * u, &r[8 * u]);
+          }
+        }
+      } else {
+        // Four lanes exchange 32-byte pieces of their rows, so that a store
+        // covers 8 lines of 128 bytes and not 32 pieces of 32: 32 requests of
+        // 5 tokens 165.1 -> 162.3 us; prompts are the same either way.
+        const int place = valid ? static_cast<int>((orow - static_cast<T*>(a.o)) / kHeadDim) : -1, quad = lane & 3;
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          uint32_t w[32];
 #pragma unroll
-          for (int k = 0; k < 16; ++k)
-            w[k] = Half2<T>::pack(__uint_as_float(r[2 * k]) * inv, __uint_as_float(r[2 * k + 1]) * inv);
-          if (a.out_v8) {
-            st_global_v8(orow + 32 * c, w);
-            st_global_v8(orow + 32 * c + 16, w + 8);
-          } else {
+          for (int c = 0; c < 2; ++c) {
+            uint32_t r[32];
+            tmem_ld32(tO + 64 * h + 32 * c, r);
+            tmem_ld_wait();
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
-              *reinterpret_cast<uint4*>(orow + 32 * c + 8 * u) =
-                  make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
+            for (int k = 0; k < 16; ++k)
+              w[16 * c + k] = Half2<T>::pack(__uint_as_float(r[2 * k]) * inv, __uint_as_float(r[2 * k + 1]) * inv);
+          }
+#pragma unroll
+          for (int d = 1; d <= 2; d <<= 1)
+#pragma unroll
+            for (int p = 0; p < 4; ++p)
+              if (!(p & d))
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  uint32_t &lo = w[8 * p + e], &hi = w[8 * (p + d) + e];
+                  const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, (quad & d) ? lo : hi, d);
+                  if (quad & d) lo = got; else hi = got;
+                }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {  // now piece `quad` of the quad's row k
+            const int at = __shfl_sync(0xFFFFFFFFu, place, (lane & ~3) + k);
+            if (at < 0) continue;
+            T* dst = static_cast<T*>(a.o) + static_cast<long long>(at) * kHeadDim + 64 * h + 16 * quad;
+            if (a.out_v8) {
+              st_global_v8(dst, &w[8 * k]);
+            } else {
+              *reinterpret_cast<uint4*>(dst) = make_uint4(w[8 * k], w[8 * k + 1], w[8 * k + 2], w[8 * k + 3]);
+              *reinterpret_cast<uint4*>(dst + 8) =
+                  make_uint4(w[8 * k + 4], w[8 * k + 5], w[8 * k + 6], w[8 * k + 7]);
+            }
           }
         }
       }
