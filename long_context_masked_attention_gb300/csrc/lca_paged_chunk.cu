@@ -26,10 +26,10 @@
 // next keys runs while the first warpgroup works on the present ones.
 //
 // Measured (whole calls, replayed graphs, 64 query heads on 8): 2048 tokens at
-// the end of 32K keys 1555-1645 us (1.38-1.46 PFLOP/s; the tensor pipe is active
-// 64 % of the time, and power decides the rest); 8 prompts of 101-2047 tokens 279
+// the end of 32K keys 1517-1641 us (1.38-1.49 PFLOP/s; the tensor pipe is active
+// 64 % of the time, and power decides the rest); 8 prompts of 101-2047 tokens 284
 // us, where an item of 9 tiles takes 18 us of which 14-15 are tiles; 5 tokens of
-// each of 32 requests at 1K-16K keys 163 us (0.78 of a copy's rate).
+// each of 32 requests at 1K-16K keys 162 us (0.78 of a copy's rate).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -659,7 +659,7 @@ __device__ __forceinline__ float row_exp(uint32_t tS, float sl2, float base) {
 //
 // One such value in a chunk of 256 tokens at 131K keys takes the call from 0.82
 // to 0.90 ms; what all calls pay for it is a look at the keys of partial tiles
-// (8 prompts 278 -> 284 us).
+// and more code (8 prompts 278 -> 284 us).
 //
 // Row `key` of the V tile (one thread per key): whether it holds such a value,
 template <typename T>
