@@ -386,6 +386,35 @@ def test_several_tiles_with_infinities(lca, lens, bads, value):
         check(o, lse, p, ref)
 
 
+@pytest.mark.parametrize("mask", MASKS, ids=lambda m: f"{m.kind}{m.window_left or ''}")
+@pytest.mark.parametrize("Hq", [8, 3])
+def test_infinities_reach_the_rows_that_attend_them(lca, mask, Hq):
+    """Under every family: a column of the values of a few keys holds infinities;
+    it is not finite in the rows that attend one of them, all else as without."""
+    import torch
+
+    from oracle.masks import segment_mask
+
+    lens = [(600, 1), (0, 200), (333, 100), (150, 5), (1000, 300)]
+    p = make(lens, 16, Hq, 1, mask, seed=Hq, device="cuda")
+    ref = reference(p)
+    o0, lse0, _ = attend(lca, p)
+    check(o0, lse0, p, ref, what=mask.kind)
+    hit = torch.zeros(p.q.shape[0], dtype=torch.bool)
+    for i, seg in enumerate(p.prob.segments):
+        bads = [2, 64, 65, 127, seg.k_len // 2, seg.k_len - 3, seg.k_len - 60]
+        bads = [b for b in bads if 0 <= b < seg.k_len]
+        for b in bads:
+            p.vc[int(p.table[i, b // 16]), b % 16, :, 77] = float("inf")
+        hit[seg.q_off:seg.q_off + seg.q_len] = torch.from_numpy(segment_mask(mask, i, seg)[:, bads].any(1))
+    for _ in range(2):
+        o, lse, st = attend(lca, p)
+        assert st == (0, 0) and torch.equal(lse, lse0)
+        assert not bool(o[hit.cuda()][:, :, 77].isfinite().any()), mask.kind
+        o[hit.cuda(), :, 77] = o0[hit.cuda(), :, 77]
+        check(o, lse, p, ref, what=mask.kind)
+
+
 def test_infinities_among_a_very_long_contexts_last_keys(lca):
     """Pieces of hundreds of thousands of keys, with one value that is not
     finite: what it costs goes by its tile, not by the piece."""
