@@ -400,7 +400,7 @@ __device__ __forceinline__ void decode_warp(const PagedAttnArgs& a, uint32_t rin
     if (!span_hits(hl, j, j + 8)) return -1;
     const int p = __ldg(table + j / a.page_size);
     if (p < 0 || p >= a.n_pages) {
-      raise_status(a.status, kStatusDeviceArg, 51);
+      paged_report(a.status, kStatusDeviceArg, 51);
       return -1;
     }
     return p;

@@ -43,6 +43,37 @@ struct Half2<__half> {
   }
 };
 
+// The status word of a call: status[0] the code, status[1] where it was raised,
+// set as one 64-bit word.  Lengths and table entries that cannot be used
+// (kStatusDeviceArg) are reported and the call goes on with what the header
+// promises for them; only a wait that ran out ends it, and replaces such a
+// report.  Of two reports of a kind the first stays.
+__device__ __forceinline__ void paged_report(int* status, int code, int where) {
+  auto* word = reinterpret_cast<unsigned long long*>(status);
+  const unsigned long long x = static_cast<unsigned>(code) | static_cast<unsigned long long>(where) << 32;
+  const unsigned long long was = atomicCAS(word, 0ull, x);
+  if (code == kStatusTimeout && was != 0 && static_cast<int>(was) != kStatusTimeout) atomicCAS(word, was, x);
+}
+__device__ __forceinline__ bool paged_timed_out(const int* status) {
+  return *reinterpret_cast<const volatile int*>(status) == kStatusTimeout;
+}
+
+// mbar_wait that gives up when its time is over or another wait's was, and for
+// no other report.
+__device__ __forceinline__ bool paged_wait(uint64_t* bar, uint32_t parity, int* status, uint64_t limit_ns, int where) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t it = 1; !mbar_try_wait(bar, parity); ++it) {
+    if ((it & 63u) != 0) continue;
+    if (paged_timed_out(status)) return false;
+    if (globaltimer_ns() - t0 > limit_ns) {
+      paged_report(status, kStatusTimeout, where);
+      return false;
+    }
+  }
+  return true;
+}
+
 __device__ __forceinline__ bool in_span(const Span& s, int j) {
   return (j >= s.a0 && j < s.b0) || (j >= s.a1 && j < s.b1);
 }

@@ -122,7 +122,7 @@ __host__ __device__ constexpr uint32_t idesc(bool b_mn_major) {
 
 // Warp-uniform wait; what follows the first test is a call, one copy of it.
 __device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, const PagedAttnArgs& a, int where) {
-  const bool ok = mbar_wait(bar, parity, a.status, a.wait_limit_ns, kStatusTimeout, where);
+  const bool ok = paged_wait(bar, parity, a.status, a.wait_limit_ns, where);
   return __all_sync(0xFFFFFFFFu, ok);
 }
 __device__ __forceinline__ bool waitw(uint64_t* bar, uint32_t parity, const PagedAttnArgs& a, int where) {
@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(1024) paged_begin_kernel(const __grid_constant
   const int room = a.max_pages * a.page_size;
   for (int i = threadIdx.x; i < a.n_seq; i += 1024) {
     const int r0 = a.q_start[i], r1 = a.q_start[i + 1], kl = a.k_len[i];
-    if (r0 < 0 || r1 < r0 || r1 > a.Tq || kl < 0 || kl > room) raise_status(a.status, kStatusDeviceArg, 50);
+    if (r0 < 0 || r1 < r0 || r1 > a.Tq || kl < 0 || kl > room) paged_report(a.status, kStatusDeviceArg, 50);
   }
   if (many) place_items(a);
 }
@@ -434,7 +434,7 @@ __device__ __forceinline__ void producer(const PagedAttnArgs& a, const CUtensorM
       if (!span_hits(inf.all, j, j + a.box_rows)) return a.n_pages;
       const int pg = __ldg(table + j / a.page_size);
       if (pg < 0 || pg >= a.n_pages) {
-        raise_status(a.status, kStatusDeviceArg, 51);
+        paged_report(a.status, kStatusDeviceArg, 51);
         return a.n_pages;
       }
       return pg;

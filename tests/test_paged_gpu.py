@@ -626,6 +626,54 @@ def test_bad_pages_and_lengths_are_reported(lca, lens):
         assert attend(lca, q)[2][0] == 6, (name, i, x)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_a_bad_request_spoils_no_other(lca, dtype):
+    """A page or a length that cannot be used, in one request of a batch whose
+    items take longer than a wait's first polls: the call goes on, and every
+    row is, bit for bit, that of a call with zeros in the page's place, or with
+    the length that the bad one is clamped to."""
+    import torch
+
+    dt = {"bf16": torch.bfloat16, "fp16": torch.float16}[dtype]
+    g = torch.Generator(device="cuda").manual_seed(5)
+    page, Hkv, G = 64, 8, 8
+    lens = [(300, 5)] + [(30000 + 17 * i, 5) if i % 2 else (200, 20) for i in range(24)] + [
+        (120000, 5), (110000, 300), (900, 1), (30000, 300), (300, 40), (64000, 1)]
+    n = len(lens)
+    need = [-(-(c + w) // page) for c, w in lens]
+    n_pages = sum(need) + 1
+    kc, vc = (torch.randn(n_pages, page, Hkv, 128, device="cuda", generator=g).to(dt) for _ in range(2))
+    table = torch.full((n, max(need)), -1, dtype=torch.int32, device="cuda")
+    at = 0
+    for i, m in enumerate(need):
+        table[i, :m] = torch.arange(at, at + m, dtype=torch.int32, device="cuda")
+        at += m
+    kc[at], vc[at] = 0, 0  # the last page
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    q_start, k_len = i32(np.cumsum([0] + [w for _, w in lens])), i32([c + w for c, w in lens])
+    q = torch.randn(int(q_start[-1]), Hkv * G, 128, device="cuda", generator=g).to(dt)
+    ws = torch.full((lca.attn_paged_workspace_size(q, kc, vc, table, CAUSAL),), 0xA5, dtype=torch.uint8, device="cuda")
+
+    def call(table, k_len):
+        o, lse = torch.full_like(q, 7.0), torch.full((Hkv * G, q.shape[0]), 7.0, device="cuda")
+        lca.attn_paged(q, kc, vc, table, q_start, k_len, CAUSAL, out=o, lse=lse, workspace=ws)
+        return o, lse, lca.read_status(ws)[0]
+
+    def put(t, *at, value):
+        t = t.clone()
+        t[at] = value
+        return t
+
+    for who in (0, n - 2, n - 1):  # served by the kernel for many rows, and by the one for few
+        want = call(put(table, who, 3, value=at), k_len)
+        bad = call(put(table, who, 3, value=-1), k_len)
+        assert want[2] == 0 and bad[2] == 6
+        assert torch.equal(want[0], bad[0]) and torch.equal(want[1], bad[1])
+    want, bad = call(table, put(k_len, 0, value=0)), call(table, put(k_len, 0, value=-5))
+    assert want[2] == 0 and bad[2] == 6
+    assert torch.equal(want[0], bad[0]) and torch.equal(want[1], bad[1])
+
+
 def test_q_rows_of_a_wider_projection_and_no_requests(lca):
     import torch
 
