@@ -298,8 +298,11 @@ typedef struct {
  * answered on the device, without a fault: an entry of free_pages outside
  * [0, n_pages) or past n_free becomes table entry -1, and a token on a page
  * outside [0, n_pages) gets slot -1; a negative length counts as 0; tokens
- * past max_pages * page_size get slot -1 and k_len stops there; rows past
- * n_rows are dropped (q_start stops there).
+ * past max_pages * page_size get slot -1 and k_len stops there, but not
+ * q_start; rows past n_rows are dropped: q_start stops there, but not k_len.
+ * So where state[2] is not 0, the last q_len of k_len tokens need not be a
+ * request's rows, and lca_attn_paged needs ctx_len as well (lca_paged_shape)
+ * to place them.
  * ctx_len, new_len [n_seq], free_pages [n_free], taken [1]: int32, device.
  * block_table: int32, device, n_seq rows of max_pages entries, table_stride
  * entries apart (>= max_pages); n_seq below 2^30.  n_rows: rows of the packed batch, at least
@@ -330,6 +333,9 @@ typedef struct {
   int32_t max_q_len;    /* no request has more new tokens than this; 0: not
                            known.  Chooses kernels, never results.           */
   float scale;          /* softmax scale; 0 selects 1/sqrt(d)                */
+  const int32_t* ctx_len; /* null, or device int32 [n_seq]: the tokens that
+                           each request had before its new ones, as given to
+                           lca_paged_plan                                    */
 } lca_paged_shape;
 
 /* Attention of new tokens over the cache: row q_start[i] + t of q is new
@@ -338,7 +344,13 @@ typedef struct {
  * keeps (positions as in lca_mask_kind, the request being the segment; the
  * new tokens' own keys must be in the cache already).  A request with one new
  * token is a decode step, one with many a prompt or a chunk of one; a batch
- * may mix them.  Masks: FULL, CAUSAL, SLIDING, CAUSAL_SLIDING, DOC,
+ * may mix them.
+ * With shape->ctx_len new token t is at position ie = t + ctx_len[i] whatever
+ * k_len[i] is, and its request has no keys past the last of its rows: the
+ * same where k_len[i] = ctx_len[i] + new tokens, and right also where
+ * lca_paged_plan had no room for some of them.  A token at or past k_len[i]
+ * has no key and attends nothing.
+ * Masks: FULL, CAUSAL, SLIDING, CAUSAL_SLIDING, DOC,
  * CAUSAL_DOC, GLOBAL_SLIDING, CAUSAL_BLOCKWISE, PREFIX_LM_CAUSAL and
  * BLOCK_CAUSAL_DOC (LCA_ERR_UNSUPPORTED for the others).
  * q: device, the cache's dtype, [Tq] rows of Hq * d dense elements, q_stride
@@ -352,8 +364,9 @@ typedef struct {
  * Nothing that lies in the cache behind a request's last key, or in keys
  * that the mask hides from all of its new tokens, reaches a result (infinities
  * and NaN included).  A table entry outside [0, n_pages) that a row needs
- * reads as zeros; q_start that decreases or leaves [0, Tq] and k_len outside
- * [0, max_pages * page_size] are clamped; each sets LCA_ERR_DEVICE_ARG in the
+ * reads as zeros; q_start that decreases or leaves [0, Tq] and k_len or
+ * ctx_len outside [0, max_pages * page_size] are clamped; each, and a token at
+ * or past k_len[i] where ctx_len is given, sets LCA_ERR_DEVICE_ARG in the
  * status word (lca_read_status). */
 LCA_API lca_status lca_attn_paged(const void* q, const lca_paged_cache* cache, const int32_t* block_table,
                                   const int32_t* q_start, const int32_t* k_len, void* o, float* lse,
@@ -464,7 +477,7 @@ LCA_API const char* lca_status_string(lca_status status);
  * changes (102: lca_mask_tile_classes reports the empty-half flags; 103:
  * outputs may be mapped host memory, and every pointer's kind is checked;
  * 104: device pointers of another device than the current one are refused;
- * 105: the paged cache). */
+ * 105: the paged cache; 106: lca_paged_shape.ctx_len). */
 LCA_API int32_t lca_version(void);
 
 #ifdef __cplusplus

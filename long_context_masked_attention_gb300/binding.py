@@ -78,7 +78,8 @@ class PagedCache_t(C.Structure):
 
 class PagedShape_t(C.Structure):
     _fields_ = [("Tq", C.c_int32), ("Hq", C.c_int32), ("n_seq", C.c_int32), ("max_pages", C.c_int32),
-                ("table_stride", C.c_int64), ("q_stride", C.c_int64), ("max_q_len", C.c_int32), ("scale", C.c_float)]
+                ("table_stride", C.c_int64), ("q_stride", C.c_int64), ("max_q_len", C.c_int32), ("scale", C.c_float),
+                ("ctx_len", C.c_void_p)]
 
 
 _lib = None
@@ -709,7 +710,7 @@ def attn_paged_workspace_size(q, k_cache, v_cache, block_table, mask, scale=0.0,
 
 
 def attn_paged(q, k_cache, v_cache, block_table, q_start, k_len, mask, scale=0.0, max_q_len=0, out=None, lse=None,
-               workspace=None, stream=None):
+               workspace=None, stream=None, ctx_len=None):
     """Attention of packed new tokens q [T, Hq, 128] (row stride free) over a
     paged cache [n_pages, page_size, Hkv, 128] (strides free), bf16 or fp16 ->
     (o [T, Hq, 128], lse [Hq, T]).  Request i owns rows q_start[i] to
@@ -717,8 +718,11 @@ def attn_paged(q, k_cache, v_cache, block_table, q_start, k_len, mask, scale=0.0
     block_table[i]; its new tokens are the last of them.  q_start, k_len and
     block_table are int32 CUDA tensors read when the kernels run.  mask: any
     interval family (see lca_attn_paged).  max_q_len: no request has more new
-    tokens (0: unknown).  After a synchronize, read_status(workspace) tells
-    whether a table entry or a length was out of range."""
+    tokens (0: unknown).  ctx_len [n_seq]: the cached tokens that paged_plan was
+    given; with it the new tokens are those that follow them, also in a request
+    that the plan had no room for all of (plan.state[2] counts those).  After
+    a synchronize, read_status(workspace) tells whether a table entry or a
+    length was out of range."""
     import torch
 
     cache = _paged_cache(k_cache, v_cache)
@@ -728,6 +732,8 @@ def attn_paged(q, k_cache, v_cache, block_table, q_start, k_len, mask, scale=0.0
     n_seq = shape.n_seq
     qsp = _ptr(q_start, "q_start", torch.int32, (n_seq + 1,), dev)
     klp = _ptr(k_len, "k_len", torch.int32, (n_seq,), dev)
+    if ctx_len is not None and n_seq:
+        shape.ctx_len = _ptr(ctx_len, "ctx_len", torch.int32, (n_seq,), dev)
     side = _side_stream(stream, dev)
     size, lsize = q.shape, (shape.Hq, shape.Tq)
     if out is None:
@@ -755,6 +761,8 @@ def attn_paged(q, k_cache, v_cache, block_table, q_start, k_len, mask, scale=0.0
     if side is not None:
         for t in (q, k_cache, v_cache, block_table, q_start, k_len, out, lse, workspace):
             t.record_stream(side)
+        if ctx_len is not None:
+            ctx_len.record_stream(side)
     _call(load().lca_attn_paged, "lca_attn_paged", dev, side, q.data_ptr(), C.byref(cache), tp, qsp, klp, op, lp,
           C.byref(shape), C.byref(md), workspace.data_ptr(), workspace.numel())
     return out, lse

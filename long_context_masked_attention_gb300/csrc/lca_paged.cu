@@ -595,20 +595,33 @@ __device__ __forceinline__ void st_row16(T* dst, const float (&x)[16]) {
   *reinterpret_cast<uint4*>(dst + 8) = make_uint4(w[4], w[5], w[6], w[7]);
 }
 
-// o = 0, lse = -inf in rows that no request owns: [0, lo) and [hi, Tq).
-__device__ __noinline__ void clear_unowned_rows(const PagedAttnArgs& a) {
-  const SegInfo s0 = a.n_seq > 0 ? paged_seg(a, 0) : SegInfo{};
-  const SegInfo s1 = a.n_seq > 0 ? paged_seg(a, a.n_seq - 1) : SegInfo{};
-  const int lo = s0.q_off, hi = s1.q_off + s1.q_len;
-  const long long n = static_cast<long long>(lo + max(a.Tq - hi, 0)) * a.Hq * 16;
+// o = 0, lse = -inf in the rows [r0, r1), by all CTAs.
+__device__ __noinline__ void clear_rows(const PagedAttnArgs& a, int r0, int r1) {
+  const long long n = static_cast<long long>(r1 - r0) * a.Hq * 16;
   for (long long t = blockIdx.x * static_cast<long long>(kDecThreads) + threadIdx.x; t < n;
        t += gridDim.x * static_cast<long long>(kDecThreads)) {
     const unsigned rh = static_cast<unsigned>(t >> 4);  // Tq Hq < 2^31
     const unsigned h = rh % a.Hq;
-    long long row = rh / a.Hq;
-    if (row >= lo) row += hi - lo;
+    const long long row = r0 + static_cast<long long>(rh / a.Hq);
     reinterpret_cast<uint4*>(a.o)[(row * a.Hq + h) * 16 + (t & 15)] = make_uint4(0, 0, 0, 0);
     if ((t & 15) == 0) a.lse[static_cast<long long>(h) * a.Tq + row] = -INFINITY;
+  }
+}
+
+// Rows outside every request, and rows of a request behind its last key.
+__device__ __forceinline__ void clear_unowned_rows(const PagedAttnArgs& a) {
+  const SegInfo s0 = a.n_seq > 0 ? paged_rows(a, 0) : SegInfo{};
+  const SegInfo s1 = a.n_seq > 0 ? paged_rows(a, a.n_seq - 1) : SegInfo{};
+  clear_rows(a, 0, s0.q_off);
+  clear_rows(a, s1.q_off + s1.q_len, a.Tq);
+  if (!a.ctx_len) return;
+  for (int base = 0; base < a.n_seq; base += kDecThreads) {
+    const int i = base + threadIdx.x;
+    if (!__syncthreads_or(i < a.n_seq && paged_seg(a, i).q_len < paged_rows(a, i).q_len)) continue;
+    for (int k = base; k < min(base + kDecThreads, a.n_seq); ++k) {
+      const SegInfo s = paged_seg(a, k);
+      clear_rows(a, s.q_off + s.q_len, s.q_off + paged_rows(a, k).q_len);
+    }
   }
 }
 

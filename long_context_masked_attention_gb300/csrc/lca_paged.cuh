@@ -78,15 +78,29 @@ __device__ __forceinline__ bool in_span(const Span& s, int j) {
   return (j >= s.a0 && j < s.b0) || (j >= s.a1 && j < s.b1);
 }
 
-// Request i with its lengths clamped to what the tensors hold (paged_begin
-// reports those that need it).
-__device__ __forceinline__ SegInfo paged_seg(const PagedAttnArgs& a, int i) {
+// Rows and keys of request i, clamped to what the tensors hold
+// (paged_begin_kernel reports lengths that need it).
+__device__ __forceinline__ SegInfo paged_rows(const PagedAttnArgs& a, int i) {
   const int r0 = a.q_start[i], r1 = a.q_start[i + 1], kl = a.k_len[i];
   const int room = a.max_pages * a.page_size;
   SegInfo s{};
   s.q_off = min(max(r0, 0), a.Tq);
   s.q_len = min(max(r1, s.q_off), a.Tq) - s.q_off;
   s.k_len = min(max(kl, 0), room);
+  return s;
+}
+
+// Those of them that attention serves.  Where ctx_len says how many tokens
+// came before the rows, the keys end with the last row and the rows with the
+// last key, so that the rows are the last of the keys again; the rows behind
+// have no key (clear_unowned_rows).
+__device__ __forceinline__ SegInfo paged_seg(const PagedAttnArgs& a, int i) {
+  SegInfo s = paged_rows(a, i);
+  if (a.ctx_len) {
+    const int first = min(max(a.ctx_len[i], 0), a.max_pages * a.page_size);
+    s.k_len = min(s.k_len, first + s.q_len);
+    s.q_len = max(s.k_len - first, 0);
+  }
   return s;
 }
 

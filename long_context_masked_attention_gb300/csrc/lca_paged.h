@@ -59,6 +59,7 @@ struct PagedAttnArgs {
   const void *kc, *vc;
   long long q_stride, page_stride, token_stride, head_stride, table_stride;  // elements
   const int *table, *q_start, *k_len;
+  const int* ctx_len;  // null: a request's rows are the last of its k_len tokens
   void* o;
   float* lse;
   int* status;

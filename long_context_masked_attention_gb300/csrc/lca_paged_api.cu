@@ -309,7 +309,7 @@ lca_status lca_attn_paged(const void* q, const lca_paged_cache* cache, const int
   const long long n_table =
       shape->n_seq > 0 && shape->max_pages > 0 ? (shape->n_seq - 1) * shape->table_stride + shape->max_pages : 0;
   if (!ints(block_table, n_table) || !ints(q_start, shape->n_seq > 0 ? shape->n_seq + 1LL : 0) ||
-      !ints(k_len, shape->n_seq) || !cache_memory(cache))
+      !ints(k_len, shape->n_seq) || (shape->ctx_len && !ints(shape->ctx_len, shape->n_seq)) || !cache_memory(cache))
     return LCA_ERR_INVALID_ARG;
   if (shape->Tq > 0) {
     if (!q || !aligned16(q) || !device_input(q) || !o || !aligned16(o) || !device_input(o) || !lse || !aligned4(lse) ||
@@ -322,7 +322,7 @@ lca_status lca_attn_paged(const void* q, const lca_paged_cache* cache, const int
     const struct {
       const void* p;
       long long bytes;
-    } t[9] = {{o, rows * heads * kHeadDim * 2},
+    } t[10] = {{o, rows * heads * kHeadDim * 2},
               {lse, rows * heads * 4},
               {workspace, static_cast<long long>(L.total)},
               {q, ((rows - 1) * shape->q_stride + heads * kHeadDim) * 2},
@@ -330,9 +330,10 @@ lca_status lca_attn_paged(const void* q, const lca_paged_cache* cache, const int
               {cache->v, extent},
               {block_table, 4 * n_table},
               {q_start, 4 * (shape->n_seq + 1LL)},
-              {k_len, 4LL * shape->n_seq}};
+              {k_len, 4LL * shape->n_seq},
+              {shape->ctx_len, shape->ctx_len ? 4LL * shape->n_seq : 0}};
     for (int i = 0; i < 3; ++i)  // the first three are written
-      for (int j = i + 1; j < 9; ++j)
+      for (int j = i + 1; j < 10; ++j)
         if (overlap(t[i].p, t[i].bytes, t[j].p, t[j].bytes)) return LCA_ERR_INVALID_ARG;
   }
   const int sms = num_sms();
@@ -349,6 +350,7 @@ lca_status lca_attn_paged(const void* q, const lca_paged_cache* cache, const int
   a.table = block_table;
   a.q_start = q_start;
   a.k_len = k_len;
+  a.ctx_len = shape->ctx_len;
   a.o = o;
   a.lse = lse;
   a.status = reinterpret_cast<int*>(ws + L.status);

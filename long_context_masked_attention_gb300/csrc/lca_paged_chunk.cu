@@ -245,6 +245,11 @@ __global__ void __launch_bounds__(1024) paged_begin_kernel(const __grid_constant
   for (int i = threadIdx.x; i < a.n_seq; i += 1024) {
     const int r0 = a.q_start[i], r1 = a.q_start[i + 1], kl = a.k_len[i];
     if (r0 < 0 || r1 < r0 || r1 > a.Tq || kl < 0 || kl > room) paged_report(a.status, kStatusDeviceArg, 50);
+    if (a.ctx_len) {
+      const int c = a.ctx_len[i];
+      if (c < 0 || c > room || paged_seg(a, i).q_len < paged_rows(a, i).q_len)
+        paged_report(a.status, kStatusDeviceArg, 52);
+    }
   }
   if (many) place_items(a);
 }

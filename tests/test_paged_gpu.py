@@ -794,3 +794,90 @@ def test_agrees_with_the_packed_forward_and_merges(lca):
     # each part is rounded to bf16 once more before the merge: twice the one call's bound
     assert bool(((o3.double().cpu() - torch.from_numpy(ref[0][96:333])).abs() <= 2 * torch.from_numpy(ref[2][96:333]) + 2.0 ** -8 * torch.from_numpy(ref[0][96:333]).abs() + 2.0 ** -7).all())
     assert bool(((lse3.double().cpu() - torch.from_numpy(ref[1][:, 96:333])).abs() <= 1e-4).all())
+
+
+FITS_NOT = {
+    # (cached, new) per request, rows of the packed batch, entries of a table row
+    "rows": ([(30, 3), (100, 40), (5, 7), (64, 1)], 20, 12),
+    "table": ([(60, 8), (10, 20), (64, 5), (3, 70), (63, 2), (0, 64), (50, 1)], 175, 4),
+    "both": ([(0, 70), (62, 3), (1, 2), (40, 300)], 200, 4),
+    "long": ([(1500, 700), (2000, 90), (2047, 1), (2048, 1), (1990, 300)], 900, 128),
+}
+
+
+@pytest.mark.parametrize("mask", MASKS, ids=lambda m: f"{m.kind}{m.window_left or ''}")
+@pytest.mark.parametrize("case", FITS_NOT)
+def test_a_batch_that_does_not_fit_keeps_its_positions(lca, case, mask):
+    """Plan, write and attention of requests that the packed rows or the
+    tables have no room for: the rows with a slot are attended at the plan's
+    positions, to keys that were written (all else in the cache is NaN); the
+    others get 0 and -inf."""
+    import torch
+
+    lens, rows, width = FITS_NOT[case]
+    page, Hq, Hkv, n = 16, 8, 2, len(lens)
+    room, g = width * page, torch.Generator().manual_seed(len(case))
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    n_pages = sum(-(-c // page) for c, _ in lens) + sum(-(-w // page) + 1 for _, w in lens)
+    perm = torch.randperm(n_pages, generator=g).to(torch.int32)
+    table, at = torch.full((n, width), -1, dtype=torch.int32), 0
+    kc, vc = (torch.full((n_pages, page, Hkv, 128), float("nan"), dtype=torch.bfloat16) for _ in range(2))
+    old = [[torch.randn(c, Hkv, 128, generator=g).to(torch.bfloat16) for _ in range(2)] for c, _ in lens]
+    for i, (c, _) in enumerate(lens):
+        m, j = -(-c // page), torch.arange(c)
+        table[i, :m] = perm[at:at + m]
+        at += m
+        for cache, x in zip((kc, vc), old[i]):
+            cache[table[i].long()[j // page], j % page] = x
+    q, k, v = (torch.randn(rows, h, 128, generator=g).to(torch.bfloat16) for h in (Hq, Hkv, Hkv))
+    kc, vc, table, qd = kc.cuda(), vc.cuda(), table.cuda(), q.cuda()
+    ctx = i32([c for c, _ in lens])
+    plan = lca.paged_plan(ctx, i32([w for _, w in lens]), perm[at:].cuda(), i32([0]), table, page, n_pages, rows)
+    lca.paged_write(k.cuda(), v.cuda(), kc, vc, plan.slots)
+    assert int(plan.state[1]) == 0 and int(plan.state[2]) > 0
+    segs, ks, vs, kat, row, behind = [], [], [], 0, 0, False
+    for i, (c, w) in enumerate(lens):
+        have = min(row + w, rows) - min(row, rows)  # its rows in the batch
+        served = min(have, room - c)
+        behind |= served < have
+        segs.append(Segment(min(row, rows), served, kat, c + served))
+        ks += [old[i][0], k[row:row + served]]
+        vs += [old[i][1], v[row:row + served]]
+        assert plan.positions[row:row + served].tolist() == list(range(c, c + served))
+        assert (plan.slots[row:row + have] >= 0).tolist() == [t < served for t in range(have)]
+        kat, row = kat + c + served, row + w
+    p = make([(0, 1)], 16, Hq, Hkv, mask)
+    p.q, p.kc, p.vc, p.table, p.q_start, p.k_len = qd, kc, vc, table, plan.q_start, plan.k_len
+    p.k, p.v = torch.cat(ks), torch.cat(vs)
+    p.prob.Tq, p.prob.Tk, p.prob.segments = rows, kat, segs
+    ref = reference(p)
+    for hint in (0, 700):
+        o, lse, st = attend(lca, p, ctx_len=ctx, max_q_len=hint)
+        assert st[0] == (6 if behind else 0)
+        check(o, lse, p, ref, what=f"{case}, max_q_len={hint}")
+
+
+@pytest.mark.parametrize("lens", [DECODE, CHUNKS, [(3000, 1), (100, 1), (2000, 40), (0, 300)]], ids=["decode", "chunks", "mixed"])
+def test_cached_lengths_change_nothing_in_a_batch_that_fits(lca, lens):
+    import torch
+
+    p = make(lens, 16, 8, 2, CAUSAL, pad=3, seed=4, device="cuda")
+    ctx = torch.tensor([c for c, _ in lens], dtype=torch.int32, device="cuda")
+    a, b = attend(lca, p), attend(lca, p, ctx_len=ctx)
+    assert a[2] == b[2] == (0, 0) and torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    o, lse = lca.attn_paged(p.q, p.kc, p.vc, p.table, p.q_start, p.k_len, CAUSAL, ctx_len=ctx, stream=s)
+    s.synchronize()
+    assert torch.equal(a[0], o) and torch.equal(a[1], lse)
+    for i, x in ((0, -3), (1, p.table.shape[1] * 16 + 1), (2, 2**31 - 1), (0, -2**31)):
+        bad = ctx.clone()
+        bad[i] = x
+        assert attend(lca, p, ctx_len=bad)[2] == (6, 52)
+    for bad in (ctx.long(), ctx[1:], ctx.cpu(), torch.stack([ctx, ctx], 1)[:, 0]):
+        with pytest.raises(ValueError, match="ctx_len"):
+            lca.attn_paged(p.q, p.kc, p.vc, p.table, p.q_start, p.k_len, CAUSAL, ctx_len=bad)
+    out = torch.empty(p.q.shape, dtype=p.q.dtype, device="cuda")
+    inside = out.view(-1).view(torch.int32)[:len(lens)]
+    with pytest.raises(lca.LcaError, match="INVALID"):
+        lca.attn_paged(p.q, p.kc, p.vc, p.table, p.q_start, p.k_len, CAUSAL, ctx_len=inside, out=out)
