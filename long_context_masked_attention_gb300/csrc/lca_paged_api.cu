@@ -316,7 +316,7 @@ lca_status lca_attn_paged(const void* q, const lca_paged_cache* cache, const int
         !device_input(lse))
       return LCA_ERR_INVALID_ARG;
   }
-  if (shape->Tq > 0) {
+  {  // an empty batch writes its workspace too
     const long long rows = shape->Tq, heads = shape->Hq;
     const long long extent = cache_extent(cache);
     const struct {
@@ -325,7 +325,7 @@ lca_status lca_attn_paged(const void* q, const lca_paged_cache* cache, const int
     } t[10] = {{o, rows * heads * kHeadDim * 2},
               {lse, rows * heads * 4},
               {workspace, static_cast<long long>(L.total)},
-              {q, ((rows - 1) * shape->q_stride + heads * kHeadDim) * 2},
+              {q, rows > 0 ? ((rows - 1) * shape->q_stride + heads * kHeadDim) * 2 : 0},
               {cache->k, extent},
               {cache->v, extent},
               {block_table, 4 * n_table},

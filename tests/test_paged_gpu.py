@@ -581,6 +581,28 @@ def test_overlapping_outputs_are_refused(lca):
             call(**kw)
 
 
+@pytest.mark.parametrize("rows", [0, 3])
+def test_a_workspace_inside_an_input_is_refused(lca, rows):
+    """Whatever the batch: one without rows writes its workspace too."""
+    import torch
+
+    p = make([(40, 3)], 16, 8, 8, CAUSAL, seed=2, device="cuda")
+    q, starts = p.q[:rows], torch.tensor([0, rows], dtype=torch.int32, device="cuda")
+    need = lca.attn_paged_workspace_size(p.q, p.kc, p.vc, p.table, CAUSAL)
+    buf = torch.zeros(need + 4096, dtype=torch.uint8, device="cuda")
+    ints = buf[1024:].view(torch.int32)
+    kc = buf[:need // 4096 // 16 * 4096 * 16].view(torch.bfloat16).view(-1, 16, 8, 128)
+    assert kc.numel() * 2 >= need - 65536
+    kw = dict(q_start=starts, k_len=p.k_len, block_table=p.table, k_cache=p.kc, v_cache=p.vc)
+    for over in (dict(k_cache=kc, v_cache=kc), dict(q_start=ints[:2]), dict(k_len=ints[:1]), dict(ctx_len=ints[:1]),
+                 dict(block_table=ints[:8].view(1, 8))):
+        with pytest.raises(lca.LcaError, match="INVALID"):
+            lca.attn_paged(q, mask=CAUSAL, workspace=buf[:need], **{**kw, **over})
+    assert not bool(buf.any())
+    lca.attn_paged(q, mask=CAUSAL, workspace=buf[:need], **kw)
+    assert lca.read_status(buf) == (0, 0)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 def test_large_scores_and_an_explicit_scale(lca, dtype):
     """Scores of some hundreds (one key takes all), and a scale of the user's own."""
