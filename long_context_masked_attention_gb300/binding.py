@@ -169,6 +169,14 @@ def _i32(seq):
     return arr, arr.ctypes.data_as(C.POINTER(C.c_int32))
 
 
+def _int32(x, name):
+    """x as a C int32 field takes it; ctypes would keep the low 32 bits."""
+    x = int(x)
+    if not -(1 << 31) <= x < 1 << 31:
+        raise ValueError(f"{name}: {x} does not fit 32 bits")
+    return x
+
+
 def marshal(Tq, Tk, Hq, Hkv, d, segments, mask, scale=0.0, device=None) -> Call:
     """segments: iterable of objects with q_off/q_len/k_off/k_len or 4-tuples."""
     import torch
@@ -604,7 +612,7 @@ def _table(t, n_seq, device):
     a, b = t.stride()
     if (n_seq and b != 1 and width > 1) or (n_seq > 1 and a < width):
         raise ValueError("block_table: each row must be contiguous, and rows must not overlap")
-    return t.data_ptr(), width, a if n_seq > 1 else width
+    return t.data_ptr(), _int32(width, "block_table: entries per row"), a if n_seq > 1 else width
 
 
 def paged_plan(ctx_len, new_len, free_pages, taken, block_table, page_size, n_pages, n_rows, q_start=None, k_len=None,
@@ -622,7 +630,8 @@ def paged_plan(ctx_len, new_len, free_pages, taken, block_table, page_size, n_pa
     for name, t in (("ctx_len", ctx_len), ("free_pages", free_pages)):
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
-    n_seq, n_free, dev, i32, n_rows = ctx_len.numel(), free_pages.numel(), ctx_len.device, torch.int32, int(n_rows)
+    n_seq, n_free = _int32(ctx_len.numel(), "ctx_len: entries"), _int32(free_pages.numel(), "free_pages: entries")
+    dev, i32, n_rows = ctx_len.device, torch.int32, int(n_rows)
     if not 0 <= n_rows < 1 << 31:  # a C int32 would keep the low bits
         raise ValueError(f"n_rows: {n_rows}, expected 0 to 2^31 - 1")
     if not 0 < page_size < 1 << 31:
@@ -677,10 +686,10 @@ def _paged_mask(mask):
     kind = mask.kind
     if not isinstance(kind, int):
         kind = MASK_KINDS.index(kind)
-    md = MaskDesc_t(kind)
+    md = MaskDesc_t(_int32(kind, "kind"))
     if kind not in _PLAIN_KINDS:
         for name in ("window_left", "window_right", "num_global", "prefix_len", "block"):
-            setattr(md, name, int(getattr(mask, name, 0) or 0))
+            setattr(md, name, _int32(getattr(mask, name, 0) or 0, name))
     return md
 
 
@@ -693,7 +702,8 @@ def _paged_shape(q, cache, k_cache, block_table, scale, max_q_len):
     qs = _rows(q, "q", None, cache.d, k_cache.dtype, dev)
     tp, width, tstride = _table(block_table, None, dev)
     shape = q.shape
-    return PagedShape_t(shape[0], shape[1], block_table.shape[0], width, tstride, qs, max_q_len, scale), tp
+    return PagedShape_t(shape[0], shape[1], block_table.shape[0], width, tstride, qs, _int32(max_q_len, "max_q_len"),
+                        scale), tp
 
 
 def _paged_size(shape, cache, md):

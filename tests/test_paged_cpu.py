@@ -255,3 +255,41 @@ def test_numbers_past_32_bits_are_not_cut(monkeypatch):
     assert not called
     lib.paged_plan(s, s, s, s[:1], t, 16, 4, 3, **outs)
     assert len(called) == 1
+
+
+@pytest.mark.parametrize("kind", ["SLIDING", "CAUSAL_SLIDING", "GLOBAL_SLIDING", "PREFIX_LM_CAUSAL", "CAUSAL_BLOCKWISE"])
+@pytest.mark.parametrize("value", [1 << 31, 1 << 32, (1 << 40) + 16, -(1 << 32) + 16])
+def test_distances_past_32_bits_are_refused(kind, value):
+    """A window of 2^32 meant as no limit would be one of 0, a block of 2^32 + 16 one of 16."""
+    for name in ("window_left", "window_right", "num_global", "prefix_len", "block"):
+        with pytest.raises(ValueError, match=name):
+            B._paged_mask(MaskSpec(kind, **{name: value}))
+        assert getattr(B._paged_mask(MaskSpec(kind, **{name: 0x7FFFFFFF})), name) == 0x7FFFFFFF
+
+
+def test_tensors_past_32_bits_are_refused():
+    meta = torch.device("meta")
+    with pytest.raises(ValueError, match="kind"):
+        B._paged_mask(MaskSpec((1 << 32) + 1))  # CAUSAL is 1
+    with pytest.raises(ValueError, match="entries"):
+        B._table(torch.empty(1, (1 << 32) + 4, dtype=torch.int32, device=meta), 1, meta)
+    s, long = torch.empty(1, dtype=torch.int32, device=meta), torch.empty((1 << 32) + 1, dtype=torch.int32, device=meta)
+    t = torch.empty(1, 4, dtype=torch.int32, device=meta)
+    for args in ((long, s, s), (s, s, long)):
+        with pytest.raises(ValueError, match="entries"):
+            lib.paged_plan(*args, s, t, 16, 4, 3)
+
+
+def test_a_longest_request_past_32_bits_is_refused():
+    meta = torch.device("meta")
+    q = torch.empty(3, 8, 128, dtype=torch.bfloat16, device=meta)
+    kc = torch.empty(4, 16, 2, 128, dtype=torch.bfloat16, device=meta)
+    table = torch.empty(2, 4, dtype=torch.int32, device=meta)
+
+    def shape(max_q_len):
+        return B._paged_shape(q, cache(), kc, table, 0.0, max_q_len)[0].max_q_len
+
+    assert shape(3) == 3
+    for n in (1 << 31, (1 << 32) + 1, -(1 << 32)):
+        with pytest.raises(ValueError, match="max_q_len"):
+            shape(n)
