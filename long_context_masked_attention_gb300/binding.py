@@ -185,19 +185,17 @@ def marshal(Tq, Tk, Hq, Hkv, d, segments, mask, scale=0.0, device=None) -> Call:
     seg_arr = (Segment_t * max(1, len(segs)))()
     for i, s in enumerate(segs):
         if isinstance(s, (tuple, list)):
-            seg_arr[i] = Segment_t(*[int(x) for x in s])
+            seg_arr[i] = Segment_t(*[_int32(x, f"segment {i}") for x in s])
         else:
-            seg_arr[i] = Segment_t(int(s.q_off), int(s.q_len), int(s.k_off), int(s.k_len))
-    shape = Shape_t(int(Tq), int(Tk), int(Hq), int(Hkv), int(d), len(segs), seg_arr, float(scale))
+            seg_arr[i] = Segment_t(*[_int32(x, f"segment {i}") for x in (s.q_off, s.q_len, s.k_off, s.k_len)])
+    dims = [_int32(x, name) for x, name in ((Tq, "Tq"), (Tk, "Tk"), (Hq, "Hq"), (Hkv, "Hkv"), (d, "d"))]
+    shape = Shape_t(*dims, len(segs), seg_arr, float(scale))
     md = MaskDesc_t()
     keep = [seg_arr]
     kind = mask.kind if isinstance(mask.kind, int) else MASK_KINDS.index(mask.kind)
-    md.kind = kind
-    md.window_left = int(getattr(mask, "window_left", 0) or 0)
-    md.window_right = int(getattr(mask, "window_right", 0) or 0)
-    md.num_global = int(getattr(mask, "num_global", 0) or 0)
-    md.prefix_len = int(getattr(mask, "prefix_len", 0) or 0)
-    md.block = int(getattr(mask, "block", 0) or 0)
+    md.kind = _int32(kind, "kind")
+    for name in ("window_left", "window_right", "num_global", "prefix_len", "block", "q_block", "kv_block"):
+        setattr(md, name, _int32(getattr(mask, name, 0) or 0, name))
     if getattr(mask, "seg_prefix", None) is not None:
         arr, ptr = _i32(mask.seg_prefix)
         keep.append(arr)
@@ -207,9 +205,7 @@ def marshal(Tq, Tk, Hq, Hkv, d, segments, mask, scale=0.0, device=None) -> Call:
         keep.append(arr)
         md.part_bounds = ptr
         md.n_part_bounds = len(arr)
-    md.q_block = int(getattr(mask, "q_block", 0) or 0)
-    md.kv_block = int(getattr(mask, "kv_block", 0) or 0)
-    md.heads_in_map = int(getattr(mask, "heads_in_map", 1) or 1)
+    md.heads_in_map = _int32(getattr(mask, "heads_in_map", 1) or 1, "heads_in_map")
     for name, cnt in (("qb_bounds", "n_qb"), ("kb_bounds", "n_kb")):
         b = getattr(mask, name, None)
         if b is not None:

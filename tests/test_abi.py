@@ -184,3 +184,26 @@ def test_binding_rejects_unsuitable_tensors_before_calling_the_library():
     # outputs may be pinned host tensors, never pageable ones
     with pytest.raises(ValueError, match="pinned"):
         B._require(q, "dq", (8, 2, 128), torch.bfloat16, host_ok=True)
+
+
+@pytest.mark.parametrize("name", ["window_left", "window_right", "num_global", "prefix_len", "block", "q_block",
+                                  "kv_block", "heads_in_map"])
+def test_mask_numbers_past_32_bits_are_refused(name):
+    """ctypes would keep the low 32 bits: a window of 2^32, meant as no limit, as one of 0."""
+    seg = [Segment(0, 256, 0, 256)]
+    for value in (1 << 31, 1 << 32, (1 << 40) + 64):
+        with pytest.raises(ValueError, match=name):
+            B.marshal(256, 256, 4, 2, 128, seg, MaskSpec("CAUSAL_SLIDING", **{name: value}))
+    assert getattr(B.marshal(256, 256, 4, 2, 128, seg, MaskSpec("SLIDING", **{name: 77})).mask, name) == 77
+
+
+def test_shapes_past_32_bits_are_refused():
+    big = (1 << 32) + 256
+    for at, name in enumerate(("Tq", "Tk", "Hq", "Hkv", "d")):
+        dims = [256, 256, 4, 2, 128]
+        dims[at] = big
+        with pytest.raises(ValueError, match=name):
+            B.marshal(*dims, [Segment(0, 256, 0, 256)], MaskSpec("CAUSAL"))
+    for seg in (Segment(0, big, 0, 256), (0, 256, 0, big)):
+        with pytest.raises(ValueError, match="segment 0"):
+            B.marshal(256, 256, 4, 2, 128, [seg], MaskSpec("CAUSAL"))
