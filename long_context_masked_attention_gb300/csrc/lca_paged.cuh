@@ -180,7 +180,9 @@ __device__ __forceinline__ void join_rows(int n, Piece piece, int row0, float& m
       mk = b + p < n ? __ldcg(piece(b + p) + stat) : -INFINITY;
       lk = b + p < n ? __ldcg(piece(b + p) + stat + kRowsOf) : 0.f;
     }
-    const float f = lk != 0.f ? ex2_approx(mk - m) : 0.f;
+    // a piece without keys leaves its values unwritten: -1 marks it.  A factor
+    // that has become 0 is still used, for values that are not finite
+    const float f = lk != 0.f ? ex2_approx(mk - m) : -1.f;
     l = fmaf(f, lk, l);
     const int here = min(W, n - b);
 #pragma unroll 1
@@ -191,7 +193,7 @@ __device__ __forceinline__ void join_rows(int n, Piece piece, int row0, float& m
 #pragma unroll
         for (int r = 0; r < R; ++r) {
           const float fk = __shfl_sync(~0u, f, r * W + min(k + u, W - 1));
-          if (k + u < here && fk != 0.f) {  // a piece without keys leaves its values unwritten
+          if (k + u < here && !(fk < 0.f)) {
             o[r][0] = fmaf(fk, z[u][r].x, o[r][0]);
             o[r][1] = fmaf(fk, z[u][r].y, o[r][1]);
             o[r][2] = fmaf(fk, z[u][r].z, o[r][2]);

@@ -415,6 +415,30 @@ def test_infinities_reach_the_rows_that_attend_them(lca, mask, Hq):
         check(o, lse, p, ref, what=mask.kind)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("new", [1, 3, 300])
+def test_an_infinity_of_small_weight_is_not_lost(lca, new, dtype):
+    """A context in pieces, whose first keys have some 2^-260 of the last ones'
+    weight: an infinity or NaN among their values still reaches every row that
+    attends it, as a weight is never zero."""
+    import torch
+
+    ctx, hit = 16000, 100
+    p = make([(ctx, new), (20, 1)], 64, 8, 1, CAUSAL, dtype, seed=new, device="cuda")
+    p.q.fill_(8.0)
+    for j in range(0, ctx + new, 64):
+        p.kc[int(p.table[0, j // 64])] = -1.0 if j < ctx // 2 else 1.0
+    o0, lse0, _ = attend(lca, p)
+    assert bool(o0.isfinite().all())
+    for value in (float("inf"), float("nan")):
+        p.vc[int(p.table[0, hit // 64]), hit % 64, 0, 77] = value
+        o, lse, st = attend(lca, p)
+        assert st == (0, 0) and torch.equal(lse, lse0)
+        assert not bool(o[:new, :, 77].isfinite().any())
+        o[:new, :, 77] = o0[:new, :, 77]
+        assert torch.equal(o, o0)
+
+
 def test_infinities_among_a_very_long_contexts_last_keys(lca):
     """Pieces of hundreds of thousands of keys, with one value that is not
     finite: what it costs goes by its tile, not by the piece."""
