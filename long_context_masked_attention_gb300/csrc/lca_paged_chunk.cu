@@ -868,7 +868,9 @@ __device__ __forceinline__ void softmax_wg(const PagedAttnArgs& a, int x, uint64
     }
     T* orow = static_cast<T*>(a.o) + (static_cast<long long>(inf.q_off + (valid ? token : 0)) * a.Hq + head) * kHeadDim;
     float* part = inf.part < 0 ? nullptr : a.chunk_parts + inf.part * static_cast<long long>(kPagedChunkPartFloats);
-    if (any && hidden[slot] == it + 1) {
+    // the other warpgroup may set the mark just now, for tiles of its own alone:
+    // a vote, since what follows takes all lanes of the warp together
+    if (__any_sync(0xFFFFFFFFu, any && hidden[slot] == it + 1)) {
       write_hidden<T>(a, inf, x, tO, valid, sp, orow, part ? part + (x * 128 + row) * kHeadDim : nullptr, l);
     } else if (any) {
       const float inv = part ? 1.f : l == 0.f ? 0.f : 1.f / l;
