@@ -17,11 +17,6 @@ struct Half2<__nv_bfloat16> {
   // sign bits set where the exponent is all ones (infinities, NaN); the other
   // bits say nothing
   static __device__ __forceinline__ uint32_t not_finite(uint32_t x) { return (x & 0x7FFF7FFFu) + 0x00800080u; }
-  // the larger magnitudes of two pairs; NaN where one is NaN
-  static __device__ __forceinline__ uint32_t abs_max(uint32_t m, uint32_t x) {
-    asm("{\n\t.reg .b32 t;\n\tabs.bf16x2 t, %1;\n\tmax.NaN.bf16x2 %0, %0, t;\n\t}" : "+r"(m) : "r"(x));
-    return m;
-  }
   static __device__ __forceinline__ float2 unpack(uint32_t x) {
     return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xFFFF0000u));
   }
@@ -34,10 +29,6 @@ struct Half2<__half> {
     return r;
   }
   static __device__ __forceinline__ uint32_t not_finite(uint32_t x) { return (x & 0x7FFF7FFFu) + 0x04000400u; }
-  static __device__ __forceinline__ uint32_t abs_max(uint32_t m, uint32_t x) {
-    asm("{\n\t.reg .b32 t;\n\tabs.f16x2 t, %1;\n\tmax.NaN.f16x2 %0, %0, t;\n\t}" : "+r"(m) : "r"(x));
-    return m;
-  }
   static __device__ __forceinline__ float2 unpack(uint32_t x) {
     return __half22float2(*reinterpret_cast<const __half2*>(&x));
   }
