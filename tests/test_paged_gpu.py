@@ -927,3 +927,40 @@ def test_cached_lengths_change_nothing_in_a_batch_that_fits(lca, lens):
     inside = out.view(-1).view(torch.int32)[:len(lens)]
     with pytest.raises(lca.LcaError, match="INVALID"):
         lca.attn_paged(p.q, p.kc, p.vc, p.table, p.q_start, p.k_len, CAUSAL, ctx_len=inside, out=out)
+
+
+@pytest.mark.parametrize("split", [32, 96, 320])
+def test_merged_parts_are_off_by_their_roundings(lca, split):
+    """A prefix of the keys in one call (FULL), the rest in another (CAUSAL),
+    merged.  With w_p = exp(L_p - L) the merged row is sum_p w_p O_p, so it is
+    off by no more than
+      sum_p w_p (bound of O_p + |O_p| d_p)   d_p: how far log w_p may be off
+      + u |O|                                its own rounding
+    where L is off by the largest bound of the L_p, and d_p by that and L_p's
+    own, each and every exp, log, product and sum in fp32 adding no more than
+    16 e (1 + |L|); (1 + 2^-6) covers products of two such errors."""
+    import torch
+
+    p = make([(0, 333)], 32, 16, 4, CAUSAL, seed=14, device="cuda")
+    q, T = p.q[split:], 333 - split
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    args = p.kc, p.vc
+    a = lca.attn_paged(q, *args, p.table, i32(0, T), i32(split), MaskSpec("FULL"))
+    b = lca.attn_paged(q, *args, p.table[:, split // 32:], i32(0, T), i32(T), CAUSAL)
+    o, lse = lca.attn_merge([a[0], b[0]], [a[1], b[1]])
+    ref = reference(p)
+    O, L = ref[0][split:], ref[1][:, split:]
+    p.q, p.prob.Tq = q, T
+    refs = []
+    for mask, seg, part in ((MaskSpec("FULL"), Segment(0, T, 0, split), a), (CAUSAL, Segment(0, T, split, T), b)):
+        p.prob.mask, p.prob.segments = mask, [seg]
+        refs.append(reference(p))
+        check(*part, p, refs[-1])
+    e, u = 2.0 ** -24, 2.0 ** -8
+    few = 16 * e * (1 + np.abs(L))
+    off_l = np.maximum(refs[0][3], refs[1][3]) + few
+    tol = u * np.abs(O)
+    for Op, Lp, to, tl in refs:
+        w, d = np.exp(Lp - L).T[:, :, None], (tl + off_l + few).T[:, :, None]
+        tol = tol + w * (to + np.abs(Op) * d)
+    check(o, lse, p, (O, L, tol * (1 + 2.0 ** -6), off_l))
