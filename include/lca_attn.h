@@ -267,7 +267,10 @@ typedef enum { LCA_BF16 = 0, LCA_F16 = 1 } lca_dtype;
  * of k and of v (device or managed memory); its d elements are contiguous.
  * Any order of the axes is fine ([page][token][head] and
  * [page][head][token] among them, and K and V as parts of one array), as long
- * as the rows of k, and those of v, do not overlap.  Strides are multiples of
+ * as the rows of k, and those of v, do not overlap.  Pages should be the
+ * outermost axis: otherwise, and with more than 128 query heads per KV head,
+ * lca_attn_paged serves prompts with the kernel made for single tokens, at
+ * about a tenth of the speed.  Strides are multiples of
  * 8 elements, 8 to 2^38; k and v are 16-byte aligned; d must be 128.
  * page_size is a multiple of 8 (LCA_ERR_UNSUPPORTED otherwise) and
  * n_pages * page_size < 2^31. */
@@ -331,7 +334,9 @@ typedef struct {
   int64_t table_stride; /* entries between table rows, >= max_pages          */
   int64_t q_stride;     /* elements between rows of q, >= Hq * d, multiple of 8 */
   int32_t max_q_len;    /* no request has more new tokens than this; 0: not
-                           known.  Chooses kernels, never results.           */
+                           known.  Chooses kernels, never results.  A decode
+                           step that gives 1 needs 26 MB of workspace and two
+                           launches, not 94 and four.                        */
   float scale;          /* softmax scale; 0 selects 1/sqrt(d)                */
   const int32_t* ctx_len; /* null, or device int32 [n_seq]: the tokens that
                            each request had before its new ones, as given to
@@ -357,13 +362,19 @@ typedef struct {
  * apart, 16-byte aligned.  block_table: int32, device.  q_start: int32
  * [n_seq + 1], k_len: int32 [n_seq], device.  o: [Tq][Hq][d] dense, the
  * cache's dtype, 16-byte aligned; lse: float [Hq][Tq], natural log, as
- * lca_attn_fwd writes it and lca_attn_merge reads it.  o, lse and the
+ * lca_attn_fwd writes it and lca_attn_merge reads it (whose o parts are bf16).
+ * The weights are rounded to the cache's dtype before their product with V;
+ * in fp16 one below 2^-31 of the row's largest may count as 0.  o, lse and the
  * workspace must not overlap one another or an input (LCA_ERR_INVALID_ARG;
  * the cache counts from its first to its last element).  Rows that attend
  * nothing, and rows outside every request, get o = 0, lse = -inf.
  * Nothing that lies in the cache behind a request's last key, or in keys
  * that the mask hides from all of its new tokens, reaches a result (infinities
- * and NaN included).  A table entry outside [0, n_pages) that a row needs
+ * and NaN included).  An infinity or NaN in the values of a key makes that
+ * element of o infinite or NaN in the rows that attend the key, and in no
+ * other (NaN also for an infinity whose weight rounds to 0).  GLOBAL_SLIDING's
+ * first num_global tokens attend all keys that are there, so a prompt taken in
+ * chunks gives them other results than one taken at once.  A table entry outside [0, n_pages) that a row needs
  * reads as zeros; q_start that decreases or leaves [0, Tq] and k_len or
  * ctx_len outside [0, max_pages * page_size] are clamped; each, and a token at
  * or past k_len[i] where ctx_len is given, sets LCA_ERR_DEVICE_ARG in the

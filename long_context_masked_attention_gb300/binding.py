@@ -724,7 +724,8 @@ def attn_paged(q, k_cache, v_cache, block_table, q_start, k_len, mask, scale=0.0
     block_table[i]; its new tokens are the last of them.  q_start, k_len and
     block_table are int32 CUDA tensors read when the kernels run.  mask: any
     interval family (see lca_attn_paged).  max_q_len: no request has more new
-    tokens (0: unknown).  ctx_len [n_seq]: the cached tokens that paged_plan was
+    tokens (0: unknown, which costs a decode step workspace and launches).  A
+    cache whose pages are not its outermost axis is slow with prompts.  ctx_len [n_seq]: the cached tokens that paged_plan was
     given; with it the new tokens are those that follow them, also in a request
     that the plan had no room for all of (plan.state[2] counts those).  After
     a synchronize, read_status(workspace) tells whether a table entry or a

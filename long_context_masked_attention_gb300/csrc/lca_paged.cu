@@ -215,25 +215,30 @@ constexpr int kSliceBytes = kSlice * 256;     // of K or V
 constexpr int kWarpBytes = kDecStages * 2 * kSliceBytes;
 constexpr int kDecSmem = kDecWarps * kWarpBytes;
 // Units per CTA from which on the line's last eighth is claimed.  Above it: 64
-// requests of 1K-32K 373 -> 356 us, 4 of 512K 1277 -> 1210.  Below it the finer
-// spans cost more than they even out: 256 requests of 1K, 134 units per CTA,
-// 174 us unclaimed and 189 claimed.
+// requests of 1K-32K (1.1M keys) 698 -> 668 us, 4 of 512K 1293 -> 1248.  Below
+// it the finer spans cost more than they even out: 256 requests of 1K, 134
+// units per CTA, 185 us unclaimed and 196 claimed.
 constexpr int kLongShare = 160;
-// What an item costs beside its units, in units; 0 against 4: 128 ragged
-// requests 294 and 250 us, 64 of 500 keys 43.2 and 37.8, 8 of 4K 43 and 39.
+// What an item costs beside its units, in units; 0 against 4: 128 requests of
+// 100-8K keys 317.5 and 315.5 us, 64 of 500 43.4 and 43.1, 8 of 4K 43.2 and 39.7.
 constexpr int kItemUnits = 4;
 // A CTA's share, where there is that much; 2, 4 and 8: one request of 1K 14.5,
-// 16.6 and 20.6 us, one of 4K 20.3, 18.7 and 20.6.
+// 16.5 and 19.5 us, one of 4K 19.1, 18.5 and 20.5.
 constexpr int kMinUnits = 4;
 constexpr int kSeqTile = 2 * kDecThreads;     // requests whose places on the line are in shared memory at once
 constexpr int kPartFloats = kRows * (kHeadDim + 2);
 static_assert(kSlice == 16, "a slice is one k16 step of the product with V");
 static_assert(kPartFloats == kPagedPartFloats, "workspace layout");
 
+// The products take 16-bit operands, so p is rounded to the type (by 2^-8 of it
+// at most in bf16, 2^-11 in fp16); l sums it unrounded.  Against 64 bits the
+// largest error of O is 0.0023 (bf16) and 0.00027 (fp16) on normal values, where
+// a p of 32 bits leaves 0.0017 and 0.00021, O's own rounding; products of 32-bit
+// values would run at a fraction of the rate.
 // bf16 has the exponents of fp32.  fp16 holds nothing below 2^-24: p, at most
 // 1, is kept times 2^12, so that keys down to 2^-36 of the largest still
-// count; O, l and their partial sums carry the factor, the quotient and the
-// LSE do not.
+// count (below 2^-26 as subnormal numbers, with fewer bits); O, l and their
+// partial sums carry the factor, the quotient and the LSE do not.
 template <typename T>
 constexpr float kBias = 0.f;
 template <>

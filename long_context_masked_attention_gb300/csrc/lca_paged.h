@@ -42,8 +42,9 @@ constexpr int kPagedChunkPartFloats = 256 * (kHeadDim + 2);
 // Requests with up to this many rows (new tokens x query heads of a group)
 // per KV head go to the kernel for few rows when both kernels run.  16 is one
 // tile of it; with 32, in two tiles that read the keys twice, 32 requests of
-// 3-4 tokens with 8 heads a group took 277 us where padded tiles of 128 rows
-// take 158, and a group of 24 heads 97 where they take 74.
+// 3-4 tokens at 1K-16K keys, 64 heads on 8, take 335 us where padded tiles of
+// 128 rows take 202; 32 of a token at 1K-8K with one group of 24 heads take 35
+// either way.
 constexpr int kPagedFewRows = 16;
 
 // An item of many rows that goes on past the span of the CTA it starts in.

@@ -79,6 +79,10 @@ MapStrides map_strides(const lca_paged_cache* c) {
 // Whether the kernel for many rows takes part: some request may have more
 // rows per KV head than the other one's tile, a token's heads fit a tile, and
 // there is a cache to map, its pages further apart than its tokens and heads.
+// The other kernel reads a request's keys again for every 16 rows: 2048 tokens
+// at 32K, 64 heads on 8, take 14.7 ms with heads or tokens as the outermost
+// axis and 1.50 with pages; 512 at 8K with one group of 136 heads 2.06 ms, of
+// 128 heads 0.22.
 bool many_rows(const lca_paged_shape* sh, const lca_paged_cache* c) {
   const long long G = sh->Hq / c->Hkv;
   const long long most = sh->max_q_len > 0 && sh->max_q_len < sh->Tq ? sh->max_q_len : sh->Tq;

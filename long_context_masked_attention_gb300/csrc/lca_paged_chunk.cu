@@ -26,10 +26,10 @@
 // next keys runs while the first warpgroup works on the present ones.
 //
 // Measured (whole calls, replayed graphs, 64 query heads on 8): 2048 tokens at
-// the end of 32K keys 1517-1641 us (1.38-1.49 PFLOP/s; the tensor pipe is active
-// 64 % of the time, and power decides the rest); 8 prompts of 101-2047 tokens 284
+// the end of 32K keys 1503-1641 us (1.38-1.51 PFLOP/s; the tensor pipe is active
+// 64 % of the time, and power decides the rest); 8 prompts of 101-2047 tokens 284-295
 // us, where an item of 9 tiles takes 18 us of which 14-15 are tiles; 5 tokens of
-// each of 32 requests at 1K-16K keys 162 us (0.78 of a copy's rate).
+// each of 32 requests at 1K-16K keys 163 us (0.78 of a copy's rate).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -53,11 +53,11 @@ constexpr int kOffCtl = kOffKV + kStages * kTileBytes;
 constexpr int kSmemBytes = kOffCtl + 1024 + 1024;
 constexpr int kItemSlots = 3;
 // A CTA's share, where there is that much; 2, 4 and 8: a chunk of 509 tokens
-// with a window of 1024 beside 15 single tokens 60.8, 60 and 63.5 us.
+// with a window of 1024 beside 15 single tokens 62.2, 62.3 and 64.1 us.
 constexpr int kMinTiles = 4;
 // What an item costs beside its tiles, in tiles; 3, 4, 5 and 6: 32 requests of
-// 5 tokens 158, 159, 161 and 161 us, 8 prompts 325, 326, 331 and 339 (before partly
-// masked tiles had a pass of their own, which took these to 271).
+// 5 tokens at 1K-16K keys 173, 173.3, 175.6 and 176.4 us, 8 prompts of 101-2047
+// 209, 206, 209 and 216.
 constexpr int kItemCost = 3;
 
 // Scores and probabilities have three barriers each: those of sub-tiles 0 and
@@ -104,8 +104,10 @@ static_assert(sizeof(Item) == 160 && 8 * B_COUNT <= 256 && kItemSlots * sizeof(I
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 
+// p is rounded to the type, as the products' operand (see lca_paged.cu).
 // fp16 holds nothing below 2^-24 and p reaches 2^8 between rescalings, so p
-// is kept times 2^7: at most 2^15, and keys down to 2^-31 of the largest count.
+// is kept times 2^7: at most 2^15, and keys down to 2^-31 of the largest count
+// (below 2^-21 as subnormal numbers, with fewer bits).
 template <typename T>
 constexpr float kBias = 0.f;
 template <>
@@ -660,7 +662,9 @@ __device__ __forceinline__ float row_exp(uint32_t tS, float sl2, float base) {
 // tile (both write the same); at the end the rows that attend such a key add
 // the values to their sums.  A weight is positive, so whatever it is, its
 // product with an infinity or NaN is that same value, and no score is needed
-// for it.
+// for it.  In a key that all rows of the item attend the value stays in the
+// product, where an infinity becomes NaN if the row's weight has rounded to 0:
+// not finite either way, and a scan of every tile is saved.
 //
 // One such value in a chunk of 256 tokens at 131K keys takes the call from 0.82
 // to 0.90 ms; what all calls pay for it is a look at the keys of partial tiles
