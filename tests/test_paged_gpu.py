@@ -964,3 +964,52 @@ def test_merged_parts_are_off_by_their_roundings(lca, split):
         w, d = np.exp(Lp - L).T[:, :, None], (tl + off_l + few).T[:, :, None]
         tol = tol + w * (to + np.abs(Op) * d)
     check(o, lse, p, (O, L, tol * (1 + 2.0 ** -6), off_l))
+
+
+def test_a_captured_step_serves_batches_that_do_not_fit(lca):
+    """One graph of plan, write and attention with the cached lengths; its
+    replays see batches that fit, that outgrow the packed rows and that outgrow
+    the tables, and give the bits of eager calls."""
+    import torch
+
+    g = torch.Generator().manual_seed(9)
+    n, page, Hq, Hkv, rows, width = 5, 16, 8, 2, 300, 6
+    n_pages = n * width + 40
+    ctx, new = (torch.zeros(n, dtype=torch.int32, device="cuda") for _ in range(2))
+    taken = torch.zeros(1, dtype=torch.int32, device="cuda")
+    table = torch.arange(n * width, dtype=torch.int32, device="cuda").view(n, width)
+    free = torch.arange(n * width, n_pages, dtype=torch.int32, device="cuda")
+    kc, vc = (torch.randn(n_pages, page, Hkv, 128, generator=g).to(torch.bfloat16).cuda() for _ in range(2))
+    q, k, v = (torch.randn(rows, h, 128, generator=g).to(torch.bfloat16).cuda() for h in (Hq, Hkv, Hkv))
+    first = [t.clone() for t in (table, kc, vc)]
+
+    def step():
+        for t, x in zip((table, kc, vc), first):
+            t.copy_(x)
+        plan = lca.paged_plan(ctx, new, free, taken, table, page, n_pages, rows)
+        lca.paged_write(k, v, kc, vc, plan.slots)
+        return *lca.attn_paged(q, kc, vc, table, plan.q_start, plan.k_len, CAUSAL, ctx_len=ctx), plan.state
+
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = step()
+    for ctxs, news in (([10, 0, 30, 5, 90], [3, 60, 1, 0, 6]), ([0, 0, 50, 9, 3], [90, 90, 40, 80, 9]),
+                       ([90, 96, 40, 95, 0], [7, 2, 70, 1, 96]), ([60] * 5, [80] * 5)):
+        ctx.copy_(torch.tensor(ctxs, dtype=torch.int32))
+        new.copy_(torch.tensor(news, dtype=torch.int32))
+        for t in outs:
+            t.fill_(7)
+        graph.replay()
+        got = [t.clone() for t in outs]
+        want = step()
+        assert all(torch.equal(a, b) for a, b in zip(got, want)) and bool(want[0].isfinite().all())
+        row = 0
+        for c, w in zip(ctxs, news):  # a request's rows behind the table's end, and no others, are empty
+            have = min(row + w, rows) - min(row, rows)
+            empty = want[1][0, row:row + have].isneginf().tolist()
+            assert empty == [c + t >= width * page for t in range(have)]
+            row += w
