@@ -251,6 +251,69 @@ LCA_API lca_status lca_cad_plan(const int32_t* doc_len, int32_t n_docs, int32_t 
                                 int32_t max_shard, double tolerance, lca_cad_shard* shards, int32_t max_shards,
                                 int32_t* n_shards, int64_t* server_cells);
 
+/* ------------------------------------------------------------------ rotary positions
+ * Between the projections and the attention kernels, the pairs of values of a
+ * query's or key's head are turned by an angle that grows with its position,
+ * so that scores depend on distances.  Pair i of a row at position p has the
+ * angle p * inv_freq[i] and becomes
+ *     scale * (a cos - b sin),  scale * (b cos + a sin)
+ * Values at and behind rot_dim are copied.  inv_freq is read during the call;
+ * the angle is found to 2^-32 of a turn at every position, cos, sin and the
+ * products are 32-bit ones, and a result is rounded once. */
+typedef struct {
+  int32_t rot_dim;        /* values of a head that take part: even, 2 to d      */
+  int32_t interleaved;    /* 0: pairs (i, i + rot_dim / 2); else (2 i, 2 i + 1) */
+  const double* inv_freq; /* host [rot_dim / 2]: radians per position, 0 to 2^20 */
+  float scale;            /* factor of the turned pairs, >= 0; 0 selects 1      */
+} lca_rope_desc;
+
+/* Rows of heads * d dense elements, strides apart (multiples of 8 elements, at
+ * least heads * d).  y is written; y = x with the same stride turns in place. */
+typedef struct {
+  const void* x;
+  void* y;
+  int32_t heads;
+  int64_t x_stride, y_stride;
+} lca_rope_rows;
+
+/* Turns row t of q and of k (either may be null) by positions[t] (int32,
+ * device; negative ones turn the other way).  back != 0: by the opposite angle,
+ * with the same scale, which takes the gradients of the results to those of
+ * q and k.  dtype: lca_dtype of all rows; d must be 128; x and y 16-byte
+ * aligned, device memory.  Rows written must not overlap positions or other
+ * rows, but for x = y; rows of one stride that lie beside one another, as parts
+ * of one projection, do not (LCA_ERR_INVALID_ARG otherwise). */
+LCA_API lca_status lca_rope(const lca_rope_rows* q, const lca_rope_rows* k, const int32_t* positions, int32_t n_rows,
+                            int32_t d, int32_t dtype, const lca_rope_desc* rope, int32_t back, void* stream);
+
+/* Tables of frequencies.  With w_i = base^(-2 i / rot_dim), L = original_len:
+ *   PLAIN   w_i
+ *   LINEAR  w_i / factor (positions are interpolated)
+ *   NTK     the same with base * factor^(rot_dim / (rot_dim - 2)) as the base
+ *   YARN    blend of w_i and w_i / factor, linear in i between the pairs that
+ *           make `fast` and `slow` turns in L positions (rounded down and up):
+ *           the faster ones stay; scale = 0.1 ln(factor) + 1
+ *   BANDS   blend of the same two, linear in the turns that pair i makes in L
+ *           positions: at least `fast`, w_i stays; at most `slow`, w_i / factor
+ * scale is 1 but for YARN.  base > 1, factor >= 1; YARN and BANDS need L >= 1
+ * and 0 < slow < fast, NTK rot_dim > 2.  Host only; no CUDA call.
+ * inv_freq: host [rot_dim / 2]. */
+typedef enum {
+  LCA_ROPE_PLAIN = 0,
+  LCA_ROPE_LINEAR = 1,
+  LCA_ROPE_NTK = 2,
+  LCA_ROPE_YARN = 3,
+  LCA_ROPE_BANDS = 4
+} lca_rope_scaling;
+typedef struct {
+  int32_t rot_dim;
+  int32_t scaling; /* lca_rope_scaling */
+  double base, factor;
+  int32_t original_len;
+  double fast, slow;
+} lca_rope_table;
+LCA_API lca_status lca_rope_frequencies(const lca_rope_table* table, double* inv_freq, float* scale);
+
 /* ------------------------------------------------------------------ paged cache
  * Serving: keys and values of earlier tokens live in pages of a cache, and a
  * batch of requests adds new tokens to it.  lca_paged_plan gives every new
@@ -388,6 +451,70 @@ LCA_API lca_status lca_attn_paged(const void* q, const lca_paged_cache* cache, c
 LCA_API lca_status lca_attn_paged_workspace_size(const lca_paged_shape* shape, const lca_paged_cache* cache,
                                                  const lca_mask_desc* mask, size_t* bytes);
 
+/* ------------------------------------------------------------------ paged cache of 8 bits
+ * A paged cache whose rows (a token's d values of one KV head) are e4m3 values
+ * times a power of two: value = e4m3 * 2^(b - 127), with a byte b per row.  It
+ * holds half the bytes of a 16-bit cache, which is what generation is bound by.
+ * Each value is off by at most 2^-4 of itself (half a step of its 3 bits), or
+ * by 2^-10 * 2^(b - 127) where that is more.  Bytes count as the nearest one of
+ * LCA_FP8_SCALE_MIN to LCA_FP8_SCALE_MAX.
+ * Token t of page p, head h: d bytes at p * page_stride + t * token_stride +
+ * h * head_stride of k and of v, and a byte at p * scale_page_stride + h *
+ * scale_head_stride + t of k_scale and of v_scale.  Strides of values are
+ * multiples of 16, those of scales of 8, all 8 to 2^38; k and v are
+ * 16-byte, the scales 8-byte aligned.  Otherwise as lca_paged_cache, whose
+ * lca_paged_plan serves both. */
+#define LCA_FP8_SCALE_MIN 79  /* 2^-48 */
+#define LCA_FP8_SCALE_MAX 175 /* 2^48 */
+typedef struct {
+  void* k;
+  void* v;
+  uint8_t* k_scale;
+  uint8_t* v_scale;
+  int32_t n_pages, page_size, Hkv, d;
+  int64_t page_stride, token_stride, head_stride;
+  int64_t scale_page_stride, scale_head_stride;
+} lca_paged_cache_fp8;
+
+/* lca_paged_write into such a cache: k and v (device, dtype's elements) are
+ * quantised as they are stored.  b is the smallest byte for which the row's
+ * largest finite magnitude is at most 448 * 2^(b - 127); values are divided by
+ * 2^(b - 127), which is exact, and rounded to the nearest e4m3 value, the even
+ * one of two.  Magnitudes past 448 * 2^48 become that; infinities and NaN are
+ * stored as NaN.  Slots, alignment and overlaps as lca_paged_write (the cache
+ * counts with its scales). */
+LCA_API lca_status lca_paged_write_fp8(const void* k, const void* v, int64_t k_stride, int64_t v_stride, int32_t dtype,
+                                       const int32_t* slots, int32_t n_rows, const lca_paged_cache_fp8* cache,
+                                       void* stream);
+
+/* Reads pages back: page i of `out` gets the 16-bit form of page pages[i] of
+ * `cache`, all of its tokens and heads, K and V.  A product of an e4m3 value
+ * and a power of two is exact in bf16; in fp16 what lies outside its range is
+ * rounded, beyond 65504 to that.  out: page_size, Hkv and d as the cache's, n_pages
+ * at least n.  An entry outside [0, cache->n_pages) leaves its page of out
+ * as it was, so the block tables of a batch, flattened, are a list of pages,
+ * and out is their cache for lca_attn_paged with the table 0, 1, 2, ...; an
+ * out of token stride Hkv * d, head stride d is rows of packed keys for
+ * lca_attn_fwd (which multiplies what lies behind a segment's last key by 0:
+ * slots that were never written must hold no NaN for it).  pages: int32, device.  out must not overlap the cache or
+ * pages (LCA_ERR_INVALID_ARG). */
+LCA_API lca_status lca_paged_read_fp8(const lca_paged_cache_fp8* cache, const int32_t* pages, int32_t n,
+                                      const lca_paged_cache* out, void* stream);
+
+/* lca_attn_paged over such a cache: the same arguments, masks, reports and
+ * rules, with q and o of the given lca_dtype.  Scores are those of the values
+ * that the cache stands for.  Weights are rounded to 16 bits before their
+ * product with V: for requests with few rows (lca_attn_paged's) to 11 bits
+ * times their row's factor, so that a key whose weight times factor is below
+ * 2^-36 of the largest may count as 0; for the others to dtype's as in
+ * lca_attn_paged.  NaN in the values of a key as there. */
+LCA_API lca_status lca_attn_paged_fp8(const void* q, int32_t dtype, const lca_paged_cache_fp8* cache,
+                                      const int32_t* block_table, const int32_t* q_start, const int32_t* k_len, void* o,
+                                      float* lse, const lca_paged_shape* shape, const lca_mask_desc* mask,
+                                      void* workspace, size_t workspace_bytes, void* stream);
+LCA_API lca_status lca_attn_paged_fp8_workspace_size(const lca_paged_shape* shape, const lca_paged_cache_fp8* cache,
+                                                     const lca_mask_desc* mask, size_t* bytes);
+
 /* Test hook: writes the mask of one segment and query head, evaluated by the
  * same device predicate the attention kernels apply, as bytes (1 = attend)
  * into `out` (device, q_len*k_len, row-major). */
@@ -488,7 +615,8 @@ LCA_API const char* lca_status_string(lca_status status);
  * changes (102: lca_mask_tile_classes reports the empty-half flags; 103:
  * outputs may be mapped host memory, and every pointer's kind is checked;
  * 104: device pointers of another device than the current one are refused;
- * 105: the paged cache; 106: lca_paged_shape.ctx_len). */
+ * 105: the paged cache; 106: lca_paged_shape.ctx_len; 107: rotary positions and
+ * the paged cache of 8 bits). */
 LCA_API int32_t lca_version(void);
 
 #ifdef __cplusplus

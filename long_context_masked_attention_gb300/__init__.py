@@ -14,6 +14,8 @@ from .binding import (  # noqa: F401
     attn_fwd,
     attn_merge,
     attn_paged,
+    attn_paged_fp8,
+    attn_paged_fp8_workspace_size,
     attn_paged_workspace_size,
     cad_plan,
     CadPlan,
@@ -24,9 +26,16 @@ from .binding import (  # noqa: F401
     mask_tile_classes,
     PagedPlan,
     paged_plan,
+    paged_read_fp8,
     paged_write,
+    paged_write_fp8,
     probe_wait_timeout,
     read_status,
+    rope,
+    rope_bwd,
+    rope_frequencies,
+    ROPE_SCALINGS,
+    RopeFreqs,
     workspace_size,
 )
 

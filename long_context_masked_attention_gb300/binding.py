@@ -27,7 +27,10 @@ EXPORTED = ("lca_workspace_size", "lca_attn_fwd", "lca_attn_bwd", "lca_mask_mate
             "lca_mask_nnz", "lca_read_status", "lca_probe_wait_timeout", "lca_set_kernel_events", "lca_launch_count",
             "lca_last_error_detail", "lca_attn_fwd_static_workspace", "lca_status_string", "lca_version",
             "lca_attn_merge", "lca_cad_plan", "lca_attn_fwd_dropout", "lca_attn_bwd_dropout", "lca_set_cta_profile",
-            "lca_paged_plan", "lca_paged_write", "lca_attn_paged", "lca_attn_paged_workspace_size")
+            "lca_paged_plan", "lca_paged_write", "lca_attn_paged", "lca_attn_paged_workspace_size", "lca_rope",
+            "lca_rope_frequencies", "lca_paged_write_fp8", "lca_paged_read_fp8", "lca_attn_paged_fp8",
+            "lca_attn_paged_fp8_workspace_size")
+ROPE_SCALINGS = ("PLAIN", "LINEAR", "NTK", "YARN", "BANDS")
 PHASES = ("fwd_plan", "fwd", "d_prepass", "dkv_plan", "dkv", "dq_plan", "dq")
 
 
@@ -82,6 +85,27 @@ class PagedShape_t(C.Structure):
                 ("ctx_len", C.c_void_p)]
 
 
+class PagedCacheFp8_t(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("k_scale", C.c_void_p), ("v_scale", C.c_void_p),
+                ("n_pages", C.c_int32), ("page_size", C.c_int32), ("Hkv", C.c_int32), ("d", C.c_int32),
+                ("page_stride", C.c_int64), ("token_stride", C.c_int64), ("head_stride", C.c_int64),
+                ("scale_page_stride", C.c_int64), ("scale_head_stride", C.c_int64)]
+
+
+class RopeDesc_t(C.Structure):
+    _fields_ = [("rot_dim", C.c_int32), ("interleaved", C.c_int32), ("inv_freq", C.c_void_p), ("scale", C.c_float)]
+
+
+class RopeRows_t(C.Structure):
+    _fields_ = [("x", C.c_void_p), ("y", C.c_void_p), ("heads", C.c_int32), ("x_stride", C.c_int64),
+                ("y_stride", C.c_int64)]
+
+
+class RopeTable_t(C.Structure):
+    _fields_ = [("rot_dim", C.c_int32), ("scaling", C.c_int32), ("base", C.c_double), ("factor", C.c_double),
+                ("original_len", C.c_int32), ("fast", C.c_double), ("slow", C.c_double)]
+
+
 _lib = None
 
 
@@ -118,6 +142,15 @@ def load(path: str = LIB_PATH):
                                    C.POINTER(MaskDesc_t), vp, C.c_size_t, vp]
     lib.lca_attn_paged_workspace_size.argtypes = [C.POINTER(PagedShape_t), C.POINTER(PagedCache_t),
                                                   C.POINTER(MaskDesc_t), C.POINTER(C.c_size_t)]
+    lib.lca_rope.argtypes = [C.POINTER(RopeRows_t), C.POINTER(RopeRows_t), vp, i32, i32, i32, C.POINTER(RopeDesc_t),
+                             i32, vp]
+    lib.lca_rope_frequencies.argtypes = [C.POINTER(RopeTable_t), C.POINTER(C.c_double), C.POINTER(C.c_float)]
+    lib.lca_paged_write_fp8.argtypes = [vp, vp, i64, i64, i32, vp, i32, C.POINTER(PagedCacheFp8_t), vp]
+    lib.lca_paged_read_fp8.argtypes = [C.POINTER(PagedCacheFp8_t), vp, i32, C.POINTER(PagedCache_t), vp]
+    lib.lca_attn_paged_fp8.argtypes = [vp, i32, C.POINTER(PagedCacheFp8_t), vp, vp, vp, vp, vp, C.POINTER(PagedShape_t),
+                                       C.POINTER(MaskDesc_t), vp, C.c_size_t, vp]
+    lib.lca_attn_paged_fp8_workspace_size.argtypes = [C.POINTER(PagedShape_t), C.POINTER(PagedCacheFp8_t),
+                                                      C.POINTER(MaskDesc_t), C.POINTER(C.c_size_t)]
     lib.lca_launch_count.restype = C.c_uint64
     lib.lca_launch_count.argtypes = []
     lib.lca_attn_fwd_static_workspace.argtypes = [vp, vp, vp, vp, vp, C.POINTER(Shape_t), C.POINTER(MaskDesc_t), vp]
@@ -689,30 +722,32 @@ def _paged_mask(mask):
     return md
 
 
-_SIZES: dict = {}  # workspace bytes of attn_paged by shape
+_SIZES: dict = {}  # workspace bytes of attn_paged and attn_paged_fp8 by shape
 _PLAIN_KINDS = tuple(MASK_KINDS.index(k) for k in ("FULL", "CAUSAL", "DOC", "CAUSAL_DOC"))  # no parameters
 
 
-def _paged_shape(q, cache, k_cache, block_table, scale, max_q_len):
+def _paged_shape(q, cache, k_cache, block_table, scale, max_q_len, dtype=None):
+    """dtype: q's, if not the cache's."""
     dev = k_cache.device
-    qs = _rows(q, "q", None, cache.d, k_cache.dtype, dev)
+    qs = _rows(q, "q", None, cache.d, dtype or k_cache.dtype, dev)
     tp, width, tstride = _table(block_table, None, dev)
     shape = q.shape
     return PagedShape_t(shape[0], shape[1], block_table.shape[0], width, tstride, qs, _int32(max_q_len, "max_q_len"),
                         scale), tp
 
 
-def _paged_size(shape, cache, md):
+def _paged_size(name, shape, cache, md):
     n = C.c_size_t(0)
-    _check(load().lca_attn_paged_workspace_size(C.byref(shape), C.byref(cache), C.byref(md), C.byref(n)),
-           "lca_attn_paged_workspace_size")
+    _check(getattr(load(), name + "_workspace_size")(C.byref(shape), C.byref(cache), C.byref(md), C.byref(n)),
+           name + "_workspace_size")
     return n.value
 
 
 def attn_paged_workspace_size(q, k_cache, v_cache, block_table, mask, scale=0.0, max_q_len=0) -> int:
     """Bytes of workspace that attn_paged needs for these tensors."""
     cache = _paged_cache(k_cache, v_cache)
-    return _paged_size(_paged_shape(q, cache, k_cache, block_table, scale, max_q_len)[0], cache, _paged_mask(mask))
+    shape, _ = _paged_shape(q, cache, k_cache, block_table, scale, max_q_len)
+    return _paged_size("lca_attn_paged", shape, cache, _paged_mask(mask))
 
 
 def attn_paged(q, k_cache, v_cache, block_table, q_start, k_len, mask, scale=0.0, max_q_len=0, out=None, lse=None,
@@ -733,8 +768,17 @@ def attn_paged(q, k_cache, v_cache, block_table, q_start, k_len, mask, scale=0.0
     import torch
 
     cache = _paged_cache(k_cache, v_cache)
-    dev, dt = k_cache.device, q.dtype
-    shape, tp = _paged_shape(q, cache, k_cache, block_table, scale, max_q_len)
+    return _attend("lca_attn_paged", cache, (k_cache, v_cache), k_cache.dtype, q, block_table, q_start, k_len, mask, scale,
+                   max_q_len, out, lse, workspace, stream, ctx_len)
+
+
+def _attend(name, cache, tensors, dt, q, block_table, q_start, k_len, mask, scale, max_q_len, out, lse, workspace, stream,
+            ctx_len):
+    """attn_paged over a cache of either kind: its descriptor and tensors, q's dtype."""
+    import torch
+
+    dev = tensors[0].device
+    shape, tp = _paged_shape(q, cache, tensors[0], block_table, scale, max_q_len, dt)
     md = _paged_mask(mask)
     n_seq = shape.n_seq
     qsp = _ptr(q_start, "q_start", torch.int32, (n_seq + 1,), dev)
@@ -755,24 +799,253 @@ def attn_paged(q, k_cache, v_cache, block_table, q_start, k_len, mask, scale=0.0
         lp = _ptr(lse, "lse", torch.float32, lsize, dev)
     if workspace is None:
         # the size depends on these alone
-        key = (shape.Tq, shape.Hq, n_seq, shape.max_q_len, cache.Hkv, min(cache.n_pages, 2), cache.page_stride,
+        key = (name, shape.Tq, shape.Hq, n_seq, shape.max_q_len, cache.Hkv, min(cache.n_pages, 2), cache.page_stride,
                cache.token_stride, cache.head_stride)
         need = _SIZES.get(key)
         if need is None:
             if len(_SIZES) >= 4096:
                 _SIZES.clear()
-            need = _SIZES[key] = _paged_size(shape, cache, md)
+            need = _SIZES[key] = _paged_size(name, shape, cache, md)
         workspace = _empty((need,), torch.uint8, dev, side)
     else:
         _ptr(workspace, "workspace", torch.uint8, (workspace.numel(),), dev)
     if side is not None:
-        for t in (q, k_cache, v_cache, block_table, q_start, k_len, out, lse, workspace):
+        for t in (q, *tensors, block_table, q_start, k_len, out, lse, workspace):
             t.record_stream(side)
         if ctx_len is not None:
             ctx_len.record_stream(side)
-    _call(load().lca_attn_paged, "lca_attn_paged", dev, side, q.data_ptr(), C.byref(cache), tp, qsp, klp, op, lp,
-          C.byref(shape), C.byref(md), workspace.data_ptr(), workspace.numel())
+    head = (q.data_ptr(),) if name == "lca_attn_paged" else (q.data_ptr(), _dtype_code(dt))
+    _call(getattr(load(), name), name, dev, side, *head, C.byref(cache), tp, qsp, klp, op, lp, C.byref(shape), C.byref(md),
+          workspace.data_ptr(), workspace.numel())
     return out, lse
+
+
+# ------------------------------------------------------------------ paged cache of 8 bits
+def _dtype_code(dt, name="q"):
+    """lca_dtype of a torch dtype."""
+    import torch
+
+    if dt is torch.bfloat16:
+        return 0
+    if dt is torch.float16:
+        return 1
+    raise ValueError(f"{name}: dtype {dt}, expected torch.bfloat16 or torch.float16")
+
+
+def _paged_cache_fp8(k, v, k_scale, v_scale):
+    """lca_paged_cache_fp8 of two [n_pages, page_size, Hkv, d] float8_e4m3fn and two [n_pages, Hkv, page_size] uint8
+    tensors."""
+    import torch
+
+    for name, t, dt in (("k_cache", k, torch.float8_e4m3fn), ("v_cache", v, torch.float8_e4m3fn),
+                        ("k_scale", k_scale, torch.uint8), ("v_scale", v_scale, torch.uint8)):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+        if not t.is_cuda:
+            raise ValueError(f"{name}: must be a CUDA tensor (got {t.device})")
+        if t.dtype is not dt:
+            raise ValueError(f"{name}: dtype {t.dtype}, expected {dt}")
+    shape, dev = k.shape, k.device
+    if len(shape) != 4:
+        raise ValueError(f"k_cache: shape {tuple(shape)}, expected [n_pages, page_size, Hkv, d]")
+    if v.shape != shape or v.device != dev:
+        raise ValueError(f"v_cache: {tuple(v.shape)} on {v.device}, expected {tuple(shape)} on {dev} as k_cache")
+    n, page, Hkv, d = shape
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        if t.shape != (n, Hkv, page) or t.device != dev:
+            raise ValueError(f"{name}: {tuple(t.shape)} on {t.device}, expected {(n, Hkv, page)} on {dev}")
+    ks, vs, kf, vf = k.stride(), v.stride(), k_scale.stride(), v_scale.stride()
+    if n <= 1 or page == 1 or Hkv == 1 or d == 1:
+        # the stride of an axis of length one (or of an empty cache) moves nothing
+        def moves(st):
+            return (st[0] if n > 1 else d, st[1] if n and page > 1 else d, st[2] if n and Hkv > 1 else d,
+                    st[3] if n and d > 1 else 1)
+
+        def moves3(st):
+            return st[0] if n > 1 else 8, st[1] if n and Hkv > 1 else 8, st[2] if n and page > 1 else 1
+
+        ks, vs, kf, vf = moves(ks), moves(vs), moves3(kf), moves3(vf)
+    if ks != vs:
+        raise ValueError(f"v_cache: strides {vs}, expected {ks} as k_cache")
+    if kf != vf:
+        raise ValueError(f"v_scale: strides {vf}, expected {kf} as k_scale")
+    if ks[3] != 1 or kf[2] != 1:
+        raise ValueError("k_cache, v_cache, k_scale, v_scale: the last dimension must be contiguous")
+    return PagedCacheFp8_t(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), n, page, Hkv, d, ks[0],
+                           ks[1], ks[2], kf[0], kf[1])
+
+
+def paged_write_fp8(k, v, k_cache, v_cache, k_scale, v_scale, slots, stream=None):
+    """Quantises rows k, v [T, Hkv, 128] (bf16 or fp16, row stride free) into slots [T] int32 of an 8-bit cache, in
+    place: values [n_pages, page_size, Hkv, 128] float8_e4m3fn (strides free) and a byte b per row, factor
+    2^(b - 127), [n_pages, Hkv, page_size] uint8 (tokens contiguous).  Rows whose slot is outside the cache (-1) are
+    skipped."""
+    cache = _paged_cache_fp8(k_cache, v_cache, k_scale, v_scale)
+    dev = k_cache.device
+    dt = getattr(k, "dtype", None)
+    ks = _rows(k, "k", cache.Hkv, cache.d, dt, dev)
+    code = _dtype_code(dt, "k")
+    vs = _rows(v, "v", cache.Hkv, cache.d, dt, dev)
+    T = k.shape[0]
+    if v.shape[0] != T:
+        raise ValueError(f"v: {v.shape[0]} rows, expected {T} as k")
+    import torch
+
+    sp = _ptr(slots, "slots", torch.int32, (T,), dev)
+    side = _side_stream(stream, dev)
+    if side is not None:
+        for t in (k, v, k_cache, v_cache, k_scale, v_scale, slots):
+            t.record_stream(side)
+    _call(load().lca_paged_write_fp8, "lca_paged_write_fp8", dev, side, k.data_ptr(), v.data_ptr(), ks, vs, code, sp,
+          _int32(T, "k: rows"), C.byref(cache))
+
+
+def paged_read_fp8(k_cache, v_cache, k_scale, v_scale, pages, dtype=None, k_out=None, v_out=None, stream=None):
+    """Pages of an 8-bit cache (see paged_write_fp8) as 16-bit values: page i of (k, v), each [n, page_size, Hkv, 128],
+    is page pages[i] of the cache (pages [n] int32).  Entries that are no page leave theirs as it was: zeros where the
+    tensors are made here (of `dtype`, bfloat16 unless given).  The results are a cache for attn_paged, and their
+    flattened pages rows of packed keys for attn_fwd."""
+    import torch
+
+    cache = _paged_cache_fp8(k_cache, v_cache, k_scale, v_scale)
+    dev = k_cache.device
+    if not isinstance(pages, torch.Tensor):
+        raise TypeError(f"pages: expected a torch.Tensor, got {type(pages).__name__}")
+    n = _int32(pages.numel(), "pages: entries")
+    pp = _ptr(pages, "pages", torch.int32, (n,), dev)
+    if (k_out is None) != (v_out is None):
+        raise ValueError("k_out and v_out: give both or neither")
+    side = _side_stream(stream, dev)
+    size = (n, cache.page_size, cache.Hkv, cache.d)
+    if k_out is None:
+        dtype = torch.bfloat16 if dtype is None else dtype
+        _dtype_code(dtype, "dtype")
+        k_out, v_out = (_empty(size, dtype, dev, side) for _ in range(2))
+        with torch.cuda.stream(side):  # None: the current one
+            k_out.zero_()
+            v_out.zero_()
+    elif dtype is not None and getattr(k_out, "dtype", dtype) is not dtype:
+        raise ValueError(f"k_out: dtype {k_out.dtype}, expected {dtype}")
+    out = _paged_cache(k_out, v_out)
+    if k_out.device != dev:
+        raise ValueError(f"k_out: on {k_out.device}, expected {dev}")
+    if tuple(k_out.shape) != size:
+        raise ValueError(f"k_out: shape {tuple(k_out.shape)}, expected {size}")
+    if side is not None:
+        for t in (k_cache, v_cache, k_scale, v_scale, pages, k_out, v_out):
+            t.record_stream(side)
+    _call(load().lca_paged_read_fp8, "lca_paged_read_fp8", dev, side, C.byref(cache), pp, n, C.byref(out))
+    return k_out, v_out
+
+
+def _q_dtype(q):
+    import torch
+
+    if not isinstance(q, torch.Tensor):
+        raise TypeError(f"q: expected a torch.Tensor, got {type(q).__name__}")
+    _dtype_code(q.dtype)
+    return q.dtype
+
+
+def attn_paged_fp8_workspace_size(q, k_cache, v_cache, k_scale, v_scale, block_table, mask, scale=0.0, max_q_len=0) -> int:
+    """Bytes of workspace that attn_paged_fp8 needs for these tensors."""
+    cache = _paged_cache_fp8(k_cache, v_cache, k_scale, v_scale)
+    shape, _ = _paged_shape(q, cache, k_cache, block_table, scale, max_q_len, _q_dtype(q))
+    return _paged_size("lca_attn_paged_fp8", shape, cache, _paged_mask(mask))
+
+
+def attn_paged_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, q_start, k_len, mask, scale=0.0, max_q_len=0,
+                   out=None, lse=None, workspace=None, stream=None, ctx_len=None):
+    """attn_paged over an 8-bit cache (see paged_write_fp8): the same arguments, masks and rules, with q and o in bf16
+    or fp16."""
+    cache = _paged_cache_fp8(k_cache, v_cache, k_scale, v_scale)
+    return _attend("lca_attn_paged_fp8", cache, (k_cache, v_cache, k_scale, v_scale), _q_dtype(q), q, block_table, q_start,
+                   k_len, mask, scale, max_q_len, out, lse, workspace, stream, ctx_len)
+
+
+# ------------------------------------------------------------------ rotary positions
+@dataclass
+class RopeFreqs:
+    """Radians per position of each pair, float64 [rot_dim / 2] on the host, and the factor of the turned values (see
+    lca_rope_desc; any object with these attributes is accepted)."""
+    inv_freq: np.ndarray
+    scale: float = 1.0
+
+
+def rope_frequencies(rot_dim=128, base=10000.0, scaling="PLAIN", factor=1.0, original_len=0, fast=None,
+                     slow=1.0) -> RopeFreqs:
+    """Frequencies of rotary positions, plain or for contexts longer than the original ones (lca_rope_table).  fast,
+    slow: the turns in original_len positions between which YARN (32 to 1) and BANDS (4 to 1) blend."""
+    kind = scaling if isinstance(scaling, int) else ROPE_SCALINGS.index(scaling)
+    if fast is None:
+        fast = 32.0 if kind == 3 else 4.0
+    rot_dim = _int32(rot_dim, "rot_dim")
+    inv = np.zeros(max(rot_dim // 2, 1))
+    out = C.c_float(0)
+    t = RopeTable_t(rot_dim, _int32(kind, "scaling"), float(base), float(factor), _int32(original_len, "original_len"),
+                    float(fast), float(slow))
+    _check(load().lca_rope_frequencies(C.byref(t), inv.ctypes.data_as(C.POINTER(C.c_double)), C.byref(out)),
+           "lca_rope_frequencies")
+    return RopeFreqs(inv, out.value)
+
+
+def _rope(q, k, positions, freqs, interleaved, q_out, k_out, stream, back):
+    import torch
+
+    first = q if q is not None else k
+    if not isinstance(first, torch.Tensor):
+        raise TypeError(f"q: expected a torch.Tensor, got {type(first).__name__}")
+    dev, dt = first.device, first.dtype
+    if not first.is_cuda:
+        raise ValueError(f"{'q' if q is not None else 'k'}: must be a CUDA tensor (got {dev})")
+    code = _dtype_code(dt, "q" if q is not None else "k")
+    T = _int32(first.shape[0] if first.dim() else 0, "rows")
+    pp = _ptr(positions, "positions", torch.int32, (T,), dev)
+    side = _side_stream(stream, dev)
+    rows, outs = [], []
+    for x, y, name in ((q, q_out, "q"), (k, k_out, "k")):
+        if x is None:
+            if y is not None:
+                raise ValueError(f"{name}_out: given without {name}")
+            rows.append(None)
+            outs.append(None)
+            continue
+        xs = _rows(x, name, None, 128, dt, dev)
+        if x.shape[0] != T:
+            raise ValueError(f"{name}: {x.shape[0]} rows, expected {T}")
+        H = x.shape[1]
+        if y is None:
+            y = _empty((T, H, 128), dt, dev, side)
+            ys = H * 128
+        else:
+            ys = _rows(y, name + "_out", H, 128, dt, dev)
+            if y.shape[0] != T:
+                raise ValueError(f"{name}_out: {y.shape[0]} rows, expected {T}")
+        rows.append(RopeRows_t(x.data_ptr(), y.data_ptr(), _int32(H, name), xs, ys))
+        outs.append(y)
+    inv = np.ascontiguousarray(np.asarray(freqs.inv_freq, dtype=np.float64))
+    if inv.ndim != 1:
+        raise ValueError(f"freqs.inv_freq: shape {inv.shape}, expected [rot_dim / 2]")
+    desc = RopeDesc_t(2 * inv.size, int(bool(interleaved)), inv.ctypes.data, float(getattr(freqs, "scale", 1.0)))
+    if side is not None:
+        for t in (q, k, positions, *outs):
+            if t is not None:
+                t.record_stream(side)
+    _call(load().lca_rope, "lca_rope", dev, side, *(C.byref(r) if r is not None else None for r in rows), pp, T, 128, code,
+          C.byref(desc), back)
+    return tuple(outs)
+
+
+def rope(q, k, positions, freqs, interleaved=False, q_out=None, k_out=None, stream=None):
+    """Rotary positions: q [T, Hq, 128] and k [T, Hkv, 128] (bf16 or fp16, row strides free, parts of one projection
+    among them; either may be None) turned by positions [T] int32 -> (q, k).  freqs: from rope_frequencies; as many
+    pairs as it has take part, pairs (i, i + half) or, interleaved, (2i, 2i + 1).  q_out, k_out may be q and k."""
+    return _rope(q, k, positions, freqs, interleaved, q_out, k_out, stream, 0)
+
+
+def rope_bwd(dq, dk, positions, freqs, interleaved=False, dq_out=None, dk_out=None, stream=None):
+    """Gradients of rope's results -> gradients of its q and k (either may be None)."""
+    return _rope(dq, dk, positions, freqs, interleaved, dq_out, dk_out, stream, 1)
 
 
 def mask_materialize(call: Call, head: int, seg: int, q_len: int, k_len: int, device="cuda", stream=None):

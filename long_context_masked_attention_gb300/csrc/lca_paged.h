@@ -59,6 +59,8 @@ struct PagedAttnArgs {
   const void* q;
   const void *kc, *vc;
   long long q_stride, page_stride, token_stride, head_stride, table_stride;  // elements
+  const uint8_t *ks, *vs;  // an 8-bit cache's factors, a byte per row
+  long long scale_page_stride, scale_head_stride;
   const int *table, *q_start, *k_len;
   const int* ctx_len;  // null: a request's rows are the last of its k_len tokens
   void* o;

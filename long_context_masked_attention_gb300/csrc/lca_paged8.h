@@ -1,0 +1,37 @@
+// lca_paged8.h — what the entry points of the 8-bit paged cache
+// (lca_paged8_api.cu) and their kernels share.
+#pragma once
+#include "lca_paged.h"
+
+namespace lca {
+
+// Rows' factors are 2^-48 to 2^48: with weights of exponent at least -126
+// (fp32's normal numbers) two keys of the same weight may have factors that far
+// apart and both count, whichever of them the running maximum goes by.
+constexpr int kScaleBias = 127;
+constexpr int kScaleMin = -48, kScaleMax = 48;
+
+// Strides of rows in elements, of the cache in bytes.
+struct PagedWrite8Args {
+  const uint16_t *k, *v;
+  uint8_t *kc, *vc, *ks, *vs;
+  long long k_stride, v_stride, page_stride, token_stride, head_stride, scale_page_stride, scale_head_stride;
+  const int* slots;
+  int n_rows, Hkv, page_size, n_slots;
+};
+void launch_paged_write8(const PagedWrite8Args& a, bool fp16, int num_sms, cudaStream_t st);
+
+struct PagedRead8Args {
+  const uint8_t *kc, *vc, *ks, *vs;
+  uint16_t *k, *v;
+  long long page_stride, token_stride, head_stride, scale_page_stride, scale_head_stride;
+  long long out_page_stride, out_token_stride, out_head_stride;
+  const int* pages;
+  int n, n_pages, Hkv, page_size;
+  bool token_first;  // tokens of a head lie closer together than its heads
+};
+void launch_paged_read8(const PagedRead8Args& a, bool fp16, int num_sms, cudaStream_t st);
+
+cudaError_t launch_paged_decode8(const PagedAttnArgs& a, bool behind, bool fp16, int num_sms, cudaStream_t st);
+
+}  // namespace lca

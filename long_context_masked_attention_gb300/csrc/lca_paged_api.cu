@@ -9,6 +9,7 @@
 #include "../../include/lca_attn.h"
 #include "lca_host.h"
 #include "lca_paged.h"
+#include "lca_paged8.h"
 
 namespace lca {
 namespace {
@@ -33,6 +34,14 @@ bool fits(long long n, int64_t stride) {
 }
 constexpr int kMostRequests = 0x3FFFFFFF;  // the kernels' loops over requests stay in 32 bits
 
+// A cache of either kind as the checks and launches see it: c has the values'
+// layout (its dtype is of no use for an 8-bit one), c8 the factors.
+struct Cache {
+  const lca_paged_cache* c;
+  const lca_paged_cache_fp8* c8;  // null: 16 bits
+  long long bytes() const { return c8 ? 1 : 2; }
+};
+
 lca_status check_cache(const lca_paged_cache* c) {
   if (!c) return LCA_ERR_INVALID_ARG;
   if (c->dtype != LCA_BF16 && c->dtype != LCA_F16) return LCA_ERR_INVALID_ARG;
@@ -56,6 +65,49 @@ long long cache_extent(const lca_paged_cache* c) {
   if (c->n_pages == 0) return 0;
   return ((c->n_pages - 1) * c->page_stride + (c->page_size - 1) * c->token_stride + (c->Hkv - 1) * c->head_stride +
           kHeadDim) * 2;
+}
+
+// The values' layout of an 8-bit cache, in elements.
+lca_paged_cache values_of(const lca_paged_cache_fp8* c) {
+  lca_paged_cache v{};
+  if (c)
+    v = {c->k, c->v, c->n_pages, c->page_size, c->Hkv, c->d, LCA_BF16, c->page_stride, c->token_stride, c->head_stride};
+  return v;
+}
+
+lca_status check_cache8(const lca_paged_cache_fp8* c) {
+  if (!c) return LCA_ERR_INVALID_ARG;
+  const lca_paged_cache v = values_of(c);
+  const lca_status r = check_cache(&v);
+  if (r != LCA_OK) return r;
+  if (c->page_stride % 16 != 0 || c->token_stride % 16 != 0 || c->head_stride % 16 != 0) return LCA_ERR_INVALID_ARG;
+  if (!stride_ok(c->scale_page_stride) || !stride_ok(c->scale_head_stride) || !fits(c->n_pages, c->scale_page_stride) ||
+      !fits(c->Hkv, c->scale_head_stride))
+    return LCA_ERR_INVALID_ARG;
+  return LCA_OK;
+}
+
+bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
+
+bool cache_memory8(const lca_paged_cache_fp8* c) {
+  if (c->n_pages == 0) return true;
+  const lca_paged_cache v = values_of(c);
+  return cache_memory(&v) && c->k_scale && c->v_scale && aligned8(c->k_scale) && aligned8(c->v_scale) &&
+         device_input(c->k_scale) && device_input(c->v_scale);
+}
+
+// The four arrays of an 8-bit cache, from their first to their last byte.
+struct Extent {
+  const void* p;
+  long long bytes;
+};
+void extents8(const lca_paged_cache_fp8* c, Extent (&e)[4]) {
+  const lca_paged_cache v = values_of(c);
+  const long long n = cache_extent(&v) / 2;
+  const long long f = c->n_pages == 0 ? 0
+                                      : (c->n_pages - 1) * c->scale_page_stride + (c->Hkv - 1) * c->scale_head_stride +
+                                            c->page_size;
+  e[0] = {c->k, n}, e[1] = {c->v, n}, e[2] = {c->k_scale, f}, e[3] = {c->v_scale, f};
 }
 
 // The cache's strides as a tensor map has them, in ascending order: token and
@@ -208,6 +260,122 @@ bool cache_map(CUtensorMap* m, const void* p, const lca_paged_cache* c, int box_
   return encode(m, p, c->dtype, 4, dims, strides, box);
 }
 
+// lca_attn_paged over a cache of either kind, q and o of `dtype`.
+lca_status attend(const Cache& any, int dtype, const void* q, const int32_t* block_table, const int32_t* q_start,
+                  const int32_t* k_len, void* o, float* lse, const lca_paged_shape* shape, const lca_mask_desc* mask,
+                  void* workspace, size_t workspace_bytes, void* stream) {
+  const lca_paged_cache* cache = any.c;
+  const lca_paged_cache_fp8* c8 = any.c8;
+  PagedAttnArgs a{};
+  const lca_status r = check_attn(shape, cache, mask, a.mask);
+  if (r != LCA_OK) return r;
+  const PagedLayout L = paged_layout(shape, cache);
+  if (!workspace || reinterpret_cast<uintptr_t>(workspace) % kAlign != 0 || workspace_bytes < L.total ||
+      !device_input(workspace))
+    return LCA_ERR_WORKSPACE;
+  const long long n_table =
+      shape->n_seq > 0 && shape->max_pages > 0 ? (shape->n_seq - 1) * shape->table_stride + shape->max_pages : 0;
+  if (!ints(block_table, n_table) || !ints(q_start, shape->n_seq > 0 ? shape->n_seq + 1LL : 0) ||
+      !ints(k_len, shape->n_seq) || (shape->ctx_len && !ints(shape->ctx_len, shape->n_seq)) || !(c8 ? cache_memory8(c8) : cache_memory(cache)))
+    return LCA_ERR_INVALID_ARG;
+  if (shape->Tq > 0) {
+    if (!q || !aligned16(q) || !device_input(q) || !o || !aligned16(o) || !device_input(o) || !lse || !aligned4(lse) ||
+        !device_input(lse))
+      return LCA_ERR_INVALID_ARG;
+  }
+  {  // an empty batch writes its workspace too
+    const long long rows = shape->Tq, heads = shape->Hq;
+    const long long extent = cache_extent(cache) / 2 * any.bytes();
+    Extent e8[4] = {};
+    if (c8) extents8(c8, e8);
+    const Extent t[12] = {{o, rows * heads * kHeadDim * 2},
+              {lse, rows * heads * 4},
+              {workspace, static_cast<long long>(L.total)},
+              {q, rows > 0 ? ((rows - 1) * shape->q_stride + heads * kHeadDim) * 2 : 0},
+              {cache->k, extent},
+              {cache->v, extent},
+              {block_table, 4 * n_table},
+              {q_start, 4 * (shape->n_seq + 1LL)},
+              {k_len, 4LL * shape->n_seq},
+              {shape->ctx_len, shape->ctx_len ? 4LL * shape->n_seq : 0},
+              e8[2],
+              e8[3]};
+    for (int i = 0; i < 3; ++i)  // the first three are written
+      for (int j = i + 1; j < 12; ++j)
+        if (overlap(t[i].p, t[i].bytes, t[j].p, t[j].bytes)) return LCA_ERR_INVALID_ARG;
+  }
+  const int sms = num_sms();
+  if (sms <= 0) return LCA_ERR_CUDA;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  a.q = q;
+  a.kc = cache->k;
+  a.vc = cache->v;
+  a.q_stride = shape->q_stride;
+  a.page_stride = cache->page_stride;
+  a.token_stride = cache->token_stride;
+  a.head_stride = cache->head_stride;
+  if (c8) {
+    a.ks = c8->k_scale;
+    a.vs = c8->v_scale;
+    a.scale_page_stride = c8->scale_page_stride;
+    a.scale_head_stride = c8->scale_head_stride;
+  }
+  a.table_stride = shape->table_stride;
+  a.table = block_table;
+  a.q_start = q_start;
+  a.k_len = k_len;
+  a.ctx_len = shape->ctx_len;
+  a.o = o;
+  a.lse = lse;
+  a.status = reinterpret_cast<int*>(ws + L.status);
+  a.arrived = reinterpret_cast<int*>(ws + L.arrived);
+  a.claims = a.arrived + kPagedMaxSpans;
+  a.parts = reinterpret_cast<float*>(ws + L.parts);
+  a.Tq = shape->Tq;
+  a.Hq = shape->Hq;
+  a.Hkv = cache->Hkv;
+  a.G = shape->Hq / cache->Hkv;
+  a.n_seq = shape->n_seq;
+  a.max_pages = shape->max_pages;
+  a.page_size = cache->page_size;
+  a.n_pages = cache->n_pages;
+  const float scale = shape->scale > 0.f ? shape->scale : 1.0f / std::sqrt(static_cast<float>(kHeadDim));
+  a.scale_log2 = scale * 1.4426950408889634f;
+  if (cache->n_pages == 0) {  // no key is read; the addresses are only given
+    a.kc = a.vc = q;
+    a.ks = a.vs = static_cast<const uint8_t*>(q);
+  }
+  const bool many = !c8 && many_rows(shape, cache) && shape->n_seq > 0;
+  a.few = many ? kPagedFewRows : 0x7FFFFFFF;
+  CUtensorMap tq, tk, tv;
+  if (many) {
+    a.tpt = tokens_per_tile(shape, cache);
+    a.box_rows = kTile;
+    while (cache->page_size % a.box_rows != 0) a.box_rows /= 2;
+    a.head_first = map_strides(cache).head_first;
+    a.max_blocks = L.max_blocks;
+    a.block0 = reinterpret_cast<int*>(ws + L.block0);
+    a.line = reinterpret_cast<long long*>(ws + L.line);
+    a.cuts = reinterpret_cast<PagedCut*>(ws + L.cuts);
+    a.chunk_parts = reinterpret_cast<float*>(ws + L.chunk_parts);
+    a.out_v8 = (reinterpret_cast<uintptr_t>(o) & 31u) == 0;
+    a.wait_limit_ns = wait_limit_ns();
+    const cuuint64_t dims[3] = {kHeadDim, static_cast<cuuint64_t>(a.Hq), static_cast<cuuint64_t>(a.Tq)};
+    const cuuint64_t strides[2] = {kHeadDim * 2, static_cast<cuuint64_t>(a.q_stride) * 2};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(a.G), static_cast<cuuint32_t>(a.tpt)};
+    if (!encode(&tq, q, dtype, 3, dims, strides, box) || !cache_map(&tk, cache->k, cache, a.box_rows) ||
+        !cache_map(&tv, cache->v, cache, a.box_rows))
+      return LCA_ERR_CUDA;
+  }
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool fp16 = dtype == LCA_F16;
+  LCA_CUDA(launch_paged_begin(a, many, st));
+  if (many) LCA_CUDA(launch_paged_chunk(tq, tk, tv, a, fp16, sms, st));
+  if (shape->Tq > 0) LCA_CUDA(c8 ? launch_paged_decode8(a, many, fp16, sms, st) : launch_paged_decode(a, many, fp16, sms, st));
+  if (many) LCA_CUDA(launch_paged_join(a, fp16, sms, st));
+  return LCA_OK;
+}
+
 }  // namespace
 }  // namespace lca
 
@@ -289,6 +457,99 @@ lca_status lca_paged_write(const void* k, const void* v, int64_t k_stride, int64
   return LCA_OK;
 }
 
+lca_status lca_paged_write_fp8(const void* k, const void* v, int64_t k_stride, int64_t v_stride, int32_t dtype,
+                               const int32_t* slots, int32_t n_rows, const lca_paged_cache_fp8* cache, void* stream) {
+  const lca_status r = check_cache8(cache);
+  if (r != LCA_OK) return r;
+  if (dtype != LCA_BF16 && dtype != LCA_F16) return LCA_ERR_INVALID_ARG;
+  const long long row = static_cast<long long>(cache->Hkv) * kHeadDim;
+  if (n_rows < 0 || k_stride < row || v_stride < row || !stride_ok(k_stride) || !stride_ok(v_stride) ||
+      !fits(n_rows, k_stride) || !fits(n_rows, v_stride))
+    return LCA_ERR_INVALID_ARG;
+  if (n_rows == 0) return LCA_OK;
+  if (!k || !v || !aligned16(k) || !aligned16(v) || !device_input(k) || !device_input(v) || !ints(slots, n_rows))
+    return LCA_ERR_INVALID_ARG;
+  if (cache->n_pages == 0) return LCA_OK;  // every slot lies outside
+  if (!cache_memory8(cache)) return LCA_ERR_INVALID_ARG;
+  Extent e[4];
+  extents8(cache, e);
+  for (const Extent& c : e)
+    if (overlap(c.p, c.bytes, k, ((n_rows - 1) * k_stride + row) * 2) ||
+        overlap(c.p, c.bytes, v, ((n_rows - 1) * v_stride + row) * 2) || overlap(c.p, c.bytes, slots, 4LL * n_rows))
+      return LCA_ERR_INVALID_ARG;
+  const int sms = num_sms();
+  if (sms <= 0) return LCA_ERR_CUDA;
+  PagedWrite8Args a{};
+  a.k = static_cast<const uint16_t*>(k);
+  a.v = static_cast<const uint16_t*>(v);
+  a.kc = static_cast<uint8_t*>(cache->k);
+  a.vc = static_cast<uint8_t*>(cache->v);
+  a.ks = cache->k_scale;
+  a.vs = cache->v_scale;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.page_stride = cache->page_stride;
+  a.token_stride = cache->token_stride;
+  a.head_stride = cache->head_stride;
+  a.scale_page_stride = cache->scale_page_stride;
+  a.scale_head_stride = cache->scale_head_stride;
+  a.slots = slots;
+  a.n_rows = n_rows;
+  a.Hkv = cache->Hkv;
+  a.page_size = cache->page_size;
+  a.n_slots = cache->n_pages * cache->page_size;
+  launch_paged_write8(a, dtype == LCA_F16, sms, static_cast<cudaStream_t>(stream));
+  LCA_CUDA(cudaGetLastError());
+  return LCA_OK;
+}
+
+lca_status lca_paged_read_fp8(const lca_paged_cache_fp8* cache, const int32_t* pages, int32_t n,
+                              const lca_paged_cache* out, void* stream) {
+  lca_status r = check_cache8(cache);
+  if (r == LCA_OK) r = check_cache(out);
+  if (r != LCA_OK) return r;
+  if (n < 0 || n > out->n_pages || out->page_size != cache->page_size || out->Hkv != cache->Hkv)
+    return LCA_ERR_INVALID_ARG;
+  if (n == 0) return LCA_OK;
+  if (!ints(pages, n) || !cache_memory(out)) return LCA_ERR_INVALID_ARG;
+  if (cache->n_pages == 0) return LCA_OK;  // every entry lies outside
+  if (!cache_memory8(cache)) return LCA_ERR_INVALID_ARG;
+  Extent e[4];
+  extents8(cache, e);
+  for (const void* p : {out->k, out->v}) {
+    const long long bytes = cache_extent(out);
+    if (overlap(p, bytes, pages, 4LL * n)) return LCA_ERR_INVALID_ARG;
+    for (const Extent& c : e)
+      if (overlap(p, bytes, c.p, c.bytes)) return LCA_ERR_INVALID_ARG;
+  }
+  const int sms = num_sms();
+  if (sms <= 0) return LCA_ERR_CUDA;
+  PagedRead8Args a{};
+  a.kc = static_cast<const uint8_t*>(cache->k);
+  a.vc = static_cast<const uint8_t*>(cache->v);
+  a.ks = cache->k_scale;
+  a.vs = cache->v_scale;
+  a.k = static_cast<uint16_t*>(out->k);
+  a.v = static_cast<uint16_t*>(out->v);
+  a.page_stride = cache->page_stride;
+  a.token_stride = cache->token_stride;
+  a.head_stride = cache->head_stride;
+  a.scale_page_stride = cache->scale_page_stride;
+  a.scale_head_stride = cache->scale_head_stride;
+  a.out_page_stride = out->page_stride;
+  a.out_token_stride = out->token_stride;
+  a.out_head_stride = out->head_stride;
+  a.pages = pages;
+  a.n = n;
+  a.n_pages = cache->n_pages;
+  a.Hkv = cache->Hkv;
+  a.page_size = cache->page_size;
+  a.token_first = cache->token_stride < cache->head_stride;
+  launch_paged_read8(a, out->dtype == LCA_F16, sms, static_cast<cudaStream_t>(stream));
+  LCA_CUDA(cudaGetLastError());
+  return LCA_OK;
+}
+
 lca_status lca_attn_paged_workspace_size(const lca_paged_shape* shape, const lca_paged_cache* cache,
                                          const lca_mask_desc* mask, size_t* bytes) {
   if (!bytes) return LCA_ERR_INVALID_ARG;
@@ -303,104 +564,28 @@ lca_status lca_attn_paged(const void* q, const lca_paged_cache* cache, const int
                           const int32_t* q_start, const int32_t* k_len, void* o, float* lse,
                           const lca_paged_shape* shape, const lca_mask_desc* mask, void* workspace,
                           size_t workspace_bytes, void* stream) {
-  PagedAttnArgs a{};
-  const lca_status r = check_attn(shape, cache, mask, a.mask);
+  return attend({cache, nullptr}, cache ? cache->dtype : 0, q, block_table, q_start, k_len, o, lse, shape, mask, workspace,
+                workspace_bytes, stream);
+}
+
+lca_status lca_attn_paged_fp8_workspace_size(const lca_paged_shape* shape, const lca_paged_cache_fp8* cache,
+                                             const lca_mask_desc* mask, size_t* bytes) {
+  const lca_status r = check_cache8(cache);
   if (r != LCA_OK) return r;
-  const PagedLayout L = paged_layout(shape, cache);
-  if (!workspace || reinterpret_cast<uintptr_t>(workspace) % kAlign != 0 || workspace_bytes < L.total ||
-      !device_input(workspace))
-    return LCA_ERR_WORKSPACE;
-  const long long n_table =
-      shape->n_seq > 0 && shape->max_pages > 0 ? (shape->n_seq - 1) * shape->table_stride + shape->max_pages : 0;
-  if (!ints(block_table, n_table) || !ints(q_start, shape->n_seq > 0 ? shape->n_seq + 1LL : 0) ||
-      !ints(k_len, shape->n_seq) || (shape->ctx_len && !ints(shape->ctx_len, shape->n_seq)) || !cache_memory(cache))
-    return LCA_ERR_INVALID_ARG;
-  if (shape->Tq > 0) {
-    if (!q || !aligned16(q) || !device_input(q) || !o || !aligned16(o) || !device_input(o) || !lse || !aligned4(lse) ||
-        !device_input(lse))
-      return LCA_ERR_INVALID_ARG;
-  }
-  {  // an empty batch writes its workspace too
-    const long long rows = shape->Tq, heads = shape->Hq;
-    const long long extent = cache_extent(cache);
-    const struct {
-      const void* p;
-      long long bytes;
-    } t[10] = {{o, rows * heads * kHeadDim * 2},
-              {lse, rows * heads * 4},
-              {workspace, static_cast<long long>(L.total)},
-              {q, rows > 0 ? ((rows - 1) * shape->q_stride + heads * kHeadDim) * 2 : 0},
-              {cache->k, extent},
-              {cache->v, extent},
-              {block_table, 4 * n_table},
-              {q_start, 4 * (shape->n_seq + 1LL)},
-              {k_len, 4LL * shape->n_seq},
-              {shape->ctx_len, shape->ctx_len ? 4LL * shape->n_seq : 0}};
-    for (int i = 0; i < 3; ++i)  // the first three are written
-      for (int j = i + 1; j < 10; ++j)
-        if (overlap(t[i].p, t[i].bytes, t[j].p, t[j].bytes)) return LCA_ERR_INVALID_ARG;
-  }
-  const int sms = num_sms();
-  if (sms <= 0) return LCA_ERR_CUDA;
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
-  a.q = q;
-  a.kc = cache->k;
-  a.vc = cache->v;
-  a.q_stride = shape->q_stride;
-  a.page_stride = cache->page_stride;
-  a.token_stride = cache->token_stride;
-  a.head_stride = cache->head_stride;
-  a.table_stride = shape->table_stride;
-  a.table = block_table;
-  a.q_start = q_start;
-  a.k_len = k_len;
-  a.ctx_len = shape->ctx_len;
-  a.o = o;
-  a.lse = lse;
-  a.status = reinterpret_cast<int*>(ws + L.status);
-  a.arrived = reinterpret_cast<int*>(ws + L.arrived);
-  a.claims = a.arrived + kPagedMaxSpans;
-  a.parts = reinterpret_cast<float*>(ws + L.parts);
-  a.Tq = shape->Tq;
-  a.Hq = shape->Hq;
-  a.Hkv = cache->Hkv;
-  a.G = shape->Hq / cache->Hkv;
-  a.n_seq = shape->n_seq;
-  a.max_pages = shape->max_pages;
-  a.page_size = cache->page_size;
-  a.n_pages = cache->n_pages;
-  const float scale = shape->scale > 0.f ? shape->scale : 1.0f / std::sqrt(static_cast<float>(kHeadDim));
-  a.scale_log2 = scale * 1.4426950408889634f;
-  if (cache->n_pages == 0) a.kc = a.vc = q;  // no key is read; the address is only given
-  const bool many = many_rows(shape, cache) && shape->n_seq > 0;
-  a.few = many ? kPagedFewRows : 0x7FFFFFFF;
-  CUtensorMap tq, tk, tv;
-  if (many) {
-    a.tpt = tokens_per_tile(shape, cache);
-    a.box_rows = kTile;
-    while (cache->page_size % a.box_rows != 0) a.box_rows /= 2;
-    a.head_first = map_strides(cache).head_first;
-    a.max_blocks = L.max_blocks;
-    a.block0 = reinterpret_cast<int*>(ws + L.block0);
-    a.line = reinterpret_cast<long long*>(ws + L.line);
-    a.cuts = reinterpret_cast<PagedCut*>(ws + L.cuts);
-    a.chunk_parts = reinterpret_cast<float*>(ws + L.chunk_parts);
-    a.out_v8 = (reinterpret_cast<uintptr_t>(o) & 31u) == 0;
-    a.wait_limit_ns = wait_limit_ns();
-    const cuuint64_t dims[3] = {kHeadDim, static_cast<cuuint64_t>(a.Hq), static_cast<cuuint64_t>(a.Tq)};
-    const cuuint64_t strides[2] = {kHeadDim * 2, static_cast<cuuint64_t>(a.q_stride) * 2};
-    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(a.G), static_cast<cuuint32_t>(a.tpt)};
-    if (!encode(&tq, q, cache->dtype, 3, dims, strides, box) || !cache_map(&tk, cache->k, cache, a.box_rows) ||
-        !cache_map(&tv, cache->v, cache, a.box_rows))
-      return LCA_ERR_CUDA;
-  }
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const bool fp16 = cache->dtype == LCA_F16;
-  LCA_CUDA(launch_paged_begin(a, many, st));
-  if (many) LCA_CUDA(launch_paged_chunk(tq, tk, tv, a, fp16, sms, st));
-  if (shape->Tq > 0) LCA_CUDA(launch_paged_decode(a, many, fp16, sms, st));
-  if (many) LCA_CUDA(launch_paged_join(a, fp16, sms, st));
-  return LCA_OK;
+  const lca_paged_cache v = values_of(cache);
+  return lca_attn_paged_workspace_size(shape, &v, mask, bytes);
+}
+
+lca_status lca_attn_paged_fp8(const void* q, int32_t dtype, const lca_paged_cache_fp8* cache, const int32_t* block_table,
+                              const int32_t* q_start, const int32_t* k_len, void* o, float* lse,
+                              const lca_paged_shape* shape, const lca_mask_desc* mask, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+  const lca_status r = check_cache8(cache);
+  if (r != LCA_OK) return r;
+  if (dtype != LCA_BF16 && dtype != LCA_F16) return LCA_ERR_INVALID_ARG;
+  const lca_paged_cache v = values_of(cache);
+  return attend({&v, cache}, dtype, q, block_table, q_start, k_len, o, lse, shape, mask, workspace, workspace_bytes,
+                stream);
 }
 
 }  // extern "C"
