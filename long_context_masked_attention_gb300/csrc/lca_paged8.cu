@@ -401,7 +401,7 @@ struct Worker8 {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) bad |= __vcmpeq4(word(v[i], k) & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+          for (int k = 0; k < 4; ++k) bad |= e4m3_nan(word(v[i], k));
         if (__any_sync(~0u, bad)) hide_nan(v, sv, j0, sa, sb, o);
       }
 #pragma unroll
@@ -443,7 +443,7 @@ struct Worker8 {
   // needed).
   static __device__ __forceinline__ void hide_nan(uint4 (&v)[4], uint32_t sv, int j0, const Span& sa, const Span& sb, float (&o)[16][4]) {
     const int c = threadIdx.x & 3;
-    auto clear = [](uint32_t& w) { w &= ~__vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu); };
+    auto clear = [](uint32_t& w) { w &= ~((e4m3_nan(w) >> 7) * 0xFFu); };
 #pragma unroll
     for (int i = 0; i < 4; ++i) clear(v[i].x), clear(v[i].y), clear(v[i].z), clear(v[i].w);
     const float nan = __uint_as_float(0x7FC00000u);

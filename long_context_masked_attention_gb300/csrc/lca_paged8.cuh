@@ -4,6 +4,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "lca_paged.cuh"
 #include "lca_paged8.h"
 
 namespace lca {
@@ -36,6 +37,9 @@ __device__ __forceinline__ uint32_t e4m3x2_hi_to_f16x2(uint32_t x) {
   return r;
 }
 __device__ __forceinline__ float2 f16x2_to_float2(uint32_t x) { return __half22float2(*reinterpret_cast<const __half2*>(&x)); }
+
+// The top bits of the bytes that are NaN.
+__device__ __forceinline__ uint32_t e4m3_nan(uint32_t x) { return ((x & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
 
 // Two 32-bit values as e4m3 (lo in the low byte); what lies past 448 becomes 448, NaN stays.
 __device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {

@@ -32,6 +32,9 @@ struct PagedRead8Args {
 };
 void launch_paged_read8(const PagedRead8Args& a, bool fp16, int num_sms, cudaStream_t st);
 
+// The maps of K and V have boxes of box_rows rows of 128 bytes.
+cudaError_t launch_paged_chunk8(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                                const PagedAttnArgs& a, bool fp16, int num_sms, cudaStream_t st);
 cudaError_t launch_paged_decode8(const PagedAttnArgs& a, bool behind, bool fp16, int num_sms, cudaStream_t st);
 
 }  // namespace lca

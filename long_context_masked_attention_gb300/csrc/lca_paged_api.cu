@@ -231,33 +231,39 @@ lca_status check_attn(const lca_paged_shape* sh, const lca_paged_cache* c, const
   return LCA_OK;
 }
 
-bool encode(CUtensorMap* m, const void* p, int dtype, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
-            const cuuint32_t* box) {
+bool encode(CUtensorMap* m, const void* p, CUtensorMapDataType type, int rank, const cuuint64_t* dims,
+            const cuuint64_t* strides, const cuuint32_t* box) {
   const auto fn = encode_fn();
   if (!fn) {
     driver_fail("cuTensorMapEncodeTiled entry point", 0);
     return false;
   }
   const cuuint32_t estr[4] = {1, 1, 1, 1};
-  const CUresult r = fn(m, dtype == LCA_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank,
-                        const_cast<void*>(p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+  const CUresult r = fn(m, type, rank, const_cast<void*>(p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) driver_fail("cuTensorMapEncodeTiled", static_cast<int>(r));
   return r == CUDA_SUCCESS;
 }
 
-bool cache_map(CUtensorMap* m, const void* p, const lca_paged_cache* c, int box_rows) {
+CUtensorMapDataType map_type(int dtype) {
+  return dtype == LCA_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+}
+
+// Boxes of box_rows rows of 128 bytes.
+bool cache_map(CUtensorMap* m, const void* p, const Cache& any, int box_rows) {
+  const lca_paged_cache* c = any.c;
+  const cuuint64_t bytes = static_cast<cuuint64_t>(any.bytes());
   const MapStrides st = map_strides(c);
   const bool hf = st.head_first;
   const cuuint64_t tokens = static_cast<cuuint64_t>(c->page_size), heads = static_cast<cuuint64_t>(c->Hkv);
   const cuuint64_t dims[4] = {kHeadDim, hf ? heads : tokens, hf ? tokens : heads, static_cast<cuuint64_t>(c->n_pages)};
-  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(hf ? st.head : st.token) * 2,
-                                 static_cast<cuuint64_t>(hf ? st.token : st.head) * 2,
-                                 static_cast<cuuint64_t>(st.page) * 2};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(hf ? st.head : st.token) * bytes,
+                                 static_cast<cuuint64_t>(hf ? st.token : st.head) * bytes,
+                                 static_cast<cuuint64_t>(st.page) * bytes};
   const cuuint32_t rows = static_cast<cuuint32_t>(box_rows);
-  const cuuint32_t box[4] = {64, hf ? 1 : rows, hf ? rows : 1, 1};
-  return encode(m, p, c->dtype, 4, dims, strides, box);
+  const cuuint32_t box[4] = {any.c8 ? 128u : 64u, hf ? 1 : rows, hf ? rows : 1, 1};
+  return encode(m, p, any.c8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : map_type(c->dtype), 4, dims, strides, box);
 }
 
 // lca_attn_paged over a cache of either kind, q and o of `dtype`.
@@ -345,7 +351,7 @@ lca_status attend(const Cache& any, int dtype, const void* q, const int32_t* blo
     a.kc = a.vc = q;
     a.ks = a.vs = static_cast<const uint8_t*>(q);
   }
-  const bool many = !c8 && many_rows(shape, cache) && shape->n_seq > 0;
+  const bool many = many_rows(shape, cache) && shape->n_seq > 0;
   a.few = many ? kPagedFewRows : 0x7FFFFFFF;
   CUtensorMap tq, tk, tv;
   if (many) {
@@ -363,15 +369,15 @@ lca_status attend(const Cache& any, int dtype, const void* q, const int32_t* blo
     const cuuint64_t dims[3] = {kHeadDim, static_cast<cuuint64_t>(a.Hq), static_cast<cuuint64_t>(a.Tq)};
     const cuuint64_t strides[2] = {kHeadDim * 2, static_cast<cuuint64_t>(a.q_stride) * 2};
     const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(a.G), static_cast<cuuint32_t>(a.tpt)};
-    if (!encode(&tq, q, dtype, 3, dims, strides, box) || !cache_map(&tk, cache->k, cache, a.box_rows) ||
-        !cache_map(&tv, cache->v, cache, a.box_rows))
+    if (!encode(&tq, q, map_type(dtype), 3, dims, strides, box) || !cache_map(&tk, cache->k, any, a.box_rows) ||
+        !cache_map(&tv, cache->v, any, a.box_rows))
       return LCA_ERR_CUDA;
   }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool fp16 = dtype == LCA_F16;
   LCA_CUDA(launch_paged_begin(a, many, st));
-  if (many) LCA_CUDA(launch_paged_chunk(tq, tk, tv, a, fp16, sms, st));
-  if (shape->Tq > 0) LCA_CUDA(c8 ? launch_paged_decode8(a, many, fp16, sms, st) : launch_paged_decode(a, many, fp16, sms, st));
+  if (many) LCA_CUDA((c8 ? launch_paged_chunk8 : launch_paged_chunk)(tq, tk, tv, a, fp16, sms, st));
+  if (shape->Tq > 0) LCA_CUDA((c8 ? launch_paged_decode8 : launch_paged_decode)(a, many, fp16, sms, st));
   if (many) LCA_CUDA(launch_paged_join(a, fp16, sms, st));
   return LCA_OK;
 }
