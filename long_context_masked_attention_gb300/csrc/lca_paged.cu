@@ -194,6 +194,11 @@ __global__ void __launch_bounds__(256) paged_write_kernel(const PagedWriteArgs a
 // 364 us (6.5 TB/s, 0.96 of a copy's rate); 4 of 512K 1246 us (6.9 TB/s); 32 of
 // 2K-16K with 16 heads of their own 249 us (6.5 TB/s); one of 4K 18.5 us, which
 // is latency: start-up, keys and the join of the pieces.
+constexpr int kUnit = 64;                     // keys per unit
+constexpr int kRows = 16;                     // rows per item
+constexpr int kSlice = kUnit / kDecWarps;     // keys per warp and unit
+static_assert(kSlice == 16, "a slice is one k16 step of the product with V");
+static_assert(kRows * (kHeadDim + 2) == kPagedPartFloats, "workspace layout");
 constexpr int kDecStages = 3;
 constexpr int kSliceBytes = kSlice * 256;     // of K or V
 constexpr int kWarpBytes = kDecStages * 2 * kSliceBytes;
@@ -256,7 +261,7 @@ __device__ __forceinline__ void decode_warp(const PagedAttnArgs& a, uint32_t rin
   auto entry = [&](int batch) -> int {  // page of this lane's group, -1 where none is needed or it is no page
     const int u = batch * 16 + (lane >> 1);
     if (u >= n) return -1;
-    const int j = un.first_key(u0 + u) + warp * kSlice + (lane & 1) * 8;
+    const int j = un.at(u0 + u) * kUnit + warp * kSlice + (lane & 1) * 8;
     if (!span_hits(hl, j, j + 8)) return -1;
     const int p = __ldg(table + j / a.page_size);
     if (p < 0 || p >= a.n_pages) {
@@ -267,7 +272,7 @@ __device__ __forceinline__ void decode_warp(const PagedAttnArgs& a, uint32_t rin
   };
   auto offset = [&](int batch, int page) -> long long {
     if (page < 0) return -1;
-    const int j = un.first_key(u0 + batch * 16 + (lane >> 1)) + warp * kSlice + (lane & 1) * 8;
+    const int j = un.at(u0 + batch * 16 + (lane >> 1)) * kUnit + warp * kSlice + (lane & 1) * 8;
     return page * a.page_stride + j % a.page_size * a.token_stride;
   };
   // a lane copies 16 bytes of every second key of a group: its first key's
@@ -288,7 +293,7 @@ __device__ __forceinline__ void decode_warp(const PagedAttnArgs& a, uint32_t rin
         off = offset(u >> 4, page_next);
         page_next = entry((u >> 4) + 1);
       }
-      const int j0 = un.first_key(u0 + u) + warp * kSlice;
+      const int j0 = un.at(u0 + u) * kUnit + warp * kSlice;
       const bool all = span_covers(hl, j0, j0 + kSlice);  // no key to leave out
       if (all || span_hits(hl, j0, j0 + kSlice)) {
         const uint32_t dst = ring + (u % kDecStages) * 2 * kSliceBytes;
@@ -336,7 +341,7 @@ __device__ __forceinline__ void decode_warp(const PagedAttnArgs& a, uint32_t rin
     if (u < 0) continue;
     cp_async_wait<2>();
     __syncwarp();
-    const int j0 = un.first_key(u0 + u) + warp * kSlice;
+    const int j0 = un.at(u0 + u) * kUnit + warp * kSlice;
     if (!span_hits(hl, j0, j0 + kSlice)) continue;
     const uint32_t sk = ring + (u % kDecStages) * 2 * kSliceBytes, sv = sk + kSliceBytes;
     float s[2][4] = {};
@@ -449,6 +454,7 @@ __device__ __forceinline__ void decode_warp(const PagedAttnArgs& a, uint32_t rin
 template <typename T>
 struct Worker16 {
   using Out = T;
+  static constexpr int kRows = lca::kRows, kUnit = lca::kUnit;
   static constexpr int kWarpBytes = lca::kWarpBytes;
   static constexpr float kBias = lca::kBias<T>;
   static __device__ __forceinline__ void run(const PagedAttnArgs& a, uint8_t* ring, int seq, const Request& sg,
@@ -482,7 +488,7 @@ template <typename T>
 __global__ void __launch_bounds__(kDecThreads, 2)
     paged_decode_kernel(const __grid_constant__ PagedAttnArgs a, bool behind) {
   extern __shared__ __align__(1024) uint8_t ring[];
-  __shared__ DecodeShared sh;
+  __shared__ DecodeShared<kRows> sh;
   launch_dependents();
   decode_span<Worker16<T>>(a, sh, ring, behind);
   clear_unowned_rows(a);

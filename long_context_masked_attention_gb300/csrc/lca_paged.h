@@ -68,7 +68,7 @@ struct PagedAttnArgs {
   int* status;
   int* arrived;  // [kPagedMaxSpans] pieces finished of the split item that starts in a span
   int* claims;   // [1] spans claimed past the CTAs' first ones
-  float* parts;  // [kPagedMaxSpans][2][kPagedPartFloats]
+  float* parts;  // [kPagedMaxSpans][2][rows of an item x (kHeadDim + 2)]
   int Tq, Hq, Hkv, G, n_seq, max_pages, page_size, n_pages;
   float scale_log2;
   int few;  // rows per KV head up to which the kernel for few rows serves a request

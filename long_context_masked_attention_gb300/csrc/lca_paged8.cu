@@ -128,7 +128,8 @@ __global__ void __launch_bounds__(256) paged_read8_kernel(const PagedRead8Args a
 }
 
 // ------------------------------------------------------------------ attention, few rows
-// A warp's share of the line in lca_paged_few.cuh: a key costs 258 bytes.
+// A warp's share of the line in lca_paged_few.cuh: a key costs 258 bytes, which
+// bounds the work once the instructions that a key costs are few enough.
 //
 // Mathematics.  With factors 2^ek and 2^ev of a key's rows and e4m3 values k8
 // and v8, s = scale 2^ek q.k8 and o = sum e^s 2^ev v8 / sum e^s.  The maximum
@@ -139,24 +140,31 @@ __global__ void __launch_bounds__(256) paged_read8_kernel(const PagedRead8Args a
 // Both products take fp16 operands, which hold e4m3 exactly.  q is scaled by a power
 // of two per row, so that its largest value is near 2^14: a bf16 q below 2^-28
 // of its row's largest loses bits, which shows in scores at 2^-38 of the largest
-// product.  w is rounded to fp16 times up to 2^12: keys down to 2^-36 of the
-// largest count, below 2^-26 with fewer bits.  The sums go by m = max - 12,
-// rounded up: where 12 is less than the last place of a huge score, w stays at
-// most 2^12.
+// product.  w is rounded to fp16 times 2^12 to 2^15: keys down to 2^-36 of the
+// largest count, below 2^-26 with fewer bits.  The sums go by m, which was max -
+// 12 when it was last set: it moves up (and the sums are rescaled) only once
+// 2^15 would be passed.  It is rounded up, so that w stays in range where 12 is
+// less than the last place of a huge score.
 //
-// A lane's operands come from shared memory by 16-byte loads and are converted
-// in registers.  The order of the 128 products of a score, and of the columns of O,
-// is free, so a lane takes the bytes that lie together: of key lane / 4 the
-// pieces lane % 4 and lane % 4 + 4 (four values are the two registers of one
-// k16 step, q permuted to fit), and of the four keys of its rows of V the
-// piece lane / 4, whose 16 columns are those of the 16 n8 tiles.  Pieces are
-// swizzled so that neither pattern has bank conflicts.
-constexpr int kStages8 = 3;
-constexpr int kSlice8 = kSlice * 128;                 // of K or V
-constexpr int kStage8 = 2 * kSlice8 + 2 * kSlice;     // with the factors' bytes
-constexpr int kWarp8 = kStages8 * kStage8;
-constexpr int kFewSmem8 = kDecWarps * kWarp8;
-static_assert(kWarp8 >= 16 * 132 * 4 && kStage8 % 16 == 0, "the ring holds a warp's sums at the end");
+// Layout.  The keys are the rows of the products and the rows of q their
+// columns: S^T = K q^T and O^T = V^T w^T, m16n8k16.  So a tile of 8 rows wastes
+// nothing where 8 query heads share a KV head, 32 rows share what a key's
+// conversion costs, and the sums of a row of O are 16 values a lane.  The
+// operands K and V^T come from shared memory by 16-byte loads and are converted in
+// registers.  The order of the 128 products of a score, and of the rows of O^T,
+// is free, so a lane takes the bytes that lie together: of keys lane / 4 and 8
+// more the pieces lane % 4 and lane % 4 + 4 (four values are two registers of one
+// k16 step, q permuted to fit), and of its four keys' values the piece
+// lane / 4, whose 16 columns are its two rows of eight m16 tiles.  Pieces are
+// swizzled so that neither pattern has bank conflicts.  The weights come as
+// (key, rows) and are needed as (row, keys): movmatrix.
+constexpr int kStages8 = 2;
+constexpr int kUnit8 = 128;                           // keys per unit
+constexpr int kKeys8 = kUnit8 / kDecWarps;            // per warp and unit, two k16 steps of the product with V
+constexpr int kSlice8 = kKeys8 * 128;                 // bytes of K or V
+constexpr int kStage8 = 2 * kSlice8 + 2 * kKeys8;     // with the factors'
+constexpr int kWarp8 = kStages8 * kStage8 > 16 * 132 * 4 ? kStages8 * kStage8 : 16 * 132 * 4;
+static_assert(kKeys8 == 32 && kStage8 % 16 == 0, "four groups of 8 keys, two steps of 16");
 
 __device__ __forceinline__ uint32_t swizzle8(int key) { return (key & 6) ^ ((key & 1) << 2); }
 
@@ -169,16 +177,22 @@ __device__ __forceinline__ uint4 lds16(uint32_t addr) {
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(addr) : "memory");
   return r;
 }
-__device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
-  uint16_t r;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(r) : "r"(addr) : "memory");
+__device__ __forceinline__ uint32_t lds_u8(uint32_t addr) {
+  uint32_t r;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(r) : "r"(addr) : "memory");
   return r;
 }
 __device__ __forceinline__ uint32_t word(const uint4& x, int i) { return i == 0 ? x.x : i == 1 ? x.y : i == 2 ? x.z : x.w; }
+// An 8 x 8 matrix of 16-bit values, a pair per lane, transposed.
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
 
-// Values of the q's row for the k16 steps, fp16 of q times 2^-e; returns e.
+// A row of q for the k16 steps, fp16 of q times 2^-e; returns e.
 template <typename T>
-__device__ __forceinline__ int load_q(const T* row, int c, uint32_t (&lo)[8], uint32_t (&hi)[8]) {
+__device__ __forceinline__ int load_q(const T* row, int c, uint32_t (&q)[8][2]) {
   uint4 x[4];  // pieces c and c + 4, 16 values each
 #pragma unroll
   for (int i = 0; i < 4; ++i) x[i] = __ldg(reinterpret_cast<const uint4*>(row + 16 * (c + 4 * (i >> 1)) + 8 * (i & 1)));
@@ -193,8 +207,8 @@ __device__ __forceinline__ int load_q(const T* row, int c, uint32_t (&lo)[8], ui
     }
   m = fmaxf(m, __shfl_xor_sync(~0u, m, 1));
   m = fmaxf(m, __shfl_xor_sync(~0u, m, 2));
-  // the largest lands in [2^14, 2^15), in steps that a float can take: 2^-e
-  // itself may be past its range
+  // the largest lands in [2^14, 2^15), in two steps: 2^-e itself may be past
+  // a float's range
   const int e = max(static_cast<int>(__float_as_uint(m) >> 23), 1) - 127 - 14;
   const float f0 = two_to(-e / 2), f1 = two_to(-e - -e / 2);
 #pragma unroll
@@ -202,38 +216,38 @@ __device__ __forceinline__ int load_q(const T* row, int c, uint32_t (&lo)[8], ui
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const float2 v = Half2<T>::unpack(word(x[i], k));
-      const uint32_t h = Half2<__half>::pack(v.x * f0 * f1, v.y * f0 * f1);
-      const int step = 2 * i + (k >> 1);  // four values a step
-      if (k & 1) hi[step] = h; else lo[step] = h;
+      q[2 * i + (k >> 1)][k & 1] = Half2<__half>::pack(v.x * f0 * f1, v.y * f0 * f1);  // four values a step
     }
   return e;
 }
 
-template <typename T>
+// kTiles: tiles of 8 rows in an item.
+template <typename T, int kTiles>
 struct Worker8 {
   using Out = T;
-  static constexpr int kWarpBytes = kWarp8;
+  static constexpr int kRows = 8 * kTiles, kUnit = kUnit8;
+  static constexpr int kWarpBytes = kWarp8 > kRows * 132 * 4 ? kWarp8 : kRows * 132 * 4;
   static constexpr float kBias = 0.f;
   static __device__ __forceinline__ void run(const PagedAttnArgs& a, uint8_t* ring_, int seq, const Request& sg,
                                              const Units& un, int tile, int head, int u0, int n, float* m_out, float* l_out) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
     const uint32_t ring = smem_u32(ring_);
-    const int rows = min(static_cast<int>(min(static_cast<long long>(sg.q_len) * a.G - static_cast<long long>(tile) * kRows, 16LL)), kRows);
-    const int r_first = tile * kRows, r_last = r_first + rows - 1;
-    const int ra = min(r_first + g, r_last), rb = min(r_first + g + 8, r_last);
-    const Span own = paged_span(a, sg.q_len, sg.k_len, min(r_first + (lane & 15), r_last) / a.G);
+    const int r_first = tile * kRows;
+    const int r_last = r_first + static_cast<int>(min(static_cast<long long>(sg.q_len) * a.G - r_first, static_cast<long long>(kRows))) - 1;
+    // lane r finds row r's keys (a row past the last one repeats it, unused); hl: what some row attends
+    const Span own = paged_span(a, sg.q_len, sg.k_len, min(r_first + lane % kRows, r_last) / a.G);
     auto row_of = [&](int r) {
       return Span{__shfl_sync(~0u, own.a0, r), __shfl_sync(~0u, own.b0, r), __shfl_sync(~0u, own.a1, r),
                   __shfl_sync(~0u, own.b1, r)};
     };
-    const Span sa = row_of(g), sb = row_of(g + 8), hl = hull_of(row_of(0), row_of(15));
+    const Span hl = hull_of(row_of(0), row_of(kRows - 1));
 
-    // pages of 8-key groups: lane 2 t + i holds group i of unit t of a batch of 16
+    // where 8-key groups lie: lane 4 t + i has group i of unit t of a batch of 8 units
     const int* table = a.table + seq * a.table_stride;
-    auto entry = [&](int batch) -> int {  // -1 where none is needed or it is no page
-      const int u = batch * 16 + (lane >> 1);
-      if (u >= n) return -1;
-      const int j = un.first_key(u0 + u) + warp * kSlice + (lane & 1) * 8;
+    auto key_of = [&](int batch) { return un.at(u0 + batch * 8 + (lane >> 2)) * kUnit8 + warp * kKeys8 + (lane & 3) * 8; };
+    auto entry = [&](int batch) -> int {  // page, -1 where none is needed or it is no page
+      if (batch * 8 + (lane >> 2) >= n) return -1;
+      const int j = key_of(batch);
       if (!span_hits(hl, j, j + 8)) return -1;
       const int p = __ldg(table + j / a.page_size);
       if (p < 0 || p >= a.n_pages) {
@@ -244,246 +258,273 @@ struct Worker8 {
     };
     // a lane copies 16 bytes of every fourth key of a group
     const uint8_t* const k_lane = static_cast<const uint8_t*>(a.kc) + head * a.head_stride + (lane >> 3) * a.token_stride + (lane & 7) * 16;
-    const long long to_v = static_cast<const char*>(a.vc) - static_cast<const char*>(a.kc);
-    const uint8_t* const s_lane = ((lane & 2) ? a.vs : a.ks) + head * a.scale_head_stride;
+    const long long to_v = static_cast<const char*>(a.vc) - static_cast<const char*>(a.kc), step = 4 * a.token_stride;
     uint32_t place[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int key = 4 * i + (lane >> 3);
       place[i] = key * 128 + (((lane & 7) ^ swizzle8(key)) << 4);
     }
-    int page_now = -1, page_next = entry(0), in_page = 0;
-    auto issue = [&](int u) {  // copies the warp's keys of unit u into stage u % kStages8
+    int page_next = entry(0);
+    long long off = -1, off_f = 0;  // of this lane's group: its first key, its factors
+    auto issue = [&](int u) {       // copies the warp's keys of unit u into stage u % kStages8
       if (u < n) {
-        if ((u & 15) == 0) {
-          page_now = page_next;
-          const int v = u + (lane >> 1);
-          in_page = v < n ? (un.first_key(u0 + v) + warp * kSlice + (lane & 1) * 8) % a.page_size : 0;
-          page_next = entry((u >> 4) + 1);
+        if ((u & 7) == 0) {
+          off = -1;
+          if (page_next >= 0) {
+            const int in = key_of(u >> 3) % a.page_size;
+            off = page_next * a.page_stride + in * a.token_stride;
+            off_f = page_next * a.scale_page_stride + head * a.scale_head_stride + in;
+          }
+          page_next = entry((u >> 3) + 1);
         }
-        const int j0 = un.first_key(u0 + u) + warp * kSlice;
-        const bool all = span_covers(hl, j0, j0 + kSlice);
-        if (all || span_hits(hl, j0, j0 + kSlice)) {
+        const int j0 = un.at(u0 + u) * kUnit8 + warp * kKeys8;
+        const bool all = span_covers(hl, j0, j0 + kKeys8);
+        if (all || span_hits(hl, j0, j0 + kKeys8)) {
           const uint32_t dst = ring + (u % kStages8) * kStage8;
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int page = __shfl_sync(~0u, page_now, 2 * (u & 15) + i), in = __shfl_sync(~0u, in_page, 2 * (u & 15) + i);
-            const uint8_t* src = k_lane + max(page, 0) * a.page_stride + in * a.token_stride;
+          for (int i = 0; i < 4; ++i) {
+            const long long base = __shfl_sync(~0u, off, 4 * (u & 7) + i);
+            const uint8_t* src = k_lane + max(base, 0LL);
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-              const uint32_t bytes = page >= 0 && (all || in_span(hl, j0 + 8 * i + 4 * k + (lane >> 3))) ? 16u : 0u;
+              const uint32_t bytes = base >= 0 && (all || in_span(hl, j0 + 8 * i + 4 * k + (lane >> 3))) ? 16u : 0u;
               cp_async_16(dst + i * 1024 + place[k], src, bytes);
               cp_async_16(dst + i * 1024 + place[k] + kSlice8, src + to_v, bytes);
-              src += 4 * a.token_stride;
+              src += step;
             }
-            // lanes i (K) and i + 2 (V): the group's factors
-            if (lane < 4 && (lane & 1) == i)
-              cp_async_8(dst + 2 * kSlice8 + (lane >> 1) * kSlice + i * 8, s_lane + max(page, 0) * a.scale_page_stride + in, page >= 0 ? 8u : 0u);
+          }
+          if ((lane >> 2) == (u & 7)) {
+            const uint32_t bytes = off >= 0 ? 8u : 0u;
+            cp_async_8(dst + 2 * kSlice8 + c * 8, a.ks + off_f, bytes);
+            cp_async_8(dst + 2 * kSlice8 + kKeys8 + c * 8, a.vs + off_f, bytes);
           }
         }
       }
       cp_async_commit();
     };
-    uint32_t qa[8][4];
-    float fa, fb;  // scores of row ra are fa times the products with q's fp16 form
-    {
-      const T* q = static_cast<const T*>(a.q);
-      uint32_t lo[8], hi[8];
-      int e = load_q(q + (sg.q_off + ra / a.G) * a.q_stride + (head * a.G + ra % a.G) * kHeadDim, c, lo, hi);
-      fa = ldexpf(a.scale_log2, e);
+    uint32_t q[kTiles][8][2];
+    float f[kTiles][2];  // scores of rows 8 t + 2 c and the next are that times the products with q's fp16 form
 #pragma unroll
-      for (int s = 0; s < 8; ++s) qa[s][0] = lo[s], qa[s][2] = hi[s];
-      e = load_q(q + (sg.q_off + rb / a.G) * a.q_stride + (head * a.G + rb % a.G) * kHeadDim, c, lo, hi);
-      fb = ldexpf(a.scale_log2, e);
-#pragma unroll
-      for (int s = 0; s < 8; ++s) qa[s][1] = lo[s], qa[s][3] = hi[s];
+    for (int t = 0; t < kTiles; ++t) {
+      const int r = min(r_first + 8 * t + g, r_last);
+      const int e = load_q(static_cast<const T*>(a.q) + (sg.q_off + r / a.G) * a.q_stride + (head * a.G + r % a.G) * kHeadDim, c, q[t]);
+      const float x = ldexpf(a.scale_log2, e);
+      f[t][0] = __shfl_sync(~0u, x, 8 * c);
+      f[t][1] = __shfl_sync(~0u, x, 8 * c + 4);
     }
-    float o[16][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    float o[kTiles][8][4], m[kTiles][2], l[kTiles][2];
 #pragma unroll
-    for (int t = 0; t < 16; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
-
+    for (int t = 0; t < kTiles; ++t) {
+      m[t][0] = m[t][1] = -INFINITY;
+      l[t][0] = l[t][1] = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[t][i][0] = o[t][i][1] = o[t][i][2] = o[t][i][3] = 0.f;
+    }
     const uint32_t k_at = g * 128 + ((c ^ swizzle8(g)) << 4);  // key g, piece c; piece c + 4 differs in one bit
     uint32_t v_at[2];                                          // keys 2 c and 2 c + 1, piece g
 #pragma unroll
     for (int i = 0; i < 2; ++i) v_at[i] = (2 * c + i) * 128 + ((g ^ swizzle8(2 * c + i)) << 4);
 #pragma unroll 1
-    for (int u = -2; u < n; ++u) {
-      issue(u + 2);
+    for (int u = 1 - kStages8; u < n; ++u) {
+      issue(u + kStages8 - 1);
       if (u < 0) continue;
-      cp_async_wait<2>();
+      cp_async_wait<kStages8 - 1>();
       __syncwarp();
-      const int j0 = un.first_key(u0 + u) + warp * kSlice;
-      if (!span_hits(hl, j0, j0 + kSlice)) continue;
+      const int j0 = un.at(u0 + u) * kUnit8 + warp * kKeys8;
+      if (!span_hits(hl, j0, j0 + kKeys8)) continue;
       const uint32_t sk = ring + (u % kStages8) * kStage8, sv = sk + kSlice8, sf = sv + kSlice8;
-      float s[2][4] = {};
+      const bool part = !__all_sync(~0u, span_covers(own, j0, j0 + kKeys8));
+      // scores of keys 16 b + g (s[..][0], s[..][1]: the lane's two rows of a tile) and 16 b + g + 8
+      float s[2][kTiles][4];
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
+      for (int b = 0; b < 2; ++b) {
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) s[b][t][0] = s[b][t][1] = s[b][t][2] = s[b][t][3] = 0.f;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const uint4 x = lds16(sk + t * 1024 + (k_at ^ (h << 6)));
+          const uint4 x = lds16(sk + b * 2048 + (k_at ^ (h << 6))), y = lds16(sk + b * 2048 + 1024 + (k_at ^ (h << 6)));
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            warp_mma(s[t], qa[4 * h + k], e4m3x2_to_f16x2(word(x, k)), e4m3x2_hi_to_f16x2(word(x, k)), __half());
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t w[4] = {e4m3x2_to_f16x2(word(x, k)), e4m3x2_to_f16x2(word(y, k)), e4m3x2_hi_to_f16x2(word(x, k)),
+                                   e4m3x2_hi_to_f16x2(word(y, k))};
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t) warp_mma(s[b][t], w, q[t][4 * h + k][0], q[t][4 * h + k][1], __half());
+          }
         }
-      // keys 2 c, 2 c + 1, 2 c + 8, 2 c + 9 of the slice: exponents of their factors
-      float ek[4], ev[4], vi[4];
+      }
+      float vi[2][2];  // 2^-ev
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const uint32_t bk = lds_u16(sf + 8 * t + 2 * c), bv = lds_u16(sf + kSlice + 8 * t + 2 * c);
+      for (int b = 0; b < 2; ++b)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          ek[2 * t + i] = two_to(factor_of((bk >> (8 * i)) & 0xFFu));
-          const int e = factor_of((bv >> (8 * i)) & 0xFFu);
-          ev[2 * t + i] = static_cast<float>(e);
-          vi[2 * t + i] = two_to(-e);
+          const float fk = two_to(factor_of(lds_u8(sf + 16 * b + 8 * i + g)));
+          const int e = factor_of(lds_u8(sf + kKeys8 + 16 * b + 8 * i + g));
+          vi[b][i] = two_to(-e);
+#pragma unroll
+          for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+              s[b][t][2 * i + r] = fmaf(s[b][t][2 * i + r] * fk, f[t][r], static_cast<float>(e));
         }
-      }
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          s[t][e] = fmaf(s[t][e] * ek[2 * t + (e & 1)], e < 2 ? fa : fb, ev[2 * t + (e & 1)]);
-      const bool part = !__all_sync(~0u, span_covers(sa, j0, j0 + kSlice) && span_covers(sb, j0, j0 + kSlice));
       if (part) {
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int t = 0; t < kTiles; ++t)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int j = j0 + 8 * t + 2 * c + (e & 1);
-            if (!in_span(e < 2 ? sa : sb, j)) s[t][e] = -INFINITY;
+          for (int r = 0; r < 2; ++r) {
+            const Span sp = row_of(8 * t + 2 * c + r);
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+                if (!in_span(sp, j0 + 16 * b + 8 * i + g)) s[b][t][2 * i + r] = -INFINITY;
           }
       }
-      float mx[2];
+      float mx[kTiles][2];
+      bool up = false;
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        mx[r] = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]));
-        mx[r] = fmaxf(mx[r], __shfl_xor_sync(~0u, mx[r], 1));
-        mx[r] = fmaxf(mx[r], __shfl_xor_sync(~0u, mx[r], 2));
-        mx[r] = fmaxf(__fadd_ru(mx[r], -12.f), m[r]);
-      }
-      if (__any_sync(~0u, mx[0] > m[0] || mx[1] > m[1])) {
+      for (int t = 0; t < kTiles; ++t)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const float f = mx[r] > m[r] ? ex2_approx(m[r] - mx[r]) : 1.f;
-          m[r] = mx[r];
-          l[r] *= f;
+          mx[t][r] = fmaxf(fmaxf(s[0][t][r], s[0][t][2 + r]), fmaxf(s[1][t][r], s[1][t][2 + r]));
 #pragma unroll
-          for (int t = 0; t < 16; ++t) {
-            o[t][2 * r] *= f;
-            o[t][2 * r + 1] *= f;
-          }
+          for (int d = 4; d < 32; d <<= 1) mx[t][r] = fmaxf(mx[t][r], __shfl_xor_sync(~0u, mx[t][r], d));
+          up |= __fadd_ru(mx[t][r], -15.f) > m[t][r];
         }
+      if (__any_sync(~0u, up)) {
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const float to = __fadd_ru(mx[t][r], -12.f);
+            if (to > m[t][r]) {
+              const float x = ex2_approx(m[t][r] - to);
+              m[t][r] = to;
+              l[t][r] *= x;
+#pragma unroll
+              for (int i = 0; i < 8; ++i) o[t][i][r] *= x, o[t][i][2 + r] *= x;
+            }
+          }
       }
-      uint32_t p[4];
+      uint32_t p[2][kTiles][2];
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const float base = m[r] == -INFINITY ? 0.f : m[r];
-        float e[4];
+      for (int t = 0; t < kTiles; ++t) {
+        const float b0 = m[t][0] == -INFINITY ? 0.f : m[t][0], b1 = m[t][1] == -INFINITY ? 0.f : m[t][1];
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int b = 0; b < 2; ++b)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const float w = ex2_approx(s[t][2 * r + i] - base);
-            e[2 * t + i] = w;
-            l[r] = fmaf(w, vi[2 * t + i], l[r]);
+            const float w0 = ex2_approx(s[b][t][2 * i] - b0), w1 = ex2_approx(s[b][t][2 * i + 1] - b1);
+            l[t][0] = fmaf(w0, vi[b][i], l[t][0]);
+            l[t][1] = fmaf(w1, vi[b][i], l[t][1]);
+            p[b][t][i] = transposed(Half2<__half>::pack(w0, w1));
           }
-        p[r] = Half2<__half>::pack(e[0], e[1]);
-        p[2 + r] = Half2<__half>::pack(e[2], e[3]);
-      }
-      // rows of V: keys 2 c, 2 c + 1, 2 c + 8, 2 c + 9, columns 16 g to 16 g + 15
-      uint4 v[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = lds16(sv + (i >> 1) * 1024 + v_at[i & 1]);
-      if (part) {
-        // NaN in a key that some row does not attend must not meet a weight of
-        // 0: it is taken out, and added where the key is attended
-        uint32_t bad = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) bad |= e4m3_nan(word(v[i], k));
-        if (__any_sync(~0u, bad)) hide_nan(v, sv, j0, sa, sb, o);
       }
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const uint32_t a0 = __byte_perm(word(v[0], k), word(v[1], k), 0x5140), a1 = __byte_perm(word(v[0], k), word(v[1], k), 0x7362);
-        const uint32_t b0 = __byte_perm(word(v[2], k), word(v[3], k), 0x5140), b1 = __byte_perm(word(v[2], k), word(v[3], k), 0x7362);
-        warp_mma(o[4 * k], p, e4m3x2_to_f16x2(a0), e4m3x2_to_f16x2(b0), __half());
-        warp_mma(o[4 * k + 1], p, e4m3x2_hi_to_f16x2(a0), e4m3x2_hi_to_f16x2(b0), __half());
-        warp_mma(o[4 * k + 2], p, e4m3x2_to_f16x2(a1), e4m3x2_to_f16x2(b1), __half());
-        warp_mma(o[4 * k + 3], p, e4m3x2_hi_to_f16x2(a1), e4m3x2_hi_to_f16x2(b1), __half());
+      for (int b = 0; b < 2; ++b) {
+        // keys 2 c, 2 c + 1, 2 c + 8, 2 c + 9 of the step, columns 16 g to 16 g + 15
+        uint4 v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = lds16(sv + b * 2048 + (i >> 1) * 1024 + v_at[i & 1]);
+        if (part) {
+          // NaN in a key that some row does not attend must not meet a weight of
+          // 0: it is taken out, and added where the key is attended
+          uint32_t bad = 0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) bad |= e4m3_nan(word(v[i], k));
+          if (__any_sync(~0u, bad)) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) finite(v[i].x), finite(v[i].y), finite(v[i].z), finite(v[i].w);
+            // a positive weight times NaN is NaN, so no weight is needed
+#pragma unroll 1
+            for (int k = 0; k < 16; ++k) {
+              const uint4 x = lds16(sv + b * 2048 + k * 128 + ((g ^ swizzle8(k & 7)) << 4));
+#pragma unroll
+              for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                  const Span sp = row_of(8 * t + 2 * c + r);
+                  if (!in_span(sp, j0 + 16 * b + k)) continue;
+#pragma unroll
+                  for (int i = 0; i < 16; ++i)
+                    if ((e4m3_nan(word(x, i >> 2)) >> (8 * (i & 3) + 7)) & 1u) o[t][i >> 1][2 * (i & 1) + r] = __uint_as_float(0x7FC00000u);
+                }
+            }
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          // (column 4 k, 4 k + 1) of two keys each, then (4 k + 2, 4 k + 3)
+          const uint32_t x0 = __byte_perm(word(v[0], k), word(v[1], k), 0x5140), x1 = __byte_perm(word(v[0], k), word(v[1], k), 0x7362);
+          const uint32_t y0 = __byte_perm(word(v[2], k), word(v[3], k), 0x5140), y1 = __byte_perm(word(v[2], k), word(v[3], k), 0x7362);
+          const uint32_t w0[4] = {e4m3x2_to_f16x2(x0), e4m3x2_hi_to_f16x2(x0), e4m3x2_to_f16x2(y0), e4m3x2_hi_to_f16x2(y0)};
+          const uint32_t w1[4] = {e4m3x2_to_f16x2(x1), e4m3x2_hi_to_f16x2(x1), e4m3x2_to_f16x2(y1), e4m3x2_hi_to_f16x2(y1)};
+#pragma unroll
+          for (int t = 0; t < kTiles; ++t) {
+            warp_mma(o[t][2 * k], w0, p[b][t][0], p[b][t][1], __half());
+            warp_mma(o[t][2 * k + 1], w1, p[b][t][0], p[b][t][1], __half());
+          }
+        }
       }
       __syncwarp();  // the stage is refilled by the next issue
     }
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      l[r] += __shfl_xor_sync(~0u, l[r], 1);
-      l[r] += __shfl_xor_sync(~0u, l[r], 2);
-    }
     cp_async_wait<0>();
     __syncwarp();
-    float* po = reinterpret_cast<float*>(ring_);  // [16][132], now that the ring is empty
-    // o[t][0], o[t][1]: row g, columns 32 c + t and 32 c + 16 + t
+    float* po = reinterpret_cast<float*>(ring_);  // [kRows][132], now that the ring is empty
 #pragma unroll
-    for (int t = 0; t < 16; t += 4)
+    for (int t = 0; t < kTiles; ++t)
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        *reinterpret_cast<float4*>(po + (g + 8 * (e >> 1)) * 132 + 32 * c + 16 * (e & 1) + t) =
-            make_float4(o[t][e], o[t + 1][e], o[t + 2][e], o[t + 3][e]);
-    if (c == 0) {
-      m_out[g] = m[0];
-      m_out[g + 8] = m[1];
-      l_out[g] = l[0];
-      l_out[g + 8] = l[1];
-    }
-  }
-
-  // NaN of the slice's rows of V: zero in v, and added to the sums of the rows
-  // that attend its key (a positive weight times NaN is NaN; so no weight is
-  // needed).
-  static __device__ __forceinline__ void hide_nan(uint4 (&v)[4], uint32_t sv, int j0, const Span& sa, const Span& sb, float (&o)[16][4]) {
-    const int c = threadIdx.x & 3;
-    auto clear = [](uint32_t& w) { w &= ~((e4m3_nan(w) >> 7) * 0xFFu); };
+      for (int r = 0; r < 2; ++r) {
+        const int row = 8 * t + 2 * c + r;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) clear(v[i].x), clear(v[i].y), clear(v[i].z), clear(v[i].w);
-    const float nan = __uint_as_float(0x7FC00000u);
-#pragma unroll 1
-    for (int k = 0; k < kSlice; ++k) {
-      const bool ta = in_span(sa, j0 + k), tb = in_span(sb, j0 + k);
-      // this lane's columns of key k: pieces 2 c and 2 c + 1
+        for (int i = 0; i < 8; i += 2)
+          *reinterpret_cast<float4*>(po + row * 132 + 16 * g + 2 * i) =
+              make_float4(o[t][i][r], o[t][i][2 + r], o[t][i + 1][r], o[t][i + 1][2 + r]);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint4 x = lds16(sv + k * 128 + (((2 * c + i) ^ swizzle8(k & 7)) << 4));
-#pragma unroll
-        for (int t = 0; t < 16; ++t) {
-          const bool is = ((word(x, t >> 2) >> (8 * (t & 3))) & 0x7Fu) == 0x7Fu;
-          if (is && ta) o[t][i] = nan;
-          if (is && tb) o[t][2 + i] = nan;
+        for (int d = 4; d < 32; d <<= 1) l[t][r] += __shfl_xor_sync(~0u, l[t][r], d);
+        if (g == 0) {
+          m_out[row] = m[t][r];
+          l_out[row] = l[t][r];
         }
       }
-    }
   }
+
+  static __device__ __forceinline__ void finite(uint32_t& w) { w &= ~((e4m3_nan(w) >> 7) * 0xFFu); }
 };
 
-template <typename T>
-__global__ void __launch_bounds__(kDecThreads, 2)
+// CTAs per SM: what registers and shared memory allow.
+template <int kTiles>
+constexpr int kPerSm = kTiles == 1 ? 3 : 2;
+
+template <typename T, int kTiles>
+__global__ void __launch_bounds__(kDecThreads, kPerSm<kTiles>)
     paged_decode8_kernel(const __grid_constant__ PagedAttnArgs a, bool behind) {
   extern __shared__ __align__(1024) uint8_t ring[];
-  __shared__ DecodeShared sh;
+  __shared__ DecodeShared<8 * kTiles> sh;
   launch_dependents();
-  decode_span<Worker8<T>>(a, sh, ring, behind);
+  decode_span<Worker8<T, kTiles>>(a, sh, ring, behind);
   clear_unowned_rows(a);
   if (behind) grid_wait();
 }
 
-template <typename T>
+template <typename T, int kTiles>
 cudaError_t launch_decode(const PagedAttnArgs& a, bool behind, int num_sms, cudaStream_t st) {
+  constexpr int kBytes = kDecWarps * Worker8<T, kTiles>::kWarpBytes;
   static std::atomic<uint64_t> done{0};
-  const cudaError_t e = allow_smem(paged_decode8_kernel<T>, kFewSmem8, done);
+  const cudaError_t e = allow_smem(paged_decode8_kernel<T, kTiles>, kBytes, done);
   if (e != cudaSuccess) return e;
   note_launches(1);
-  return launch_after(paged_decode8_kernel<T>, dim3(std::min(2 * num_sms, kPagedMaxCtas)), kDecThreads, kFewSmem8, st, a,
-                      behind);
+  return launch_after(paged_decode8_kernel<T, kTiles>, dim3(std::min(kPerSm<kTiles> * num_sms, kPagedMaxCtas)), kDecThreads, kBytes,
+                      st, a, behind);
+}
+
+template <typename T>
+cudaError_t launch_decode_of(const PagedAttnArgs& a, int rows, bool behind, int num_sms, cudaStream_t st) {
+  if (rows <= 8) return launch_decode<T, 1>(a, behind, num_sms, st);
+  if (rows <= 16) return launch_decode<T, 2>(a, behind, num_sms, st);
+  return launch_decode<T, 4>(a, behind, num_sms, st);
 }
 
 }  // namespace
@@ -510,8 +551,9 @@ void launch_paged_read8(const PagedRead8Args& a, bool fp16, int num_sms, cudaStr
     paged_read8_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(a);
 }
 
-cudaError_t launch_paged_decode8(const PagedAttnArgs& a, bool behind, bool fp16, int num_sms, cudaStream_t st) {
-  return fp16 ? launch_decode<__half>(a, behind, num_sms, st) : launch_decode<__nv_bfloat16>(a, behind, num_sms, st);
+cudaError_t launch_paged_decode8(const PagedAttnArgs& a, int rows, bool behind, bool fp16, int num_sms, cudaStream_t st) {
+  return fp16 ? launch_decode_of<__half>(a, rows, behind, num_sms, st)
+              : launch_decode_of<__nv_bfloat16>(a, rows, behind, num_sms, st);
 }
 
 }  // namespace lca

@@ -35,6 +35,8 @@ void launch_paged_read8(const PagedRead8Args& a, bool fp16, int num_sms, cudaStr
 // The maps of K and V have boxes of box_rows rows of 128 bytes.
 cudaError_t launch_paged_chunk8(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                                 const PagedAttnArgs& a, bool fp16, int num_sms, cudaStream_t st);
-cudaError_t launch_paged_decode8(const PagedAttnArgs& a, bool behind, bool fp16, int num_sms, cudaStream_t st);
+// Attention over few rows, in items of `rows` of them (8, 16 or 32).
+constexpr int kPaged8MaxRows = 32;
+cudaError_t launch_paged_decode8(const PagedAttnArgs& a, int rows, bool behind, bool fp16, int num_sms, cudaStream_t st);
 
 }  // namespace lca

@@ -148,7 +148,16 @@ struct PagedLayout {
   int max_blocks = 0;
 };
 
-PagedLayout paged_layout(const lca_paged_shape* sh, const lca_paged_cache* c) {
+// Rows of an item of the kernel for few rows: a 16-bit cache's has 16; an
+// 8-bit one's 8, 16 or 32, by what the longest request has or, where that is not
+// known, a single token.
+int few_tile(const lca_paged_shape* sh, const lca_paged_cache* c, bool eight) {
+  if (!eight) return 16;
+  const long long G = sh->Hq / c->Hkv, rows = sh->max_q_len > 0 ? sh->max_q_len * G : G;
+  return rows <= 8 ? 8 : rows <= 16 ? 16 : kPaged8MaxRows;
+}
+
+PagedLayout paged_layout(const lca_paged_shape* sh, const lca_paged_cache* c, bool eight) {
   PagedLayout L;
   size_t o = 0;
   auto take = [&](size_t bytes) {
@@ -158,7 +167,9 @@ PagedLayout paged_layout(const lca_paged_shape* sh, const lca_paged_cache* c) {
   };
   L.status = take(16);
   L.arrived = take(sizeof(int) * (kPagedMaxSpans + 1));
-  L.parts = take(sizeof(float) * 2 * kPagedMaxSpans * kPagedPartFloats);
+  // a workspace for an unknown longest request serves every hint
+  const int rows = eight && sh->max_q_len == 0 ? kPaged8MaxRows : few_tile(sh, c, eight);
+  L.parts = take(sizeof(float) * 2 * kPagedMaxSpans * rows * (kHeadDim + 2));
   if (many_rows(sh, c)) {
     L.max_blocks = sh->Tq / (2 * tokens_per_tile(sh, c)) + sh->n_seq;
     L.block0 = take(sizeof(int) * (sh->n_seq + 1LL));
@@ -275,7 +286,7 @@ lca_status attend(const Cache& any, int dtype, const void* q, const int32_t* blo
   PagedAttnArgs a{};
   const lca_status r = check_attn(shape, cache, mask, a.mask);
   if (r != LCA_OK) return r;
-  const PagedLayout L = paged_layout(shape, cache);
+  const PagedLayout L = paged_layout(shape, cache, c8 != nullptr);
   if (!workspace || reinterpret_cast<uintptr_t>(workspace) % kAlign != 0 || workspace_bytes < L.total ||
       !device_input(workspace))
     return LCA_ERR_WORKSPACE;
@@ -377,7 +388,9 @@ lca_status attend(const Cache& any, int dtype, const void* q, const int32_t* blo
   const bool fp16 = dtype == LCA_F16;
   LCA_CUDA(launch_paged_begin(a, many, st));
   if (many) LCA_CUDA((c8 ? launch_paged_chunk8 : launch_paged_chunk)(tq, tk, tv, a, fp16, sms, st));
-  if (shape->Tq > 0) LCA_CUDA((c8 ? launch_paged_decode8 : launch_paged_decode)(a, many, fp16, sms, st));
+  if (shape->Tq > 0)
+    LCA_CUDA(c8 ? launch_paged_decode8(a, few_tile(shape, cache, true), many, fp16, sms, st)
+                : launch_paged_decode(a, many, fp16, sms, st));
   if (many) LCA_CUDA(launch_paged_join(a, fp16, sms, st));
   return LCA_OK;
 }
@@ -562,7 +575,7 @@ lca_status lca_attn_paged_workspace_size(const lca_paged_shape* shape, const lca
   MaskCtx m;
   const lca_status r = check_attn(shape, cache, mask, m);
   if (r != LCA_OK) return r;
-  *bytes = paged_layout(shape, cache).total;
+  *bytes = paged_layout(shape, cache, false).total;
   return LCA_OK;
 }
 
@@ -576,10 +589,15 @@ lca_status lca_attn_paged(const void* q, const lca_paged_cache* cache, const int
 
 lca_status lca_attn_paged_fp8_workspace_size(const lca_paged_shape* shape, const lca_paged_cache_fp8* cache,
                                              const lca_mask_desc* mask, size_t* bytes) {
-  const lca_status r = check_cache8(cache);
+  lca_status r = check_cache8(cache);
   if (r != LCA_OK) return r;
+  if (!bytes) return LCA_ERR_INVALID_ARG;
   const lca_paged_cache v = values_of(cache);
-  return lca_attn_paged_workspace_size(shape, &v, mask, bytes);
+  MaskCtx m;
+  r = check_attn(shape, &v, mask, m);
+  if (r != LCA_OK) return r;
+  *bytes = paged_layout(shape, &v, true).total;
+  return LCA_OK;
 }
 
 lca_status lca_attn_paged_fp8(const void* q, int32_t dtype, const lca_paged_cache_fp8* cache, const int32_t* block_table,

@@ -13,25 +13,25 @@ namespace lca {
 namespace {
 
 // Attention is bound here by reading K and V once: with G query heads per KV
-// head and t new tokens a request has G t rows per KV head, and 16 of them
-// take part in every product, so a key costs its bytes from HBM and little
-// arithmetic.  The work is a line of units of 64 keys (request, KV head, row
-// tile, unit) cut into equal spans, one per CTA, two CTAs per SM, whatever
+// head and t new tokens a request has G t rows per KV head, and a tile of them
+// takes part in every product, so a key costs its bytes from HBM and little
+// arithmetic.  The work is a line of units of keys (request, KV head, row
+// tile, unit) cut into equal spans, one per CTA, a few CTAs per SM, whatever
 // the lengths; of a long line the last part is cut finer and claimed by the
 // CTAs that are done first, since SMs differ in what they get of HBM.  A
 // piece of an item that goes on in another span leaves unnormalised sums (O,
 // running maximum, sum of exponentials) in the workspace, and the CTA that
 // finishes an item's last piece joins them in the order of the keys.  Each CTA
 // finds its span itself from the lengths, so there is no planning launch.
-// Within a CTA each of 4 warps owns 16 of a unit's 64 keys and keeps its own
+// Within a CTA each of 4 warps owns a quarter of a unit's keys and keeps its own
 // running maximum and sums; the warps meet once per piece.
 //
-// The constants' measurements are of 16-bit caches.
-constexpr int kUnit = 64;                     // keys per unit
-constexpr int kRows = 16;                     // rows per item
+// A worker W says what a warp does with its share of a piece, and how many rows
+// an item and keys a unit have (W::kRows, W::kUnit).  The constants'
+// measurements are of 16-bit caches, whose units of 64 keys are 32 KB; those of an
+// 8-bit cache have 128 keys and as many bytes.
 constexpr int kDecWarps = 4;
 constexpr int kDecThreads = 32 * kDecWarps;
-constexpr int kSlice = kUnit / kDecWarps;     // keys per warp and unit
 // Units per CTA from which on the line's last eighth is claimed.  Above it: 64
 // requests of 1K-32K (1.1M keys) 698 -> 668 us, 4 of 512K 1293 -> 1248.  Below
 // it the finer spans cost more than they even out: 256 requests of 1K, 134
@@ -44,9 +44,6 @@ constexpr int kItemUnits = 4;
 // 16.5 and 19.5 us, one of 4K 19.1, 18.5 and 20.5.
 constexpr int kMinUnits = 4;
 constexpr int kSeqTile = 2 * kDecThreads;     // requests whose places on the line are in shared memory at once
-constexpr int kPartFloats = kRows * (kHeadDim + 2);
-static_assert(kSlice == 16, "a slice is one k16 step of the product with V");
-static_assert(kPartFloats == kPagedPartFloats, "workspace layout");
 
 __device__ __forceinline__ void warp_mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1,
                                          __nv_bfloat16) {
@@ -75,8 +72,9 @@ __device__ __forceinline__ void cp_async_wait() {
 // The units of a hull: n0 from t0 on, then n1 from t1 on.
 struct Units {
   int t0, n0, t1, n1;
-  __device__ __forceinline__ int first_key(int u) const { return (u < n0 ? t0 + u : t1 + u - n0) * kUnit; }
+  __device__ __forceinline__ int at(int u) const { return u < n0 ? t0 + u : t1 + u - n0; }
 };
+template <int kUnit>
 __device__ __forceinline__ Units units_of(const Span& h) {
   Units u;
   u.t0 = h.a0 / kUnit;
@@ -86,6 +84,7 @@ __device__ __forceinline__ Units units_of(const Span& h) {
   return u;
 }
 
+template <int kRows>
 __device__ __forceinline__ int row_tiles(const PagedAttnArgs& a, int q_len) {
   return static_cast<int>((static_cast<long long>(q_len) * a.G + kRows - 1) / kRows);
 }
@@ -98,6 +97,7 @@ struct Request {
   Units un;
 };
 
+template <int kRows>
 struct DecodeShared {
   long long start[kSeqTile + 1];  // first unit of each request of the tile, relative to the tile's
   Request req[kSeqTile];
@@ -107,7 +107,8 @@ struct DecodeShared {
 };
 
 // Places of the requests [base, base + kSeqTile) on the line; returns their units.
-__device__ __forceinline__ long long place_requests(const PagedAttnArgs& a, DecodeShared& sh, int base) {
+template <typename W>
+__device__ __forceinline__ long long place_requests(const PagedAttnArgs& a, DecodeShared<W::kRows>& sh, int base) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   __syncthreads();  // earlier readers
   long long n0 = 0, mine = 0;
@@ -117,8 +118,8 @@ __device__ __forceinline__ long long place_requests(const PagedAttnArgs& a, Deco
     if (i >= a.n_seq) break;
     const SegInfo sg = paged_seg(a, i);
     if (sg.q_len > 0 && few_rows(a, sg.q_len)) {
-      const Units u = units_of(hull(a, sg.q_len, sg.k_len, 0, sg.q_len));
-      mine += static_cast<long long>(row_tiles(a, sg.q_len)) * a.Hkv * (max(u.n0 + u.n1, 1) + kItemUnits);
+      const Units u = units_of<W::kUnit>(hull(a, sg.q_len, sg.k_len, 0, sg.q_len));
+      mine += static_cast<long long>(row_tiles<W::kRows>(a, sg.q_len)) * a.Hkv * (max(u.n0 + u.n1, 1) + kItemUnits);
       sh.req[2 * tid + k] = Request{sg.q_off, sg.q_len, sg.k_len, u};
     }
     if (k == 0) n0 = mine;
@@ -163,13 +164,13 @@ struct Spans {
   }
 };
 
-template <typename T>
-__device__ __forceinline__ void st_row16(T* dst, const float (&x)[16]) {
-  uint32_t w[8];
+template <typename T, int N>
+__device__ __forceinline__ void st_row(T* dst, const float (&x)[N]) {
 #pragma unroll
-  for (int k = 0; k < 8; ++k) w[k] = Half2<T>::pack(x[2 * k], x[2 * k + 1]);
-  *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-  *reinterpret_cast<uint4*>(dst + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+  for (int k = 0; k < N; k += 8)
+    *reinterpret_cast<uint4*>(dst + k) =
+        make_uint4(Half2<T>::pack(x[k], x[k + 1]), Half2<T>::pack(x[k + 2], x[k + 3]), Half2<T>::pack(x[k + 4], x[k + 5]),
+                   Half2<T>::pack(x[k + 6], x[k + 7]));
 }
 
 // o = 0, lse = -inf in the rows [r0, r1), by all CTAs.
@@ -202,21 +203,22 @@ __device__ __forceinline__ void clear_unowned_rows(const PagedAttnArgs& a) {
   }
 }
 
-// The line's work of this CTA.  A worker W does a warp's share of a piece:
-// W::run takes units [u0, u0 + n) of an item, keys [16 warp, 16 warp + 16) of
-// each, through its W::kWarpBytes of shared memory, and leaves there the sums
-// of the 16 rows as [16][132] floats, and in m and l their maxima and sums of
-// exponentials.  W::Out is o's type; the sums carry a factor of 2^W::kBias.
+// The line's work of this CTA.  W::run takes units [u0, u0 + n) of an item, this
+// warp's keys of each, through its W::kWarpBytes of shared memory, and leaves
+// there the sums of the rows as [W::kRows][132] floats, and in m and l their maxima
+// and sums of exponentials.  W::Out is o's type; the sums carry a factor of 2^W::kBias.
 template <typename W>
-__device__ __forceinline__ void decode_span(const PagedAttnArgs& a, DecodeShared& sh, uint8_t* ring, bool behind) {
+__device__ __forceinline__ void decode_span(const PagedAttnArgs& a, DecodeShared<W::kRows>& sh, uint8_t* ring, bool behind) {
   using T = typename W::Out;
+  constexpr int kRows = W::kRows, kPartFloats = kRows * (kHeadDim + 2);
+  constexpr int kCols = kRows;  // columns of a row per thread: 128 threads, kRows x 128 values
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   // requests whose rows do not overlap make fewer than 2^52 units; a q_start
   // that lets them overlap may make more, and is reported and not served then
   constexpr long long kMost = 1LL << 52;
   long long total = 0;
   for (int base = 0; base < a.n_seq; base += kSeqTile)
-    total = min(total + place_requests(a, sh, base), kMost);
+    total = min(total + place_requests<W>(a, sh, base), kMost);
   if (!behind) grid_wait();  // counts and status are cleared
   if (total == 0 || total == kMost) return;
   const Spans sp(total, gridDim.x);
@@ -241,7 +243,7 @@ __device__ __forceinline__ void decode_span(const PagedAttnArgs& a, DecodeShared
       base += kSeqTile;
       if (base >= a.n_seq) return;  // only if the lengths changed meanwhile
       tile0 = tile1;
-      tile1 += place_requests(a, sh, base);
+      tile1 += place_requests<W>(a, sh, base);
     }
     int lo = 0, hi = min(kSeqTile, a.n_seq - base);  // the last request that starts at or before pos
     while (hi - lo > 1) {
@@ -261,7 +263,7 @@ __device__ __forceinline__ void decode_span(const PagedAttnArgs& a, DecodeShared
     pos += to - from;
     const int u0 = max(from - kItemUnits, 0), n = to - kItemUnits - u0;
     if (n <= 0) continue;
-    const int tiles = row_tiles(a, sg.q_len);
+    const int tiles = row_tiles<kRows>(a, sg.q_len);
     const int head = static_cast<int>(line_div(item, tiles));
     const int tile = static_cast<int>(item - static_cast<long long>(head) * tiles);
 
@@ -271,9 +273,10 @@ __device__ __forceinline__ void decode_span(const PagedAttnArgs& a, DecodeShared
     W::run(a, ring + warp * W::kWarpBytes, seq, sg, un, tile, head, u0, un.n0 + un.n1 > 0 ? n : 0, sh.m[warp],
            sh.l[warp]);
     __syncthreads();
-    const int row = tid >> 3, col = (tid & 7) * 16;
-    // the four warps' sums of row `row`, columns col .. col + 15
-    float m = -INFINITY, l = 0.f, x[16] = {};
+    constexpr int kPer = kDecThreads / kRows;  // threads per row
+    const int row = tid / kPer, col = tid % kPer * kCols;
+    // the four warps' sums of row `row`, columns col .. col + kCols - 1
+    float m = -INFINITY, l = 0.f, x[kCols] = {};
 #pragma unroll
     for (int w = 0; w < kDecWarps; ++w) m = fmaxf(m, sh.m[w][row]);
 #pragma unroll
@@ -282,7 +285,7 @@ __device__ __forceinline__ void decode_span(const PagedAttnArgs& a, DecodeShared
       l = fmaf(f, sh.l[w][row], l);
       const float* pw = reinterpret_cast<const float*>(ring + w * W::kWarpBytes) + row * 132 + col;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < kCols / 4; ++k) {
         const float4 y = *reinterpret_cast<const float4*>(pw + 4 * k);
         x[4 * k] = fmaf(f, y.x, x[4 * k]);
         x[4 * k + 1] = fmaf(f, y.y, x[4 * k + 1]);
@@ -299,10 +302,10 @@ __device__ __forceinline__ void decode_span(const PagedAttnArgs& a, DecodeShared
       float* part = slot(span);
       if (row < rows) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int k = 0; k < kCols / 4; ++k)
           __stcg(reinterpret_cast<float4*>(part + row * kHeadDim + col) + k,
                  make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]));
-        if ((tid & 7) == 0) {
+        if (tid % kPer == 0) {
           __stcg(part + kRows * kHeadDim + row, m);
           __stcg(part + kRows * kHeadDim + kRows + row, l);
         }
@@ -342,12 +345,12 @@ __device__ __forceinline__ void decode_span(const PagedAttnArgs& a, DecodeShared
     } else if (row < rows) {
       const float inv = l == 0.f ? 0.f : 1.f / l;  // a NaN stays one
 #pragma unroll
-      for (int k = 0; k < 16; ++k) x[k] *= inv;
+      for (int k = 0; k < kCols; ++k) x[k] *= inv;
       const long long r = static_cast<long long>(tile) * kRows + row;
       const long long token = sg.q_off + r / a.G;
       const int h = head * a.G + static_cast<int>(r % a.G);
-      st_row16(static_cast<T*>(a.o) + (token * a.Hq + h) * kHeadDim + col, x);
-      if ((tid & 7) == 0)
+      st_row(static_cast<T*>(a.o) + (token * a.Hq + h) * kHeadDim + col, x);
+      if (tid % kPer == 0)
         a.lse[static_cast<long long>(h) * a.Tq + token] =
             l == 0.f ? -INFINITY : (m + log2f(l) - W::kBias) * 0.6931471805599453f;
     }
