@@ -93,7 +93,7 @@ cudaError_t launch_paged_decode(const PagedAttnArgs& a, bool behind, bool fp16, 
 // box_rows tokens of one page and head x 64, 128-byte swizzled.
 cudaError_t launch_paged_chunk(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                                const PagedAttnArgs& a, bool fp16, int num_sms, cudaStream_t st);
-cudaError_t launch_paged_join(const PagedAttnArgs& a, bool fp16, int num_sms, cudaStream_t st);
+cudaError_t launch_paged_join(const PagedAttnArgs& a, bool fp16, bool eight, int num_sms, cudaStream_t st);
 
 // Lets `kernel` use `bytes` of dynamic shared memory on the current device;
 // asks CUDA once per device.  One `done` per kernel, bit d for device d.

@@ -391,7 +391,7 @@ lca_status attend(const Cache& any, int dtype, const void* q, const int32_t* blo
   if (shape->Tq > 0)
     LCA_CUDA(c8 ? launch_paged_decode8(a, few_tile(shape, cache, true), many, fp16, sms, st)
                 : launch_paged_decode(a, many, fp16, sms, st));
-  if (many) LCA_CUDA(launch_paged_join(a, fp16, sms, st));
+  if (many) LCA_CUDA(launch_paged_join(a, fp16, c8 != nullptr, sms, st));
   return LCA_OK;
 }
 

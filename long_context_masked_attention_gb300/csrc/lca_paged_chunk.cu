@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(1024) paged_begin_kernel(const __grid_constant
 // L2, so the loads of two pieces of all four rows are under way at once; launched
 // alone and cold 6.5 us for 32 requests of 5 tokens, 10.9 for 8 prompts.
 constexpr int kJoinRows = 32;
-template <typename T>
+template <typename T, bool k8>
 __global__ void __launch_bounds__(8 * kJoinRows, 3) paged_join_kernel(const __grid_constant__ PagedAttnArgs a) {
   launch_dependents();
   grid_wait();
@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(8 * kJoinRows, 3) paged_join_kernel(const __gr
         make_uint2(Half2<T>::pack(o[r][0] * inv, o[r][1] * inv), Half2<T>::pack(o[r][2] * inv, o[r][3] * inv));
     if (lane == 0)
       a.lse[static_cast<long long>(head) * a.Tq + cut.q_off + token] =
-          lr == 0.f ? -INFINITY : (mr + log2f(lr) - kBias<T>) * kLn2;
+          lr == 0.f ? -INFINITY : (mr + log2f(lr) - kBias<Operand<T, k8>>) * kLn2;
   }
 }
 
@@ -123,11 +123,13 @@ cudaError_t launch_paged_chunk(const CUtensorMap& tq, const CUtensorMap& tk, con
               : launch_chunk<__nv_bfloat16, false>(tq, tk, tv, a, num_sms, st);
 }
 
-cudaError_t launch_paged_join(const PagedAttnArgs& a, bool fp16, int num_sms, cudaStream_t st) {
+cudaError_t launch_paged_join(const PagedAttnArgs& a, bool fp16, bool eight, int num_sms, cudaStream_t st) {
   const dim3 grid(std::min(num_sms, kPagedMaxChunkCtas), 256 / kJoinRows);
   note_launches(1);
-  return launch_after(fp16 ? paged_join_kernel<__half> : paged_join_kernel<__nv_bfloat16>, grid, 8 * kJoinRows, 0, st,
-                      a);
+  const auto kernel = fp16    ? (eight ? paged_join_kernel<__half, true> : paged_join_kernel<__half, false>)
+                      : eight ? paged_join_kernel<__nv_bfloat16, true>
+                              : paged_join_kernel<__nv_bfloat16, false>;
+  return launch_after(kernel, grid, 8 * kJoinRows, 0, st, a);
 }
 
 }  // namespace lca

@@ -49,6 +49,7 @@ namespace {
 constexpr uint32_t kTileBytes = 32768;   // 128 rows x 128 values of 16 bits
 constexpr uint32_t kChunkBytes = 16384;  // 128 rows x 64 values, 128-byte swizzled; or 128 rows of 8 bits
 constexpr int kItemSlots = 3;
+constexpr int kExpSlots = 4;
 // A CTA's share, where there is that much; 2, 4 and 8: a chunk of 509 tokens
 // with a window of 1024 beside 15 single tokens 62.2, 62.3 and 64.1 us.
 constexpr int kMinTiles = 4;
@@ -73,7 +74,9 @@ struct Chunk {
   static constexpr int kOffKV = 2 * kTileBytes;
   static constexpr int kOffRaw = kOffKV + kStages * kTileBytes;
   static constexpr int kOffCtl = kOffRaw + kRaw * kChunkBytes;
-  static constexpr int kSmemBytes = kOffCtl + 1024 + 1024;
+  static constexpr int kOffItems = k8 ? 320 : 256;  // in the control part
+  static constexpr int kOffExp = 1024;              // exponents of the rows of two items' q
+  static constexpr int kSmemBytes = kOffCtl + 1024 + (k8 ? 512 : 0) + 1024;
   enum : int {
     QFULL = 0,
     QEMPTY = 1,
@@ -87,9 +90,12 @@ struct Chunk {
     DRAIN = ITEMPTY + kItemSlots,
     RAWFULL = DRAIN + 1,
     RAWEMPTY = RAWFULL + kRaw,
-    COUNT = RAWEMPTY + kRaw
+    QREADY = RAWEMPTY + kRaw,
+    MAXFULL = QREADY + (k8 ? 1 : 0),
+    EXFULL = MAXFULL + (k8 ? 1 : 0),
+    COUNT = EXFULL + (k8 ? kExpSlots : 0)
   };
-  static_assert(8 * COUNT <= 256, "the items lie behind the barriers");
+  static_assert(8 * COUNT <= kOffItems && kOffItems + 480 <= 896 && kSmemBytes <= 232448, "barriers, items, the rest");
 };
 
 // What the scheduler tells the other roles about a piece of an item.
@@ -125,6 +131,11 @@ template <typename T>
 constexpr float kBias = 0.f;
 template <>
 constexpr float kBias<__half> = 7.f;
+
+// The type of the products' operands: an 8-bit cache's are fp16, which holds
+// e4m3 exactly.
+template <typename T, bool k8>
+using Operand = std::conditional_t<k8, __half, T>;
 
 template <typename T>
 constexpr uint32_t kAbFormat = 0;  // fields of A and B format that idesc_bf16_f32 sets and T clears
@@ -436,59 +447,166 @@ __device__ __forceinline__ void producer(const PagedAttnArgs& a, const CUtensorM
 }
 
 // ------------------------------------------------------------------ converters
-// An 8-bit cache: the four last warps make the 16-bit tiles that the products
-// read.  A thread has one key's row of a tile, 128 bytes that it turns into 128
-// values times the row's factor (exact in bf16), pieces swizzled on both sides
-// so that eight rows meet in no bank.  So the products, the softmax and the
-// masks are those of a 16-bit cache, and HBM and L2 are read for half the bytes.
+// An 8-bit cache: the four last warps make the tiles that the products read, in
+// fp16, which holds e4m3 exactly.  What this costs in instructions decides (a
+// product with the row's factor in 32 bits and a rounding to bf16 took a chunk of
+// 2048 tokens at 32K keys 2555 us, a conversion and a product of pairs takes
+// TODO), so factors are made to fit fp16: those of a tile are relative to the
+// largest of its attended keys' (which becomes 2^7, so that values end below
+// 2^16), and the softmax warps learn it from `exps`.  A row whose factor is less
+// than 2^-22 of the largest in its tile loses bits, 2^-24 of a value that is at
+// most 2^16.  bf16 queries are turned into fp16 first, each row by a power of
+// two that brings its largest value to 2^14 (see lca_paged8.cu).
+//
+// A thread has one key's row of a tile, 128 bytes, pieces swizzled on both sides
+// so that eight rows meet in no bank.
+__device__ __forceinline__ uint32_t half_power(int e) {  // 2^e twice in fp16, e <= 15; 0 below 2^-24
+  const uint32_t h = e >= -14 ? static_cast<uint32_t>(e + 15) << 10 : e >= -24 ? 1u << (e + 24) : 0u;
+  return h | h << 16;
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// By 32-bit addresses: through a pointer whose memory the compiler does not
+// know these would be generic loads and stores.
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+  uint4 r;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(at) : "memory");
+  return r;
+}
+__device__ __forceinline__ void sts128(uint32_t at, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
+// Row `row` of q's sub-tile as fp16 times 2^-e; returns e.
+__device__ __forceinline__ int halve_q_row(uint32_t q, int row) {
+  float m = 0.f;
+#pragma unroll 4
+  for (int i = 0; i < 16; ++i) {
+    const uint4 w = lds128(q + (i >> 3) * kChunkBytes + row * 128 + (((i ^ row) & 7) << 4));
+    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 v = Half2<__nv_bfloat16>::unpack(x[k]);
+      m = fmaxf(m, fabsf(v.x) < INFINITY ? fabsf(v.x) : 0.f);  // a NaN counts as 0 too
+      m = fmaxf(m, fabsf(v.y) < INFINITY ? fabsf(v.y) : 0.f);
+    }
+  }
+  const int e = max(static_cast<int>(__float_as_uint(m) >> 23) - 127 - 14, -128);  // of 8 bits
+  const float f0 = two_to(-e / 2), f1 = two_to(-e - -e / 2);
+#pragma unroll 4
+  for (int i = 0; i < 16; ++i) {
+    const uint32_t at = q + (i >> 3) * kChunkBytes + row * 128 + (((i ^ row) & 7) << 4);
+    const uint4 w = lds128(at);
+    uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 v = Half2<__nv_bfloat16>::unpack(x[k]);
+      x[k] = Half2<__half>::pack(v.x * f0 * f1, v.y * f0 * f1);
+    }
+    sts128(at, x[0], x[1], x[2], x[3]);
+  }
+  return e;
+}
+
+// What converters leave in the control part: per tile (round robin) the
+// exponents that its K and V are relative to, per item (two of them) those of
+// q's rows; and the warps' largest of a tile, of two tiles in turn.
+struct Exps {
+  int tile[kExpSlots][2];
+  int most[2][4][2];
+};
+
 template <typename T>
-__device__ __forceinline__ void converter(const PagedAttnArgs& a, const uint8_t* raw, uint8_t* sKV, uint64_t* bar,
-                                          const Item* items) {
+__device__ __forceinline__ void converter(const PagedAttnArgs& a, uint8_t* sQ, const uint8_t* raw, uint8_t* sKV, uint64_t* bar,
+                                          const Item* items, Exps* exps, int8_t* q_exp) {
   using C = Chunk<true>;
-  const int lane = threadIdx.x & 31, row = threadIdx.x & 127;
-  uint32_t kv_iter = 0;
+  const int lane = threadIdx.x & 31, row = threadIdx.x & 127, wq = row >> 5;
+  uint32_t tiles = 0;  // before this item
   for (int it = 0;; ++it) {
     const int slot = it % kItemSlots;
     if (!waitw(&bar[C::ITFULL + slot], (it / kItemSlots) & 1, a, 90)) return;
     const Item& inf = items[slot];
     if (!inf.valid) return;
     const int n = inf.n;
+    if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+      if (!waitw(&bar[C::QFULL], it & 1, a, 93)) return;
+#pragma unroll 1
+      for (int x = 0; x < (inf.narrow ? 1 : 2); ++x)
+        q_exp[(it & 1) * 256 + x * 128 + row] = static_cast<int8_t>(halve_q_row(smem_u32(sQ) + x * kTileBytes, row));
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar[C::QREADY]);
+    }
     const int* table = a.table + inf.seq * a.table_stride;
     const long long head = inf.head * a.scale_head_stride;
-    // place of this row's factors in tile t, -1 where no row attends the key or it has no page
-    auto place = [&](int t) -> long long {
+    // page of this row's key in tile t, -1 where no row attends the key
+    auto page_of = [&](int t) -> int {
       if (t >= n) return -1;
       const int j = inf.tile(t) * kTile + row;
-      if (!in_span(inf.all, j)) return -1;
-      const int page = __ldg(table + j / a.page_size);
-      return page < 0 || page >= a.n_pages ? -1 : page * a.scale_page_stride + head + j % a.page_size;
+      return in_span(inf.all, j) ? __ldg(table + j / a.page_size) : -1;
     };
-    auto byte = [&](const uint8_t* p, long long at) -> uint32_t { return at < 0 ? kScaleBias : __ldg(p + at); };
-    // factors come a tile ahead, their places two
-    long long at = place(0);
-    uint32_t bk = byte(a.ks, at), bv = byte(a.vs, at);
-    at = place(1);
+    // the exponents of this row's factors, and what the warp's largest are, for the
+    // other warps.  A page is asked for two tiles ahead and looked at one tile
+    // ahead, where the factors are asked for; a warp waits where it first looks
+    int ek = 0, ev = 0;
+    bool own = false;
+    uint32_t bk = 0, bv = 0;
+    auto ask = [&](int t, int page) {
+      own = page >= 0 && page < a.n_pages;
+      if (!own) return;
+      const long long at = page * a.scale_page_stride + head + (inf.tile(t) * kTile + row) % a.page_size;
+      bk = __ldg(a.ks + at);
+      bv = __ldg(a.vs + at);
+    };
+    auto meet = [&](uint32_t tile) {
+      ek = own ? factor_of(bk) : kScaleMin;
+      ev = own ? factor_of(bv) : kScaleMin;
+      const int mk = __reduce_max_sync(0xFFFFFFFFu, ek), mv = __reduce_max_sync(0xFFFFFFFFu, ev);
+      if (lane == 0) {
+        *reinterpret_cast<int2*>(exps->most[tile & 1][wq]) = make_int2(mk, mv);
+        mbar_arrive(&bar[C::MAXFULL]);
+      }
+    };
+    ask(0, page_of(0));
+    if (n > 0) meet(tiles);
+    int page = page_of(1);
     for (int t = 0; t < n; ++t) {
-      const float f[2] = {two_to(factor_of(bk)), two_to(factor_of(bv))};
-      bk = byte(a.ks, at), bv = byte(a.vs, at);
-      at = place(t + 2);
+      const uint32_t tile = tiles + t;
+      if (!waitw(&bar[C::MAXFULL], tile & 1, a, 94)) return;
+      int mk = kScaleMin, mv = kScaleMin;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const int2 x = *reinterpret_cast<const int2*>(exps->most[tile & 1][w]);
+        mk = max(mk, x.x), mv = max(mv, x.y);
+      }
+      const uint32_t fk = half_power(own ? ek - mk + 7 : 0), fv = half_power(own ? ev - mv + 7 : 0);
+      if (row == 0) *reinterpret_cast<int2*>(exps->tile[tile % kExpSlots]) = make_int2(mk, mv);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar[C::EXFULL + tile % kExpSlots]);
+      ask(t + 1, page);
+      page = page_of(t + 2);
 #pragma unroll 1
       for (int which = 0; which < 2; ++which) {  // K(t) then V(t)
-        const uint32_t idx = kv_iter + 2 * t + which;
+        const uint32_t idx = 2 * tile + which;
         const int rs = idx % C::kRaw, stg = idx % C::kStages;
         if (!waitw(&bar[C::RAWFULL + rs], (idx / C::kRaw) & 1, a, 91)) return;
         if (idx >= C::kStages && !waitw(&bar[C::KVEMPTY + stg], ((idx / C::kStages) - 1) & 1, a, 92)) return;
-        const uint8_t* src = raw + rs * kChunkBytes + row * 128;
-        uint8_t* dst = sKV + stg * kTileBytes + row * 128;
-        const float fx = which ? f[1] : f[0];
+        const uint32_t src = smem_u32(raw) + rs * kChunkBytes + row * 128, dst = smem_u32(sKV) + stg * kTileBytes + row * 128;
+        const uint32_t f = which ? fv : fk;
+        auto lo = [&](uint32_t w) { return hmul2(e4m3x2_to_f16x2(w), f); };
+        auto hi = [&](uint32_t w) { return hmul2(e4m3x2_hi_to_f16x2(w), f); };
+        uint4 x[8];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {  // 16 values
-          const uint4 x = *reinterpret_cast<const uint4*>(src + ((c ^ (row & 7)) << 4));
-          const uint2 p = Dequant<T>::quad(x.x, fx), q = Dequant<T>::quad(x.y, fx), r = Dequant<T>::quad(x.z, fx),
-                      s = Dequant<T>::quad(x.w, fx);
-          uint8_t* half = dst + (c >> 2) * kChunkBytes;
-          *reinterpret_cast<uint4*>(half + (((2 * c) ^ row) & 7) * 16) = make_uint4(p.x, p.y, q.x, q.y);
-          *reinterpret_cast<uint4*>(half + (((2 * c + 1) ^ row) & 7) * 16) = make_uint4(r.x, r.y, s.x, s.y);
+        for (int c = 0; c < 8; ++c) x[c] = lds128(src + ((c ^ (row & 7)) << 4));  // 16 values
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const uint32_t half = dst + (c >> 2) * kChunkBytes;
+          sts128(half + (((2 * c) ^ row) & 7) * 16, lo(x[c].x), hi(x[c].x), lo(x[c].y), hi(x[c].y));
+          sts128(half + (((2 * c + 1) ^ row) & 7) * 16, lo(x[c].z), hi(x[c].z), lo(x[c].w), hi(x[c].w));
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -496,9 +614,10 @@ __device__ __forceinline__ void converter(const PagedAttnArgs& a, const uint8_t*
           mbar_arrive(&bar[C::RAWEMPTY + rs]);
           mbar_arrive(&bar[C::KVFULL + stg]);
         }
+        if (which == 0 && t + 1 < n) meet(tile + 1);
       }
     }
-    kv_iter += 2 * n;
+    tiles += n;
     __syncwarp();
     if (lane == 0) mbar_arrive(&bar[C::ITEMPTY + slot]);
   }
@@ -510,8 +629,10 @@ __device__ __forceinline__ void mma_issuer(const PagedAttnArgs& a, uint8_t* sQ, 
                                            const Item* items, uint32_t tbase) {
   using C = Chunk<k8>;
   constexpr int kStages = C::kStages;
-  constexpr uint32_t kIdescS = idesc<T>(false);  // S = Q K^T (both K-major)
-  constexpr uint32_t kIdescO = idesc<T>(true);   // O += P V (P in TMEM, V N-major)
+  using M = Operand<T, k8>;
+  constexpr uint32_t kIdescS = idesc<M>(false);  // S = Q K^T (both K-major)
+  constexpr uint32_t kIdescO = idesc<M>(true);   // O += P V (P in TMEM, V N-major)
+  constexpr int kQ = std::is_same<T, M>::value ? C::QFULL : C::QREADY;
   const uint64_t dQ0 = sdesc_sw128(smem_u32(sQ), 16, 1024);
   const uint64_t dK0 = sdesc_sw128(smem_u32(sKV), 16, 1024);
   const uint64_t dV0 = sdesc_sw128(smem_u32(sKV), kChunkBytes, 1024);
@@ -543,7 +664,7 @@ __device__ __forceinline__ void mma_issuer(const PagedAttnArgs& a, uint8_t* sQ, 
       const Item& inf = items[slot];
       if (!inf.valid) return;
       const int n = inf.n;
-      if (!waitw(&bar[C::QFULL], it & 1, a, 71)) goto abort;
+      if (!waitw(&bar[kQ], it & 1, a, 71)) goto abort;
       auto kv_full = [&](uint32_t idx) { return waitw(&bar[C::KVFULL + idx % kStages], (idx / kStages) & 1, a, 72); };
       if (inf.narrow) {
         // S(0), S(1), PV(0), S(2), PV(1), ...: tile t in score buffer t & 1
@@ -734,8 +855,8 @@ __device__ __forceinline__ void clear_v_row(uint8_t* v, int key) {
 // them from the cache; all lanes take part.  tO: the products' sums.
 template <typename T, bool k8>
 __device__ __noinline__ void write_hidden(const PagedAttnArgs& a, const Item& inf, int x, uint32_t tO, bool valid,
-                                          Span sp, T* orow, float* part, float l) {
-  const float inv = part ? 1.f : l == 0.f ? 0.f : 1.f / l;
+                                          Span sp, T* orow, float* part, float l, float unit) {
+  const float inv = part ? unit : l == 0.f ? 0.f : unit / l;
   const int* table = a.table + inf.seq * a.table_stride;
   using V = std::conditional_t<k8, uint8_t, T>;
   const V* v = static_cast<const V*>(a.vc) + inf.head * a.head_stride;
@@ -810,14 +931,15 @@ __device__ __noinline__ void write_hidden(const PagedAttnArgs& a, const Item& in
 
 template <typename T, bool k8>
 __device__ __forceinline__ void softmax_wg(const PagedAttnArgs& a, int x, uint64_t* bar, const Item* items,
-                                           uint8_t* sKV, volatile int* hidden, uint32_t tbase) {
+                                           uint8_t* sKV, volatile int* hidden, const Exps* exps, const int8_t* q_exp,
+                                           uint32_t tbase) {
   using C = Chunk<k8>;
+  using M = Operand<T, k8>;
   constexpr int kStages = C::kStages;
   const int wq = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
   const int row = wq * 32 + lane;  // TMEM lane = row of the sub-tile
   const uint32_t tl = static_cast<uint32_t>(wq * 32) << 16;
   const uint32_t tO = tbase + tl + 256 + 128 * x;
-  const float sl2 = a.scale_log2;
   uint32_t s_cnt = 0, s_odd = 0;  // phases of the score barriers so far
   uint32_t o_cnt = 0;          // products into this sub-tile's O so far
   uint32_t kv_iter = 0;
@@ -841,6 +963,7 @@ __device__ __forceinline__ void softmax_wg(const PagedAttnArgs& a, int x, uint64
     const Span sp = paged_span(a, inf.q_len, inf.k_len, min(token, inf.q_len - 1));
     float m = -INFINITY, l = 0.f;
     bool any = false;
+    int v_exp = 0;  // an 8-bit cache: O is relative to 2^v_exp
     for (int t = 0; t < n; ++t) {
       const int kt = inf.tile(t);
       const uint32_t cls = inf.cls(x, kt);
@@ -851,6 +974,24 @@ __device__ __forceinline__ void softmax_wg(const PagedAttnArgs& a, int x, uint64
       if (!waitw(&bar[C::SFULL + full], (odd ? s_odd : s_cnt) & 1, a, 82 + x)) return;
       if (odd) ++s_odd; else ++s_cnt;
       tc_fence_after();
+      float sl2 = a.scale_log2;
+      int shift = 0;  // of p, as the tile's V is relative to less than O
+      float lower = 1.f;  // of O, as it becomes relative to more
+      if constexpr (k8) {
+        // the scores show that the converters have been here; they are at most
+        // two tiles further on, so the wait sees its phase
+        const uint32_t tile = kv_iter / 2 + t;
+        if (!waitw(&bar[C::EXFULL + tile % kExpSlots], (tile / kExpSlots) & 1, a, 78 + x)) return;
+        const int2 e = *reinterpret_cast<const int2*>(exps->tile[tile % kExpSlots]);
+        if constexpr (!std::is_same<T, M>::value) sl2 = ldexpf(sl2, q_exp[(it & 1) * 256 + x * 128 + row]);
+        sl2 = fmaxf(sl2 * two_to(e.x - 7), 1.2e-38f);  // not 0, which times -inf is no number
+        if (!any) v_exp = e.y;
+        if (e.y > v_exp) {
+          lower = two_to(v_exp - e.y);
+          v_exp = e.y;
+        }
+        shift = e.y - v_exp;
+      }
       if (!span_covers(inf.every, kt * kTile, kt * kTile + kTile)) {
         // only now: a warpgroup that skipped a narrow item runs ahead of the
         // loads, and the scores show that the ring has come to this tile
@@ -860,11 +1001,11 @@ __device__ __forceinline__ void softmax_wg(const PagedAttnArgs& a, int x, uint64
         uint8_t* v = sKV + (vidx % kStages) * kTileBytes;
         if (!in_span(inf.all, j)) {
           clear_v_row(v, row);
-        } else if (!in_span(inf.every, j) && bad_v_row<T>(v, row)) {
+        } else if (!in_span(inf.every, j) && bad_v_row<M>(v, row)) {
           // the other warpgroup may find the value gone, but then the mark set
           hidden[slot] = it + 1;
           __threadfence_block();
-          finite_v_row<T>(v, row);
+          finite_v_row<M>(v, row);
         }
         fence_proxy_async_smem();
         if (cls != kTileFull) mask_scores(tS, sp, kt * kTile);
@@ -880,9 +1021,14 @@ __device__ __forceinline__ void softmax_wg(const PagedAttnArgs& a, int x, uint64
         need = true;
         m = m_new;
       }
-      const float base = k8 ? __fadd_ru(m == -INFINITY ? 0.f : m, -kBias<T>) : (m == -INFINITY ? 0.f : m) - kBias<T>;
-      const float sum = row_exp<T>(tS, sl2, base);
-      l = l * factor + sum;
+      float base = m == -INFINITY ? 0.f : m;
+      base = k8 ? __fadd_ru(base, -kBias<M> - shift) : base - kBias<M>;
+      const float sum = row_exp<M>(tS, sl2, base);
+      l = l * factor + (k8 ? sum * two_to(-shift) : sum);
+      if constexpr (k8) {
+        need |= lower != 1.f;
+        factor *= lower;
+      }
       const bool rescale = __any_sync(0xFFFFFFFFu, need);
       // The product before this one must have finished before O is rescaled.
       // In a narrow item nothing else tells that it has (the next scores do
@@ -920,15 +1066,20 @@ __device__ __forceinline__ void softmax_wg(const PagedAttnArgs& a, int x, uint64
     // the other warpgroup may set the mark just now, for tiles of its own alone:
     // a vote, since what follows takes all lanes of the warp together
     if (__any_sync(0xFFFFFFFFu, any && hidden[slot] == it + 1)) {
-      write_hidden<T, k8>(a, inf, x, tO, valid, sp, orow, part ? part + (x * 128 + row) * kHeadDim : nullptr, l);
+      write_hidden<T, k8>(a, inf, x, tO, valid, sp, orow, part ? part + (x * 128 + row) * kHeadDim : nullptr, l,
+                          k8 ? two_to(v_exp - 7) : 1.f);
     } else if (any) {
-      const float inv = part ? 1.f : l == 0.f ? 0.f : 1.f / l;
+      const float unit = k8 ? two_to(v_exp - 7) : 1.f;
+      const float inv = part ? unit : l == 0.f ? 0.f : unit / l;
       if (part) {
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
           uint32_t r[32];
           tmem_ld32(tO + 32 * c, r);
           tmem_ld_wait();
+          if constexpr (k8)
+#pragma unroll
+            for (int k = 0; k < 32; ++k) r[k] = __float_as_uint(__uint_as_float(r[k]) * inv);
           if (valid) {
             float* dst = part + (x * 128 + row) * kHeadDim + 32 * c;
 #pragma unroll
@@ -987,7 +1138,7 @@ __device__ __forceinline__ void softmax_wg(const PagedAttnArgs& a, int x, uint64
       part[256 * kHeadDim + 256 + x * 128 + row] = any ? l : 0.f;
     } else if (valid) {
       a.lse[static_cast<long long>(head) * a.Tq + inf.q_off + token] =
-          !any || l == 0.f ? -INFINITY : (m + log2f(l) - kBias<T>) * kLn2;
+          !any || l == 0.f ? -INFINITY : (m + log2f(l) - kBias<M>) * kLn2;
     }
     tc_fence_before();
     __syncwarp();
@@ -1005,11 +1156,14 @@ __global__ void __launch_bounds__(Chunk<k8>::kThreads, 1)
   uint8_t* sQ = sm + C::kOffQ;
   uint8_t* sKV = sm + C::kOffKV;
   uint64_t* bar = reinterpret_cast<uint64_t*>(sm + C::kOffCtl);
-  Item* items = reinterpret_cast<Item*>(sm + C::kOffCtl + 256);
+  Item* items = reinterpret_cast<Item*>(sm + C::kOffCtl + C::kOffItems);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + C::kOffCtl + 896);
   // per item slot: the last item (from 1) with values that write_hidden adds;
   // a warp may be that many items ahead of another
   int* hidden = reinterpret_cast<int*>(sm + C::kOffCtl + 904);
+  Exps* exps = reinterpret_cast<Exps*>(sm + C::kOffCtl + 920);
+  static_assert(920 + sizeof(Exps) <= 1024, "the control part");
+  int8_t* q_exp = reinterpret_cast<int8_t*>(sm + C::kOffCtl + C::kOffExp);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (warp == 8) {
     tmem_alloc(tmem_slot, 512);
@@ -1020,6 +1174,9 @@ __global__ void __launch_bounds__(Chunk<k8>::kThreads, 1)
     if constexpr (k8) {  // one arrival per converter warp
       for (int x = 0; x < C::kStages; ++x) mbar_init(&bar[C::KVFULL + x], 4);
       for (int x = 0; x < C::kRaw; ++x) mbar_init(&bar[C::RAWEMPTY + x], 4);
+      for (int x = 0; x < kExpSlots; ++x) mbar_init(&bar[C::EXFULL + x], 4);
+      mbar_init(&bar[C::QREADY], 4);
+      mbar_init(&bar[C::MAXFULL], 4);
     }
     for (int x = 0; x < 3; ++x) mbar_init(&bar[C::PFULL + x], 4);  // one arrival per softmax warp
     for (int x = 0; x < kItemSlots; ++x) hidden[x] = 0;
@@ -1046,9 +1203,9 @@ __global__ void __launch_bounds__(Chunk<k8>::kThreads, 1)
   } else if (warp == 8) {
     mma_issuer<T, k8>(a, sQ, sKV, bar, items, tbase);
   } else if (warp < 8) {
-    softmax_wg<T, k8>(a, warp >> 2, bar, items, sKV, hidden, tbase);
+    softmax_wg<T, k8>(a, warp >> 2, bar, items, sKV, hidden, exps, q_exp, tbase);
   } else if constexpr (k8) {
-    if (warp >= 12) converter<T>(a, sm + C::kOffRaw, sKV, bar, items);
+    if (warp >= 12) converter<T>(a, sQ, sm + C::kOffRaw, sKV, bar, items, exps, q_exp);
   }
   tc_fence_before();
   __syncthreads();
