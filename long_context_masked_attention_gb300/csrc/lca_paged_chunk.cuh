@@ -526,6 +526,7 @@ __device__ __forceinline__ void converter(const PagedAttnArgs& a, uint8_t* sQ, c
   using C = Chunk<true>;
   const int lane = threadIdx.x & 31, row = threadIdx.x & 127, wq = row >> 5;
   uint32_t tiles = 0;  // before this item
+  const uint32_t at0 = row * 128 + ((row & 7) << 4), raw0 = smem_u32(raw) + at0, kv0 = smem_u32(sKV) + at0;
   for (int it = 0;; ++it) {
     const int slot = it % kItemSlots;
     if (!waitw(&bar[C::ITFULL + slot], (it / kItemSlots) & 1, a, 90)) return;
@@ -595,18 +596,22 @@ __device__ __forceinline__ void converter(const PagedAttnArgs& a, uint8_t* sQ, c
         const int rs = idx % C::kRaw, stg = idx % C::kStages;
         if (!waitw(&bar[C::RAWFULL + rs], (idx / C::kRaw) & 1, a, 91)) return;
         if (idx >= C::kStages && !waitw(&bar[C::KVEMPTY + stg], ((idx / C::kStages) - 1) & 1, a, 92)) return;
-        const uint32_t src = smem_u32(raw) + rs * kChunkBytes + row * 128, dst = smem_u32(sKV) + stg * kTileBytes + row * 128;
+        // addresses of piece 0; piece c differs in the bits of 16 c
+        const uint32_t src = raw0 + rs * kChunkBytes, dst = kv0 + stg * kTileBytes;
         const uint32_t f = which ? fv : fk;
         auto lo = [&](uint32_t w) { return hmul2(e4m3x2_to_f16x2(w), f); };
         auto hi = [&](uint32_t w) { return hmul2(e4m3x2_hi_to_f16x2(w), f); };
-        uint4 x[8];
+#pragma unroll 1
+        for (int b = 0; b < 8; b += 4) {
+          uint4 x[4];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) x[c] = lds128(src + ((c ^ (row & 7)) << 4));  // 16 values
+          for (int c = 0; c < 4; ++c) x[c] = lds128(src ^ ((b + c) << 4));  // 16 values
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          const uint32_t half = dst + (c >> 2) * kChunkBytes;
-          sts128(half + (((2 * c) ^ row) & 7) * 16, lo(x[c].x), hi(x[c].x), lo(x[c].y), hi(x[c].y));
-          sts128(half + (((2 * c + 1) ^ row) & 7) * 16, lo(x[c].z), hi(x[c].z), lo(x[c].w), hi(x[c].w));
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t to = (dst ^ (((b + c) & 3) << 5)) + ((b + c) >> 2) * kChunkBytes;
+            sts128(to, lo(x[c].x), hi(x[c].x), lo(x[c].y), hi(x[c].y));
+            sts128(to ^ 16, lo(x[c].z), hi(x[c].z), lo(x[c].w), hi(x[c].w));
+          }
         }
         fence_proxy_async_smem();
         __syncwarp();
