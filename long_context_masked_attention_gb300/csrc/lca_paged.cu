@@ -455,6 +455,7 @@ template <typename T>
 struct Worker16 {
   using Out = T;
   static constexpr int kRows = lca::kRows, kUnit = lca::kUnit;
+  static __device__ constexpr Claims claims() { return {160, 8, 2, 0x7FFFFFFF}; }
   static constexpr int kWarpBytes = lca::kWarpBytes;
   static constexpr float kBias = lca::kBias<T>;
   static __device__ __forceinline__ void run(const PagedAttnArgs& a, uint8_t* ring, int seq, const Request& sg,

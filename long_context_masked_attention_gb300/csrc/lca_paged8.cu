@@ -226,6 +226,10 @@ template <typename T, int kTiles>
 struct Worker8 {
   using Out = T;
   static constexpr int kRows = 8 * kTiles, kUnit = kUnit8;
+  // Units per CTA 64: 64 requests of 1K-32K keys (83 units) 209 -> 199 us, 32 of
+  // 16K (74) 188 -> 179, 256 of 1K (54) 100 -> 104 were they claimed.  One request of
+  // 512K (8 heads) 193 -> 226 were its, in twice as many pieces; four 662 -> 651.
+  static __device__ constexpr Claims claims() { return {64, 8, 1, 16}; }
   static constexpr int kWarpBytes = kWarp8 > kRows * 132 * 4 ? kWarp8 : kRows * 132 * 4;
   static constexpr float kBias = 0.f;
   static __device__ __forceinline__ void run(const PagedAttnArgs& a, uint8_t* ring_, int seq, const Request& sg,

@@ -32,11 +32,15 @@ namespace {
 // 8-bit cache have 128 keys and as many bytes.
 constexpr int kDecWarps = 4;
 constexpr int kDecThreads = 32 * kDecWarps;
-// Units per CTA from which on the line's last eighth is claimed.  Above it: 64
-// requests of 1K-32K (1.1M keys) 698 -> 668 us, 4 of 512K 1293 -> 1248.  Below
+// How the last part of a long line is claimed: from `share` units per CTA on,
+// one in `part` of it, in `spans` spans per CTA.  For a 16-bit cache, above it:
+// 64 requests of 1K-32K (1.1M keys) 698 -> 668 us, 4 of 512K 1293 -> 1248.  Below
 // it the finer spans cost more than they even out: 256 requests of 1K, 134
-// units per CTA, 185 us unclaimed and 196 claimed.
-constexpr int kLongShare = 160;
+// units per CTA, 185 us unclaimed and 196 claimed.  Not where an item would have
+// more than `pieces` pieces, which one CTA joins.
+struct Claims {
+  int share, part, spans, pieces;
+};
 // What an item costs beside its units, in units; 0 against 4: 128 requests of
 // 100-8K keys 317.5 and 315.5 us, 64 of 500 43.4 and 43.1, 8 of 4K 43.2 and 39.7.
 constexpr int kItemUnits = 4;
@@ -146,14 +150,14 @@ __device__ __forceinline__ long long place_requests(const PagedAttnArgs& a, Deco
 }
 
 // The line's spans: one per CTA over its first `big` units and, where a CTA's
-// share is long, two more per CTA over the rest.
+// share is long, some more per CTA over the rest.
 struct Spans {
   long long total, big;
   int first, rest;
-  __device__ __forceinline__ Spans(long long t, int grid) : total(t) {
+  __device__ __forceinline__ Spans(long long t, int grid, long long heads, Claims c) : total(t) {
     first = static_cast<int>(min(static_cast<long long>(grid), max(total / kMinUnits, 1LL)));
-    rest = total / first >= kLongShare ? 2 * first : 0;
-    big = rest > 0 ? total - total / 8 : total;
+    rest = total / first >= c.share && first / c.pieces <= heads ? c.spans * first : 0;
+    big = rest > 0 ? total - total / c.part : total;
   }
   __device__ __forceinline__ long long start(int c) const {
     return c <= first ? line_div(c * big, first) : big + line_div((c - first) * (total - big), rest);
@@ -221,7 +225,7 @@ __device__ __forceinline__ void decode_span(const PagedAttnArgs& a, DecodeShared
     total = min(total + place_requests<W>(a, sh, base), kMost);
   if (!behind) grid_wait();  // counts and status are cleared
   if (total == 0 || total == kMost) return;
-  const Spans sp(total, gridDim.x);
+  const Spans sp(total, gridDim.x, static_cast<long long>(a.n_seq) * a.Hkv, W::claims());
   if (blockIdx.x >= sp.first) return;
   int base = a.n_seq > kSeqTile ? -kSeqTile : 0;      // requests in sh.start begin at base
   long long tile0 = 0, tile1 = a.n_seq > kSeqTile ? 0 : total;  // their units
