@@ -989,51 +989,58 @@ def rope_frequencies(rot_dim=128, base=10000.0, scaling="PLAIN", factor=1.0, ori
     return RopeFreqs(inv, out.value)
 
 
+def _rope_rows(x, y, name, T, dtype, device, side):
+    """lca_rope_rows of [T, H, 128] tensors x and y (made here if None), and y."""
+    xs = _rows(x, name, None, 128, dtype, device)
+    rows, H, _ = x.shape
+    if rows != T:
+        raise ValueError(f"{name}: {rows} rows, expected {T}")
+    if y is None:
+        y = _empty((T, H, 128), dtype, device, side)
+        ys = H * 128
+    else:
+        ys = _rows(y, name + "_out", H, 128, dtype, device)
+        if y.shape[0] != T:
+            raise ValueError(f"{name}_out: {y.shape[0]} rows, expected {T}")
+    return RopeRows_t(x.data_ptr(), y.data_ptr(), _int32(H, name), xs, ys), y
+
+
 def _rope(q, k, positions, freqs, interleaved, q_out, k_out, stream, back):
     import torch
 
-    first = q if q is not None else k
+    first, name = (q, "q") if q is not None else (k, "k")
     if not isinstance(first, torch.Tensor):
-        raise TypeError(f"q: expected a torch.Tensor, got {type(first).__name__}")
-    dev, dt = first.device, first.dtype
+        raise TypeError(f"{name}: expected a torch.Tensor, got {type(first).__name__}")
     if not first.is_cuda:
-        raise ValueError(f"{'q' if q is not None else 'k'}: must be a CUDA tensor (got {dev})")
-    code = _dtype_code(dt, "q" if q is not None else "k")
+        raise ValueError(f"{name}: must be a CUDA tensor (got {first.device})")
+    dev, dt = first.device, first.dtype
+    code = _dtype_code(dt, name)
     T = _int32(first.shape[0] if first.dim() else 0, "rows")
     pp = _ptr(positions, "positions", torch.int32, (T,), dev)
     side = _side_stream(stream, dev)
-    rows, outs = [], []
-    for x, y, name in ((q, q_out, "q"), (k, k_out, "k")):
-        if x is None:
-            if y is not None:
-                raise ValueError(f"{name}_out: given without {name}")
-            rows.append(None)
-            outs.append(None)
-            continue
-        xs = _rows(x, name, None, 128, dt, dev)
-        if x.shape[0] != T:
-            raise ValueError(f"{name}: {x.shape[0]} rows, expected {T}")
-        H = x.shape[1]
-        if y is None:
-            y = _empty((T, H, 128), dt, dev, side)
-            ys = H * 128
-        else:
-            ys = _rows(y, name + "_out", H, 128, dt, dev)
-            if y.shape[0] != T:
-                raise ValueError(f"{name}_out: {y.shape[0]} rows, expected {T}")
-        rows.append(RopeRows_t(x.data_ptr(), y.data_ptr(), _int32(H, name), xs, ys))
-        outs.append(y)
-    inv = np.ascontiguousarray(np.asarray(freqs.inv_freq, dtype=np.float64))
+    qr = kr = None
+    if q is not None:
+        qr, q_out = _rope_rows(q, q_out, "q", T, dt, dev, side)
+    elif q_out is not None:
+        raise ValueError("q_out: given without q")
+    if k is not None:
+        kr, k_out = _rope_rows(k, k_out, "k", T, dt, dev, side)
+    elif k_out is not None:
+        raise ValueError("k_out: given without k")
+    inv = freqs.inv_freq
+    if type(inv) is not np.ndarray or inv.dtype != np.float64 or not inv.flags.c_contiguous:
+        inv = np.ascontiguousarray(np.asarray(inv, dtype=np.float64))
     if inv.ndim != 1:
         raise ValueError(f"freqs.inv_freq: shape {inv.shape}, expected [rot_dim / 2]")
-    desc = RopeDesc_t(2 * inv.size, int(bool(interleaved)), inv.ctypes.data, float(getattr(freqs, "scale", 1.0)))
+    desc = RopeDesc_t(2 * len(inv), 1 if interleaved else 0, inv.__array_interface__["data"][0],
+                      getattr(freqs, "scale", 1.0))
     if side is not None:
-        for t in (q, k, positions, *outs):
+        for t in (q, k, positions, q_out, k_out):
             if t is not None:
                 t.record_stream(side)
-    _call(load().lca_rope, "lca_rope", dev, side, *(C.byref(r) if r is not None else None for r in rows), pp, T, 128, code,
-          C.byref(desc), back)
-    return tuple(outs)
+    _call(load().lca_rope, "lca_rope", dev, side, None if qr is None else C.byref(qr), None if kr is None else C.byref(kr), pp,
+          T, 128, code, C.byref(desc), back)
+    return q_out, k_out
 
 
 def rope(q, k, positions, freqs, interleaved=False, q_out=None, k_out=None, stream=None):

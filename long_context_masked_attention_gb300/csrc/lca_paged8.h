@@ -29,6 +29,7 @@ struct PagedRead8Args {
   const int* pages;
   int n, n_pages, Hkv, page_size;
   bool token_first;  // tokens of a head lie closer together than its heads
+  bool out_v8;       // every 16 values of the result start on a 32-byte boundary
 };
 void launch_paged_read8(const PagedRead8Args& a, bool fp16, int num_sms, cudaStream_t st);
 

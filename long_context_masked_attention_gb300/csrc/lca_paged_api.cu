@@ -530,6 +530,7 @@ lca_status lca_paged_read_fp8(const lca_paged_cache_fp8* cache, const int32_t* p
   if (n < 0 || n > out->n_pages || out->page_size != cache->page_size || out->Hkv != cache->Hkv)
     return LCA_ERR_INVALID_ARG;
   if (n == 0) return LCA_OK;
+  if (static_cast<long long>(cache->page_size) * cache->Hkv > 0x7FFFFF00LL) return LCA_ERR_UNSUPPORTED;
   if (!ints(pages, n) || !cache_memory(out)) return LCA_ERR_INVALID_ARG;
   if (cache->n_pages == 0) return LCA_OK;  // every entry lies outside
   if (!cache_memory8(cache)) return LCA_ERR_INVALID_ARG;
@@ -564,6 +565,8 @@ lca_status lca_paged_read_fp8(const lca_paged_cache_fp8* cache, const int32_t* p
   a.Hkv = cache->Hkv;
   a.page_size = cache->page_size;
   a.token_first = cache->token_stride < cache->head_stride;
+  a.out_v8 = ((reinterpret_cast<uintptr_t>(out->k) | reinterpret_cast<uintptr_t>(out->v)) & 31u) == 0 &&
+             out->page_stride % 16 == 0 && out->token_stride % 16 == 0 && out->head_stride % 16 == 0;
   launch_paged_read8(a, out->dtype == LCA_F16, sms, static_cast<cudaStream_t>(stream));
   LCA_CUDA(cudaGetLastError());
   return LCA_OK;

@@ -187,8 +187,9 @@ constexpr long long kMostStride = 1LL << 38;
 uint64_t turns_of(double w) {
   const double hi = 0.15915494309189535, lo = -9.839338337591243e-18;  // 1 / (2 pi)
   const double p = w * hi, e = std::fma(w, hi, -p) + w * lo;
-  return static_cast<uint64_t>(std::ldexp(p - std::floor(p), 64)) +
-         static_cast<uint64_t>(static_cast<int64_t>(std::llrint(std::ldexp(e, 64))));
+  constexpr double k64 = 18446744073709551616.0;  // 2^64
+  const double whole = static_cast<double>(static_cast<int64_t>(p));  // p is below 2^18
+  return static_cast<uint64_t>((p - whole) * k64) + static_cast<uint64_t>(static_cast<int64_t>(e * k64));
 }
 
 // Bytes from the first element of the rows to the last.
