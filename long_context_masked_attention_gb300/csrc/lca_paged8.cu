@@ -129,7 +129,15 @@ __global__ void __launch_bounds__(256) paged_read8_kernel(const PagedRead8Args a
   for (long long b = blockIdx.x; b < n; b += gridDim.x) {
     const long long i = line_div(b, parts);
     const unsigned row0 = static_cast<unsigned>(b - i * parts) * (32 * kRows) + (threadIdx.x >> 3);
-    const int page = __ldg(a.pages + i);
+    int page;
+    if (a.map) {
+      const long long seq = line_div(i, a.max_pages);
+      const int entry = static_cast<int>(i - seq * a.max_pages);
+      page = static_cast<long long>(entry) * a.page_size < __ldg(a.k_len + seq) ? __ldg(a.pages + seq * a.table_stride + entry) : -1;
+      if (b == i * parts && threadIdx.x == 0) a.map[i] = page >= 0 && page < a.n_pages ? static_cast<int>(i) : -1;
+    } else {
+      page = __ldg(a.pages + i);
+    }
     if (page < 0 || page >= a.n_pages) continue;
     uint4 x[kRows], y[kRows];
     uint32_t bk[kRows], bv[kRows];

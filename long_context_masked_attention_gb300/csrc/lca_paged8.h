@@ -28,6 +28,13 @@ struct PagedRead8Args {
   long long out_page_stride, out_token_stride, out_head_stride;
   const int* pages;
   int n, n_pages, Hkv, page_size;
+  // Where `map` is given, `pages` are the rows of a block table, n in all, and
+  // those that hold one of a request's keys are read; map[i] becomes i, -1 for
+  // the others and for entries that are no page.
+  long long table_stride;
+  int max_pages;
+  const int* k_len;
+  int* map;
   bool token_first;  // tokens of a head lie closer together than its heads
   bool out_v8;       // every 16 values of the result start on a 32-byte boundary
 };

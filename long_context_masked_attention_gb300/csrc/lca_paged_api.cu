@@ -181,6 +181,57 @@ PagedLayout paged_layout(const lca_paged_shape* sh, const lca_paged_cache* c, bo
   return L;
 }
 
+// Whether a call over an 8-bit cache makes a 16-bit copy of its tables' pages
+// first and runs on that: it has so many rows per request that reading the keys
+// as 8 bits costs more than the copy.  2048 tokens at 32K keys, 64 heads on 8,
+// take 1876 us as they are and 1545 copied (33 of it the copy); with R rows per
+// request and KV head the copy is some R / 1400 of what it saves, if the tables are full.
+constexpr long long kCopyRows = 4096;
+constexpr long long kCopyBytes = 1LL << 30;
+long long copy_bytes(const lca_paged_shape* sh, const lca_paged_cache* c) {  // of K or V
+  return static_cast<long long>(sh->n_seq) * sh->max_pages * c->page_size * c->Hkv * kHeadDim * 2;
+}
+bool copies(const lca_paged_shape* sh, const lca_paged_cache* c) {
+  const long long n = sh->n_seq, hint = sh->max_q_len;
+  const long long rows = hint > 0 && hint * n < sh->Tq ? hint * n : sh->Tq;
+  // in doubles: none of these is small enough to multiply unseen
+  const double bytes = static_cast<double>(n) * sh->max_pages * c->page_size * c->Hkv * kHeadDim * 4;
+  return n > 0 && sh->max_pages > 0 && c->n_pages > 0 && bytes <= static_cast<double>(kCopyBytes) &&
+         rows * (sh->Hq / c->Hkv) >= kCopyRows * n && static_cast<long long>(c->page_size) * c->Hkv <= 0x7FFFFF00LL;
+}
+// The copy's layout: [page of a table][head][token][128].
+lca_paged_cache copy_of(const lca_paged_shape* sh, const lca_paged_cache* c, int dtype, uint8_t* at) {
+  const int64_t head = static_cast<int64_t>(c->page_size) * kHeadDim;
+  return {at, at + copy_bytes(sh, c), sh->n_seq * sh->max_pages, c->page_size, c->Hkv, kHeadDim, dtype, head * c->Hkv,
+          kHeadDim, head};
+}
+
+// Workspace of a call over an 8-bit cache; where it copies, `copy` and `map` (the
+// tables of the copy) lie behind what the call over the copy needs.
+struct Layout8 {
+  PagedLayout run;
+  size_t copy = 0, map = 0, total = 0;
+  bool copies = false;
+};
+Layout8 layout8(const lca_paged_shape* sh, const lca_paged_cache* c) {
+  Layout8 L;
+  L.copies = copies(sh, c);
+  if (!L.copies) {
+    L.run = paged_layout(sh, c, true);
+    L.total = L.run.total;
+    return L;
+  }
+  const lca_paged_cache v = copy_of(sh, c, LCA_BF16, nullptr);
+  L.run = paged_layout(sh, &v, false);
+  L.copy = L.run.total;
+  L.map = align_up(L.copy + 2 * static_cast<size_t>(copy_bytes(sh, c)));
+  L.total = align_up(L.map + sizeof(int) * sh->n_seq * static_cast<size_t>(sh->max_pages));
+  // a shorter longest request may make it a call without a copy
+  const size_t other = paged_layout(sh, c, true).total;
+  if (sh->max_q_len == 0 && other > L.total) L.total = other;
+  return L;
+}
+
 lca_status check_attn(const lca_paged_shape* sh, const lca_paged_cache* c, const lca_mask_desc* md, MaskCtx& m) {
   if (!sh || !md) return LCA_ERR_INVALID_ARG;
   const lca_status r = check_cache(c);
@@ -277,6 +328,30 @@ bool cache_map(CUtensorMap* m, const void* p, const Cache& any, int box_rows) {
   return encode(m, p, any.c8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : map_type(c->dtype), 4, dims, strides, box);
 }
 
+// What the kernel that reads pages back needs to know of a cache and its copy.
+void read_args(const lca_paged_cache_fp8* cache, const lca_paged_cache* out, PagedRead8Args& a) {
+  a.kc = static_cast<const uint8_t*>(cache->k);
+  a.vc = static_cast<const uint8_t*>(cache->v);
+  a.ks = cache->k_scale;
+  a.vs = cache->v_scale;
+  a.k = static_cast<uint16_t*>(out->k);
+  a.v = static_cast<uint16_t*>(out->v);
+  a.page_stride = cache->page_stride;
+  a.token_stride = cache->token_stride;
+  a.head_stride = cache->head_stride;
+  a.scale_page_stride = cache->scale_page_stride;
+  a.scale_head_stride = cache->scale_head_stride;
+  a.out_page_stride = out->page_stride;
+  a.out_token_stride = out->token_stride;
+  a.out_head_stride = out->head_stride;
+  a.n_pages = cache->n_pages;
+  a.Hkv = cache->Hkv;
+  a.page_size = cache->page_size;
+  a.token_first = cache->token_stride < cache->head_stride;
+  a.out_v8 = ((reinterpret_cast<uintptr_t>(out->k) | reinterpret_cast<uintptr_t>(out->v)) & 31u) == 0 &&
+             out->page_stride % 16 == 0 && out->token_stride % 16 == 0 && out->head_stride % 16 == 0;
+}
+
 // lca_attn_paged over a cache of either kind, q and o of `dtype`.
 lca_status attend(const Cache& any, int dtype, const void* q, const int32_t* block_table, const int32_t* q_start,
                   const int32_t* k_len, void* o, float* lse, const lca_paged_shape* shape, const lca_mask_desc* mask,
@@ -286,8 +361,15 @@ lca_status attend(const Cache& any, int dtype, const void* q, const int32_t* blo
   PagedAttnArgs a{};
   const lca_status r = check_attn(shape, cache, mask, a.mask);
   if (r != LCA_OK) return r;
-  const PagedLayout L = paged_layout(shape, cache, c8 != nullptr);
-  if (!workspace || reinterpret_cast<uintptr_t>(workspace) % kAlign != 0 || workspace_bytes < L.total ||
+  Layout8 L8;
+  if (c8) {
+    L8 = layout8(shape, cache);
+  } else {
+    L8.run = paged_layout(shape, cache, false);
+    L8.total = L8.run.total;
+  }
+  const PagedLayout& L = L8.run;
+  if (!workspace || reinterpret_cast<uintptr_t>(workspace) % kAlign != 0 || workspace_bytes < L8.total ||
       !device_input(workspace))
     return LCA_ERR_WORKSPACE;
   const long long n_table =
@@ -307,7 +389,7 @@ lca_status attend(const Cache& any, int dtype, const void* q, const int32_t* blo
     if (c8) extents8(c8, e8);
     const Extent t[12] = {{o, rows * heads * kHeadDim * 2},
               {lse, rows * heads * 4},
-              {workspace, static_cast<long long>(L.total)},
+              {workspace, static_cast<long long>(L8.total)},
               {q, rows > 0 ? ((rows - 1) * shape->q_stride + heads * kHeadDim) * 2 : 0},
               {cache->k, extent},
               {cache->v, extent},
@@ -324,6 +406,29 @@ lca_status attend(const Cache& any, int dtype, const void* q, const int32_t* blo
   const int sms = num_sms();
   if (sms <= 0) return LCA_ERR_CUDA;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool fp16 = dtype == LCA_F16;
+  Cache run = any;
+  lca_paged_cache copy{};
+  long long table_stride = shape->table_stride;
+  if (L8.copies) {
+    copy = copy_of(shape, cache, dtype, ws + L8.copy);
+    PagedRead8Args c{};
+    read_args(c8, &copy, c);
+    c.pages = block_table;
+    c.n = shape->n_seq * shape->max_pages;
+    c.table_stride = shape->table_stride;
+    c.max_pages = shape->max_pages;
+    c.k_len = k_len;
+    c.map = reinterpret_cast<int*>(ws + L8.map);
+    launch_paged_read8(c, fp16, sms, st);
+    LCA_CUDA(cudaGetLastError());
+    run = {&copy, nullptr};
+    cache = run.c;
+    c8 = nullptr;
+    block_table = c.map;
+    table_stride = shape->max_pages;
+  }
   a.q = q;
   a.kc = cache->k;
   a.vc = cache->v;
@@ -337,7 +442,7 @@ lca_status attend(const Cache& any, int dtype, const void* q, const int32_t* blo
     a.scale_page_stride = c8->scale_page_stride;
     a.scale_head_stride = c8->scale_head_stride;
   }
-  a.table_stride = shape->table_stride;
+  a.table_stride = table_stride;
   a.table = block_table;
   a.q_start = q_start;
   a.k_len = k_len;
@@ -380,12 +485,10 @@ lca_status attend(const Cache& any, int dtype, const void* q, const int32_t* blo
     const cuuint64_t dims[3] = {kHeadDim, static_cast<cuuint64_t>(a.Hq), static_cast<cuuint64_t>(a.Tq)};
     const cuuint64_t strides[2] = {kHeadDim * 2, static_cast<cuuint64_t>(a.q_stride) * 2};
     const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(a.G), static_cast<cuuint32_t>(a.tpt)};
-    if (!encode(&tq, q, map_type(dtype), 3, dims, strides, box) || !cache_map(&tk, cache->k, any, a.box_rows) ||
-        !cache_map(&tv, cache->v, any, a.box_rows))
+    if (!encode(&tq, q, map_type(dtype), 3, dims, strides, box) || !cache_map(&tk, cache->k, run, a.box_rows) ||
+        !cache_map(&tv, cache->v, run, a.box_rows))
       return LCA_ERR_CUDA;
   }
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const bool fp16 = dtype == LCA_F16;
   LCA_CUDA(launch_paged_begin(a, many, st));
   if (many) LCA_CUDA((c8 ? launch_paged_chunk8 : launch_paged_chunk)(tq, tk, tv, a, fp16, sms, st));
   if (shape->Tq > 0)
@@ -545,28 +648,9 @@ lca_status lca_paged_read_fp8(const lca_paged_cache_fp8* cache, const int32_t* p
   const int sms = num_sms();
   if (sms <= 0) return LCA_ERR_CUDA;
   PagedRead8Args a{};
-  a.kc = static_cast<const uint8_t*>(cache->k);
-  a.vc = static_cast<const uint8_t*>(cache->v);
-  a.ks = cache->k_scale;
-  a.vs = cache->v_scale;
-  a.k = static_cast<uint16_t*>(out->k);
-  a.v = static_cast<uint16_t*>(out->v);
-  a.page_stride = cache->page_stride;
-  a.token_stride = cache->token_stride;
-  a.head_stride = cache->head_stride;
-  a.scale_page_stride = cache->scale_page_stride;
-  a.scale_head_stride = cache->scale_head_stride;
-  a.out_page_stride = out->page_stride;
-  a.out_token_stride = out->token_stride;
-  a.out_head_stride = out->head_stride;
+  read_args(cache, out, a);
   a.pages = pages;
   a.n = n;
-  a.n_pages = cache->n_pages;
-  a.Hkv = cache->Hkv;
-  a.page_size = cache->page_size;
-  a.token_first = cache->token_stride < cache->head_stride;
-  a.out_v8 = ((reinterpret_cast<uintptr_t>(out->k) | reinterpret_cast<uintptr_t>(out->v)) & 31u) == 0 &&
-             out->page_stride % 16 == 0 && out->token_stride % 16 == 0 && out->head_stride % 16 == 0;
   launch_paged_read8(a, out->dtype == LCA_F16, sms, static_cast<cudaStream_t>(stream));
   LCA_CUDA(cudaGetLastError());
   return LCA_OK;
@@ -599,7 +683,7 @@ lca_status lca_attn_paged_fp8_workspace_size(const lca_paged_shape* shape, const
   MaskCtx m;
   r = check_attn(shape, &v, mask, m);
   if (r != LCA_OK) return r;
-  *bytes = paged_layout(shape, &v, true).total;
+  *bytes = layout8(shape, &v).total;
   return LCA_OK;
 }
 

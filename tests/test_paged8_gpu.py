@@ -780,3 +780,125 @@ def test_a_batch_that_does_not_fit_keeps_its_positions(lca, case, mask):
         o, lse, st = attend(lca, p, ctx_len=ctx, max_q_len=hint)
         assert st[0] == (6 if behind else 0)
         check8(o, lse, p, ref, what=f"{case}, max_q_len={hint}")
+
+
+# ------------------------------------------------------------------ prompts of so many rows that the pages are copied first
+LONG = [(300, 1100), (0, 1200), (700, 1), (1025, 900)]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("layout,page", [("nhd", 16), ("hnd", 64), ("kv", 24), ("nhd", 256)])
+def test_long_prompts(lca, layout, page, dtype):
+    """6 heads of a group, so that the four requests have more than 4096 rows on average; beside them padding rows, and
+    NaN wherever no request's token lies."""
+    p = make8(LONG, page, 12, 2, CAUSAL, dtype, layout, pad=7, seed=page, device="cuda")
+    ref = reference8(p)
+    sizes = [lca.attn_paged_fp8_workspace_size(p.q, p.kc, p.vc, p.ks, p.vs, p.table, CAUSAL, max_q_len=h) for h in (0, 1200, 500, 1)]
+    assert sizes[0] == max(sizes)  # a workspace for an unknown longest request serves every hint
+    for kw in (dict(), dict(max_q_len=1200)):
+        o, lse, st = attend(lca, p, **kw)
+        check8(o, lse, p, ref)
+        assert st == (0, 0)
+
+
+@pytest.mark.parametrize("mask", MASKS, ids=lambda m: f"{m.kind}{m.window_left or ''}")
+def test_masks_of_long_prompts(lca, mask):
+    p = make8([(300, 600), (0, 700)], 16, 8, 1, mask, seed=5, device="cuda")
+    o, lse, st = attend(lca, p)
+    check8(o, lse, p, what=mask.kind)
+    assert st == (0, 0)
+
+
+def test_long_prompts_with_pages_gone_or_bad(lca):
+    """Pages before a window are gone and hold NaN; entries that are no page read as zeros and are reported, ones that
+    no row needs are not; the next call on the same workspace sees nothing of them."""
+    import torch
+
+    mask = MaskSpec("CAUSAL_SLIDING", window_left=100)
+    p = make8([(900, 600), (0, 520)], 16, 8, 1, mask, seed=6, device="cuda")
+    ref = reference8(p)
+    for e in range((900 - 100) // 16):
+        for t in (p.kc, p.vc):
+            t.view(torch.uint8)[int(p.table[0, e])] = 0x7F
+        p.table[0, e] = -1 if e % 2 else 1 << 30
+    o, lse, st = attend(lca, p)
+    assert st == (0, 0)
+    check8(o, lse, p, ref)
+    q = make8([(900, 600), (0, 520)], 16, 8, 1, CAUSAL, seed=6, device="cuda")
+    good = q.table.clone()
+    q.table[0, 5] = q.kc.shape[0]
+    o, lse, st = attend(lca, q)
+    assert st[0] == 6
+    k, v = q.k.clone(), q.v.clone()
+    q.k[80:96] = 0
+    q.v[80:96] = 0
+    check8(o, lse, q)
+    q.table, q.k, q.v = good, k, v
+    o, lse, st = attend(lca, q)
+    assert st == (0, 0)
+    check8(o, lse, q)
+
+
+def test_nan_in_long_prompts_and_lengths_that_do_not_fit(lca):
+    """A NaN reaches the rows that attend it, in its column; cached lengths place the rows of a request that the tables
+    have no room for; a bad length is clamped and reported."""
+    import torch
+
+    p = make8([(40, 1100)], 32, 8, 2, CAUSAL, seed=8, device="cuda")
+    ref = reference8(p)
+    o0, lse0, _ = attend(lca, p)
+    check8(o0, lse0, p, ref)
+    p.vc.view(torch.uint8)[int(p.table[0, 500 // 32]), 500 % 32, 0, 9] = 0x7F
+    o, lse, st = attend(lca, p)
+    assert st == (0, 0) and torch.equal(lse, lse0)
+    assert bool(o[460:, :4, 9].isnan().all())
+    o[460:, :4, 9] = o0[460:, :4, 9]
+    check8(o, lse, p, ref)
+    p = make8([(40, 1100)], 32, 8, 2, CAUSAL, seed=8, device="cuda")
+    ctx = torch.tensor([40], dtype=torch.int32, device="cuda")
+    room = 30 * 32
+    p.table = p.table[:, :30].contiguous()
+    p.k_len[0] = room
+    o, lse, st = attend(lca, p, ctx_len=ctx)
+    assert st[0] == 6
+    assert bool(torch.isneginf(lse[:, room - 40:]).all()) and float(o[room - 40:].abs().max()) == 0
+    p.prob.segments[0].q_len, p.prob.segments[0].k_len = room - 40, room
+    check8(o, lse, p)
+    p.k_len[0] = -1
+    assert attend(lca, p)[2][0] == 6
+
+
+def test_a_captured_long_prompt(lca):
+    """One graph; its replays see other pages, lengths and queries."""
+    import torch
+
+    ps = [make8([(c, n)], 16, 8, 1, CAUSAL, seed=30 + c, device="cuda") for c, n in ((100, 700), (428, 400), (0, 800))]
+    n = max(p.kc.shape[0] for p in ps)
+    kc, vc = (torch.zeros(n, 16, 1, 128, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn) for _ in range(2))
+    ks, vs = (torch.zeros(n, 1, 16, dtype=torch.uint8, device="cuda") for _ in range(2))
+    table = torch.full((1, max(p.table.shape[1] for p in ps)), -1, dtype=torch.int32, device="cuda")
+    q = torch.zeros(800, 8, 128, dtype=torch.bfloat16, device="cuda")
+    qs, kl = (torch.zeros(m, dtype=torch.int32, device="cuda") for m in (2, 1))
+
+    def step():
+        return lca.attn_paged_fp8(q, kc, vc, ks, vs, table, qs, kl, CAUSAL)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o, lse = step()
+    for p in ps:
+        m, T = p.kc.shape[0], p.q.shape[0]
+        for to, of in ((kc, p.kc), (vc, p.vc)):
+            to.view(torch.uint8)[:m] = of.view(torch.uint8)
+        ks[:m], vs[:m] = p.ks, p.vs
+        table.fill_(-1)
+        table[:, :p.table.shape[1]] = p.table
+        q.zero_()
+        q[:T] = p.q
+        qs.copy_(p.q_start), kl.copy_(p.k_len)
+        graph.replay()
+        torch.cuda.synchronize()
+        check8(o[:T], lse[:, :T], p)
+        assert float(o[T:].abs().sum()) == 0 and bool(torch.isneginf(lse[:, T:]).all())
