@@ -780,27 +780,27 @@ def _attend(name, cache, tensors, dt, q, block_table, q_start, k_len, mask, scal
     dev = tensors[0].device
     shape, tp = _paged_shape(q, cache, tensors[0], block_table, scale, max_q_len, dt)
     md = _paged_mask(mask)
-    n_seq = shape.n_seq
-    qsp = _ptr(q_start, "q_start", torch.int32, (n_seq + 1,), dev)
-    klp = _ptr(k_len, "k_len", torch.int32, (n_seq,), dev)
+    size, i32 = q.shape, torch.int32
+    T, Hq, _ = size
+    n_seq, width = block_table.shape
+    qsp = _ptr(q_start, "q_start", i32, (n_seq + 1,), dev)
+    klp = _ptr(k_len, "k_len", i32, (n_seq,), dev)
     if ctx_len is not None and n_seq:
-        shape.ctx_len = _ptr(ctx_len, "ctx_len", torch.int32, (n_seq,), dev)
+        shape.ctx_len = _ptr(ctx_len, "ctx_len", i32, (n_seq,), dev)
     side = _side_stream(stream, dev)
-    size, lsize = q.shape, (shape.Hq, shape.Tq)
     if out is None:
         out = _empty(size, dt, dev, side)
         op = out.data_ptr()
     else:
         op = _ptr(out, "out", dt, size, dev)
     if lse is None:
-        lse = _empty(lsize, torch.float32, dev, side)
+        lse = _empty((Hq, T), torch.float32, dev, side)
         lp = lse.data_ptr()
     else:
-        lp = _ptr(lse, "lse", torch.float32, lsize, dev)
+        lp = _ptr(lse, "lse", torch.float32, (Hq, T), dev)
     if workspace is None:
         # the size depends on these alone
-        key = (name, shape.Tq, shape.Hq, n_seq, shape.max_q_len, cache.Hkv, min(cache.n_pages, 2), cache.page_stride,
-               cache.token_stride, cache.head_stride)
+        key = (name, T, Hq, n_seq, width, max_q_len, tensors[0].shape, tensors[0].stride())
         need = _SIZES.get(key)
         if need is None:
             if len(_SIZES) >= 4096:
@@ -808,7 +808,8 @@ def _attend(name, cache, tensors, dt, q, block_table, q_start, k_len, mask, scal
             need = _SIZES[key] = _paged_size(name, shape, cache, md)
         workspace = _empty((need,), torch.uint8, dev, side)
     else:
-        _ptr(workspace, "workspace", torch.uint8, (workspace.numel(),), dev)
+        need = workspace.numel()
+        _ptr(workspace, "workspace", torch.uint8, (need,), dev)
     if side is not None:
         for t in (q, *tensors, block_table, q_start, k_len, out, lse, workspace):
             t.record_stream(side)
@@ -816,7 +817,7 @@ def _attend(name, cache, tensors, dt, q, block_table, q_start, k_len, mask, scal
             ctx_len.record_stream(side)
     head = (q.data_ptr(),) if name == "lca_attn_paged" else (q.data_ptr(), _dtype_code(dt))
     _call(getattr(load(), name), name, dev, side, *head, C.byref(cache), tp, qsp, klp, op, lp, C.byref(shape), C.byref(md),
-          workspace.data_ptr(), workspace.numel())
+          workspace.data_ptr(), need)
     return out, lse
 
 

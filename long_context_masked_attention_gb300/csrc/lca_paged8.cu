@@ -119,8 +119,10 @@ __global__ void __launch_bounds__(256) paged_write8_kernel(const PagedWrite8Args
 // at a time, each thread kRows of them, so that their loads are under way at
 // once: 131K tokens of 8 heads 160 us one by one, 134 in fours, 150 in eights; and
 // stores of 32 bytes take it to 126 (6.4 TB/s, 0.94 of a copy's rate).
-template <typename T, int kRows>
-__global__ void __launch_bounds__(256) paged_read8_kernel(const PagedRead8Args a) {
+// page_of(i, first) is the page whose copy page i of the result is (first: one thread asks
+// so for each i); one that is none leaves it as it was.
+template <typename T, int kRows, typename Page>
+__device__ __forceinline__ void read_pages(const PagedRead8Args& a, Page page_of) {
   const unsigned rows = static_cast<unsigned>(a.page_size) * a.Hkv;  // of a page, below 2^31
   const unsigned parts = (rows + 32 * kRows - 1) / (32 * kRows);
   const long long n = static_cast<long long>(a.n) * parts;
@@ -129,15 +131,7 @@ __global__ void __launch_bounds__(256) paged_read8_kernel(const PagedRead8Args a
   for (long long b = blockIdx.x; b < n; b += gridDim.x) {
     const long long i = line_div(b, parts);
     const unsigned row0 = static_cast<unsigned>(b - i * parts) * (32 * kRows) + (threadIdx.x >> 3);
-    int page;
-    if (a.map) {
-      const long long seq = line_div(i, a.max_pages);
-      const int entry = static_cast<int>(i - seq * a.max_pages);
-      page = static_cast<long long>(entry) * a.page_size < __ldg(a.k_len + seq) ? __ldg(a.pages + seq * a.table_stride + entry) : -1;
-      if (b == i * parts && threadIdx.x == 0) a.map[i] = page >= 0 && page < a.n_pages ? static_cast<int>(i) : -1;
-    } else {
-      page = __ldg(a.pages + i);
-    }
+    const int page = page_of(i, b == i * parts && threadIdx.x == 0);
     if (page < 0 || page >= a.n_pages) continue;
     uint4 x[kRows], y[kRows];
     uint32_t bk[kRows], bv[kRows];
@@ -173,6 +167,29 @@ __global__ void __launch_bounds__(256) paged_read8_kernel(const PagedRead8Args a
       put(a.v + to[u], y[u], two_to(factor_of(bv[u])));
     }
   }
+}
+
+template <typename T, int kRows>
+__global__ void __launch_bounds__(256) paged_read8_kernel(const PagedRead8Args a) {
+  read_pages<T, kRows>(a, [&](long long i, bool) { return __ldg(a.pages + i); });
+}
+
+// The same for the block tables of a batch (their entries one after another are
+// the result's pages): of each request the pages with keys that some of its rows
+// attends.  map gets the result's tables, -1 for the others.
+template <typename T, int kRows>
+__global__ void __launch_bounds__(256)
+    paged_copy8_kernel(const __grid_constant__ PagedRead8Args a, const __grid_constant__ PagedAttnArgs m, int* map) {
+  read_pages<T, kRows>(a, [&](long long i, bool first) {
+    const long long seq = line_div(i, m.max_pages);
+    const int entry = static_cast<int>(i - seq * m.max_pages);
+    int page = -1;
+    const SegInfo sg = paged_seg(m, static_cast<int>(seq));
+    if (sg.q_len > 0 && span_hits(hull(m, sg.q_len, sg.k_len, 0, sg.q_len), entry * m.page_size, (entry + 1) * m.page_size))
+      page = __ldg(m.table + seq * m.table_stride + entry);
+    if (first) map[i] = page >= 0 && page < a.n_pages ? static_cast<int>(i) : -1;
+    return page;
+  });
 }
 
 // ------------------------------------------------------------------ attention, few rows
@@ -600,6 +617,16 @@ void launch_paged_write8(const PagedWrite8Args& a, bool fp16, int num_sms, cudaS
     write8<__half>(a, num_sms, st);
   else
     write8<__nv_bfloat16>(a, num_sms, st);
+}
+
+void launch_paged_copy8(const PagedRead8Args& a, const PagedAttnArgs& m, int* map, bool fp16, int num_sms, cudaStream_t st) {
+  const long long rows = static_cast<long long>(a.page_size) * a.Hkv;
+  const int grid = static_cast<int>(std::min<long long>(a.n * ((rows + 127) / 128), num_sms * 8LL));
+  note_launches(1);
+  if (fp16)
+    paged_copy8_kernel<__half, 4><<<grid, 256, 0, st>>>(a, m, map);
+  else
+    paged_copy8_kernel<__nv_bfloat16, 4><<<grid, 256, 0, st>>>(a, m, map);
 }
 
 template <typename T>

@@ -28,13 +28,6 @@ struct PagedRead8Args {
   long long out_page_stride, out_token_stride, out_head_stride;
   const int* pages;
   int n, n_pages, Hkv, page_size;
-  // Where `map` is given, `pages` are the rows of a block table, n in all, and
-  // those that hold one of a request's keys are read; map[i] becomes i, -1 for
-  // the others and for entries that are no page.
-  long long table_stride;
-  int max_pages;
-  const int* k_len;
-  int* map;
   bool token_first;  // tokens of a head lie closer together than its heads
   bool out_v8;       // every 16 values of the result start on a 32-byte boundary
 };
@@ -43,6 +36,10 @@ void launch_paged_read8(const PagedRead8Args& a, bool fp16, int num_sms, cudaStr
 // The maps of K and V have boxes of box_rows rows of 128 bytes.
 cudaError_t launch_paged_chunk8(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                                 const PagedAttnArgs& a, bool fp16, int num_sms, cudaStream_t st);
+// The pages that the batch m needs, of its tables, n = n_seq max_pages; map: its
+// tables over the copy.
+void launch_paged_copy8(const PagedRead8Args& a, const PagedAttnArgs& m, int* map, bool fp16, int num_sms, cudaStream_t st);
+
 // Attention over few rows, in items of `rows` of them (8, 16 or 32).
 constexpr int kPaged8MaxRows = 32;
 cudaError_t launch_paged_decode8(const PagedAttnArgs& a, int rows, bool behind, bool fp16, int num_sms, cudaStream_t st);

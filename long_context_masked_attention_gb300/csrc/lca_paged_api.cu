@@ -408,26 +408,30 @@ lca_status attend(const Cache& any, int dtype, const void* q, const int32_t* blo
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool fp16 = dtype == LCA_F16;
+  a.table_stride = shape->table_stride;
+  a.table = block_table;
+  a.q_start = q_start;
+  a.k_len = k_len;
+  a.ctx_len = shape->ctx_len;
+  a.Tq = shape->Tq;
+  a.n_seq = shape->n_seq;
+  a.max_pages = shape->max_pages;
+  a.page_size = cache->page_size;
   Cache run = any;
   lca_paged_cache copy{};
-  long long table_stride = shape->table_stride;
   if (L8.copies) {
     copy = copy_of(shape, cache, dtype, ws + L8.copy);
     PagedRead8Args c{};
     read_args(c8, &copy, c);
-    c.pages = block_table;
-    c.n = shape->n_seq * shape->max_pages;
-    c.table_stride = shape->table_stride;
-    c.max_pages = shape->max_pages;
-    c.k_len = k_len;
-    c.map = reinterpret_cast<int*>(ws + L8.map);
-    launch_paged_read8(c, fp16, sms, st);
+    c.n = copy.n_pages;
+    int* map = reinterpret_cast<int*>(ws + L8.map);
+    launch_paged_copy8(c, a, map, fp16, sms, st);
     LCA_CUDA(cudaGetLastError());
     run = {&copy, nullptr};
     cache = run.c;
     c8 = nullptr;
-    block_table = c.map;
-    table_stride = shape->max_pages;
+    a.table = map;
+    a.table_stride = shape->max_pages;
   }
   a.q = q;
   a.kc = cache->k;
@@ -442,24 +446,15 @@ lca_status attend(const Cache& any, int dtype, const void* q, const int32_t* blo
     a.scale_page_stride = c8->scale_page_stride;
     a.scale_head_stride = c8->scale_head_stride;
   }
-  a.table_stride = table_stride;
-  a.table = block_table;
-  a.q_start = q_start;
-  a.k_len = k_len;
-  a.ctx_len = shape->ctx_len;
   a.o = o;
   a.lse = lse;
   a.status = reinterpret_cast<int*>(ws + L.status);
   a.arrived = reinterpret_cast<int*>(ws + L.arrived);
   a.claims = a.arrived + kPagedMaxSpans;
   a.parts = reinterpret_cast<float*>(ws + L.parts);
-  a.Tq = shape->Tq;
   a.Hq = shape->Hq;
   a.Hkv = cache->Hkv;
   a.G = shape->Hq / cache->Hkv;
-  a.n_seq = shape->n_seq;
-  a.max_pages = shape->max_pages;
-  a.page_size = cache->page_size;
   a.n_pages = cache->n_pages;
   const float scale = shape->scale > 0.f ? shape->scale : 1.0f / std::sqrt(static_cast<float>(kHeadDim));
   a.scale_log2 = scale * 1.4426950408889634f;

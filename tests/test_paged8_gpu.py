@@ -801,6 +801,17 @@ def test_long_prompts(lca, layout, page, dtype):
         assert st == (0, 0)
 
 
+def test_long_prompts_over_tables_and_pages_of_several_widths(lca):
+    """Calls of the same rows whose workspaces differ, none of them given: wider tables, larger pages, a larger cache."""
+    for page, more in ((16, 0), (16, 40), (64, 0), (16, 200), (64, 30)):
+        import torch
+
+        p = make8([(300, 600)], page, 8, 1, CAUSAL, seed=9, device="cuda")
+        p.table = torch.nn.functional.pad(p.table, (0, more), value=-1)
+        o, lse = lca.attn_paged_fp8(p.q, p.kc, p.vc, p.ks, p.vs, p.table, p.q_start, p.k_len, CAUSAL)
+        check8(o, lse, p, what=f"{page}, {more}")
+
+
 @pytest.mark.parametrize("mask", MASKS, ids=lambda m: f"{m.kind}{m.window_left or ''}")
 def test_masks_of_long_prompts(lca, mask):
     p = make8([(300, 600), (0, 700)], 16, 8, 1, mask, seed=5, device="cuda")
@@ -902,3 +913,22 @@ def test_a_captured_long_prompt(lca):
         torch.cuda.synchronize()
         check8(o[:T], lse[:, :T], p)
         assert float(o[T:].abs().sum()) == 0 and bool(torch.isneginf(lse[:, T:]).all())
+
+
+def test_a_long_prompt_with_a_window_copies_what_it_needs(lca):
+    """500K cached tokens, most of them before the window, whose entries of the table are no page."""
+    import torch
+
+    page, Hkv, ctx, new = 64, 1, 500000, 600
+    mask = MaskSpec("CAUSAL_SLIDING", window_left=1000)
+    p = make8([(1400, new)], page, 8, Hkv, mask, seed=7, device="cuda")
+    ref = reference8(p)
+    o, lse, _ = attend(lca, p)
+    check8(o, lse, p, ref)
+    gone = (ctx - ctx % page - 1400 + 1400 % page) // page  # whole pages put before the request
+    table = torch.full((1, gone + p.table.shape[1]), -1, dtype=torch.int32, device="cuda")
+    table[:, gone:] = p.table
+    p.table, p.k_len = table, p.k_len + gone * page
+    o, lse, st = attend(lca, p)  # tiles of 128 keys may begin elsewhere, so other bits, within the same bounds
+    assert st == (0, 0)
+    check8(o, lse, p, ref)
