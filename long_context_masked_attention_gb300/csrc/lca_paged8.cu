@@ -213,8 +213,9 @@ __global__ void __launch_bounds__(256)
 //
 // Layout.  The keys are the rows of the products and the rows of q their
 // columns: S^T = K q^T and O^T = V^T w^T, m16n8k16.  So a tile of 8 rows wastes
-// nothing where 8 query heads share a KV head, 32 rows share what a key's
-// conversion costs, and the sums of a row of O are 16 values a lane.  The
+// nothing where 8 query heads share a KV head, and two of them share what a
+// key's conversion costs (four spill their sums: 32 rows took 260 us where the
+// kernel for many rows takes 194).  The
 // operands K and V^T come from shared memory by 16-byte loads and are converted in
 // registers.  The order of the 128 products of a score, and of the rows of O^T,
 // is free, so a lane takes the bytes that lie together: of keys lane / 4 and 8
@@ -591,9 +592,7 @@ cudaError_t launch_decode(const PagedAttnArgs& a, bool behind, int num_sms, cuda
 
 template <typename T>
 cudaError_t launch_decode_of(const PagedAttnArgs& a, int rows, bool behind, int num_sms, cudaStream_t st) {
-  if (rows <= 8) return launch_decode<T, 1>(a, behind, num_sms, st);
-  if (rows <= 16) return launch_decode<T, 2>(a, behind, num_sms, st);
-  return launch_decode<T, 4>(a, behind, num_sms, st);
+  return rows == 8 ? launch_decode<T, 1>(a, behind, num_sms, st) : launch_decode<T, 2>(a, behind, num_sms, st);
 }
 
 }  // namespace

@@ -40,8 +40,7 @@ cudaError_t launch_paged_chunk8(const CUtensorMap& tq, const CUtensorMap& tk, co
 // tables over the copy.
 void launch_paged_copy8(const PagedRead8Args& a, const PagedAttnArgs& m, int* map, bool fp16, int num_sms, cudaStream_t st);
 
-// Attention over few rows, in items of `rows` of them (8, 16 or 32).
-constexpr int kPaged8MaxRows = 32;
+// Attention over few rows, in items of `rows` of them (8 or 16).
 cudaError_t launch_paged_decode8(const PagedAttnArgs& a, int rows, bool behind, bool fp16, int num_sms, cudaStream_t st);
 
 }  // namespace lca

@@ -148,16 +148,15 @@ struct PagedLayout {
   int max_blocks = 0;
 };
 
-// Rows of an item of the kernel for few rows: a 16-bit cache's has 16; an
-// 8-bit one's 8, 16 or 32, by what the longest request has or, where that is not
-// known, a single token.
-int few_tile(const lca_paged_shape* sh, const lca_paged_cache* c, bool eight) {
-  if (!eight) return 16;
-  const long long G = sh->Hq / c->Hkv, rows = sh->max_q_len > 0 ? sh->max_q_len * G : G;
-  return rows <= 8 ? 8 : rows <= 16 ? 16 : kPaged8MaxRows;
+// Rows of an item of the kernel for few rows over an 8-bit cache (a 16-bit one's
+// has 16): 8 where that holds the longest request or, where that one goes to the
+// kernel for many rows or is not known, a single token.
+int few_tile(const lca_paged_shape* sh, const lca_paged_cache* c) {
+  const long long G = sh->Hq / c->Hkv, rows = sh->max_q_len * G;
+  return (rows > 0 && rows <= kPagedFewRows ? rows : G) <= 8 ? 8 : 16;
 }
 
-PagedLayout paged_layout(const lca_paged_shape* sh, const lca_paged_cache* c, bool eight) {
+PagedLayout paged_layout(const lca_paged_shape* sh, const lca_paged_cache* c) {
   PagedLayout L;
   size_t o = 0;
   auto take = [&](size_t bytes) {
@@ -167,9 +166,7 @@ PagedLayout paged_layout(const lca_paged_shape* sh, const lca_paged_cache* c, bo
   };
   L.status = take(16);
   L.arrived = take(sizeof(int) * (kPagedMaxSpans + 1));
-  // a workspace for an unknown longest request serves every hint
-  const int rows = eight && sh->max_q_len == 0 ? kPaged8MaxRows : few_tile(sh, c, eight);
-  L.parts = take(sizeof(float) * 2 * kPagedMaxSpans * rows * (kHeadDim + 2));
+  L.parts = take(sizeof(float) * 2 * kPagedMaxSpans * kPagedPartFloats);
   if (many_rows(sh, c)) {
     L.max_blocks = sh->Tq / (2 * tokens_per_tile(sh, c)) + sh->n_seq;
     L.block0 = take(sizeof(int) * (sh->n_seq + 1LL));
@@ -217,17 +214,17 @@ Layout8 layout8(const lca_paged_shape* sh, const lca_paged_cache* c) {
   Layout8 L;
   L.copies = copies(sh, c);
   if (!L.copies) {
-    L.run = paged_layout(sh, c, true);
+    L.run = paged_layout(sh, c);
     L.total = L.run.total;
     return L;
   }
   const lca_paged_cache v = copy_of(sh, c, LCA_BF16, nullptr);
-  L.run = paged_layout(sh, &v, false);
+  L.run = paged_layout(sh, &v);
   L.copy = L.run.total;
   L.map = align_up(L.copy + 2 * static_cast<size_t>(copy_bytes(sh, c)));
   L.total = align_up(L.map + sizeof(int) * sh->n_seq * static_cast<size_t>(sh->max_pages));
   // a shorter longest request may make it a call without a copy
-  const size_t other = paged_layout(sh, c, true).total;
+  const size_t other = paged_layout(sh, c).total;
   if (sh->max_q_len == 0 && other > L.total) L.total = other;
   return L;
 }
@@ -365,7 +362,7 @@ lca_status attend(const Cache& any, int dtype, const void* q, const int32_t* blo
   if (c8) {
     L8 = layout8(shape, cache);
   } else {
-    L8.run = paged_layout(shape, cache, false);
+    L8.run = paged_layout(shape, cache);
     L8.total = L8.run.total;
   }
   const PagedLayout& L = L8.run;
@@ -487,7 +484,7 @@ lca_status attend(const Cache& any, int dtype, const void* q, const int32_t* blo
   LCA_CUDA(launch_paged_begin(a, many, st));
   if (many) LCA_CUDA((c8 ? launch_paged_chunk8 : launch_paged_chunk)(tq, tk, tv, a, fp16, sms, st));
   if (shape->Tq > 0)
-    LCA_CUDA(c8 ? launch_paged_decode8(a, few_tile(shape, cache, true), many, fp16, sms, st)
+    LCA_CUDA(c8 ? launch_paged_decode8(a, few_tile(shape, cache), many, fp16, sms, st)
                 : launch_paged_decode(a, many, fp16, sms, st));
   if (many) LCA_CUDA(launch_paged_join(a, fp16, c8 != nullptr, sms, st));
   return LCA_OK;
@@ -657,7 +654,7 @@ lca_status lca_attn_paged_workspace_size(const lca_paged_shape* shape, const lca
   MaskCtx m;
   const lca_status r = check_attn(shape, cache, mask, m);
   if (r != LCA_OK) return r;
-  *bytes = paged_layout(shape, cache, false).total;
+  *bytes = paged_layout(shape, cache).total;
   return LCA_OK;
 }
 
