@@ -213,9 +213,10 @@ __global__ void __launch_bounds__(256)
 //
 // Layout.  The keys are the rows of the products and the rows of q their
 // columns: S^T = K q^T and O^T = V^T w^T, m16n8k16.  So a tile of 8 rows wastes
-// nothing where 8 query heads share a KV head, and two of them share what a
-// key's conversion costs (four spill their sums: 32 rows took 260 us where the
-// kernel for many rows takes 194).  The
+// nothing where 8 query heads share a KV head, and more of them share what a
+// key's conversion costs: 32 requests of 1K-16K keys take 99 us with 16 rows, 128
+// with 24, 160 with 32, where the kernel for many rows takes 194 (40 rows spill
+// their sums and take 300).  The
 // operands K and V^T come from shared memory by 16-byte loads and are converted in
 // registers.  The order of the 128 products of a score, and of the rows of O^T,
 // is free, so a lane takes the bytes that lie together: of keys lane / 4 and 8
@@ -242,6 +243,17 @@ __device__ __forceinline__ uint4 lds16(uint32_t addr) {
   uint4 r;
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(addr) : "memory");
   return r;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+  uint2 r;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(addr) : "memory");
+  return r;
+}
+__device__ __forceinline__ void sts64(uint32_t addr, uint32_t x, uint32_t y) {
+  asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(x), "r"(y) : "memory");
+}
+__device__ __forceinline__ void sts32(uint32_t addr, uint32_t x) {
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(x) : "memory");
 }
 __device__ __forceinline__ uint32_t lds_u8(uint32_t addr) {
   uint32_t r;
@@ -297,6 +309,11 @@ struct Worker8 {
   // 512K (8 heads) 193 -> 226 were its, in twice as many pieces; four 662 -> 651.
   static __device__ constexpr Claims claims() { return {64, 8, 1, 16}; }
   static constexpr int kWarpBytes = kWarp8 > kRows * 132 * 4 ? kWarp8 : kRows * 132 * 4;
+  // With many tiles q does not fit the registers: it lies in shared memory for all
+  // warps, and a unit's two steps of 16 keys go one after the other.
+  static constexpr bool kShareQ = kTiles > 2;
+  static constexpr int kSteps = kShareQ ? 1 : 2;
+  static constexpr int kQBytes = kShareQ ? kTiles * (8 * 32 * 8 + 8 * 4) : 0;  // and a factor per row
   static constexpr float kBias = 0.f;
   static __device__ __forceinline__ void run(const PagedAttnArgs& a, uint8_t* ring_, int seq, const Request& sg,
                                              const Units& un, int tile, int head, int u0, int n, float* m_out, float* l_out) {
@@ -373,16 +390,27 @@ struct Worker8 {
       }
       cp_async_commit();
     };
-    uint32_t q[kTiles][8][2];
-    float f[kTiles][2];  // scores of rows 8 t + 2 c and the next are that times the products with q's fp16 form
+    // q as B operands, and by what the products with a row's fp16 form give its scores
+    uint32_t q[kShareQ ? 1 : kTiles][8][2];
+    float f[kShareQ ? 1 : kTiles][2];
+    const uint32_t shared_q = ring + (kDecWarps - warp) * kWarpBytes;
+    const uint32_t shared_f = shared_q + kTiles * 8 * 32 * 8;
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) {
-      const int r = min(r_first + 8 * t + g, r_last);
-      const int e = load_q(static_cast<const T*>(a.q) + (sg.q_off + r / a.G) * a.q_stride + (head * a.G + r % a.G) * kHeadDim, c, q[t]);
+      if (kShareQ && t % kDecWarps != warp) continue;
+      const int r = min(r_first + 8 * t + g, r_last), at = kShareQ ? 0 : t;
+      const int e = load_q(static_cast<const T*>(a.q) + (sg.q_off + r / a.G) * a.q_stride + (head * a.G + r % a.G) * kHeadDim, c, q[at]);
       const float x = ldexpf(a.scale_log2, e);
-      f[t][0] = __shfl_sync(~0u, x, 8 * c);
-      f[t][1] = __shfl_sync(~0u, x, 8 * c + 4);
+      if constexpr (kShareQ) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sts64(shared_q + ((t * 8 + i) * 32 + lane) * 8, q[0][i][0], q[0][i][1]);
+        if (c == 0) sts32(shared_f + (8 * t + g) * 4, __float_as_uint(x));
+      } else {
+        f[at][0] = __shfl_sync(~0u, x, 8 * c);
+        f[at][1] = __shfl_sync(~0u, x, 8 * c + 4);
+      }
     }
+    if constexpr (kShareQ) __syncthreads();  // all warps have the same item
     float o[kTiles][8][4], m[kTiles][2], l[kTiles][2];
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) {
@@ -405,136 +433,160 @@ struct Worker8 {
       if (!span_hits(hl, j0, j0 + kKeys8)) continue;
       const uint32_t sk = ring + (u % kStages8) * kStage8, sv = sk + kSlice8, sf = sv + kSlice8;
       const bool part = !__all_sync(~0u, span_covers(own, j0, j0 + kKeys8));
-      // scores of keys 16 b + g (s[..][0], s[..][1]: the lane's two rows of a tile) and 16 b + g + 8
-      float s[2][kTiles][4];
+#pragma unroll 1
+      for (int b0 = 0; b0 < 2; b0 += kSteps) {
+        // scores of keys 16 b + g (s[..][0], s[..][1]: the lane's two rows of a tile) and 16 b + g + 8
+        float s[kSteps][kTiles][4];
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < kSteps; ++b)
 #pragma unroll
-        for (int t = 0; t < kTiles; ++t) s[b][t][0] = s[b][t][1] = s[b][t][2] = s[b][t][3] = 0.f;
+          for (int t = 0; t < kTiles; ++t) s[b][t][0] = s[b][t][1] = s[b][t][2] = s[b][t][3] = 0.f;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint4 x = lds16(sk + b * 2048 + (k_at ^ (h << 6))), y = lds16(sk + b * 2048 + 1024 + (k_at ^ (h << 6)));
+        for (int b = 0; b < kSteps; ++b)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t w[4] = {e4m3x2_to_f16x2(word(x, k)), e4m3x2_to_f16x2(word(y, k)), e4m3x2_hi_to_f16x2(word(x, k)),
-                                   e4m3x2_hi_to_f16x2(word(y, k))};
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t at = sk + (b0 + b) * 2048 + (k_at ^ (h << 6));
+            const uint4 x = lds16(at), y = lds16(at + 1024);
 #pragma unroll
-            for (int t = 0; t < kTiles; ++t) warp_mma(s[b][t], w, q[t][4 * h + k][0], q[t][4 * h + k][1], __half());
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t w[4] = {e4m3x2_to_f16x2(word(x, k)), e4m3x2_to_f16x2(word(y, k)), e4m3x2_hi_to_f16x2(word(x, k)),
+                                     e4m3x2_hi_to_f16x2(word(y, k))};
+#pragma unroll
+              for (int t = 0; t < kTiles; ++t) {
+                uint2 z;
+                if constexpr (kShareQ) {
+                  z = lds64(shared_q + ((t * 8 + 4 * h + k) * 32 + lane) * 8);
+                } else {
+                  z = make_uint2(q[t][4 * h + k][0], q[t][4 * h + k][1]);
+                }
+                warp_mma(s[b][t], w, z.x, z.y, __half());
+              }
+            }
           }
-        }
-      }
-      float vi[2][2];  // 2^-ev
+        float vi[kSteps][2];  // 2^-ev
 #pragma unroll
-      for (int b = 0; b < 2; ++b)
+        for (int b = 0; b < kSteps; ++b)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float fk = two_to(factor_of(lds_u8(sf + 16 * b + 8 * i + g)));
-          const int e = factor_of(lds_u8(sf + kKeys8 + 16 * b + 8 * i + g));
-          vi[b][i] = two_to(-e);
+          for (int i = 0; i < 2; ++i) {
+            const int key = 16 * (b0 + b) + 8 * i + g;
+            const float fk = two_to(factor_of(lds_u8(sf + key)));
+            const int e = factor_of(lds_u8(sf + kKeys8 + key));
+            vi[b][i] = two_to(-e);
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t) {
+              float2 ft;
+              if constexpr (kShareQ) {
+                const uint2 z = lds64(shared_f + (8 * t + 2 * c) * 4);
+                ft = make_float2(__uint_as_float(z.x), __uint_as_float(z.y));
+              } else {
+                ft = make_float2(f[t][0], f[t][1]);
+              }
+              s[b][t][2 * i] = fmaf(s[b][t][2 * i] * fk, ft.x, static_cast<float>(e));
+              s[b][t][2 * i + 1] = fmaf(s[b][t][2 * i + 1] * fk, ft.y, static_cast<float>(e));
+            }
+          }
+        if (part) {
 #pragma unroll
           for (int t = 0; t < kTiles; ++t)
 #pragma unroll
-            for (int r = 0; r < 2; ++r)
-              s[b][t][2 * i + r] = fmaf(s[b][t][2 * i + r] * fk, f[t][r], static_cast<float>(e));
-        }
-      if (part) {
+            for (int r = 0; r < 2; ++r) {
+              const Span sp = row_of(8 * t + 2 * c + r);
 #pragma unroll
-        for (int t = 0; t < kTiles; ++t)
+              for (int b = 0; b < kSteps; ++b)
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const Span sp = row_of(8 * t + 2 * c + r);
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-#pragma unroll
-              for (int i = 0; i < 2; ++i)
-                if (!in_span(sp, j0 + 16 * b + 8 * i + g)) s[b][t][2 * i + r] = -INFINITY;
-          }
-      }
-      float mx[kTiles][2];
-      bool up = false;
-#pragma unroll
-      for (int t = 0; t < kTiles; ++t)
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          mx[t][r] = fmaxf(fmaxf(s[0][t][r], s[0][t][2 + r]), fmaxf(s[1][t][r], s[1][t][2 + r]));
-#pragma unroll
-          for (int d = 4; d < 32; d <<= 1) mx[t][r] = fmaxf(mx[t][r], __shfl_xor_sync(~0u, mx[t][r], d));
-          up |= __fadd_ru(mx[t][r], -15.f) > m[t][r];
-        }
-      if (__any_sync(~0u, up)) {
-#pragma unroll
-        for (int t = 0; t < kTiles; ++t)
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const float to = __fadd_ru(mx[t][r], -12.f);
-            if (to > m[t][r]) {
-              const float x = ex2_approx(m[t][r] - to);
-              m[t][r] = to;
-              l[t][r] *= x;
-#pragma unroll
-              for (int i = 0; i < 8; ++i) o[t][i][r] *= x, o[t][i][2 + r] *= x;
+                for (int i = 0; i < 2; ++i)
+                  if (!in_span(sp, j0 + 16 * (b0 + b) + 8 * i + g)) s[b][t][2 * i + r] = -INFINITY;
             }
-          }
-      }
-      uint32_t p[2][kTiles][2];
+        }
+        auto most = [&](int t, int r) {  // of this lane's keys
+          float x = fmaxf(s[0][t][r], s[0][t][2 + r]);
+          if constexpr (kSteps == 2) x = fmaxf(x, fmaxf(s[1][t][r], s[1][t][2 + r]));
+          return x;
+        };
+        bool up = false;
 #pragma unroll
-      for (int t = 0; t < kTiles; ++t) {
-        const float b0 = m[t][0] == -INFINITY ? 0.f : m[t][0], b1 = m[t][1] == -INFINITY ? 0.f : m[t][1];
+        for (int t = 0; t < kTiles; ++t)
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
+          for (int r = 0; r < 2; ++r) up |= __fadd_ru(most(t, r), -15.f) > m[t][r];
+        if (__any_sync(~0u, up)) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float w0 = ex2_approx(s[b][t][2 * i] - b0), w1 = ex2_approx(s[b][t][2 * i + 1] - b1);
-            l[t][0] = fmaf(w0, vi[b][i], l[t][0]);
-            l[t][1] = fmaf(w1, vi[b][i], l[t][1]);
-            p[b][t][i] = transposed(Half2<__half>::pack(w0, w1));
-          }
-      }
+          for (int t = 0; t < kTiles; ++t)
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        // keys 2 c, 2 c + 1, 2 c + 8, 2 c + 9 of the step, columns 16 g to 16 g + 15
-        uint4 v[4];
+            for (int r = 0; r < 2; ++r) {
+              float to = most(t, r);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = lds16(sv + b * 2048 + (i >> 1) * 1024 + v_at[i & 1]);
-        if (part) {
-          // NaN in a key that some row does not attend must not meet a weight of
-          // 0: it is taken out, and added where the key is attended
-          uint32_t bad = 0;
+              for (int d = 4; d < 32; d <<= 1) to = fmaxf(to, __shfl_xor_sync(~0u, to, d));
+              to = __fadd_ru(to, -12.f);
+              if (to > m[t][r]) {
+                const float x = ex2_approx(m[t][r] - to);
+                m[t][r] = to;
+                l[t][r] *= x;
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < 8; ++i) o[t][i][r] *= x, o[t][i][2 + r] *= x;
+              }
+            }
+        }
+        uint32_t p[kSteps][kTiles][2];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) bad |= e4m3_nan(word(v[i], k));
-          if (__any_sync(~0u, bad)) {
+        for (int t = 0; t < kTiles; ++t) {
+          const float b0_ = m[t][0] == -INFINITY ? 0.f : m[t][0], b1_ = m[t][1] == -INFINITY ? 0.f : m[t][1];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) finite(v[i].x), finite(v[i].y), finite(v[i].z), finite(v[i].w);
-            // a positive weight times NaN is NaN, so no weight is needed
+          for (int b = 0; b < kSteps; ++b)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float w0 = ex2_approx(s[b][t][2 * i] - b0_), w1 = ex2_approx(s[b][t][2 * i + 1] - b1_);
+              l[t][0] = fmaf(w0, vi[b][i], l[t][0]);
+              l[t][1] = fmaf(w1, vi[b][i], l[t][1]);
+              p[b][t][i] = transposed(Half2<__half>::pack(w0, w1));
+            }
+        }
+#pragma unroll
+        for (int b = 0; b < kSteps; ++b) {
+          // keys 2 c, 2 c + 1, 2 c + 8, 2 c + 9 of the step, columns 16 g to 16 g + 15
+          const uint32_t sv_b = sv + (b0 + b) * 2048;
+          uint4 v[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = lds16(sv_b + (i >> 1) * 1024 + v_at[i & 1]);
+          if (part) {
+            // NaN in a key that some row does not attend must not meet a weight of
+            // 0: it is taken out, and added where the key is attended
+            uint32_t bad = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) bad |= e4m3_nan(word(v[i], k));
+            if (__any_sync(~0u, bad)) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) finite(v[i].x), finite(v[i].y), finite(v[i].z), finite(v[i].w);
+              // a positive weight times NaN is NaN, so no weight is needed
 #pragma unroll 1
-            for (int k = 0; k < 16; ++k) {
-              const uint4 x = lds16(sv + b * 2048 + k * 128 + ((g ^ swizzle8(k & 7)) << 4));
+              for (int k = 0; k < 16; ++k) {
+                const uint4 x = lds16(sv_b + k * 128 + ((g ^ swizzle8(k & 7)) << 4));
 #pragma unroll
-              for (int t = 0; t < kTiles; ++t)
+                for (int t = 0; t < kTiles; ++t)
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                  const Span sp = row_of(8 * t + 2 * c + r);
-                  if (!in_span(sp, j0 + 16 * b + k)) continue;
+                  for (int r = 0; r < 2; ++r) {
+                    const Span sp = row_of(8 * t + 2 * c + r);
+                    if (!in_span(sp, j0 + 16 * (b0 + b) + k)) continue;
 #pragma unroll
-                  for (int i = 0; i < 16; ++i)
-                    if ((e4m3_nan(word(x, i >> 2)) >> (8 * (i & 3) + 7)) & 1u) o[t][i >> 1][2 * (i & 1) + r] = __uint_as_float(0x7FC00000u);
-                }
+                    for (int i = 0; i < 16; ++i)
+                      if ((e4m3_nan(word(x, i >> 2)) >> (8 * (i & 3) + 7)) & 1u) o[t][i >> 1][2 * (i & 1) + r] = __uint_as_float(0x7FC00000u);
+                  }
+              }
             }
           }
-        }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          // (column 4 k, 4 k + 1) of two keys each, then (4 k + 2, 4 k + 3)
-          const uint32_t x0 = __byte_perm(word(v[0], k), word(v[1], k), 0x5140), x1 = __byte_perm(word(v[0], k), word(v[1], k), 0x7362);
-          const uint32_t y0 = __byte_perm(word(v[2], k), word(v[3], k), 0x5140), y1 = __byte_perm(word(v[2], k), word(v[3], k), 0x7362);
-          const uint32_t w0[4] = {e4m3x2_to_f16x2(x0), e4m3x2_hi_to_f16x2(x0), e4m3x2_to_f16x2(y0), e4m3x2_hi_to_f16x2(y0)};
-          const uint32_t w1[4] = {e4m3x2_to_f16x2(x1), e4m3x2_hi_to_f16x2(x1), e4m3x2_to_f16x2(y1), e4m3x2_hi_to_f16x2(y1)};
+          for (int k = 0; k < 4; ++k) {
+            // (column 4 k, 4 k + 1) of two keys each, then (4 k + 2, 4 k + 3)
+            const uint32_t x0 = __byte_perm(word(v[0], k), word(v[1], k), 0x5140), x1 = __byte_perm(word(v[0], k), word(v[1], k), 0x7362);
+            const uint32_t y0 = __byte_perm(word(v[2], k), word(v[3], k), 0x5140), y1 = __byte_perm(word(v[2], k), word(v[3], k), 0x7362);
+            const uint32_t w0[4] = {e4m3x2_to_f16x2(x0), e4m3x2_hi_to_f16x2(x0), e4m3x2_to_f16x2(y0), e4m3x2_hi_to_f16x2(y0)};
+            const uint32_t w1[4] = {e4m3x2_to_f16x2(x1), e4m3x2_hi_to_f16x2(x1), e4m3x2_to_f16x2(y1), e4m3x2_hi_to_f16x2(y1)};
 #pragma unroll
-          for (int t = 0; t < kTiles; ++t) {
-            warp_mma(o[t][2 * k], w0, p[b][t][0], p[b][t][1], __half());
-            warp_mma(o[t][2 * k + 1], w1, p[b][t][0], p[b][t][1], __half());
+            for (int t = 0; t < kTiles; ++t) {
+              warp_mma(o[t][2 * k], w0, p[b][t][0], p[b][t][1], __half());
+              warp_mma(o[t][2 * k + 1], w1, p[b][t][0], p[b][t][1], __half());
+            }
           }
         }
       }
@@ -581,7 +633,7 @@ __global__ void __launch_bounds__(kDecThreads, kPerSm<kTiles>)
 
 template <typename T, int kTiles>
 cudaError_t launch_decode(const PagedAttnArgs& a, bool behind, int num_sms, cudaStream_t st) {
-  constexpr int kBytes = kDecWarps * Worker8<T, kTiles>::kWarpBytes;
+  constexpr int kBytes = kDecWarps * Worker8<T, kTiles>::kWarpBytes + Worker8<T, kTiles>::kQBytes;
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = allow_smem(paged_decode8_kernel<T, kTiles>, kBytes, done);
   if (e != cudaSuccess) return e;
@@ -592,7 +644,10 @@ cudaError_t launch_decode(const PagedAttnArgs& a, bool behind, int num_sms, cuda
 
 template <typename T>
 cudaError_t launch_decode_of(const PagedAttnArgs& a, int rows, bool behind, int num_sms, cudaStream_t st) {
-  return rows == 8 ? launch_decode<T, 1>(a, behind, num_sms, st) : launch_decode<T, 2>(a, behind, num_sms, st);
+  if (rows == 8) return launch_decode<T, 1>(a, behind, num_sms, st);
+  if (rows == 16) return launch_decode<T, 2>(a, behind, num_sms, st);
+  if (rows == 24) return launch_decode<T, 3>(a, behind, num_sms, st);
+  return launch_decode<T, 4>(a, behind, num_sms, st);
 }
 
 }  // namespace

@@ -40,7 +40,9 @@ cudaError_t launch_paged_chunk8(const CUtensorMap& tq, const CUtensorMap& tk, co
 // tables over the copy.
 void launch_paged_copy8(const PagedRead8Args& a, const PagedAttnArgs& m, int* map, bool fp16, int num_sms, cudaStream_t st);
 
-// Attention over few rows, in items of `rows` of them (8 or 16).
+// Attention over few rows, in items of `rows` of them, a multiple of 8.
+// Where no request has more than these, the call needs no kernel for many rows.
+constexpr int kPaged8FewRows = 32;
 cudaError_t launch_paged_decode8(const PagedAttnArgs& a, int rows, bool behind, bool fp16, int num_sms, cudaStream_t st);
 
 }  // namespace lca

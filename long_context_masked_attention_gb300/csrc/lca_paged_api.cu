@@ -3,6 +3,7 @@
 // launches.  Nothing here allocates or throws.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdio>
 
@@ -135,10 +136,12 @@ MapStrides map_strides(const lca_paged_cache* c) {
 // at 32K, 64 heads on 8, take 14.7 ms with heads or tokens as the outermost
 // axis and 1.50 with pages; 512 at 8K with one group of 136 heads 2.06 ms, of
 // 128 heads 0.22.
-bool many_rows(const lca_paged_shape* sh, const lca_paged_cache* c) {
-  const long long G = sh->Hq / c->Hkv;
-  const long long most = sh->max_q_len > 0 && sh->max_q_len < sh->Tq ? sh->max_q_len : sh->Tq;
-  return most * G > kPagedFewRows && G <= kTile && c->n_pages > 0 && map_strides(c).ordered;
+long long most_rows(const lca_paged_shape* sh, const lca_paged_cache* c) {  // of a request and KV head
+  return static_cast<long long>(sh->max_q_len > 0 && sh->max_q_len < sh->Tq ? sh->max_q_len : sh->Tq) * (sh->Hq / c->Hkv);
+}
+bool many_rows(const lca_paged_shape* sh, const lca_paged_cache* c, bool eight) {
+  return most_rows(sh, c) > (eight ? kPaged8FewRows : kPagedFewRows) && sh->Hq / c->Hkv <= kTile && c->n_pages > 0 &&
+         map_strides(c).ordered;
 }
 
 int tokens_per_tile(const lca_paged_shape* sh, const lca_paged_cache* c) { return kTile / (sh->Hq / c->Hkv); }
@@ -149,14 +152,14 @@ struct PagedLayout {
 };
 
 // Rows of an item of the kernel for few rows over an 8-bit cache (a 16-bit one's
-// has 16): 8 where that holds the longest request or, where that one goes to the
-// kernel for many rows or is not known, a single token.
+// has 16): as many as the longest request has, or a single token where that one
+// goes to the kernel for many rows.
 int few_tile(const lca_paged_shape* sh, const lca_paged_cache* c) {
-  const long long G = sh->Hq / c->Hkv, rows = sh->max_q_len * G;
-  return (rows > 0 && rows <= kPagedFewRows ? rows : G) <= 8 ? 8 : 16;
+  const long long rows = many_rows(sh, c, true) ? std::min<long long>(sh->Hq / c->Hkv, kPagedFewRows) : most_rows(sh, c);
+  return static_cast<int>(rows >= kPaged8FewRows ? kPaged8FewRows : rows <= 8 ? 8 : (rows + 7) / 8 * 8);
 }
 
-PagedLayout paged_layout(const lca_paged_shape* sh, const lca_paged_cache* c) {
+PagedLayout paged_layout(const lca_paged_shape* sh, const lca_paged_cache* c, bool eight) {
   PagedLayout L;
   size_t o = 0;
   auto take = [&](size_t bytes) {
@@ -166,8 +169,9 @@ PagedLayout paged_layout(const lca_paged_shape* sh, const lca_paged_cache* c) {
   };
   L.status = take(16);
   L.arrived = take(sizeof(int) * (kPagedMaxSpans + 1));
-  L.parts = take(sizeof(float) * 2 * kPagedMaxSpans * kPagedPartFloats);
-  if (many_rows(sh, c)) {
+  const int rows = eight ? few_tile(sh, c) : 16;
+  L.parts = take(sizeof(float) * 2 * kPagedMaxSpans * rows * (kHeadDim + 2));
+  if (many_rows(sh, c, eight)) {
     L.max_blocks = sh->Tq / (2 * tokens_per_tile(sh, c)) + sh->n_seq;
     L.block0 = take(sizeof(int) * (sh->n_seq + 1LL));
     L.line = take(sizeof(long long) * (L.max_blocks + 1LL));
@@ -214,17 +218,17 @@ Layout8 layout8(const lca_paged_shape* sh, const lca_paged_cache* c) {
   Layout8 L;
   L.copies = copies(sh, c);
   if (!L.copies) {
-    L.run = paged_layout(sh, c);
+    L.run = paged_layout(sh, c, true);
     L.total = L.run.total;
     return L;
   }
   const lca_paged_cache v = copy_of(sh, c, LCA_BF16, nullptr);
-  L.run = paged_layout(sh, &v);
+  L.run = paged_layout(sh, &v, false);
   L.copy = L.run.total;
   L.map = align_up(L.copy + 2 * static_cast<size_t>(copy_bytes(sh, c)));
   L.total = align_up(L.map + sizeof(int) * sh->n_seq * static_cast<size_t>(sh->max_pages));
   // a shorter longest request may make it a call without a copy
-  const size_t other = paged_layout(sh, c).total;
+  const size_t other = paged_layout(sh, c, true).total;
   if (sh->max_q_len == 0 && other > L.total) L.total = other;
   return L;
 }
@@ -362,7 +366,7 @@ lca_status attend(const Cache& any, int dtype, const void* q, const int32_t* blo
   if (c8) {
     L8 = layout8(shape, cache);
   } else {
-    L8.run = paged_layout(shape, cache);
+    L8.run = paged_layout(shape, cache, false);
     L8.total = L8.run.total;
   }
   const PagedLayout& L = L8.run;
@@ -459,7 +463,7 @@ lca_status attend(const Cache& any, int dtype, const void* q, const int32_t* blo
     a.kc = a.vc = q;
     a.ks = a.vs = static_cast<const uint8_t*>(q);
   }
-  const bool many = many_rows(shape, cache) && shape->n_seq > 0;
+  const bool many = many_rows(shape, cache, c8 != nullptr) && shape->n_seq > 0;
   a.few = many ? kPagedFewRows : 0x7FFFFFFF;
   CUtensorMap tq, tk, tv;
   if (many) {
@@ -654,7 +658,7 @@ lca_status lca_attn_paged_workspace_size(const lca_paged_shape* shape, const lca
   MaskCtx m;
   const lca_status r = check_attn(shape, cache, mask, m);
   if (r != LCA_OK) return r;
-  *bytes = paged_layout(shape, cache).total;
+  *bytes = paged_layout(shape, cache, false).total;
   return LCA_OK;
 }
 

@@ -215,7 +215,8 @@ template <typename W>
 __device__ __forceinline__ void decode_span(const PagedAttnArgs& a, DecodeShared<W::kRows>& sh, uint8_t* ring, bool behind) {
   using T = typename W::Out;
   constexpr int kRows = W::kRows, kPartFloats = kRows * (kHeadDim + 2);
-  constexpr int kCols = kRows;  // columns of a row per thread: 128 threads, kRows x 128 values
+  constexpr int kAtOnce = kRows < 16 ? kRows : 16;  // rows that the CTA's threads take at a time,
+  constexpr int kCols = kAtOnce;                    // so many columns each
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   // requests whose rows do not overlap make fewer than 2^52 units; a q_start
   // that lets them overlap may make more, and is reported and not served then
@@ -277,34 +278,39 @@ __device__ __forceinline__ void decode_span(const PagedAttnArgs& a, DecodeShared
     W::run(a, ring + warp * W::kWarpBytes, seq, sg, un, tile, head, u0, un.n0 + un.n1 > 0 ? n : 0, sh.m[warp],
            sh.l[warp]);
     __syncthreads();
-    constexpr int kPer = kDecThreads / kRows;  // threads per row
-    const int row = tid / kPer, col = tid % kPer * kCols;
-    // the four warps' sums of row `row`, columns col .. col + kCols - 1
-    float m = -INFINITY, l = 0.f, x[kCols] = {};
-#pragma unroll
-    for (int w = 0; w < kDecWarps; ++w) m = fmaxf(m, sh.m[w][row]);
-#pragma unroll
-    for (int w = 0; w < kDecWarps; ++w) {
-      const float f = sh.l[w][row] != 0.f ? ex2_approx(sh.m[w][row] - m) : 0.f;
-      l = fmaf(f, sh.l[w][row], l);
-      const float* pw = reinterpret_cast<const float*>(ring + w * W::kWarpBytes) + row * 132 + col;
-#pragma unroll
-      for (int k = 0; k < kCols / 4; ++k) {
-        const float4 y = *reinterpret_cast<const float4*>(pw + 4 * k);
-        x[4 * k] = fmaf(f, y.x, x[4 * k]);
-        x[4 * k + 1] = fmaf(f, y.y, x[4 * k + 1]);
-        x[4 * k + 2] = fmaf(f, y.z, x[4 * k + 2]);
-        x[4 * k + 3] = fmaf(f, y.w, x[4 * k + 3]);
-      }
-    }
-    if (n < nu) {
+    const bool cut = n < nu;
+    int c0 = 0, c1 = 0, late = 0;
+    if (cut) {
       // first and last span of the item; span c's first piece is in slot 2 c
       // and a later, unfinished one in slot 2 c + 1
-      const int c0 = sp.of(i0), c1 = sp.of(i0 + nu - 1);
-      const int late = sp.start(c0) < i0 - kItemUnits ? 1 : 0;
-      auto slot = [&](int c) { return a.parts + (2 * c + (c == c0 ? late : 0)) * static_cast<long long>(kPartFloats); };
-      float* part = slot(span);
-      if (row < rows) {
+      c0 = sp.of(i0), c1 = sp.of(i0 + nu - 1);
+      late = sp.start(c0) < i0 - kItemUnits ? 1 : 0;
+    }
+    auto slot = [&](int c) { return a.parts + (2 * c + (c == c0 ? late : 0)) * static_cast<long long>(kPartFloats); };
+    constexpr int kPer = kDecThreads / kAtOnce;  // threads per row
+    const int col = tid % kPer * kCols;
+#pragma unroll 1
+    for (int row = tid / kPer; row < rows; row += kAtOnce) {
+      // the four warps' sums of row `row`, columns col .. col + kCols - 1
+      float m = -INFINITY, l = 0.f, x[kCols] = {};
+#pragma unroll
+      for (int w = 0; w < kDecWarps; ++w) m = fmaxf(m, sh.m[w][row]);
+#pragma unroll
+      for (int w = 0; w < kDecWarps; ++w) {
+        const float f = sh.l[w][row] != 0.f ? ex2_approx(sh.m[w][row] - m) : 0.f;
+        l = fmaf(f, sh.l[w][row], l);
+        const float* pw = reinterpret_cast<const float*>(ring + w * W::kWarpBytes) + row * 132 + col;
+#pragma unroll
+        for (int k = 0; k < kCols / 4; ++k) {
+          const float4 y = *reinterpret_cast<const float4*>(pw + 4 * k);
+          x[4 * k] = fmaf(f, y.x, x[4 * k]);
+          x[4 * k + 1] = fmaf(f, y.y, x[4 * k + 1]);
+          x[4 * k + 2] = fmaf(f, y.z, x[4 * k + 2]);
+          x[4 * k + 3] = fmaf(f, y.w, x[4 * k + 3]);
+        }
+      }
+      if (cut) {
+        float* part = slot(span);
 #pragma unroll
         for (int k = 0; k < kCols / 4; ++k)
           __stcg(reinterpret_cast<float4*>(part + row * kHeadDim + col) + k,
@@ -313,7 +319,20 @@ __device__ __forceinline__ void decode_span(const PagedAttnArgs& a, DecodeShared
           __stcg(part + kRows * kHeadDim + row, m);
           __stcg(part + kRows * kHeadDim + kRows + row, l);
         }
+      } else {
+        const float inv = l == 0.f ? 0.f : 1.f / l;  // a NaN stays one
+#pragma unroll
+        for (int k = 0; k < kCols; ++k) x[k] *= inv;
+        const long long r = static_cast<long long>(tile) * kRows + row;
+        const long long token = sg.q_off + r / a.G;
+        const int h = head * a.G + static_cast<int>(r % a.G);
+        st_row(static_cast<T*>(a.o) + (token * a.Hq + h) * kHeadDim + col, x);
+        if (tid % kPer == 0)
+          a.lse[static_cast<long long>(h) * a.Tq + token] =
+              l == 0.f ? -INFINITY : (m + log2f(l) - W::kBias) * 0.6931471805599453f;
       }
+    }
+    if (cut) {
       __syncthreads();
       if (tid == 0) {  // its fences cover what the barrier has ordered before and after them
         __threadfence();
@@ -322,13 +341,10 @@ __device__ __forceinline__ void decode_span(const PagedAttnArgs& a, DecodeShared
       }
       __syncthreads();
       if (sh.last) {
-        auto piece = [&](int k) {
-          return a.parts + (2 * (c0 + k) + (k == 0 ? late : 0)) * static_cast<long long>(kPartFloats);
-        };
 #pragma unroll 1
         for (int i = 2 * warp; i < rows; i += 2 * kDecWarps) {
           float mr, lr, y[2][4];
-          join_rows<kRows, 2, 8>(c1 - c0 + 1, piece, i, mr, lr, y);
+          join_rows<kRows, 2, 8>(c1 - c0 + 1, [&](int k) { return slot(c0 + k); }, i, mr, lr, y);
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const float mk = __shfl_sync(~0u, mr, 16 * k), lk = __shfl_sync(~0u, lr, 16 * k);
@@ -346,17 +362,6 @@ __device__ __forceinline__ void decode_span(const PagedAttnArgs& a, DecodeShared
           }
         }
       }
-    } else if (row < rows) {
-      const float inv = l == 0.f ? 0.f : 1.f / l;  // a NaN stays one
-#pragma unroll
-      for (int k = 0; k < kCols; ++k) x[k] *= inv;
-      const long long r = static_cast<long long>(tile) * kRows + row;
-      const long long token = sg.q_off + r / a.G;
-      const int h = head * a.G + static_cast<int>(r % a.G);
-      st_row(static_cast<T*>(a.o) + (token * a.Hq + h) * kHeadDim + col, x);
-      if (tid % kPer == 0)
-        a.lse[static_cast<long long>(h) * a.Tq + token] =
-            l == 0.f ? -INFINITY : (m + log2f(l) - W::kBias) * 0.6931471805599453f;
     }
     __syncthreads();  // the ring is refilled
   }

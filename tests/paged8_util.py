@@ -100,6 +100,8 @@ def reference8(p: Paged8):
       weights   are rounded to 2^-11 or the type's u, whichever is more in the kernel that serves the row, and lose
                 2^-37 of the largest weight: times 448 2^ev and against a sum that has the largest key's weight (its
                 row's largest value at least 224 2^ev, or a row of zeros), 2^-36 of the largest |v| for each key
+      O         in fp16 a result below 2^-14 is rounded to a multiple of 2^-24, off by 2^-25 however small it is, so u |O|
+                alone does not hold its own rounding
       LSE       the maximum and the logarithm of the sum, each at most |LSE| + 34 + B, cancel: 4 e of both"""
     import torch
 
@@ -120,7 +122,7 @@ def reference8(p: Paged8):
         B = qn[r] * kn * p.prob.softmax_scale
         sc = 130 * e * B + 3 * e * (34 + B)
         n = (s.k_len + 16) * e
-        tol_o[r] = u * np.abs(O[r]) + A[r] * (u + 2 * (sc + n))[:, :, None] * (1 + u) + (s.k_len * 2.0 ** -36 * vm)[None, :, None] + 1e-30
+        tol_o[r] = u * np.abs(O[r]) + A[r] * (u + 2 * (sc + n))[:, :, None] * (1 + u) + (s.k_len * 2.0 ** -36 * vm)[None, :, None] + (2.0 ** -25 if u == 2.0 ** -11 else 1e-30)
         fin = np.isfinite(L[:, r])
         tol_l[:, r] = np.where(fin, sc.T + n + 4 * e * (2 * np.abs(np.where(fin, L[:, r], 0)) + 68 + 2 * B.T), 0)
     return O, L, tol_o, tol_l

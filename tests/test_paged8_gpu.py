@@ -932,3 +932,38 @@ def test_a_long_prompt_with_a_window_copies_what_it_needs(lca):
     o, lse, st = attend(lca, p)  # tiles of 128 keys may begin elsewhere, so other bits, within the same bounds
     assert st == (0, 0)
     check8(o, lse, p, ref)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("Hq,Hkv,new", [(8, 1, 1), (8, 2, 3), (8, 1, 2), (8, 1, 3), (12, 2, 4), (8, 1, 4), (3, 1, 7), (1, 1, 31), (32, 1, 1),
+                                        (5, 1, 5), (28, 4, 4)])
+def test_tiles_of_every_size(lca, Hq, Hkv, new, dtype):
+    """Drafts of up to 32 rows per KV head, which one kernel serves in tiles of 8 to 32, beside shorter requests, and
+    with hints that are larger than needed."""
+    lens = [(700, new), (0, new), (33, 1), (5, 0), (1290, new), (64, max(1, new - 1))]
+    for mask in (CAUSAL, MaskSpec("CAUSAL_SLIDING", window_left=50), MaskSpec("GLOBAL_SLIDING", window_left=70, window_right=0, num_global=5)):
+        p = make8(lens, 24, Hq, Hkv, mask, dtype, pad=3, seed=new, device="cuda")
+        ref = reference8(p)
+        for hint in (new, 0, 400):
+            o, lse, st = attend(lca, p, max_q_len=hint)
+            check8(o, lse, p, ref, what=f"{mask.kind}, max_q_len={hint}")
+            assert st == (0, 0)
+
+
+@pytest.mark.parametrize("new", [2, 3, 4])
+def test_nan_in_drafts(lca, new):
+    """Every tile size: a NaN in the values of the drafts' own keys reaches the rows at and after it."""
+    import torch
+
+    p = make8([(600, new), (30, new)], 16, 8, 1, CAUSAL, seed=new, device="cuda")
+    o0, lse0, _ = attend(lca, p, max_q_len=new)
+    check8(o0, lse0, p)
+    for i, c in enumerate((600, 30)):
+        j = c + 1
+        p.vc.view(torch.uint8)[int(p.table[i, j // 16]), j % 16, 0, 40] = 0xFF
+    o, lse, st = attend(lca, p, max_q_len=new)
+    assert st == (0, 0) and torch.equal(lse, lse0)
+    hit = torch.tensor([t >= 1 for _ in range(2) for t in range(new)], device="cuda")
+    assert bool(o[hit][:, :, 40].isnan().all()) and bool(o[~hit].isfinite().all())
+    o[hit, :, 40] = o0[hit, :, 40]
+    assert torch.equal(o, o0)
