@@ -52,6 +52,23 @@ __device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
   return r;
 }
 
+// Two fp16 values as e4m3, likewise.
+__device__ __forceinline__ uint32_t f16x2_to_e4m3x2(uint32_t x) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 p;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 p, %1;\n\t"
+      "cvt.u32.u16 %0, p;\n\t}"
+      : "=r"(r)
+      : "r"(x));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 // Four e4m3 values times 2^e as two pairs of T.  In bf16 the product is exact;
 // in fp16 it is rounded and ends at the type's largest.
 template <typename T>

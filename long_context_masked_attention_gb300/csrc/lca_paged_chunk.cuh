@@ -448,10 +448,12 @@ __device__ __forceinline__ void producer(const PagedAttnArgs& a, const CUtensorM
 
 // ------------------------------------------------------------------ converters
 // An 8-bit cache: the four last warps make the tiles that the products read, in
-// fp16, which holds e4m3 exactly.  What this costs in instructions decides (a
+// fp16, which holds e4m3 exactly.  What this costs in instructions decides: a
 // product with the row's factor in 32 bits and a rounding to bf16 took a chunk of
-// 2048 tokens at 32K keys 2555 us, a conversion and a product of pairs takes
-// TODO), so factors are made to fit fp16: those of a tile are relative to the
+// 2048 tokens at 32K keys 2555 us, a conversion and a product of pairs takes 1875
+// (with a 16-bit cache the tensor pipe and power take 1510; here it is the softmax
+// warps that are slowed, by four more warps and 128 registers a thread).  So factors
+// are made to fit fp16: those of a tile are relative to the
 // largest of its attended keys' (which becomes 2^7, so that values end below
 // 2^16), and the softmax warps learn it from `exps`.  A row whose factor is less
 // than 2^-22 of the largest in its tile loses bits, 2^-24 of a value that is at
@@ -459,17 +461,12 @@ __device__ __forceinline__ void producer(const PagedAttnArgs& a, const CUtensorM
 // two that brings its largest value to 2^14 (see lca_paged8.cu).
 //
 // A thread has one key's row of a tile, 128 bytes, pieces swizzled on both sides
-// so that eight rows meet in no bank.
+// so that eight rows meet in no bank, half of it at a time in a short loop (a whole
+// row unrolled 1916 us: instructions come too late).
 __device__ __forceinline__ uint32_t half_power(int e) {  // 2^e twice in fp16, e <= 15; 0 below 2^-24
   const uint32_t h = e >= -14 ? static_cast<uint32_t>(e + 15) << 10 : e >= -24 ? 1u << (e + 24) : 0u;
   return h | h << 16;
 }
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-
 // By 32-bit addresses: through a pointer whose memory the compiler does not
 // know these would be generic loads and stores.
 __device__ __forceinline__ uint4 lds128(uint32_t at) {
