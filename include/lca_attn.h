@@ -268,7 +268,8 @@ typedef struct {
 } lca_rope_desc;
 
 /* Rows of heads * d dense elements, strides apart (multiples of 8 elements, at
- * least heads * d).  y is written; y = x with the same stride turns in place. */
+ * least heads * d).  y is written; y = x with the same stride turns in place.
+ * q and k have fewer than 2^24 heads together (LCA_ERR_UNSUPPORTED). */
 typedef struct {
   const void* x;
   void* y;
@@ -462,8 +463,8 @@ LCA_API lca_status lca_attn_paged_workspace_size(const lca_paged_shape* shape, c
  * h * head_stride of k and of v, and a byte at p * scale_page_stride + h *
  * scale_head_stride + t of k_scale and of v_scale.  Strides of values are
  * multiples of 16, those of scales of 8, all 8 to 2^38; k and v are
- * 16-byte, the scales 8-byte aligned.  Otherwise as lca_paged_cache, whose
- * lca_paged_plan serves both. */
+ * 16-byte, the scales 8-byte aligned; Hkv is below 2^24 (LCA_ERR_UNSUPPORTED).
+ * Otherwise as lca_paged_cache, whose lca_paged_plan serves both. */
 #define LCA_FP8_SCALE_MIN 79  /* 2^-48 */
 #define LCA_FP8_SCALE_MAX 175 /* 2^48 */
 typedef struct {
@@ -496,22 +497,34 @@ LCA_API lca_status lca_paged_write_fp8(const void* k, const void* v, int64_t k_s
  * and out is their cache for lca_attn_paged with the table 0, 1, 2, ...; an
  * out of token stride Hkv * d, head stride d is rows of packed keys for
  * lca_attn_fwd (which multiplies what lies behind a segment's last key by 0:
- * slots that were never written must hold no NaN for it).  pages: int32, device.  out must not overlap the cache or
- * pages (LCA_ERR_INVALID_ARG). */
+ * slots that were never written must hold no NaN for it).  pages: int32,
+ * device.  out must not overlap the cache or pages (LCA_ERR_INVALID_ARG).
+ * page_size * Hkv is below 2^31 - 256 (LCA_ERR_UNSUPPORTED). */
 LCA_API lca_status lca_paged_read_fp8(const lca_paged_cache_fp8* cache, const int32_t* pages, int32_t n,
                                       const lca_paged_cache* out, void* stream);
 
 /* lca_attn_paged over such a cache: the same arguments, masks, reports and
- * rules, with q and o of the given lca_dtype.  Scores are those of the values
- * that the cache stands for.  Weights are rounded to 16 bits before their
- * product with V: for requests with few rows (lca_attn_paged's) to 11 bits
- * times their row's factor, so that a key whose weight times factor is below
- * 2^-36 of the largest may count as 0; for the others to dtype's as in
- * lca_attn_paged.  NaN in the values of a key as there. */
+ * rules, with q and o of the given lca_dtype; Hq is below 2^24.  Scores are those
+ * of the values that the cache stands for.  A request's new tokens times Hq / Hkv
+ * are its rows per KV head, and how weights are rounded before their product with
+ * V depends on them and on the batch:
+ *  * where no request can have more than 32 (max_q_len, or Tq), and in other
+ *    batches for those of at most 16: to 11 bits times their key's factor; a key
+ *    whose weight times factor is below 2^-36 of the largest may count as 0.
+ *  * otherwise to 11 bits too, and the factors of V are taken relative to the
+ *    largest among 128 keys that lie together: what a key adds below 2^-22 of
+ *    what that one could loses bits.
+ *  * where requests have 4096 rows and more on average (max_q_len or Tq /
+ *    n_seq), and the tables' entries, all of them, are 1 GiB as 16-bit K and V at
+ *    most: the pages that rows attend are read back (lca_paged_read_fp8, fp16
+ *    ends at 65504) into the workspace first, and weights are rounded to dtype.
+ *    A workspace may so need up to 1 GiB more.
+ * NaN in the values of a key as in lca_attn_paged. */
 LCA_API lca_status lca_attn_paged_fp8(const void* q, int32_t dtype, const lca_paged_cache_fp8* cache,
                                       const int32_t* block_table, const int32_t* q_start, const int32_t* k_len, void* o,
                                       float* lse, const lca_paged_shape* shape, const lca_mask_desc* mask,
                                       void* workspace, size_t workspace_bytes, void* stream);
+/* As lca_attn_paged_workspace_size.  What max_q_len = 0 needs serves every other. */
 LCA_API lca_status lca_attn_paged_fp8_workspace_size(const lca_paged_shape* shape, const lca_paged_cache_fp8* cache,
                                                      const lca_mask_desc* mask, size_t* bytes);
 

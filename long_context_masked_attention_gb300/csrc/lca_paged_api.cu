@@ -34,6 +34,7 @@ bool fits(long long n, int64_t stride) {
   return n <= 1 || static_cast<double>(n - 1) * static_cast<double>(stride) <= 1e15;
 }
 constexpr int kMostRequests = 0x3FFFFFFF;  // the kernels' loops over requests stay in 32 bits
+constexpr int kMostHeads = 0xFFFFFF;       // and so do a row's elements
 
 // A cache of either kind as the checks and launches see it: c has the values'
 // layout (its dtype is of no use for an 8-bit one), c8 the factors.
@@ -81,6 +82,7 @@ lca_status check_cache8(const lca_paged_cache_fp8* c) {
   const lca_paged_cache v = values_of(c);
   const lca_status r = check_cache(&v);
   if (r != LCA_OK) return r;
+  if (c->Hkv > kMostHeads) return LCA_ERR_UNSUPPORTED;
   if (c->page_stride % 16 != 0 || c->token_stride % 16 != 0 || c->head_stride % 16 != 0) return LCA_ERR_INVALID_ARG;
   if (!stride_ok(c->scale_page_stride) || !stride_ok(c->scale_head_stride) || !fits(c->n_pages, c->scale_page_stride) ||
       !fits(c->Hkv, c->scale_head_stride))
@@ -248,7 +250,7 @@ lca_status check_attn(const lca_paged_shape* sh, const lca_paged_cache* c, const
   // sums of two lengths or of a length and a window stay in 32 bits, so do the launch grids
   if (static_cast<long long>(sh->max_pages) * c->page_size > 0x3FFFFF00LL || sh->Tq > 0x3FFFFFFF)
     return LCA_ERR_UNSUPPORTED;
-  if (static_cast<long long>(sh->Tq) * sh->Hq > 0x7FFFFFFFLL) return LCA_ERR_UNSUPPORTED;
+  if (static_cast<long long>(sh->Tq) * sh->Hq > 0x7FFFFFFFLL || sh->Hq > kMostHeads) return LCA_ERR_UNSUPPORTED;
   m = MaskCtx{};
   m.kind = md->kind;
   m.wl = md->window_left;

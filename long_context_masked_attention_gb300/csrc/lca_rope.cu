@@ -181,6 +181,7 @@ void launch(const RopeArgs& a, int vec, bool inter, int grid, cudaStream_t st) {
 
 constexpr double kMostFrequency = 1048576.0;  // radians per position
 constexpr long long kMostStride = 1LL << 38;
+constexpr int kMostHeads = 0xFFFFFF;  // a row's elements stay in 32 bits
 
 // Turns per position modulo 1 as a 64-bit fraction: w / (2 pi) in twice the
 // 53 bits of a double, since a position multiplies what is lost by up to 2^31.
@@ -264,7 +265,7 @@ lca_status lca_rope(const lca_rope_rows* q, const lca_rope_rows* k, const int32_
   for (int i = 0; i < r / 2; ++i)
     if (!(rope->inv_freq[i] >= 0.0 && rope->inv_freq[i] <= kMostFrequency)) return LCA_ERR_INVALID_ARG;
   if (!rows_ok(q, n_rows) || !rows_ok(k, n_rows)) return LCA_ERR_INVALID_ARG;
-  if (static_cast<long long>(q->heads) + k->heads > 0x3FFFFFFF) return LCA_ERR_UNSUPPORTED;
+  if (static_cast<long long>(q->heads) + k->heads > kMostHeads) return LCA_ERR_UNSUPPORTED;
   const int heads = q->heads + k->heads;
   if (n_rows == 0 || heads == 0) return LCA_OK;
   if (!rows_memory(q) || !rows_memory(k) || !positions || (reinterpret_cast<uintptr_t>(positions) & 3u) != 0 ||

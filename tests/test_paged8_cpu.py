@@ -72,6 +72,7 @@ BAD_CACHE = [
     (dict(scale_page_stride=0), INVALID), (dict(scale_page_stride=36), INVALID), (dict(scale_head_stride=12), INVALID),
     (dict(scale_head_stride=-16), INVALID), (dict(scale_page_stride=1 << 39), INVALID),
     (dict(n_pages=100000, scale_page_stride=1 << 38), INVALID), (dict(Hkv=1 << 20, head_stride=1 << 38), INVALID),
+    (dict(Hkv=1 << 24), UNSUPPORTED),
 ]
 
 
@@ -110,6 +111,7 @@ def test_nothing_to_do(L):
     (dict(q_stride=1028), INVALID), (dict(max_q_len=-1), INVALID), (dict(scale=-1.0), INVALID),
     (dict(scale=float("nan")), INVALID), (dict(scale=3e38), INVALID), (dict(max_pages=1 << 26, table_stride=1 << 26), UNSUPPORTED),
     (dict(Tq=1 << 30), UNSUPPORTED), (dict(n_seq=1 << 30), UNSUPPORTED),
+    (dict(Tq=1, Hq=1 << 24, q_stride=1 << 31), UNSUPPORTED),
 ], ids=str)
 def test_bad_shapes_are_refused(L, kw, code):
     assert attn(L, shape(**kw), cache()) == code

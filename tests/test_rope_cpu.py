@@ -104,6 +104,7 @@ def call(L, q=None, k=None, positions=FAKE + 0x800000, n_rows=8, d=128, dtype=0,
     (dict(inv=(float("nan"), 1.0)), INVALID), (dict(inv=(1.0, 2.0 ** 21)), INVALID), (dict(inv=(float("inf"),)), INVALID),
     (dict(q=rows(heads=-1)), INVALID), (dict(q=rows(x_stride=504)), INVALID), (dict(q=rows(y_stride=516)), INVALID),
     (dict(q=rows(x_stride=1 << 39)), INVALID), (dict(k=rows(x_stride=1 << 38), n_rows=1 << 30), INVALID),
+    (dict(q=rows(heads=1 << 24, x_stride=1 << 31, y_stride=1 << 31)), UNSUPPORTED),
     (dict(q=rows(heads=1 << 29, x_stride=1 << 36, y_stride=1 << 36), k=rows(heads=1 << 29, x_stride=1 << 36, y_stride=1 << 36)), UNSUPPORTED),
     # pointers that CUDA does not know, misaligned ones, none
     (dict(), INVALID), (dict(q=rows(x=FAKE + 8)), INVALID), (dict(q=rows(y=None)), INVALID), (dict(positions=None), INVALID),
