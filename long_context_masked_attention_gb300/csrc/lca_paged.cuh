@@ -65,6 +65,17 @@ __device__ __forceinline__ bool paged_wait(uint64_t* bar, uint32_t parity, int* 
   return true;
 }
 
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// j / page_size for j in [0, 2^30) (see page_divisor), without a division's chain of instructions.
+__device__ __forceinline__ int page_index(const PagedAttnArgs& a, int j) {
+  return static_cast<int>(__umulhi(static_cast<uint32_t>(j), a.page_mul) >> a.page_shift);
+}
+
 __device__ __forceinline__ bool in_span(const Span& s, int j) {
   return (j >= s.a0 && j < s.b0) || (j >= s.a1 && j < s.b1);
 }

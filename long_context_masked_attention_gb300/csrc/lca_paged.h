@@ -70,6 +70,8 @@ struct PagedAttnArgs {
   int* claims;   // [1] spans claimed past the CTAs' first ones
   float* parts;  // [kPagedMaxSpans][2][rows of an item x (kHeadDim + 2)]
   int Tq, Hq, Hkv, G, n_seq, max_pages, page_size, n_pages;
+  uint32_t page_mul;  // page_divisor's
+  int page_shift;
   float scale_log2;
   int few;  // rows per KV head up to which the kernel for few rows serves a request
   // the kernel for many rows

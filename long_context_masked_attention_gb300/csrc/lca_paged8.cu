@@ -254,10 +254,6 @@ static_assert(kKeys8 == 32 && kStage8 % 16 == 0, "four groups of 8 keys, two ste
 
 __device__ __forceinline__ uint32_t swizzle8(int key) { return (key & 6) ^ ((key & 1) << 2); }
 
-// 8 bytes, of which those past `bytes` (0 or 8) are zero
-__device__ __forceinline__ void cp_async_8(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
 __device__ __forceinline__ uint4 lds16(uint32_t addr) {
   uint4 r;
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(addr) : "memory");
@@ -273,11 +269,6 @@ __device__ __forceinline__ void sts64(uint32_t addr, uint32_t x, uint32_t y) {
 }
 __device__ __forceinline__ void sts32(uint32_t addr, uint32_t x) {
   asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(x) : "memory");
-}
-__device__ __forceinline__ uint32_t lds_u8(uint32_t addr) {
-  uint32_t r;
-  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(r) : "r"(addr) : "memory");
-  return r;
 }
 __device__ __forceinline__ uint32_t word(const uint4& x, int i) { return i == 0 ? x.x : i == 1 ? x.y : i == 2 ? x.z : x.w; }
 // An 8 x 8 matrix of 16-bit values, a pair per lane, transposed.

@@ -355,6 +355,17 @@ void read_args(const lca_paged_cache_fp8* cache, const lca_paged_cache* out, Pag
              out->page_stride % 16 == 0 && out->token_stride % 16 == 0 && out->head_stride % 16 == 0;
 }
 
+// What divides a key's index by the page size as a product: with 2^s the power of
+// two at or above page_size and mul = ceil(2^(30 + s) / page_size), which is
+// less than 2^31 + 1, mul page_size passes 2^(30 + s) by less than 2^s, so
+// floor(j mul / 2^(30 + s)) is exact for j < 2^30.
+void page_divisor(PagedAttnArgs& a) {
+  int s = 3;
+  while ((1LL << s) < a.page_size) ++s;
+  a.page_mul = static_cast<uint32_t>(((1ULL << (30 + s)) + a.page_size - 1) / a.page_size);
+  a.page_shift = s - 2;
+}
+
 // lca_attn_paged over a cache of either kind, q and o of `dtype`.
 lca_status attend(const Cache& any, int dtype, const void* q, const int32_t* block_table, const int32_t* q_start,
                   const int32_t* k_len, void* o, float* lse, const lca_paged_shape* shape, const lca_mask_desc* mask,
@@ -420,6 +431,7 @@ lca_status attend(const Cache& any, int dtype, const void* q, const int32_t* blo
   a.n_seq = shape->n_seq;
   a.max_pages = shape->max_pages;
   a.page_size = cache->page_size;
+  page_divisor(a);
   Cache run = any;
   lca_paged_cache copy{};
   if (L8.copies) {
