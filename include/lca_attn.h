@@ -514,7 +514,7 @@ LCA_API lca_status lca_paged_read_fp8(const lca_paged_cache_fp8* cache, const in
  *  * otherwise to 11 bits too, and the factors of V are taken relative to the
  *    largest among 128 keys that lie together: what a key adds below 2^-22 of
  *    what that one could loses bits.
- *  * where requests have 4096 rows and more on average (max_q_len or Tq /
+ *  * where requests have 1536 rows and more on average (max_q_len or Tq /
  *    n_seq), and the tables' entries, all of them, are 1 GiB as 16-bit K and V at
  *    most: the pages that rows attend are read back (lca_paged_read_fp8, fp16
  *    ends at 65504) into the workspace first, and weights are rounded to dtype.

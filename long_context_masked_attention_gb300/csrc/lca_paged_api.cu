@@ -186,10 +186,12 @@ PagedLayout paged_layout(const lca_paged_shape* sh, const lca_paged_cache* c, bo
 
 // Whether a call over an 8-bit cache makes a 16-bit copy of its tables' pages
 // first and runs on that: it has so many rows per request that reading the keys
-// as 8 bits costs more than the copy.  2048 tokens at 32K keys, 64 heads on 8,
-// take 1876 us as they are and 1545 copied (33 of it the copy); with R rows per
-// request and KV head the copy is some R / 1400 of what it saves, if the tables are full.
-constexpr long long kCopyRows = 4096;
+// as 8 bits costs more than the copy.  64 query heads on 8, as they are and copied:
+// 2048 tokens at the end of 32K keys 1812 and 1555 us (33 of it the copy), 8
+// fresh prompts of 101-2047 tokens 466 and 306; 8 requests of 256, 192, 128 and 64
+// tokens at 16K keys 936 and 912, 711 and 720, 490 and 536, 268 and 352, at 1K keys
+// 154 and 130, 122 and 103, 88 and 83, 57 and 62.
+constexpr long long kCopyRows = 1536;
 constexpr long long kCopyBytes = 1LL << 30;
 long long copy_bytes(const lca_paged_shape* sh, const lca_paged_cache* c) {  // of K or V
   return static_cast<long long>(sh->n_seq) * sh->max_pages * c->page_size * c->Hkv * kHeadDim * 2;
