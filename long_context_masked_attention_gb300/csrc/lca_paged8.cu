@@ -214,6 +214,11 @@ __global__ void __launch_bounds__(256)
 // ------------------------------------------------------------------ attention, few rows
 // A warp's share of the line in lca_paged_few.cuh: a key costs 258 bytes, which
 // bounds the work once the instructions that a key costs are few enough.
+// Measured, whole calls: 64 requests of 1K-32K keys, 64 heads on 8, 198 us (6.0 TB/s,
+// 0.89 of a copy's rate; 215 on another GPU), 32 of 2K-16K with 16 heads of their
+// own, fp16, 138 us (5.9 TB/s), 4 of 512K 649 us (6.7 TB/s), one of 4K 15 us.  What
+// is left of the first is rows of 128 bytes, tokens apart: with the tokens of a
+// head together, 32 of 16K take 175 us where they take 193.
 //
 // Mathematics.  With factors 2^ek and 2^ev of a key's rows and e4m3 values k8
 // and v8, s = scale 2^ek q.k8 and o = sum e^s 2^ev v8 / sum e^s.  The maximum
@@ -233,10 +238,9 @@ __global__ void __launch_bounds__(256)
 // Layout.  The keys are the rows of the products and the rows of q their
 // columns: S^T = K q^T and O^T = V^T w^T, m16n8k16.  So a tile of 8 rows wastes
 // nothing where 8 query heads share a KV head, and more of them share what a
-// key's conversion costs: 32 requests of 1K-16K keys take 99 us with 16 rows, 128
-// with 24, 160 with 32, where the kernel for many rows takes 194 (40 rows spill
-// their sums and take 300).  The
-// operands K and V^T come from shared memory by 16-byte loads and are converted in
+// key's conversion costs: 32 requests of 1K-16K keys take 99 us with 16 rows, 127
+// with 24, 157 with 32; with 40 their sums spill and they take 300, the kernel for
+// many rows 165.  The operands K and V^T come from shared memory by 16-byte loads and are converted in
 // registers.  The order of the 128 products of a score, and of the rows of O^T,
 // is free, so a lane takes the bytes that lie together: of keys lane / 4 and 8
 // more the pieces lane % 4 and lane % 4 + 4 (four values are two registers of one

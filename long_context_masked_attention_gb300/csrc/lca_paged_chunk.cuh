@@ -30,6 +30,9 @@
 // 64 % of the time, and power decides the rest); 8 prompts of 101-2047 tokens 284-295
 // us, where an item of 9 tiles takes 18 us of which 14-15 are tiles; 5 tokens of
 // each of 32 requests at 1K-16K keys 163 us (0.78 of a copy's rate).
+// Over an 8-bit cache (see the converters) the last take 165 us, which no one thing
+// bounds: without the conversions they would take 142, without the softmax 155,
+// without both 133.  Longer prompts do not come here with 8 bits (lca_paged_api.cu).
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -453,7 +456,7 @@ __device__ __forceinline__ void producer(const PagedAttnArgs& a, const CUtensorM
 // An 8-bit cache: the four last warps make the tiles that the products read, in
 // fp16, which holds e4m3 exactly.  What this costs in instructions decides: a
 // product with the row's factor in 32 bits and a rounding to bf16 took a chunk of
-// 2048 tokens at 32K keys 2555 us, a conversion and a product of pairs takes 1875
+// 2048 tokens at 32K keys 2555 us, a conversion and a product of pairs takes 1812
 // (with a 16-bit cache the tensor pipe and power take 1510; here it is the softmax
 // warps that are slowed, by four more warps and 128 registers a thread).  So factors
 // are made to fit fp16: those of a tile are relative to the
