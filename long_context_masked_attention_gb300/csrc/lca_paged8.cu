@@ -16,10 +16,9 @@ namespace lca {
 namespace {
 
 // ------------------------------------------------------------------ write
-// 16 threads per (row, head), for K and V together, as in the 16-bit write:
-// each reads 16 bytes of both, the half-warp finds the two rows' largest
-// magnitudes (as integers: a positive float's bits are in its order), and each
-// thread writes 8 bytes of both.  The factor is a power of two, so dividing by
+// 8 threads per (row, head), for K and V together: each reads 32 bytes of both,
+// the quarter-warp finds the two rows' largest magnitudes (as integers: a positive
+// float's bits are in its order), and each thread writes 16 bytes of both.  The factor is a power of two, so dividing by
 // it is an exact product and the only rounding is e4m3's.  Reads 512 bytes a
 // row and head and writes 258.
 template <typename T>
@@ -35,14 +34,26 @@ struct Magnitude<__half> {
   static __device__ __forceinline__ float value(uint32_t m) { return __half2float(__ushort_as_half(static_cast<unsigned short>(m))); }
 };
 
-// Largest magnitude of eight values, as the type's bits; with kFinite of those
+// 16 values; v8: by one load, the address being a multiple of 32.
+__device__ __forceinline__ void load32(const uint16_t* p, bool v8, uint4 (&x)[2]) {
+  if (v8) {
+    asm("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        : "=r"(x[0].x), "=r"(x[0].y), "=r"(x[0].z), "=r"(x[0].w), "=r"(x[1].x), "=r"(x[1].y), "=r"(x[1].z), "=r"(x[1].w)
+        : "l"(p));
+  } else {
+    x[0] = __ldg(reinterpret_cast<const uint4*>(p));
+    x[1] = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+  }
+}
+
+// Largest magnitude of 16 values, as the type's bits; with kFinite of those
 // that are finite.
 template <typename T, bool kFinite>
-__device__ __forceinline__ uint32_t largest(const uint4& x) {
+__device__ __forceinline__ uint32_t largest(const uint4& x, const uint4& y) {
   uint32_t m = 0;
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 8; ++i) {
     const uint32_t a = w[i] & 0x7FFF7FFFu;
     m = __vmaxu2(m, kFinite ? a & __vcmpltu2(a, Magnitude<T>::kInf) : a);
   }
@@ -79,33 +90,34 @@ __device__ __forceinline__ uint2 quantise(const uint4& x, int e) {
   return make_uint2(r[0] | r[1] << 16, r[2] | r[3] << 16);
 }
 
-// A half-warp takes kHeads heads of a row, so that as many loads of K and of V are
-// under way and the slot is looked up once: 16.5K fp16 rows of 8 heads 26.0 us with
-// one head each, 22.9 with two, 21.3 with four, 22.3 with eight.  Few rows take one
-// each: the latency of more would show (64 rows 2.3 us).  Then instructions were
-// the bound (the integer and conversion pipe 71 % active): values that are not finite
-// are looked for only where the row's largest says that there are some, and
-// fp16 is scaled in pairs; 19.2 us now, 17.8 in bf16 (5.7 TB/s, 0.84 of a copy's rate).
+// A quarter-warp takes kHeads heads of a row, so that as many loads of K and of V are
+// under way and the slot is looked up once: 16.5K fp16 rows of 8 heads 17.1 us with
+// two each, 17.8 with four; bf16 rows, tokens outermost, 16.0 (6.4 TB/s, 0.94 of a
+// copy's rate) and 16.9.  Few rows take one each: the latency of more would show (64
+// rows 2.4 us).  Before, instructions were the bound: with half-warps, 16 bytes a
+// thread and four heads 19.2 us, and 21.3 while every value was looked at for being
+// finite (now only where the row's largest says that some is not) and fp16 was
+// scaled value by value.
 template <typename T, int kHeads>
 __global__ void __launch_bounds__(256) paged_write8_kernel(const PagedWrite8Args a) {
   const int groups = (a.Hkv + kHeads - 1) / kHeads;
-  const long long n = static_cast<long long>(a.n_rows) * groups * 16;  // a multiple of 16: half-warps stay together
-  const int piece = threadIdx.x & 15;
-  const uint32_t half = 0xFFFFu << (threadIdx.x & 16);
+  const long long n = static_cast<long long>(a.n_rows) * groups * 8;  // a multiple of 8: quarter-warps stay together
+  const int piece = threadIdx.x & 7;
+  const uint32_t quarter = 0xFFu << (threadIdx.x & 24);
   for (long long t = blockIdx.x * 256LL + threadIdx.x; t < n; t += gridDim.x * 256LL) {
-    const long long row = line_div(t >> 4, groups);
-    const int head0 = static_cast<int>((t >> 4) - row * groups) * kHeads;
+    const long long row = line_div(t >> 3, groups);
+    const int head0 = static_cast<int>((t >> 3) - row * groups) * kHeads;
     const int slot = __ldg(a.slots + row);
     if (slot < 0 || slot >= a.n_slots) continue;
     const int page = slot / a.page_size, token = slot % a.page_size;
-    const uint16_t* k = a.k + row * a.k_stride + head0 * kHeadDim + piece * 8;
-    const uint16_t* v = a.v + row * a.v_stride + head0 * kHeadDim + piece * 8;
-    uint4 x[kHeads], y[kHeads];
+    const uint16_t* k = a.k + row * a.k_stride + head0 * kHeadDim + piece * 16;
+    const uint16_t* v = a.v + row * a.v_stride + head0 * kHeadDim + piece * 16;
+    uint4 x[kHeads][2], y[kHeads][2];
 #pragma unroll
     for (int h = 0; h < kHeads; ++h)
       if (head0 + h < a.Hkv) {
-        x[h] = __ldg(reinterpret_cast<const uint4*>(k + h * kHeadDim));
-        y[h] = __ldg(reinterpret_cast<const uint4*>(v + h * kHeadDim));
+        load32(k + h * kHeadDim, a.in_v8, x[h]);
+        load32(v + h * kHeadDim, a.in_v8, y[h]);
       }
     int factor = 0;  // lane 2 h keeps K's of head h, lane 2 h + 1 V's
 #pragma unroll
@@ -113,16 +125,21 @@ __global__ void __launch_bounds__(256) paged_write8_kernel(const PagedWrite8Args
       if (head0 + h >= a.Hkv) break;
       auto of_row = [&](uint32_t m) {
 #pragma unroll
-        for (int d = 8; d > 0; d >>= 1) m = __vmaxu2(m, __shfl_xor_sync(half, m, d));
+        for (int d = 4; d > 0; d >>= 1) m = __vmaxu2(m, __shfl_xor_sync(quarter, m, d));
         return m;
       };
-      uint32_t m = of_row(largest<T, false>(x[h]) | largest<T, false>(y[h]) << 16);
+      uint32_t m = of_row(largest<T, false>(x[h][0], x[h][1]) | largest<T, false>(y[h][0], y[h][1]) << 16);
       const bool all = __vcmpgeu2(m, Magnitude<T>::kInf) != 0;  // some value is not finite
-      if (all) m = of_row(largest<T, true>(x[h]) | largest<T, true>(y[h]) << 16);
+      if (all) m = of_row(largest<T, true>(x[h][0], x[h][1]) | largest<T, true>(y[h][0], y[h][1]) << 16);
       const int ek = row_factor(Magnitude<T>::value(m & 0xFFFFu)), ev = row_factor(Magnitude<T>::value(m >> 16));
-      const long long at = page * a.page_stride + token * a.token_stride + (head0 + h) * a.head_stride + piece * 8;
-      *reinterpret_cast<uint2*>(a.kc + at) = all ? quantise<T, true>(x[h], ek) : quantise<T, false>(x[h], ek);
-      *reinterpret_cast<uint2*>(a.vc + at) = all ? quantise<T, true>(y[h], ev) : quantise<T, false>(y[h], ev);
+      const long long at = page * a.page_stride + token * a.token_stride + (head0 + h) * a.head_stride + piece * 16;
+      auto put = [&](uint8_t* to, const uint4(&z)[2], int e) {
+        const uint2 lo = all ? quantise<T, true>(z[0], e) : quantise<T, false>(z[0], e);
+        const uint2 hi = all ? quantise<T, true>(z[1], e) : quantise<T, false>(z[1], e);
+        *reinterpret_cast<uint4*>(to) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+      };
+      put(a.kc + at, x[h], ek);
+      put(a.vc + at, y[h], ev);
       if (piece >> 1 == h) factor = (piece & 1) ? ev : ek;
     }
     const int head = head0 + (piece >> 1);
@@ -668,13 +685,13 @@ cudaError_t launch_decode_of(const PagedAttnArgs& a, int rows, bool behind, int 
 
 template <typename T>
 void write8(const PagedWrite8Args& a, int num_sms, cudaStream_t st) {
-  // four heads a half-warp where that still fills the GPU
-  const long long one = static_cast<long long>(a.n_rows) * a.Hkv * 16;
-  const bool many = a.Hkv >= 4 && one >= 4LL * 2048 * num_sms;
-  const long long blocks = ((many ? static_cast<long long>(a.n_rows) * ((a.Hkv + 3) / 4) * 16 : one) + 255) / 256;
+  // two heads a quarter-warp where that still fills the GPU
+  const long long one = static_cast<long long>(a.n_rows) * a.Hkv * 8;
+  const bool many = a.Hkv >= 2 && one >= 2LL * 2048 * num_sms;
+  const long long blocks = ((many ? static_cast<long long>(a.n_rows) * ((a.Hkv + 1) / 2) * 8 : one) + 255) / 256;
   const int grid = static_cast<int>(std::min<long long>(blocks, num_sms * 8LL));
   if (many)
-    paged_write8_kernel<T, 4><<<grid, 256, 0, st>>>(a);
+    paged_write8_kernel<T, 2><<<grid, 256, 0, st>>>(a);
   else
     paged_write8_kernel<T, 1><<<grid, 256, 0, st>>>(a);
 }

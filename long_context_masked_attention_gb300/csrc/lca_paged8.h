@@ -1,5 +1,5 @@
 // lca_paged8.h — what the entry points of the 8-bit paged cache
-// (lca_paged8_api.cu) and their kernels share.
+// (lca_paged_api.cu) and their kernels share.
 #pragma once
 #include "lca_paged.h"
 
@@ -18,6 +18,7 @@ struct PagedWrite8Args {
   long long k_stride, v_stride, page_stride, token_stride, head_stride, scale_page_stride, scale_head_stride;
   const int* slots;
   int n_rows, Hkv, page_size, n_slots;
+  bool in_v8;  // every 16 values of k and v start on a 32-byte boundary
 };
 void launch_paged_write8(const PagedWrite8Args& a, bool fp16, int num_sms, cudaStream_t st);
 

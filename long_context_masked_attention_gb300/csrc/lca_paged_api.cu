@@ -632,6 +632,8 @@ lca_status lca_paged_write_fp8(const void* k, const void* v, int64_t k_stride, i
   a.Hkv = cache->Hkv;
   a.page_size = cache->page_size;
   a.n_slots = cache->n_pages * cache->page_size;
+  a.in_v8 = ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 31u) == 0 && k_stride % 16 == 0 &&
+            v_stride % 16 == 0;
   launch_paged_write8(a, dtype == LCA_F16, sms, static_cast<cudaStream_t>(stream));
   LCA_CUDA(cudaGetLastError());
   return LCA_OK;
