@@ -59,6 +59,37 @@ def test_write(lca, T, Hkv, page, layout, dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("Hkv", [5, 8])
+@pytest.mark.parametrize("T,extra,first", [(16001, 0, 0), (16001, 8, 8), (37, 8, 0), (37, 16, 8)])
+def test_write_of_many_rows_and_of_rows_off_32_bytes(lca, T, extra, first, Hkv, dtype):
+    """So many rows that threads take two heads each; rows that start on 16 bytes only; an infinity among them."""
+    import torch
+
+    g = torch.Generator().manual_seed(T + extra + Hkv)
+    page, W = 16, Hkv * 128
+    n_pages = T // page + 2
+    x = torch.randn(T, 2 * W + extra + first, generator=g) * torch.randint(-9, 9, (T, 1), generator=g).float().exp2()
+    x[T // 2, first + 130] = float("inf")
+    x = x.to(torch_type(dtype))
+    slots = torch.randperm(n_pages * page, generator=g)[:T].to(torch.int32)
+    slots[3::11] = -1
+    parts, dev = random_cache(n_pages, page, Hkv, "hnd", g)
+    d = x.cuda()
+    k, v = (t.unflatten(1, (Hkv, 128)) for t in (d[:, first:first + W], d[:, first + W:first + 2 * W]))
+    lca.paged_write_fp8(k, v, *dev, slots.cuda())
+    ok = (slots >= 0).nonzero().flatten()
+    at = slots[ok].long()
+    for rows, c, s in ((k.cpu(), parts[0], parts[2]), (v.cpu(), parts[1], parts[3])):
+        y, e = quantise(rows[ok].double().numpy())
+        c[at // page, at % page] = to_bits(y).view(torch.uint8)
+        s[at // page, :, at % page] = torch.from_numpy(e + 127).to(torch.uint8)
+    for got, want in zip(dev, parts):
+        got, want = got.view(torch.uint8).cpu(), want
+        nan = (want & 0x7F == 0x7F) & (got & 0x7F == 0x7F) if got.dim() == 4 else torch.zeros_like(want, dtype=torch.bool)
+        assert bool(((got == want) | nan).all())  # a NaN's sign is free
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 def test_write_of_edges(lca, dtype):
     """Rows of zeros, of one value, of the type's largest and smallest, of values that lie between two e4m3 ones, and
     rows with infinities and NaN, which are NaN and do not raise the factor."""
@@ -140,6 +171,30 @@ def test_read(lca, n, Hkv, page, layout, dtype):
         for z, rest in ((x, 7.0), (y, 0.0)):
             assert torch.equal(torch.nan_to_num(z.cpu()[ok].double(), nan=3e300), torch.nan_to_num(want.double(), nan=3e300))
             assert bool((z.cpu()[~ok] == rest).all())
+
+
+@pytest.mark.parametrize("first", [0, 8])
+@pytest.mark.parametrize("layout,dtype", [("nhd", "bf16"), ("hnd", "fp16")])
+def test_read_of_many_pages(lca, layout, dtype, first):
+    """So many rows that threads take four each, pages of a number of rows that 128 does not divide; results that
+    start on 16 bytes only; nothing written beside them."""
+    import torch
+
+    n, page, Hkv = 90, 200, 9
+    g = torch.Generator().manual_seed(first + 1)
+    (lk, lv, lks, lvs), dev = random_cache(50, page, Hkv, layout, g)
+    pages = torch.randint(-1, 51, (n,), generator=g).to(torch.int32)
+    dt, size = torch_type(dtype), n * page * Hkv * 128
+    flat = [torch.full((size + 16,), 7.0, dtype=dt, device="cuda") for _ in range(2)]
+    outs = [x[first:first + size].view(n, page, Hkv, 128) for x in flat]
+    lca.paged_read_fp8(*dev, pages.cuda(), k_out=outs[0], v_out=outs[1])
+    ok = (pages >= 0) & (pages < 50)
+    for c, s, x, f in ((lk, lks, outs[0], flat[0]), (lv, lvs, outs[1], flat[1])):
+        e = s.transpose(1, 2).float().clamp(79, 175) - 127
+        want = c.view(torch.float8_e4m3fn).float() * e.exp2()[..., None]
+        want = (want.clamp(-65504, 65504) if dtype == "fp16" else want).to(dt)[pages[ok].long()]
+        assert torch.equal(torch.nan_to_num(x.cpu()[ok].float(), nan=3e30), torch.nan_to_num(want.float(), nan=3e30))
+        assert bool((x.cpu()[~ok] == 7).all()) and bool((f[:first] == 7).all()) and bool((f[first + size:] == 7).all())
 
 
 def test_reads_that_overlap_or_do_not_fit_are_refused(lca):
