@@ -597,7 +597,7 @@ def test_overlapping_memory_is_refused(lca):
     n = p.kc.shape[0]
     kc = buf[:p.kc.numel()].view(torch.float8_e4m3fn).view(p.kc.shape)
     ks = buf[1024:1024 + p.ks.numel()].view(p.ks.shape)
-    for kw in (dict(out=p.q), dict(out=p.kc.view(torch.bfloat16).view(-1)[:3072 // 2 * 2][:3 * 8 * 128].view(3, 8, 128)),
+    for kw in (dict(out=p.q), dict(out=p.kc.view(torch.bfloat16).view(-1)[:3 * 8 * 128].view(3, 8, 128)),
                dict(out=flat[:1536].view(torch.bfloat16).view(3, 8, 128), lse=flat[1000:1024].view(8, 3)),
                dict(k_cache=kc, workspace=buf[:need]), dict(v_cache=kc, workspace=buf[:need]), dict(k_scale=ks, workspace=buf[:need]),
                dict(v_scale=ks, workspace=buf[:need]), dict(v_scale=flat.view(torch.uint8)[:p.ks.numel()].view(p.ks.shape), lse=flat[8:32].view(8, 3))):
