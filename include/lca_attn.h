@@ -505,15 +505,16 @@ LCA_API lca_status lca_paged_read_fp8(const lca_paged_cache_fp8* cache, const in
 
 /* lca_attn_paged over such a cache: the same arguments, masks, reports and
  * rules, with q and o of the given lca_dtype; Hq is below 2^24.  Scores are those
- * of the values that the cache stands for.  A request's new tokens times Hq / Hkv
- * are its rows per KV head, and how weights are rounded before their product with
- * V depends on them and on the batch:
+ * of the values that the cache stands for; values of q below 2^-28 of the largest
+ * of their row (a token's d values of one head) may lose bits.  A request's new
+ * tokens times Hq / Hkv are its rows per KV head, and how weights are rounded
+ * before their product with V depends on them and on the batch:
  *  * where no request can have more than 32 (max_q_len, or Tq), and in other
  *    batches for those of at most 16: to 11 bits times their key's factor; a key
- *    whose weight times factor is below 2^-36 of the largest may count as 0.
- *  * otherwise to 11 bits too, and the factors of V are taken relative to the
- *    largest among 128 keys that lie together: what a key adds below 2^-22 of
- *    what that one could loses bits.
+ *    whose weight times factor is below 2^-36 of the row's largest may count as 0.
+ *  * otherwise likewise, with 2^-24; and where factors of 32 keys that lie together
+ *    are below 2^-22 (K) or 2^-8 (V) of the largest among 128, these 128 keys take
+ *    about twice the time.
  *  * where requests have 1536 rows and more on average (max_q_len or Tq /
  *    n_seq), and the tables' entries, all of them, are 1 GiB as 16-bit K and V at
  *    most: the pages that rows attend are read back (lca_paged_read_fp8, fp16

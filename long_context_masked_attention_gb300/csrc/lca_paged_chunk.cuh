@@ -30,7 +30,7 @@
 // 64 % of the time, and power decides the rest); 8 prompts of 101-2047 tokens 284-295
 // us, where an item of 9 tiles takes 18 us of which 14-15 are tiles; 5 tokens of
 // each of 32 requests at 1K-16K keys 163 us (0.78 of a copy's rate).
-// Over an 8-bit cache (see the converters) the last take 165 us, which no one thing
+// Over an 8-bit cache (see the converters) the last take 170 us, which no one thing
 // bounds: without the conversions they would take 142, without the softmax 155,
 // without both 133.  Longer prompts do not come here with 8 bits (lca_paged_api.cu).
 #pragma once
@@ -461,9 +461,14 @@ __device__ __forceinline__ void producer(const PagedAttnArgs& a, const CUtensorM
 // warps that are slowed, by four more warps and 128 registers a thread).  So factors
 // are made to fit fp16: those of a tile are relative to the
 // largest of its attended keys' (which becomes 2^7, so that values end below
-// 2^16), and the softmax warps learn it from `exps`.  A row whose factor is less
-// than 2^-22 of the largest in its tile loses bits, 2^-24 of a value that is at
-// most 2^16.  bf16 queries are turned into fp16 first, each row by a power of
+// 2^16), and the softmax warps learn it from `exps`.  That is exact where a key's
+// factor is at least 2^-kNearK of the largest: a value is a multiple of 2^-9 and fp16
+// holds multiples of 2^-24.  V's largest factor also says what unit a row's
+// weights have (softmax_wg), so it may be 2^kNearV above what a row attends.
+// Where one of a warp's 32 keys is further below, their values go as they
+// are, K times 1 and V times 2^7, and the softmax warps read the keys' factors
+// themselves (far_scores).
+// bf16 queries are turned into fp16 first, each row by a power of
 // two that brings its largest value to 2^14 (see lca_paged8.cu).
 //
 // A thread has one key's row of a tile, 128 bytes, pieces swizzled on both sides
@@ -515,12 +520,16 @@ __device__ __forceinline__ int halve_q_row(uint32_t q, int row) {
   return e;
 }
 
+constexpr int kNearK = 22, kNearV = 8;
+
 // What converters leave in the control part: per tile (round robin) the
-// exponents that its K and V are relative to, per item (two of them) those of
-// q's rows; and the warps' largest of a tile, of two tiles in turn.
-struct Exps {
+// exponents that its K and V are relative to, and of which warps' keys the factors
+// are too far apart for it; per item (two of them) the exponents of q's rows; and
+// the warps' largest of a tile, of two tiles in turn (16 bits each of K and V).
+struct alignas(16) Exps {
+  uint32_t most[2][4];
   int tile[kExpSlots][2];
-  int most[2][4][2];
+  uint8_t far[kExpSlots][4];
 };
 
 template <typename T>
@@ -568,8 +577,8 @@ __device__ __forceinline__ void converter(const PagedAttnArgs& a, uint8_t* sQ, c
       }
       cp_async_commit();
     };
-    // the exponents of this row's factors (the least where no row attends its key), and
-    // what the warp's largest are, for the other warps
+    // the exponents of this row's factors (of a key that no row attends any, not the
+    // largest and not far from it), and what the warp's largest are, for the other warps
     int ek = 0, ev = 0;
     auto meet = [&](int t) {
       const uint32_t tile = tiles + t;
@@ -580,9 +589,10 @@ __device__ __forceinline__ void converter(const PagedAttnArgs& a, uint8_t* sQ, c
       ev = own ? factor_of(lds_u8(ask0 + (t & 1) * 64 + 32 + lane)) : kScaleMin;
       const int mk = __reduce_max_sync(0xFFFFFFFFu, ek), mv = __reduce_max_sync(0xFFFFFFFFu, ev);
       if (lane == 0) {
-        *reinterpret_cast<int2*>(exps->most[tile & 1][wq]) = make_int2(mk, mv);
+        exps->most[tile & 1][wq] = (mk & 0xFFFF) | mv << 16;
         mbar_arrive(&bar[C::MAXFULL]);
       }
+      if (!own) ek = ev = kScaleMax;
     };
     {
       const int p0 = page_of(0), p1 = page_of(1);
@@ -594,14 +604,13 @@ __device__ __forceinline__ void converter(const PagedAttnArgs& a, uint8_t* sQ, c
     for (int t = 0; t < n; ++t) {
       const uint32_t tile = tiles + t;
       if (!waitw(&bar[C::MAXFULL], tile & 1, a, 94)) return;
-      int mk = kScaleMin, mv = kScaleMin;
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const int2 x = *reinterpret_cast<const int2*>(exps->most[tile & 1][w]);
-        mk = max(mk, x.x), mv = max(mv, x.y);
-      }
-      const uint32_t fk = half_power(ek - mk + 7), fv = half_power(ev - mv + 7);
+      const uint4 x = *reinterpret_cast<const uint4*>(exps->most[tile & 1]);
+      const uint32_t most = __vmaxs2(__vmaxs2(x.x, x.y), __vmaxs2(x.z, x.w));
+      const int mk = static_cast<int16_t>(most), mv = static_cast<int>(most) >> 16;
+      const bool far = __any_sync(0xFFFFFFFFu, mk - ek > kNearK || mv - ev > kNearV);
+      const uint32_t fk = half_power(far ? 0 : ek - mk + 7), fv = half_power(far ? 7 : ev - mv + 7);
       if (row == 0) *reinterpret_cast<int2*>(exps->tile[tile % kExpSlots]) = make_int2(mk, mv);
+      if (lane == 0) exps->far[tile % kExpSlots][wq] = far;
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar[C::EXFULL + tile % kExpSlots]);
       ask(t + 2, page);  // into the place of tile t's, which all lanes have read
@@ -768,6 +777,69 @@ __device__ __forceinline__ void mask_scores(uint32_t tS, const Span& sp, int j0)
     tmem_st32(tS + 32 * c, r);
   }
   tmem_st_wait();
+}
+
+// A tile of an 8-bit cache with keys whose factors are far apart: the scores in
+// TMEM become t = s log2(e) + the exponent that the key's V is relative to, which is
+// its own where exps->far has the warp's 32 keys.  Lane j of a warp finds the
+// factors of keys j, j + 32, ... again.  Returned is the row's sum of 2^(t - its
+// maximum) without V's exponents.  q_exp: of this item's rows, null for fp16 queries.
+// A batch of drafts all of whose tiles are so (factors spread over 2^30) takes 2.4
+// times as long as one of near factors.
+__device__ __noinline__ float far_scores(const PagedAttnArgs& a, const Item& inf, int kt, uint32_t tS, const Exps* exps,
+                                         uint32_t slot, const int8_t* q_exp) {
+  const int2 e = *reinterpret_cast<const int2*>(exps->tile[slot]);
+  const int qe = q_exp ? q_exp[threadIdx.x] : 0;
+  const float sl2 = fmaxf(a.scale_log2 * two_to(qe >> 1) * two_to(qe - (qe >> 1)), 1.2e-38f);
+  uint32_t eks = 0, evs = 0;  // a byte each
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const int j = kt * kTile + 32 * c + (threadIdx.x & 31);
+    int ek = e.x - 7, ev = e.y;  // K's 2^7 is taken out, V's stays in O
+    if (exps->far[slot][c]) {
+      uint32_t bk = 0, bv = 0;  // as the converters have it where there is no page
+      if (in_span(inf.all, j)) {
+        const int at = page_index(a, j), page = __ldg(a.table + inf.seq * a.table_stride + at);
+        if (page >= 0 && page < a.n_pages) {
+          const long long f = page * a.scale_page_stride + inf.head * a.scale_head_stride + (j - at * a.page_size);
+          bk = __ldg(a.ks + f), bv = __ldg(a.vs + f);
+        }
+      }
+      ek = factor_of(bk), ev = factor_of(bv);
+    }
+    eks |= static_cast<uint32_t>(ek & 255) << (8 * c);
+    evs |= static_cast<uint32_t>(ev & 255) << (8 * c);
+  }
+  float m = -INFINITY;
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    const float fk = two_to(static_cast<int8_t>(eks >> (8 * c))), fv = static_cast<float>(static_cast<int8_t>(evs >> (8 * c)));
+    uint32_t r[32];
+    __syncwarp();
+    tmem_ld32(tS + 32 * c, r);
+    tmem_ld_wait();
+#pragma unroll
+    for (int k = 0; k < 32; ++k) {
+      const float t = fmaf(__uint_as_float(r[k]) * __shfl_sync(0xFFFFFFFFu, fk, k), sl2, __shfl_sync(0xFFFFFFFFu, fv, k));
+      m = fmaxf(m, t);
+      r[k] = __float_as_uint(t);
+    }
+    tmem_st32(tS + 32 * c, r);
+  }
+  tmem_st_wait();
+  if (m == -INFINITY) m = 0.f;
+  float sum = 0.f;
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    const float f = two_to(-static_cast<int>(static_cast<int8_t>(evs >> (8 * c))));
+    uint32_t r[32];
+    __syncwarp();
+    tmem_ld32(tS + 32 * c, r);
+    tmem_ld_wait();
+#pragma unroll
+    for (int k = 0; k < 32; ++k) sum = fmaf(ex2_approx(__uint_as_float(r[k]) - m), __shfl_sync(0xFFFFFFFFu, f, k), sum);
+  }
+  return sum;
 }
 
 // Maximum of the thread's 128 scores, 64 columns at a time: eight independent
@@ -950,6 +1022,15 @@ __device__ __noinline__ void write_hidden(const PagedAttnArgs& a, const Item& in
   }
 }
 
+// Over an 8-bit cache a row's sums go by the maximum m of t = s log2(e) + the
+// exponent that the key's V is relative to, much as the kernel for few rows has
+// it: O is the sum of 2^(t - m + 7) V, and l gets each weight without that
+// exponent.  So keys of large values that a row does not attend, or hardly, change
+// nothing: weights are fp16, kept times 2^7, and a key counts while its weight times
+// 2^ev is above 2^-32 of the largest, or 2^-24 where V is relative to a key of
+// 2^kNearV times the factor that the row does not attend.  (While O went by the
+// largest factor so far, whatever its key weighed, one key of 2^32 times the others'
+// values left zeros in all rows behind it.)
 template <typename T, bool k8>
 __device__ __forceinline__ void softmax_wg(const PagedAttnArgs& a, int x, uint64_t* bar, const Item* items,
                                            uint8_t* sKV, volatile int* hidden, const Exps* exps, const int8_t* q_exp,
@@ -984,7 +1065,6 @@ __device__ __forceinline__ void softmax_wg(const PagedAttnArgs& a, int x, uint64
     const Span sp = paged_span(a, inf.q_len, inf.k_len, min(token, inf.q_len - 1));
     float m = -INFINITY, l = 0.f;
     bool any = false;
-    int v_exp = 0;  // an 8-bit cache: O is relative to 2^v_exp
     for (int t = 0; t < n; ++t) {
       const int kt = inf.tile(t);
       const uint32_t cls = inf.cls(x, kt);
@@ -996,45 +1076,49 @@ __device__ __forceinline__ void softmax_wg(const PagedAttnArgs& a, int x, uint64
       if (odd) ++s_odd; else ++s_cnt;
       tc_fence_after();
       float sl2 = a.scale_log2;
-      int shift = 0;  // of p, as the tile's V is relative to less than O
-      float lower = 1.f;  // of O, as it becomes relative to more
+      float v_exp = 0.f;  // what the tile's V is relative to
+      float without = 1.f, rest = 0.f;  // l gets the weights times `without` and, relative to the tile's maximum, `rest`
       if constexpr (k8) {
         // the scores show that the converters have been here; they are at most
         // two tiles further on, so the wait sees its phase
         const uint32_t tile = kv_iter / 2 + t;
         if (!waitw(&bar[C::EXFULL + tile % kExpSlots], (tile / kExpSlots) & 1, a, 78 + x)) return;
         const int2 e = *reinterpret_cast<const int2*>(exps->tile[tile % kExpSlots]);
+        const uint32_t far = *reinterpret_cast<const uint32_t*>(exps->far[tile % kExpSlots]);
         int ex = e.x - 7;
-        if constexpr (!std::is_same<T, M>::value) ex += q_exp[(it & 1) * 256 + x * 128 + row];
+        if constexpr (!std::is_same<T, M>::value) ex += q_exp[(it & 1) * 256 + threadIdx.x];
         // in two steps: 2^ex itself may be past a float's range; not 0, which times -inf is no number
         sl2 = fmaxf(sl2 * two_to(ex >> 1) * two_to(ex - (ex >> 1)), 1.2e-38f);
-        if (!any) v_exp = e.y;
-        if (e.y > v_exp) {
-          lower = two_to(v_exp - e.y);
-          v_exp = e.y;
-        }
-        shift = e.y - v_exp;
+        v_exp = static_cast<float>(e.y);
+        without = two_to(-e.y);
+        if (far) sl2 = 1.f, v_exp = 0.f, without = 0.f;
       }
-      if (!span_covers(inf.every, kt * kTile, kt * kTile + kTile)) {
-        // only now: a warpgroup that skipped a narrow item runs ahead of the
-        // loads, and the scores show that the ring has come to this tile
-        const uint32_t vidx = kv_iter + 2 * t + 1;
-        if (!waitw(&bar[C::KVFULL + vidx % kStages], (vidx / kStages) & 1, a, 88 + x)) return;
-        const int j = kt * kTile + row;
-        uint8_t* v = sKV + (vidx % kStages) * kTileBytes;
-        if (!in_span(inf.all, j)) {
-          clear_v_row(v, row);
-        } else if (!in_span(inf.every, j) && bad_v_row<M>(v, row)) {
-          // the other warpgroup may find the value gone, but then the mark set
-          hidden[slot] = it + 1;
-          __threadfence_block();
-          finite_v_row<M>(v, row);
+      const bool covered = span_covers(inf.every, kt * kTile, kt * kTile + kTile);
+      if (!covered || (k8 && without == 0.f)) {
+        if (!covered) {
+          // only now: a warpgroup that skipped a narrow item runs ahead of the
+          // loads, and the scores show that the ring has come to this tile
+          const uint32_t vidx = kv_iter + 2 * t + 1;
+          if (!waitw(&bar[C::KVFULL + vidx % kStages], (vidx / kStages) & 1, a, 88 + x)) return;
+          const int j = kt * kTile + row;
+          uint8_t* v = sKV + (vidx % kStages) * kTileBytes;
+          if (!in_span(inf.all, j)) {
+            clear_v_row(v, row);
+          } else if (!in_span(inf.every, j) && bad_v_row<M>(v, row)) {
+            // the other warpgroup may find the value gone, but then the mark set
+            hidden[slot] = it + 1;
+            __threadfence_block();
+            finite_v_row<M>(v, row);
+          }
+          fence_proxy_async_smem();
+          if (cls != kTileFull) mask_scores(tS, sp, kt * kTile);
         }
-        fence_proxy_async_smem();
-        if (cls != kTileFull) mask_scores(tS, sp, kt * kTile);
+        if (k8 && without == 0.f)
+          rest = far_scores(a, inf, kt, tS, exps, (kv_iter / 2 + t) % kExpSlots,
+                            std::is_same<T, M>::value ? nullptr : q_exp + (it & 1) * 256);
       }
       const float mx = row_max(tS);
-      const float m_new = fmaxf(m, mx * sl2);
+      const float m_new = fmaxf(m, k8 ? __fmaf_ru(mx, sl2, v_exp) : mx * sl2);
       float factor = 1.f;
       bool need = false;
       if (!any) {
@@ -1045,12 +1129,13 @@ __device__ __forceinline__ void softmax_wg(const PagedAttnArgs& a, int x, uint64
         m = m_new;
       }
       float base = m == -INFINITY ? 0.f : m;
-      base = k8 ? __fadd_ru(base, -kBias<M> - shift) : base - kBias<M>;
-      const float sum = row_exp<M>(tS, sl2, base);
-      l = l * factor + (k8 ? sum * two_to(-shift) : sum);
+      base = k8 ? __fadd_ru(base, -kBias<M> - v_exp) : base - kBias<M>;
       if constexpr (k8) {
-        need |= lower != 1.f;
-        factor *= lower;
+        l = fmaf(rest, ex2_approx(fmaf(mx, sl2, -base)), l * factor);
+        l = fmaf(row_exp<M>(tS, sl2, base), without, l);
+      } else {
+        const float sum = row_exp<M>(tS, sl2, base);
+        l = l * factor + sum;
       }
       const bool rescale = __any_sync(0xFFFFFFFFu, need);
       // The product before this one must have finished before O is rescaled.
@@ -1090,9 +1175,9 @@ __device__ __forceinline__ void softmax_wg(const PagedAttnArgs& a, int x, uint64
     // a vote, since what follows takes all lanes of the warp together
     if (__any_sync(0xFFFFFFFFu, any && hidden[slot] == it + 1)) {
       write_hidden<T, k8>(a, inf, x, tO, valid, sp, orow, part ? part + (x * 128 + row) * kHeadDim : nullptr, l,
-                          k8 ? two_to(v_exp - 7) : 1.f);
+                          k8 ? 0x1p-7f : 1.f);
     } else if (any) {
-      const float unit = k8 ? two_to(v_exp - 7) : 1.f;
+      constexpr float unit = k8 ? 0x1p-7f : 1.f;  // V's 2^7
       const float inv = part ? unit : l == 0.f ? 0.f : unit / l;
       if (part) {
 #pragma unroll 1
@@ -1184,8 +1269,11 @@ __global__ void __launch_bounds__(Chunk<k8>::kThreads, 1)
   // per item slot: the last item (from 1) with values that write_hidden adds;
   // a warp may be that many items ahead of another
   int* hidden = reinterpret_cast<int*>(sm + C::kOffCtl + 904);
-  Exps* exps = reinterpret_cast<Exps*>(sm + C::kOffCtl + 920);
-  static_assert(920 + sizeof(Exps) <= 1024, "the control part");
+  constexpr int kOffExps = 928;
+  static_assert(C::kOffCtl % 16 == 0 && kOffExps % alignof(Exps) == 0 && 904 + 4 * kItemSlots <= kOffExps &&
+                    kOffExps + sizeof(Exps) <= 1024,
+                "the control part");
+  Exps* exps = reinterpret_cast<Exps*>(sm + C::kOffCtl + kOffExps);
   int8_t* q_exp = reinterpret_cast<int8_t*>(sm + C::kOffCtl + C::kOffExp);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (warp == 8) {
