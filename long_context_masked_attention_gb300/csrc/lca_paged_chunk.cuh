@@ -467,7 +467,8 @@ __device__ __forceinline__ void producer(const PagedAttnArgs& a, const CUtensorM
 // weights have (softmax_wg), so it may be 2^kNearV above what a row attends.
 // Where one of a warp's 32 keys is further below, their values go as they
 // are, K times 1 and V times 2^7, and the softmax warps read the keys' factors
-// themselves (far_scores).
+// themselves (far_scores), which also rounds the scores before their maximum is
+// taken off, so that a warp whose rows of q could make huge ones asks for it too.
 // bf16 queries are turned into fp16 first, each row by a power of
 // two that brings its largest value to 2^14 (see lca_paged8.cu).
 //
@@ -489,23 +490,30 @@ __device__ __forceinline__ void sts128(uint32_t at, uint32_t x, uint32_t y, uint
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 
-// Row `row` of q's sub-tile as fp16 times 2^-e; returns e.
-__device__ __forceinline__ int halve_q_row(uint32_t q, int row) {
+// The exponent e for which the largest finite value of row `row` of q's sub-tile, a
+// row of T, is in [2^(14 + e), 2^(15 + e)).  Here and below a short loop: instructions
+// that come late cost the other warps more (four at a time: 32 requests of 5 tokens 144
+// us, 138 so; 8 prompts 472 and 449).
+template <typename T>
+__device__ __forceinline__ int q_row_exponent(uint32_t q, int row) {
   float m = 0.f;
-#pragma unroll 4
+#pragma unroll 1
   for (int i = 0; i < 16; ++i) {
     const uint4 w = lds128(q + (i >> 3) * kChunkBytes + row * 128 + (((i ^ row) & 7) << 4));
     const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const float2 v = Half2<__nv_bfloat16>::unpack(x[k]);
+      const float2 v = Half2<T>::unpack(x[k]);
       m = fmaxf(m, fabsf(v.x) < INFINITY ? fabsf(v.x) : 0.f);  // a NaN counts as 0 too
       m = fmaxf(m, fabsf(v.y) < INFINITY ? fabsf(v.y) : 0.f);
     }
   }
-  const int e = max(static_cast<int>(__float_as_uint(m) >> 23) - 127 - 14, -128);  // of 8 bits
+  return max(static_cast<int>(__float_as_uint(m) >> 23) - 127 - 14, -128);  // of 8 bits
+}
+// A bf16 row as fp16 times 2^-e.
+__device__ __forceinline__ void halve_q_row(uint32_t q, int row, int e) {
   const float f0 = two_to(-e / 2), f1 = two_to(-e - -e / 2);
-#pragma unroll 4
+#pragma unroll 1
   for (int i = 0; i < 16; ++i) {
     const uint32_t at = q + (i >> 3) * kChunkBytes + row * 128 + (((i ^ row) & 7) << 4);
     const uint4 w = lds128(at);
@@ -517,7 +525,6 @@ __device__ __forceinline__ int halve_q_row(uint32_t q, int row) {
     }
     sts128(at, x[0], x[1], x[2], x[3]);
   }
-  return e;
 }
 
 constexpr int kNearK = 22, kNearV = 8;
@@ -538,6 +545,9 @@ __device__ __forceinline__ void converter(const PagedAttnArgs& a, uint8_t* sQ, c
   using C = Chunk<true>;
   const int lane = threadIdx.x & 31, row = threadIdx.x & 127, wq = row >> 5;
   uint32_t tiles = 0;  // before this item
+  // a sum of 128 products of values below 2^15 and 2^16 is below 2^38: from this sum
+  // of q's and K's exponents on (less K's 2^7) a score may be 2^22 (see kHugeScore)
+  const int huge = 22 - 38 + 7 - (static_cast<int>(__float_as_uint(a.scale_log2) >> 23) - 126);
   const uint32_t ask0 = smem_u32(asked) + wq * 128;
   const uint32_t at0 = row * 128 + ((row & 7) << 4), raw0 = smem_u32(raw) + at0, kv0 = smem_u32(sKV) + at0;
   for (int it = 0;; ++it) {
@@ -546,11 +556,23 @@ __device__ __forceinline__ void converter(const PagedAttnArgs& a, uint8_t* sQ, c
     const Item inf = items[slot];
     if (!inf.valid) return;
     const int n = inf.n;
-    if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+    int q_most = -128;  // exponent of the warp's rows
+    // fp16 queries of an item without tiles: the products do not wait for this
+    // warp, so that the queries may be those of a later item by now
+    if (std::is_same<T, __nv_bfloat16>::value || n > 0) {
       if (!waitw(&bar[C::QFULL], it & 1, a, 93)) return;
 #pragma unroll 1
-      for (int x = 0; x < (inf.narrow ? 1 : 2); ++x)
-        q_exp[(it & 1) * 256 + x * 128 + row] = static_cast<int8_t>(halve_q_row(smem_u32(sQ) + x * kTileBytes, row));
+      for (int x = 0; x < (inf.narrow ? 1 : 2); ++x) {
+        const int e = q_row_exponent<T>(smem_u32(sQ) + x * kTileBytes, row), tok = row / a.G;
+        if (tok < a.tpt && inf.tok0 + x * a.tpt + tok < inf.q_len) q_most = max(q_most, e);
+        if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+          q_exp[(it & 1) * 256 + x * 128 + row] = static_cast<int8_t>(e);
+          halve_q_row(smem_u32(sQ) + x * kTileBytes, row, e);
+        }
+      }
+      q_most = __reduce_max_sync(0xFFFFFFFFu, q_most);
+    }
+    if constexpr (std::is_same<T, __nv_bfloat16>::value) {
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar[C::QREADY]);
@@ -607,7 +629,7 @@ __device__ __forceinline__ void converter(const PagedAttnArgs& a, uint8_t* sQ, c
       const uint4 x = *reinterpret_cast<const uint4*>(exps->most[tile & 1]);
       const uint32_t most = __vmaxs2(__vmaxs2(x.x, x.y), __vmaxs2(x.z, x.w));
       const int mk = static_cast<int16_t>(most), mv = static_cast<int>(most) >> 16;
-      const bool far = __any_sync(0xFFFFFFFFu, mk - ek > kNearK || mv - ev > kNearV);
+      const bool far = mk + q_most >= huge || __any_sync(0xFFFFFFFFu, mk - ek > kNearK || mv - ev > kNearV);
       const uint32_t fk = half_power(far ? 0 : ek - mk + 7), fv = half_power(far ? 7 : ev - mv + 7);
       if (row == 0) *reinterpret_cast<int2*>(exps->tile[tile % kExpSlots]) = make_int2(mk, mv);
       if (lane == 0) exps->far[tile % kExpSlots][wq] = far;
@@ -897,6 +919,29 @@ __device__ __forceinline__ float row_exp(uint32_t tS, float sl2, float base) {
   return f2lo(t) + f2hi(t);
 }
 
+// A row's maximum m of 2^22 and more has a last place of 2^-1 and more (bf16 holds
+// what p may become by 2^5, at 2^28), which is too coarse to be taken off the product
+// that row_exp has not rounded: p would leave fp16, or be 0 for every key.  The
+// warp's scores are rounded first then, as m is.  (Over an 8-bit cache far_scores
+// does it.)
+template <typename M>
+constexpr float kHugeScore = 0x1p28f;
+template <>
+constexpr float kHugeScore<__half> = 0x1p22f;
+__device__ __noinline__ void round_scores(uint32_t tS, float sl2) {
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    uint32_t r[32];
+    __syncwarp();
+    tmem_ld32(tS + 32 * c, r);
+    tmem_ld_wait();
+#pragma unroll
+    for (int k = 0; k < 32; ++k) r[k] = __float_as_uint(__uint_as_float(r[k]) * sl2);
+    tmem_st32(tS + 32 * c, r);
+  }
+  tmem_st_wait();
+}
+
 // Values that are not finite in keys that only some rows of an item attend
 // must not meet a p of 0.  Before a tile's product they are set to zero in
 // shared memory, value by value, by each warpgroup that has a product with the
@@ -1118,7 +1163,7 @@ __device__ __forceinline__ void softmax_wg(const PagedAttnArgs& a, int x, uint64
                             std::is_same<T, M>::value ? nullptr : q_exp + (it & 1) * 256);
       }
       const float mx = row_max(tS);
-      const float m_new = fmaxf(m, k8 ? __fmaf_ru(mx, sl2, v_exp) : mx * sl2);
+      const float m_new = fmaxf(m, k8 ? fmaf(mx, sl2, v_exp) : mx * sl2);
       float factor = 1.f;
       bool need = false;
       if (!any) {
@@ -1129,7 +1174,15 @@ __device__ __forceinline__ void softmax_wg(const PagedAttnArgs& a, int x, uint64
         m = m_new;
       }
       float base = m == -INFINITY ? 0.f : m;
-      base = k8 ? __fadd_ru(base, -kBias<M> - v_exp) : base - kBias<M>;
+      if constexpr (k8) {
+        base = __fadd_ru(base, -kBias<M> - v_exp);
+      } else if (__any_sync(0xFFFFFFFFu, valid && fabsf(base) >= kHugeScore<M>)) {
+        round_scores(tS, sl2);
+        sl2 = 1.f;
+        base = __fadd_ru(base, -kBias<M>);
+      } else {
+        base -= kBias<M>;
+      }
       if constexpr (k8) {
         l = fmaf(rest, ex2_approx(fmaf(mx, sl2, -base)), l * factor);
         l = fmaf(row_exp<M>(tS, sl2, base), without, l);

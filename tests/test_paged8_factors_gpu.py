@@ -68,20 +68,21 @@ def on_gpu(b, page, layout="nhd", extra=0, seed=0):
     return (b.q.cuda(), *lay_out8(*parts, layout, "cuda"), table.cuda(), i32(q_start), i32(c + w for c, w in b.lens))
 
 
-def bounds(b):
+def bounds(b, copied=False):
     """(O, LSE, how far each element of O and LSE may be off), from the definition in 64 bits.
 
     A score is off by at most d_j = 130 e |q| |k_j| scale + 3 e (34 + |s_j|), e = 2^-24: its products and their sum, and
     the two roundings of score plus exponent (at most 48 ln 2 = 34).  A weight is w_j = 1 / (1 + sum of the others' e^(s_i
     - s_j)), so it lies between the values that it has with its own score off one way and all others the other way.
-    Weights are rounded to 11 bits, and the sums of n terms in 32 bits cost (n + 16) e.  A weight in fp16 may also be off
-    by 2^-25 however small it is; the unit is at most twice the largest w_j 2^ev_j (the header's border of 2^-24), a
-    term's value at most |v8_j| in it.
+    Weights are rounded to 11 bits, or to the type's in the kernel over a copy of the pages, and the sums of n terms in
+    32 bits cost (n + 16) e.  A weight in fp16 may also be off by 2^-25 however small it is (bf16 has the exponents of 32
+    bits); the unit is at most twice the largest w_j 2^ev_j (the header's border of 2^-24), a term's value at most |v8_j|
+    in it.
     O's own rounding: half a step, in fp16 at least 2^-25."""
     import torch
 
     u = torch.finfo(b.q.dtype).eps / 2
-    u_w = 2.0 ** -11
+    u_w = u if copied else 2.0 ** -11
     q = b.q.double().numpy()
     T, G = q.shape[0], b.Hq // b.Hkv
     O, tol_o = np.zeros((T, b.Hq, D)), np.zeros((T, b.Hq, D))
@@ -120,7 +121,8 @@ def bounds(b):
                 O[r, head] = w @ v
                 L[head, r] = lse[:, 0]
                 err = (off + w * (u_w + 2 * (n + 16) * E32)) @ np.abs(v)
-                err += 2.0 ** -24 * (w * f).max(1, keepdims=True) * (seen @ np.abs(v8))
+                if not copied:
+                    err += 2.0 ** -24 * (w * f).max(1, keepdims=True) * (seen @ np.abs(v8))
                 tol_o[r, head] = u * np.abs(O[r, head]) + err * (1 + u) + (2.0 ** -25 if u == 2.0 ** -11 else 1e-38)
                 tol_l[head, r] = np.maximum(total(hi) - lse, lse - total(lo))[:, 0] + n[:, 0] * E32 + 16 * E32 + \
                     4 * E32 * (2 * np.abs(lse[:, 0]) + 68)
@@ -150,9 +152,11 @@ def attend(lca, b, page, layout="nhd", **kw):
 
 
 # ------------------------------------------------------------------ batches
-# requests of few and of many rows
+# requests of few and of many rows; prompts whose pages are copied first (bf16 queries)
 DIRECT = [(300, 40), (90, 3), (500, 75)]
-KINDS = {"direct": (DIRECT, 8, 2)}
+COPIED = [(300, 260), (0, 320)]
+KINDS = {"direct": (DIRECT, 8, 2), "copied": (COPIED, 8, 1)}
+CASES = [("direct", "bf16"), ("direct", "fp16"), ("copied", "bf16")]
 
 
 def values_hidden(b, by):
@@ -218,7 +222,12 @@ def keys_that_take_all(b, by):
         ke[c // 2] += by
 
 
-KEYS = {"hidden": keys_hidden, "against": keys_against, "any": keys_any, "take_all": keys_that_take_all}
+def keys_all_large(b, by):
+    for ke in b.ke:
+        ke += by
+
+
+KEYS = {"all_large": keys_all_large, "hidden": keys_hidden, "against": keys_against, "any": keys_any, "take_all": keys_that_take_all}
 
 
 def batch(kind, dtype, change, by, window=FAR, seed=1):
@@ -260,25 +269,54 @@ def test_the_bound_of_scores(name):
 
 # ------------------------------------------------------------------ values
 @pytest.mark.gpu
-@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
-@pytest.mark.parametrize("kind", list(KINDS))
+@pytest.mark.parametrize("kind,dtype", CASES)
 @pytest.mark.parametrize("by", [6, 9, 14, 24, 33, 45])
 @pytest.mark.parametrize("name", list(VALUES))
 def test_values_of_far_sizes(lca, name, by, kind, dtype):
     change, window = VALUES[name]
     b = batch(kind, dtype, change, 2 * by if "any" in name else by, window)
-    ref = bounds(b)
+    ref = bounds(b, kind == "copied")
     for page, layout in ((16, "nhd"), (64, "hnd")):
         close(*attend(lca, b, page, layout), ref, f"{name}, pages of {page}")
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
-@pytest.mark.parametrize("kind", list(KINDS))
+@pytest.mark.parametrize("kind,dtype", CASES)
 @pytest.mark.parametrize("by", [6, 20, 26, 40])
 @pytest.mark.parametrize("name", list(KEYS))
 def test_keys_of_far_sizes(lca, name, by, kind, dtype):
     b = batch(kind, dtype, KEYS[name], by)
-    ref = bounds(b)
+    ref = bounds(b, kind == "copied")
     for page, layout in ((16, "nhd"), (64, "hnd")):
         close(*attend(lca, b, page, layout), ref, f"{name}, pages of {page}")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("by", [6, 26, 40])
+def test_large_scores_over_the_cache_read_back(lca, by):
+    """The same through lca_attn_paged over a 16-bit cache of the same values: prompts, whose kernel is shared."""
+    import torch
+
+    b = make([(300, 40), (500, 75)], 8, 2, "bf16", 3)
+    keys_all_large(b, by)
+    q, kc, vc, ks, vs, table, q_start, k_len = on_gpu(b, 16)
+    k, v = lca.paged_read_fp8(kc, vc, ks, vs, torch.arange(kc.shape[0], dtype=torch.int32, device="cuda"))
+    close(*lca.attn_paged(q, k, v, table, q_start, k_len, b.mask), bounds(b, copied=True))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_many_requests_without_keys_beside_one_with(lca, dtype):
+    """Rows of requests that hold no keys, more blocks of them than CTAs, before, between and behind one that does."""
+    import torch
+
+    lens = [(0, 300)] * 40 + [(200, 70)] + [(0, 260)] * 40 + [(500, 33)] + [(0, 300)] * 5
+    b = make(lens, 8, 2, dtype, 4)
+    q, kc, vc, ks, vs, table, q_start, k_len = on_gpu(b, 16)
+    held = torch.tensor([c > 0 for c, _ in lens], device="cuda")
+    o, lse = lca.attn_paged_fp8(q, kc, vc, ks, vs, table, q_start, torch.where(held, k_len, 0).to(torch.int32), b.mask)
+    kept = held.repeat_interleave(torch.tensor([w for _, w in lens], device="cuda"))
+    assert not bool(o[~kept].any()) and bool(torch.isneginf(lse[:, ~kept]).all())
+    some = [i for i, (c, _) in enumerate(lens) if c > 0]
+    part = Batch([lens[i] for i in some], 8, 2, *([x[i] for i in some] for x in (b.k8, b.ke, b.v8, b.ve)), b.q[kept.cpu()])
+    close(o[kept], lse[:, kept], bounds(part))
