@@ -515,17 +515,18 @@ LCA_API lca_status lca_paged_read_fp8(const lca_paged_cache_fp8* cache, const in
  *  * otherwise likewise, with 2^-24; and where factors of 32 keys that lie together
  *    are below 2^-22 (K) or 2^-8 (V) of the largest among 128, these 128 keys take
  *    about twice the time.
- *  * where requests have 1536 rows and more on average (max_q_len or Tq /
- *    n_seq), and the tables' entries, all of them, are 1 GiB as 16-bit K and V at
- *    most: the pages that rows attend are read back (lca_paged_read_fp8, fp16
- *    ends at 65504) into the workspace first, and weights are rounded to dtype.
- *    A workspace may so need up to 1 GiB more.
+ *  * where q is bf16, requests have 1536 rows and more on average (max_q_len or
+ *    Tq / n_seq), and the tables' entries, all of them, are 1 GiB as 16-bit K and
+ *    V at most: the pages that rows attend are read back (lca_paged_read_fp8, exact
+ *    in bf16) into the workspace first, and weights are rounded to bf16.  A
+ *    workspace may so need up to 1 GiB more.
  * NaN in the values of a key as in lca_attn_paged. */
 LCA_API lca_status lca_attn_paged_fp8(const void* q, int32_t dtype, const lca_paged_cache_fp8* cache,
                                       const int32_t* block_table, const int32_t* q_start, const int32_t* k_len, void* o,
                                       float* lse, const lca_paged_shape* shape, const lca_mask_desc* mask,
                                       void* workspace, size_t workspace_bytes, void* stream);
-/* As lca_attn_paged_workspace_size.  What max_q_len = 0 needs serves every other. */
+/* As lca_attn_paged_workspace_size.  What max_q_len = 0 needs serves every other,
+ * and queries of both types are served (fp16 ones need no room for a copy). */
 LCA_API lca_status lca_attn_paged_fp8_workspace_size(const lca_paged_shape* shape, const lca_paged_cache_fp8* cache,
                                                      const lca_mask_desc* mask, size_t* bytes);
 

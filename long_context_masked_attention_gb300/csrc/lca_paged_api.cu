@@ -191,6 +191,9 @@ PagedLayout paged_layout(const lca_paged_shape* sh, const lca_paged_cache* c, bo
 // fresh prompts of 101-2047 tokens 466 and 306; 8 requests of 256, 192, 128 and 64
 // tokens at 16K keys 936 and 912, 711 and 720, 490 and 536, 268 and 352, at 1K keys
 // 154 and 130, 122 and 103, 88 and 83, 57 and 62.
+// Only for bf16 queries, whose copy holds every value as it is: fp16 ends at 65504
+// and has nothing below 2^-24, and the same request must not get other scores for
+// the rows that come with it.
 constexpr long long kCopyRows = 1536;
 constexpr long long kCopyBytes = 1LL << 30;
 long long copy_bytes(const lca_paged_shape* sh, const lca_paged_cache* c) {  // of K or V
@@ -218,9 +221,9 @@ struct Layout8 {
   size_t copy = 0, map = 0, total = 0;
   bool copies = false;
 };
-Layout8 layout8(const lca_paged_shape* sh, const lca_paged_cache* c) {
+Layout8 layout8(const lca_paged_shape* sh, const lca_paged_cache* c, bool bf16) {
   Layout8 L;
-  L.copies = copies(sh, c);
+  L.copies = bf16 && copies(sh, c);
   if (!L.copies) {
     L.run = paged_layout(sh, c, true);
     L.total = L.run.total;
@@ -379,7 +382,7 @@ lca_status attend(const Cache& any, int dtype, const void* q, const int32_t* blo
   if (r != LCA_OK) return r;
   Layout8 L8;
   if (c8) {
-    L8 = layout8(shape, cache);
+    L8 = layout8(shape, cache, dtype == LCA_BF16);
   } else {
     L8.run = paged_layout(shape, cache, false);
     L8.total = L8.run.total;
@@ -697,7 +700,7 @@ lca_status lca_attn_paged_fp8_workspace_size(const lca_paged_shape* shape, const
   MaskCtx m;
   r = check_attn(shape, &v, mask, m);
   if (r != LCA_OK) return r;
-  *bytes = layout8(shape, &v).total;
+  *bytes = std::max(layout8(shape, &v, true).total, layout8(shape, &v, false).total);  // q's type is not known here
   return LCA_OK;
 }
 

@@ -156,7 +156,7 @@ def attend(lca, b, page, layout="nhd", **kw):
 DIRECT = [(300, 40), (90, 3), (500, 75)]
 COPIED = [(300, 260), (0, 320)]
 KINDS = {"direct": (DIRECT, 8, 2), "copied": (COPIED, 8, 1)}
-CASES = [("direct", "bf16"), ("direct", "fp16"), ("copied", "bf16")]
+CASES = [(kind, dtype) for kind in KINDS for dtype in ("bf16", "fp16")]
 
 
 def values_hidden(b, by):
@@ -275,7 +275,7 @@ def test_the_bound_of_scores(name):
 def test_values_of_far_sizes(lca, name, by, kind, dtype):
     change, window = VALUES[name]
     b = batch(kind, dtype, change, 2 * by if "any" in name else by, window)
-    ref = bounds(b, kind == "copied")
+    ref = bounds(b, (kind, dtype) == ("copied", "bf16"))
     for page, layout in ((16, "nhd"), (64, "hnd")):
         close(*attend(lca, b, page, layout), ref, f"{name}, pages of {page}")
 
@@ -286,7 +286,7 @@ def test_values_of_far_sizes(lca, name, by, kind, dtype):
 @pytest.mark.parametrize("name", list(KEYS))
 def test_keys_of_far_sizes(lca, name, by, kind, dtype):
     b = batch(kind, dtype, KEYS[name], by)
-    ref = bounds(b, kind == "copied")
+    ref = bounds(b, (kind, dtype) == ("copied", "bf16"))
     for page, layout in ((16, "nhd"), (64, "hnd")):
         close(*attend(lca, b, page, layout), ref, f"{name}, pages of {page}")
 
@@ -320,3 +320,21 @@ def test_many_requests_without_keys_beside_one_with(lca, dtype):
     some = [i for i, (c, _) in enumerate(lens) if c > 0]
     part = Batch([lens[i] for i in some], 8, 2, *([x[i] for i in some] for x in (b.k8, b.ke, b.v8, b.ve)), b.q[kept.cpu()])
     close(o[kept], lse[:, kept], bounds(part))
+
+
+@pytest.mark.gpu
+def test_a_request_gets_the_same_alone_and_in_a_prompt_of_many_rows(lca):
+    """fp16 queries and keys that would pass 65504 as fp16 values: a few tokens alone, in a call that takes the kernel
+    for few rows, and as the last ones of a long prompt."""
+    import torch
+
+    b = make([(0, 500)], 8, 1, "fp16", 6)
+    b.k8[0][:, :, 64:] = 0
+    b.ke[0][::7] += 18
+    b.q[..., :64] *= 2.0 ** -14
+    ref = bounds(b)
+    o, lse = attend(lca, b, 16)
+    close(o, lse, ref)
+    few = Batch([(497, 3)], 8, 1, b.k8, b.ke, b.v8, b.ve, b.q[497:])
+    o3, lse3 = attend(lca, few, 16, max_q_len=3)
+    close(o3, lse3, tuple(x[497:] if i in (0, 2) else x[:, 497:] for i, x in enumerate(ref)))
