@@ -516,8 +516,8 @@ LCA_API lca_status lca_paged_read_fp8(const lca_paged_cache_fp8* cache, const in
  *    are below 2^-22 (K) or 2^-8 (V) of the largest among 128, these 128 keys take
  *    about twice the time.
  *  * where q is bf16, requests have 1536 rows and more on average (max_q_len or
- *    Tq / n_seq), and the tables' entries, all of them, are 1 GiB as 16-bit K and
- *    V at most: the pages that rows attend are read back (lca_paged_read_fp8, exact
+ *    Tq / n_seq), Hq / Hkv is 128 at most, and the tables' entries, all of them,
+ *    are 1 GiB as 16-bit K and V at most: the pages that rows attend are read back (lca_paged_read_fp8, exact
  *    in bf16) into the workspace first, and weights are rounded to bf16.  A
  *    workspace may so need up to 1 GiB more.
  * NaN in the values of a key as in lca_attn_paged. */

@@ -205,7 +205,8 @@ bool copies(const lca_paged_shape* sh, const lca_paged_cache* c) {
   // in doubles: none of these is small enough to multiply unseen
   const double bytes = static_cast<double>(n) * sh->max_pages * c->page_size * c->Hkv * kHeadDim * 4;
   return n > 0 && sh->max_pages > 0 && c->n_pages > 0 && bytes <= static_cast<double>(kCopyBytes) &&
-         rows * (sh->Hq / c->Hkv) >= kCopyRows * n && static_cast<long long>(c->page_size) * c->Hkv <= 0x7FFFFF00LL;
+         rows * (sh->Hq / c->Hkv) >= kCopyRows * n && static_cast<long long>(c->page_size) * c->Hkv <= 0x7FFFFF00LL &&
+         sh->Hq / c->Hkv <= kTile;  // wider groups are not for the kernel that gains by it (many_rows)
 }
 // The copy's layout: [page of a table][head][token][128].
 lca_paged_cache copy_of(const lca_paged_shape* sh, const lca_paged_cache* c, int dtype, uint8_t* at) {

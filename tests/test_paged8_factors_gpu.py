@@ -338,3 +338,15 @@ def test_a_request_gets_the_same_alone_and_in_a_prompt_of_many_rows(lca):
     few = Batch([(497, 3)], 8, 1, b.k8, b.ke, b.v8, b.ve, b.q[497:])
     o3, lse3 = attend(lca, few, 16, max_q_len=3)
     close(o3, lse3, tuple(x[497:] if i in (0, 2) else x[:, 497:] for i, x in enumerate(ref)))
+
+
+@pytest.mark.gpu
+def test_prompts_of_wider_groups_are_not_copied(lca):
+    """136 query heads of a KV head have no use for a copy of the pages: no workspace for one, and the results."""
+    import torch
+
+    b = make([(40, 30)], 136, 1, "bf16", 7)
+    close(*attend(lca, b, 16), bounds(b))
+    _, kc, vc, ks, vs, table, _, _ = on_gpu(b, 16, extra=1 << 14)
+    narrow, wide = (lca.attn_paged_fp8_workspace_size(b.q.cuda(), kc, vc, ks, vs, t, b.mask) for t in (table[:, :8].contiguous(), table))
+    assert narrow == wide
