@@ -211,8 +211,9 @@ __global__ void __launch_bounds__(256) paged_read8_kernel(const PagedRead8Args a
 }
 
 // The same for the block tables of a batch (their entries one after another are
-// the result's pages): of each request the pages with keys that some of its rows
-// attends.  map gets the result's tables, -1 for the others.
+// the result's pages): of each request that the kernel for many rows serves the pages
+// with keys that some of its rows attends.  map gets the result's tables, -1 for
+// the others.
 template <typename T, int kRows>
 __global__ void __launch_bounds__(256)
     paged_copy8_kernel(const __grid_constant__ PagedRead8Args a, const __grid_constant__ PagedAttnArgs m, int* map) {
@@ -221,7 +222,7 @@ __global__ void __launch_bounds__(256)
     const int entry = static_cast<int>(i - seq * m.max_pages);
     int page = -1;
     const SegInfo sg = paged_seg(m, static_cast<int>(seq));
-    if (sg.q_len > 0 && span_hits(hull(m, sg.q_len, sg.k_len, 0, sg.q_len), entry * m.page_size, (entry + 1) * m.page_size))
+    if (sg.q_len > 0 && !few_rows(m, sg.q_len) && span_hits(hull(m, sg.q_len, sg.k_len, 0, sg.q_len), entry * m.page_size, (entry + 1) * m.page_size))
       page = __ldg(m.table + seq * m.table_stride + entry);
     if (first) map[i] = page >= 0 && page < a.n_pages ? static_cast<int>(i) : -1;
     return page;

@@ -155,9 +155,9 @@ struct PagedLayout {
 
 // Rows of an item of the kernel for few rows over an 8-bit cache (a 16-bit one's
 // has 16): as many as the longest request has, or a single token where that one
-// goes to the kernel for many rows.
-int few_tile(const lca_paged_shape* sh, const lca_paged_cache* c) {
-  const long long rows = many_rows(sh, c, true) ? std::min<long long>(sh->Hq / c->Hkv, kPagedFewRows) : most_rows(sh, c);
+// goes to the kernel for many rows (many).
+int few_tile(const lca_paged_shape* sh, const lca_paged_cache* c, bool many) {
+  const long long rows = many ? std::min<long long>(sh->Hq / c->Hkv, kPagedFewRows) : most_rows(sh, c);
   return static_cast<int>(rows >= kPaged8FewRows ? kPaged8FewRows : rows <= 8 ? 8 : (rows + 7) / 8 * 8);
 }
 
@@ -171,7 +171,7 @@ PagedLayout paged_layout(const lca_paged_shape* sh, const lca_paged_cache* c, bo
   };
   L.status = take(16);
   L.arrived = take(sizeof(int) * (kPagedMaxSpans + 1));
-  const int rows = eight ? few_tile(sh, c) : 16;
+  const int rows = eight ? few_tile(sh, c, many_rows(sh, c, true)) : kPagedFewRows;
   L.parts = take(sizeof(float) * 2 * kPagedMaxSpans * rows * (kHeadDim + 2));
   if (many_rows(sh, c, eight)) {
     L.max_blocks = sh->Tq / (2 * tokens_per_tile(sh, c)) + sh->n_seq;
@@ -185,7 +185,8 @@ PagedLayout paged_layout(const lca_paged_shape* sh, const lca_paged_cache* c, bo
 }
 
 // Whether a call over an 8-bit cache makes a 16-bit copy of its tables' pages
-// first and runs on that: it has so many rows per request that reading the keys
+// first, on which its requests of many rows run (those of few stay with the 8-bit
+// kernel and its items of 8 or 16 rows): it has so many rows per request that reading the keys
 // as 8 bits costs more than the copy.  64 query heads on 8, as they are and copied:
 // 2048 tokens at the end of 32K keys 1812 and 1555 us (33 of it the copy), 8
 // fresh prompts of 101-2047 tokens 466 and 306; 8 requests of 256, 192, 128 and 64
@@ -438,35 +439,8 @@ lca_status attend(const Cache& any, int dtype, const void* q, const int32_t* blo
   a.max_pages = shape->max_pages;
   a.page_size = cache->page_size;
   page_divisor(a);
-  Cache run = any;
-  lca_paged_cache copy{};
-  if (L8.copies) {
-    copy = copy_of(shape, cache, dtype, ws + L8.copy);
-    PagedRead8Args c{};
-    read_args(c8, &copy, c);
-    c.n = copy.n_pages;
-    int* map = reinterpret_cast<int*>(ws + L8.map);
-    launch_paged_copy8(c, a, map, fp16, sms, st);
-    LCA_CUDA(cudaGetLastError());
-    run = {&copy, nullptr};
-    cache = run.c;
-    c8 = nullptr;
-    a.table = map;
-    a.table_stride = shape->max_pages;
-  }
   a.q = q;
-  a.kc = cache->k;
-  a.vc = cache->v;
   a.q_stride = shape->q_stride;
-  a.page_stride = cache->page_stride;
-  a.token_stride = cache->token_stride;
-  a.head_stride = cache->head_stride;
-  if (c8) {
-    a.ks = c8->k_scale;
-    a.vs = c8->v_scale;
-    a.scale_page_stride = c8->scale_page_stride;
-    a.scale_head_stride = c8->scale_head_stride;
-  }
   a.o = o;
   a.lse = lse;
   a.status = reinterpret_cast<int*>(ws + L.status);
@@ -476,21 +450,54 @@ lca_status attend(const Cache& any, int dtype, const void* q, const int32_t* blo
   a.Hq = shape->Hq;
   a.Hkv = cache->Hkv;
   a.G = shape->Hq / cache->Hkv;
-  a.n_pages = cache->n_pages;
   const float scale = shape->scale > 0.f ? shape->scale : 1.0f / std::sqrt(static_cast<float>(kHeadDim));
   a.scale_log2 = scale * 1.4426950408889634f;
-  if (cache->n_pages == 0) {  // no key is read; the addresses are only given
-    a.kc = a.vc = q;
-    a.ks = a.vs = static_cast<const uint8_t*>(q);
+  auto over = [&](const Cache& x) {
+    a.kc = x.c->k;
+    a.vc = x.c->v;
+    a.page_stride = x.c->page_stride;
+    a.token_stride = x.c->token_stride;
+    a.head_stride = x.c->head_stride;
+    a.n_pages = x.c->n_pages;
+    if (x.c8) {
+      a.ks = x.c8->k_scale;
+      a.vs = x.c8->v_scale;
+      a.scale_page_stride = x.c8->scale_page_stride;
+      a.scale_head_stride = x.c8->scale_head_stride;
+    }
+    if (x.c->n_pages == 0) {  // no key is read; the addresses are only given
+      a.kc = a.vc = q;
+      a.ks = a.vs = static_cast<const uint8_t*>(q);
+    }
+  };
+  over(any);
+  // with a copy the kernel for many rows has other arguments than the one for few
+  Cache run = any;
+  lca_paged_cache copy{};
+  if (L8.copies) {
+    copy = copy_of(shape, cache, dtype, ws + L8.copy);
+    run = {&copy, nullptr};
   }
-  const bool many = many_rows(shape, cache, c8 != nullptr) && shape->n_seq > 0;
+  const bool many = many_rows(shape, run.c, run.c8 != nullptr) && shape->n_seq > 0;
   a.few = many ? kPagedFewRows : 0x7FFFFFFF;
+  const PagedAttnArgs direct = a;
+  if (L8.copies) {
+    PagedRead8Args c{};
+    read_args(c8, &copy, c);
+    c.n = copy.n_pages;
+    int* map = reinterpret_cast<int*>(ws + L8.map);
+    launch_paged_copy8(c, a, map, fp16, sms, st);
+    LCA_CUDA(cudaGetLastError());
+    over(run);
+    a.table = map;
+    a.table_stride = shape->max_pages;
+  }
   CUtensorMap tq, tk, tv;
   if (many) {
     a.tpt = tokens_per_tile(shape, cache);
     a.box_rows = kTile;
     while (cache->page_size % a.box_rows != 0) a.box_rows /= 2;
-    a.head_first = map_strides(cache).head_first;
+    a.head_first = map_strides(run.c).head_first;
     a.max_blocks = L.max_blocks;
     a.block0 = reinterpret_cast<int*>(ws + L.block0);
     a.line = reinterpret_cast<long long*>(ws + L.line);
@@ -501,16 +508,16 @@ lca_status attend(const Cache& any, int dtype, const void* q, const int32_t* blo
     const cuuint64_t dims[3] = {kHeadDim, static_cast<cuuint64_t>(a.Hq), static_cast<cuuint64_t>(a.Tq)};
     const cuuint64_t strides[2] = {kHeadDim * 2, static_cast<cuuint64_t>(a.q_stride) * 2};
     const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(a.G), static_cast<cuuint32_t>(a.tpt)};
-    if (!encode(&tq, q, map_type(dtype), 3, dims, strides, box) || !cache_map(&tk, cache->k, run, a.box_rows) ||
-        !cache_map(&tv, cache->v, run, a.box_rows))
+    if (!encode(&tq, q, map_type(dtype), 3, dims, strides, box) || !cache_map(&tk, run.c->k, run, a.box_rows) ||
+        !cache_map(&tv, run.c->v, run, a.box_rows))
       return LCA_ERR_CUDA;
   }
   LCA_CUDA(launch_paged_begin(a, many, st));
-  if (many) LCA_CUDA((c8 ? launch_paged_chunk8 : launch_paged_chunk)(tq, tk, tv, a, fp16, sms, st));
+  if (many) LCA_CUDA((run.c8 ? launch_paged_chunk8 : launch_paged_chunk)(tq, tk, tv, a, fp16, sms, st));
   if (shape->Tq > 0)
-    LCA_CUDA(c8 ? launch_paged_decode8(a, few_tile(shape, cache), many, fp16, sms, st)
-                : launch_paged_decode(a, many, fp16, sms, st));
-  if (many) LCA_CUDA(launch_paged_join(a, fp16, c8 != nullptr, sms, st));
+    LCA_CUDA(c8 ? launch_paged_decode8(direct, few_tile(shape, cache, many), many, fp16, sms, st)
+                : launch_paged_decode(direct, many, fp16, sms, st));
+  if (many) LCA_CUDA(launch_paged_join(a, fp16, run.c8 != nullptr, sms, st));
   return LCA_OK;
 }
 

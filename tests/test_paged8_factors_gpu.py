@@ -350,3 +350,17 @@ def test_prompts_of_wider_groups_are_not_copied(lca):
     _, kc, vc, ks, vs, table, _, _ = on_gpu(b, 16, extra=1 << 14)
     narrow, wide = (lca.attn_paged_fp8_workspace_size(b.q.cuda(), kc, vc, ks, vs, t, b.mask) for t in (table[:, :8].contiguous(), table))
     assert narrow == wide
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name,by", [("all_large", 26), ("all_large", 40), ("hidden", 40), ("any", 40)])
+def test_few_rows_beside_prompts_whose_pages_are_copied(lca, name, by):
+    """Single tokens and drafts in the batch of such prompts: as exact as they are without it."""
+    b = make([(300, 500), (200, 1), (0, 520), (60, 2)], 8, 1, "bf16", 2)
+    KEYS[name](b, by)
+    o, lse = attend(lca, b, 16)
+    ref = bounds(b, copied=True)
+    close(o, lse, ref)
+    few = [500, 1021, 1022]
+    near = bounds(b)
+    close(o[few], lse[:, few], tuple(x[few] if i in (0, 2) else x[:, few] for i, x in enumerate(near)))
