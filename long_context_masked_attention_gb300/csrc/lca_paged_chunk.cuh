@@ -1032,7 +1032,7 @@ __device__ __noinline__ void write_hidden(const PagedAttnArgs& a, const Item& in
             }
           }
         }
-        for (uint32_t keys = __ballot_sync(0xFFFFFFFFu, bad & 0x80008000u); keys != 0; keys &= keys - 1) {
+        for (uint32_t keys = __ballot_sync(0xFFFFFFFFu, bad & (k8 ? 0x80808080u : 0x80008000u)); keys != 0; keys &= keys - 1) {
           const int j = __ffs(keys) - 1;
           const V* vj = v + __shfl_sync(0xFFFFFFFFu, at, j) + 32 * c;
           if (!in_span(sp, j0 + j)) continue;

@@ -364,3 +364,36 @@ def test_few_rows_beside_prompts_whose_pages_are_copied(lca, name, by):
     few = [500, 1021, 1022]
     near = bounds(b)
     close(o[few], lse[:, few], tuple(x[few] if i in (0, 2) else x[:, few] for i, x in enumerate(near)))
+
+
+# ------------------------------------------------------------------ far factors and everything else
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("by,col", [(0, 40), (0, 41), (0, 42), (0, 43), (40, 0), (40, 127)])
+def test_nan_beside_far_sizes(lca, by, col, dtype):
+    """A NaN in a key, or in its values, whose factors are 2^by times the others': the rows that do not attend it are
+    those of the batch without it, bit for bit; those that do are NaN, in its column if it is in the values."""
+    import torch
+
+    b = make([(300, 60), (40, 200)], 8, 2, dtype, 8)
+    values_hidden(b, by)
+    if dtype == "fp16":
+        for ve in b.ve:
+            ve -= max(ve.max() - 5, 0)
+    at = [330, 140]  # hidden from the requests' first new tokens: 30 of 60, 100 of 200
+    q, kc, vc, ks, vs, table, q_start, k_len = on_gpu(b, 16)
+    call = lambda: lca.attn_paged_fp8(q, kc, vc, ks, vs, table, q_start, k_len, b.mask)  # noqa: E731
+    o0, lse0 = call()
+    seen = torch.cat([torch.arange(60) >= 30, torch.arange(200) >= 100]).cuda()
+    for c, cols in ((vc, [col]), (kc, slice(None))):
+        old = c.view(torch.uint8).clone()
+        for i, j in enumerate(at):
+            c.view(torch.uint8)[int(table[i, j // 16]), j % 16, 1, col] = 0x7F
+        o, lse = call()
+        assert torch.equal(o[~seen], o0[~seen]) and torch.equal(lse[:, ~seen], lse0[:, ~seen])
+        assert torch.equal(o[:, :4], o0[:, :4])  # the other KV head's
+        assert bool(o[seen][:, 4:, cols].isnan().all())
+        if cols != slice(None):
+            rest = [x for x in range(D) if x != col]
+            assert torch.equal(o[:, :, rest], o0[:, :, rest]) and torch.equal(lse, lse0)
+        c.view(torch.uint8)[:] = old
