@@ -368,6 +368,16 @@ def test_few_rows_beside_prompts_whose_pages_are_copied(lca, name, by):
 
 # ------------------------------------------------------------------ far factors and everything else
 @pytest.mark.gpu
+@pytest.mark.parametrize("name,by", [("hidden", 45), ("negligible", 33), ("descending", 45), ("any", 90), ("any_window", 60)])
+def test_values_of_far_sizes_split_over_keys(lca, name, by):
+    """Items that several CTAs share, whose sums are joined."""
+    change, window = VALUES[name]
+    b = make([(5000, 40), (1000, 130), (0, 33)], 8, 2, "bf16", 5, window)
+    change(b, by)
+    close(*attend(lca, b, 64), bounds(b))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 @pytest.mark.parametrize("by,col", [(0, 40), (0, 41), (0, 42), (0, 43), (40, 0), (40, 127)])
 def test_nan_beside_far_sizes(lca, by, col, dtype):
