@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(256)
 // nothing where 8 query heads share a KV head, and more of them share what a
 // key's conversion costs: 32 requests of 1K-16K keys take 99 us with 16 rows, 127
 // with 24, 157 with 32; with 40 their sums spill and they take 300, the kernel for
-// many rows 165.  The operands K and V^T come from shared memory by 16-byte loads and are converted in
+// many rows 172.  The operands K and V^T come from shared memory by 16-byte loads and are converted in
 // registers.  The order of the 128 products of a score, and of the rows of O^T,
 // is free, so a lane takes the bytes that lie together: of keys lane / 4 and 8
 // more the pieces lane % 4 and lane % 4 + 4 (four values are two registers of one

@@ -186,15 +186,15 @@ PagedLayout paged_layout(const lca_paged_shape* sh, const lca_paged_cache* c, bo
 
 // Whether a call over an 8-bit cache makes a 16-bit copy of its tables' pages
 // first, on which its requests of many rows run (those of few stay with the 8-bit
-// kernel and its items of 8 or 16 rows): it has so many rows per request that reading the keys
-// as 8 bits costs more than the copy.  64 query heads on 8, as they are and copied:
-// 2048 tokens at the end of 32K keys 1812 and 1555 us (33 of it the copy), 8
-// fresh prompts of 101-2047 tokens 466 and 306; 8 requests of 256, 192, 128 and 64
-// tokens at 16K keys 936 and 912, 711 and 720, 490 and 536, 268 and 352, at 1K keys
-// 154 and 130, 122 and 103, 88 and 83, 57 and 62.
+// kernel and its items of 8 or 16 rows): it has so many rows per request that
+// reading the keys as 8 bits costs more than the copy.  64 query heads on 8, as
+// they are and copied: 2048 tokens at the end of 32K keys 1865 and 1565 us (33 of it
+// the copy), 8 fresh prompts of 101-2047 tokens 460 and 307; 8 requests of 256, 192,
+// 128 and 64 tokens at 16K keys 967 and 925, 737 and 727, 509 and 536, 275 and 352, at
+// 1K keys 155 and 124, 122 and 103, 90 and 83, 59 and 62.
 // Only for bf16 queries, whose copy holds every value as it is: fp16 ends at 65504
 // and has nothing below 2^-24, and the same request must not get other scores for
-// the rows that come with it.
+// the rows that come with it (that chunk takes 1824 us, those prompts 448).
 constexpr long long kCopyRows = 1536;
 constexpr long long kCopyBytes = 1LL << 30;
 long long copy_bytes(const lca_paged_shape* sh, const lca_paged_cache* c) {  // of K or V

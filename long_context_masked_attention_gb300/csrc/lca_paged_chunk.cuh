@@ -30,9 +30,10 @@
 // 64 % of the time, and power decides the rest); 8 prompts of 101-2047 tokens 284-295
 // us, where an item of 9 tiles takes 18 us of which 14-15 are tiles; 5 tokens of
 // each of 32 requests at 1K-16K keys 163 us (0.78 of a copy's rate).
-// Over an 8-bit cache (see the converters) the last take 170 us, which no one thing
-// bounds: without the conversions they would take 142, without the softmax 155,
-// without both 133.  Longer prompts do not come here with 8 bits (lca_paged_api.cu).
+// Over an 8-bit cache (see the converters) the last take 172 us, fp16 171, which no
+// one thing bounds: of 165 at the time, 142 were left without the conversions, 155
+// without the softmax, 133 without both.  2048 tokens at 32K take 1865 us from 8 bits;
+// bf16 prompts come here as a 16-bit copy where it fits (lca_paged_api.cu).
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -380,7 +381,7 @@ __device__ __forceinline__ void producer(const PagedAttnArgs& a, const CUtensorM
   constexpr int kStages = k8 ? C::kRaw : C::kStages, kFull = k8 ? C::RAWFULL : C::KVFULL, kEmpty = k8 ? C::RAWEMPTY : C::KVEMPTY;
   constexpr int kHalves = k8 ? 1 : 2;  // of a row, 128 bytes each
   constexpr uint32_t kBytes = kHalves * kChunkBytes;
-  // Pages by products: 32 requests of 5 tokens over an 8-bit cache 170 -> 165 us.  A
+  // Pages by products: 32 requests of 5 tokens over an 8-bit cache 170 -> 165 us then.  A
   // 16-bit one's prompts gain 1 % and a chunk of 2048 at 32K loses 0.7, so it divides.
   const int lane = threadIdx.x & 31;
   const int boxes = kTile / a.box_rows;  // per tile and half
@@ -456,7 +457,7 @@ __device__ __forceinline__ void producer(const PagedAttnArgs& a, const CUtensorM
 // An 8-bit cache: the four last warps make the tiles that the products read, in
 // fp16, which holds e4m3 exactly.  What this costs in instructions decides: a
 // product with the row's factor in 32 bits and a rounding to bf16 took a chunk of
-// 2048 tokens at 32K keys 2555 us, a conversion and a product of pairs takes 1812
+// 2048 tokens at 32K keys 2555 us, a conversion and a product of pairs takes 1865
 // (with a 16-bit cache the tensor pipe and power take 1510; here it is the softmax
 // warps that are slowed, by four more warps and 128 registers a thread).  So factors
 // are made to fit fp16: those of a tile are relative to the
@@ -469,6 +470,8 @@ __device__ __forceinline__ void producer(const PagedAttnArgs& a, const CUtensorM
 // are, K times 1 and V times 2^7, and the softmax warps read the keys' factors
 // themselves (far_scores), which also rounds the scores before their maximum is
 // taken off, so that a warp whose rows of q could make huge ones asks for it too.
+// The looks for such keys and rows cost 2-4 % where there are none (that chunk 1805
+// -> 1865 us, the drafts above 165 -> 172).
 // bf16 queries are turned into fp16 first, each row by a power of
 // two that brings its largest value to 2^14 (see lca_paged8.cu).
 //
@@ -923,7 +926,7 @@ __device__ __forceinline__ float row_exp(uint32_t tS, float sl2, float base) {
 // what p may become by 2^5, at 2^28), which is too coarse to be taken off the product
 // that row_exp has not rounded: p would leave fp16, or be 0 for every key.  The
 // warp's scores are rounded first then, as m is.  (Over an 8-bit cache far_scores
-// does it.)
+// does it.)  The look for them costs prompts over 16 bits 0.3-0.8 %.
 template <typename M>
 constexpr float kHugeScore = 0x1p28f;
 template <>
