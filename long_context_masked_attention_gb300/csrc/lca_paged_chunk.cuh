@@ -559,23 +559,29 @@ __device__ __forceinline__ void converter(const PagedAttnArgs& a, uint8_t* sQ, c
     const Item inf = items[slot];
     if (!inf.valid) return;
     const int n = inf.n;
+    if (!waitw(&bar[C::QFULL], it & 1, a, 93)) return;
+    // QREADY holds the products back also where q stays as it is: a barrier that is
+    // waited for by parity must not go on by two phases meanwhile.  An item without
+    // tiles may then lose its q at once, so nothing is read of it.
+    constexpr bool kHalve = std::is_same<T, __nv_bfloat16>::value;
+    if constexpr (!kHalve) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar[C::QREADY]);
+    }
     int q_most = -128;  // exponent of the warp's rows
-    // fp16 queries of an item without tiles: the products do not wait for this
-    // warp, so that the queries may be those of a later item by now
-    if (std::is_same<T, __nv_bfloat16>::value || n > 0) {
-      if (!waitw(&bar[C::QFULL], it & 1, a, 93)) return;
+    if (kHalve || n > 0) {
 #pragma unroll 1
       for (int x = 0; x < (inf.narrow ? 1 : 2); ++x) {
         const int e = q_row_exponent<T>(smem_u32(sQ) + x * kTileBytes, row), tok = row / a.G;
         if (tok < a.tpt && inf.tok0 + x * a.tpt + tok < inf.q_len) q_most = max(q_most, e);
-        if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+        if constexpr (kHalve) {
           q_exp[(it & 1) * 256 + x * 128 + row] = static_cast<int8_t>(e);
           halve_q_row(smem_u32(sQ) + x * kTileBytes, row, e);
         }
       }
       q_most = __reduce_max_sync(0xFFFFFFFFu, q_most);
     }
-    if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+    if constexpr (kHalve) {
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar[C::QREADY]);
@@ -687,7 +693,6 @@ __device__ __forceinline__ void mma_issuer(const PagedAttnArgs& a, uint8_t* sQ, 
   using M = Operand<T, k8>;
   constexpr uint32_t kIdescS = idesc<M>(false);  // S = Q K^T (both K-major)
   constexpr uint32_t kIdescO = idesc<M>(true);   // O += P V (P in TMEM, V N-major)
-  constexpr int kQ = std::is_same<T, M>::value ? C::QFULL : C::QREADY;
   const uint64_t dQ0 = sdesc_sw128(smem_u32(sQ), 16, 1024);
   const uint64_t dK0 = sdesc_sw128(smem_u32(sKV), 16, 1024);
   const uint64_t dV0 = sdesc_sw128(smem_u32(sKV), kChunkBytes, 1024);
@@ -719,7 +724,8 @@ __device__ __forceinline__ void mma_issuer(const PagedAttnArgs& a, uint8_t* sQ, 
       const Item& inf = items[slot];
       if (!inf.valid) return;
       const int n = inf.n;
-      if (!waitw(&bar[kQ], it & 1, a, 71)) goto abort;
+      if (std::is_same<T, M>::value && !waitw(&bar[C::QFULL], it & 1, a, 71)) goto abort;
+      if (k8 && !waitw(&bar[C::QREADY], it & 1, a, 71)) goto abort;
       auto kv_full = [&](uint32_t idx) { return waitw(&bar[C::KVFULL + idx % kStages], (idx / kStages) & 1, a, 72); };
       if (inf.narrow) {
         // S(0), S(1), PV(0), S(2), PV(1), ...: tile t in score buffer t & 1

@@ -305,13 +305,15 @@ def test_large_scores_over_the_cache_read_back(lca, by):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("by", [0, 26])
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
-def test_many_requests_without_keys_beside_one_with(lca, dtype):
+def test_many_requests_without_keys_beside_one_with(lca, dtype, by):
     """Rows of requests that hold no keys, more blocks of them than CTAs, before, between and behind one that does."""
     import torch
 
     lens = [(0, 300)] * 40 + [(200, 70)] + [(0, 260)] * 40 + [(500, 33)] + [(0, 300)] * 5
     b = make(lens, 8, 2, dtype, 4)
+    keys_all_large(b, by)
     q, kc, vc, ks, vs, table, q_start, k_len = on_gpu(b, 16)
     held = torch.tensor([c > 0 for c, _ in lens], device="cuda")
     o, lse = lca.attn_paged_fp8(q, kc, vc, ks, vs, table, q_start, torch.where(held, k_len, 0).to(torch.int32), b.mask)
