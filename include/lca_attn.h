@@ -515,11 +515,12 @@ LCA_API lca_status lca_paged_read_fp8(const lca_paged_cache_fp8* cache, const in
  *  * otherwise likewise, with 2^-24; and where factors of 32 keys that lie together
  *    are below 2^-22 (K) or 2^-8 (V) of the largest among 128, these 128 keys take
  *    about twice the time.
- *  * where q is bf16, requests have 1536 rows and more on average (max_q_len or
- *    Tq / n_seq), Hq / Hkv is 128 at most, and the tables' entries, all of them,
- *    are 1 GiB as 16-bit K and V at most: the pages that rows attend are read back (lca_paged_read_fp8, exact
- *    in bf16) into the workspace first, and weights are rounded to bf16.  A
- *    workspace may so need up to 1 GiB more.
+ *  * instead of that, where q is bf16, requests have 1536 rows and more on average
+ *    (max_q_len or Tq / n_seq), Hq / Hkv is 128 at most, and the tables' entries,
+ *    all of them, are 1 GiB as 16-bit K and V at most: the pages that those rows
+ *    attend are read back (lca_paged_read_fp8, exact in bf16) into the workspace
+ *    first, and weights are rounded to bf16, ones below 2^-126 of the row's
+ *    largest to 0.  A workspace may so need up to 1 GiB more.
  * NaN in the values of a key as in lca_attn_paged. */
 LCA_API lca_status lca_attn_paged_fp8(const void* q, int32_t dtype, const lca_paged_cache_fp8* cache,
                                       const int32_t* block_table, const int32_t* q_start, const int32_t* k_len, void* o,

@@ -292,16 +292,17 @@ def test_keys_of_far_sizes(lca, name, by, kind, dtype):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("by", [6, 26, 40])
-def test_large_scores_over_the_cache_read_back(lca, by):
+@pytest.mark.parametrize("dtype,by,q_by", [("bf16", 6, 0), ("bf16", 26, 0), ("bf16", 40, 0), ("fp16", 6, 0), ("fp16", 13, 7), ("fp16", 13, 12)])
+def test_large_scores_over_the_cache_read_back(lca, dtype, by, q_by):
     """The same through lca_attn_paged over a 16-bit cache of the same values: prompts, whose kernel is shared."""
     import torch
 
-    b = make([(300, 40), (500, 75)], 8, 2, "bf16", 3)
+    b = make([(300, 40), (500, 75)], 8, 2, dtype, 3)
     keys_all_large(b, by)
+    b.q *= 2.0 ** q_by
     q, kc, vc, ks, vs, table, q_start, k_len = on_gpu(b, 16)
-    k, v = lca.paged_read_fp8(kc, vc, ks, vs, torch.arange(kc.shape[0], dtype=torch.int32, device="cuda"))
-    close(*lca.attn_paged(q, k, v, table, q_start, k_len, b.mask), bounds(b, copied=True))
+    k, v = lca.paged_read_fp8(kc, vc, ks, vs, torch.arange(kc.shape[0], dtype=torch.int32, device="cuda"), dtype=b.q.dtype)
+    close(*lca.attn_paged(q, k, v, table, q_start, k_len, b.mask), bounds(b, copied=dtype == "bf16"))
 
 
 @pytest.mark.gpu
