@@ -608,8 +608,9 @@ __device__ __forceinline__ void converter(const PagedAttnArgs& a, uint8_t* sQ, c
       }
       cp_async_commit();
     };
-    // the exponents of this row's factors (of a key that no row attends any, not the
-    // largest and not far from it), and what the warp's largest are, for the other warps
+    // the exponents of this row's factors (where no row attends its key, ones that neither
+    // count as the largest nor lie below it), and what the warp's largest are, for the
+    // other warps
     int ek = 0, ev = 0;
     auto meet = [&](int t) {
       const uint32_t tile = tiles + t;
